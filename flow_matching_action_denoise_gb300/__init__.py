@@ -23,6 +23,10 @@ __all__ = [
     "FMT_BF16", "FMT_FP8", "FMT_NVFP4", "FLAG_USE_GRAPH", "FLAG_USE_PDL", "FLAG_FUSED_CONSUMERS",
     "FLAG_O_CONSUMER_IN_GEMM", "COND_TIME", "COND_GIVEN",
     "ABI_VERSION", "STATUS",
+    "KvCache", "KvBatch", "Rope", "refresh_prefix_pages", "kv_workspace_size", "kv_reserve", "kv_fork", "kv_release",
+    "kv_compact", "rope_table", "rope_append", "paged_attention_workspace_size", "paged_attention", "norm_quant",
+    "ROPE_HALF", "ROPE_INTERLEAVED", "ROPE_PLAIN", "ROPE_LINEAR", "ROPE_BASE", "ROPE_BY_PARTS",
+    "KV_NO_PAGES", "KV_BAD_ENTRY", "KV_ROW_FULL",
 ]
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -32,6 +36,9 @@ ABI_VERSION = 3
 FMT_BF16, FMT_FP8, FMT_NVFP4 = 0, 1, 2
 FLAG_USE_GRAPH, FLAG_USE_PDL, FLAG_FUSED_CONSUMERS, FLAG_O_CONSUMER_IN_GEMM = 1, 2, 4, 8
 COND_TIME, COND_GIVEN = 0, 1
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+ROPE_PLAIN, ROPE_LINEAR, ROPE_BASE, ROPE_BY_PARTS = 0, 1, 2, 3
+KV_NO_PAGES, KV_BAD_ENTRY, KV_ROW_FULL = 1, 2, 4   # bits of status[0] of the kv_* calls
 STATUS = {0: "FM_OK", 1: "FM_ERR_INVALID_ARG", 2: "FM_ERR_SHAPE", 3: "FM_ERR_ALIGN",
           4: "FM_ERR_WORKSPACE", 5: "FM_ERR_CUDA", 6: "FM_ERR_STATE_MISMATCH",
           7: "FM_ERR_DEVICE", 8: "FM_ERR_UNSUPPORTED"}
@@ -46,6 +53,8 @@ EXPORTS = [
     "fm_session_workspace_size", "fm_session_create", "fm_session_fork", "fm_abi_sizes", "fm_standalone_status",
     "fm_warm_trace_size", "fm_decode_warm_trace", "fm_test_launch_kernel", "fm_decode_timeline",
     "fm_test_skinny_gemm_tile", "fm_test_pdl_chain", "fm_test_grid_barrier", "fm_test_attn_plan",
+    "refresh_prefix_pages", "fm_kv_workspace_size", "fm_kv_reserve", "fm_kv_fork", "fm_kv_release", "fm_kv_compact",
+    "fm_rope_table", "fm_rope_append", "fm_paged_attention_workspace_size", "fm_paged_attention", "fm_norm_quant",
 ]
 
 
@@ -80,6 +89,33 @@ class FmWeights(ctypes.Structure):
     _fields_ = [("layers", ctypes.POINTER(FmLayerWeights))] + [
         (n, ctypes.c_void_p) for n in
         ("w_in", "b_in", "w_out", "b_out", "gamma_f", "w_mod_f", "b_mod_f", "conds")]
+
+
+class FmKvCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("fmt", ctypes.c_int),
+                ("layers", ctypes.c_int), ("pages", ctypes.c_int), ("page_tokens", ctypes.c_int),
+                ("Hkv", ctypes.c_int), ("Dh", ctypes.c_int),
+                ("layer_stride", ctypes.c_int64), ("page_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("table", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("refs", ctypes.c_void_p),
+                ("seqs", ctypes.c_int), ("table_stride", ctypes.c_int)]
+
+
+class FmKvBatch(ctypes.Structure):
+    _fields_ = [("start", ctypes.c_void_p), ("seq", ctypes.c_void_p), ("n", ctypes.c_int), ("tokens", ctypes.c_int),
+                ("max_tokens", ctypes.c_int), ("max_len", ctypes.c_int)]
+
+
+class FmRopeConfig(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int), ("scaling", ctypes.c_int), ("theta", ctypes.c_double),
+                ("factor", ctypes.c_double), ("original_len", ctypes.c_double), ("beta_fast", ctypes.c_double),
+                ("beta_slow", ctypes.c_double)]
+
+
+class FmRope(ctypes.Structure):
+    _fields_ = [("freq", ctypes.c_void_p), ("rotary_dim", ctypes.c_int), ("layout", ctypes.c_int),
+                ("magnitude", ctypes.c_float)]
 
 
 _lib = None
@@ -144,6 +180,21 @@ def load() -> ctypes.CDLL:
         "fm_test_pdl_chain": (i, [i, i, i, i, i, i, i, vp, sz, ctypes.POINTER(ctypes.c_float)]),
         "fm_test_grid_barrier": (i, [i, i, i, i, ctypes.c_ulonglong, vp, vp, vp]),
         "fm_test_attn_plan": (i, [vp, ctypes.POINTER(i), ctypes.POINTER(i)]),
+        # structs by address (the binding keeps them beside the tensors they point at)
+        "refresh_prefix_pages": (i, [vp, i, i, vp, i, i, vp]),
+        "fm_kv_workspace_size": (i, [vp, i, ctypes.POINTER(sz)]),
+        "fm_kv_reserve": (i, [vp, vp, vp, i, vp, vp, sz, vp]),
+        "fm_kv_fork": (i, [vp, vp, vp, i, vp, vp]),
+        "fm_kv_release": (i, [vp, vp, vp, i, vp, vp]),
+        "fm_kv_compact": (i, [vp, vp, vp, sz, vp]),
+        "fm_rope_table": (i, [vp, vp, vp]),
+        "fm_rope_append": (i, [vp, i, vp, vp, vp, ctypes.c_int64, i, vp, ctypes.c_int64, vp, ctypes.c_int64, vp,
+                               ctypes.c_int64, vp, vp]),
+        "fm_paged_attention_workspace_size": (i, [vp, vp, i, ctypes.POINTER(sz)]),
+        "fm_paged_attention": (i, [vp, i, vp, vp, ctypes.c_int64, i, ctypes.c_float, i, i, vp, ctypes.c_int64, vp, sz,
+                                   vp]),
+        "fm_norm_quant": (i, [vp, ctypes.c_int64, i, vp, ctypes.c_int64, vp, i, i, ctypes.c_float, vp, ctypes.c_int64,
+                              vp, vp, i, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -491,6 +542,257 @@ def fm_test_layer(p: int, x_in, layer: int, step: int, x_out, q_out, stream=None
            "fm_test_layer", p)
 
 
+# ---------------------------------------------------------------- the paged prefix cache
+
+def _bad(where: str, why: str):
+    raise FmError(1, where, why)
+
+
+def _tensor(x, where: str, name: str, dtypes, device, shape=None):
+    """x's address after checking what the C side cannot see: the type, the device and the shape (None: any extent)."""
+    if x.dtype not in dtypes:
+        _bad(where, f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {x.dtype}")
+    if x.device != device:
+        _bad(where, f"{name} is on {x.device}, expected {device}")
+    if shape is not None and (x.dim() != len(shape) or any(a is not None and a != b for a, b in zip(shape, x.shape))):
+        _bad(where, f"{name} must have shape {shape}, got {tuple(x.shape)}")
+    return x.data_ptr()
+
+
+def _rows(x, where: str, name: str, dtypes, device, shape):
+    """(address, elements between rows) of x [rows][heads][dim] or [rows][dim] with the rows' own elements contiguous."""
+    ptr = _tensor(x, where, name, dtypes, device, shape)
+    inner = 1
+    for size, stride in zip(reversed(x.shape[1:]), reversed(x.stride()[1:])):
+        if size != 1 and stride != inner:
+            _bad(where, f"{name}: a row's elements must be contiguous")
+        inner *= size
+    return ptr, (x.stride(0) if x.shape[0] > 1 else inner)
+
+
+def _ints(x, where: str, name: str, device, count: int):
+    import torch
+    ptr = _tensor(x, where, name, (torch.int32,), device)
+    if not x.is_contiguous() or x.numel() < count:
+        _bad(where, f"{name} must be contiguous with at least {count} elements")
+    return ptr
+
+
+def _here(device, stream, where: str):
+    """The stream to use on `device`: the given one, or that device's current one. The library works on the current
+    device, so the two must agree."""
+    import torch
+    if torch.cuda.current_device() != device.index:
+        _bad(where, f"the tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
+    return _stream(stream)
+
+
+class KvCache:
+    """A paged cache over caller-owned tensors (kept alive here).
+
+    k, v: [layers][pages][page_tokens][Hkv][Dh], bfloat16 or float8_e4m3fn, last dim contiguous, the other strides
+    free (heads may lie outside of the tokens) and the same for both; table: int32 [seqs][max pages] (-1 = none);
+    lens: int32 [seqs]; refs: int32 [pages], needed by the kv_* calls; k_scale, v_scale: float32 [layers] for FP8.
+    """
+
+    def __init__(self, k, v, table, lens, refs=None, k_scale=None, v_scale=None):
+        import torch
+        where = "KvCache"
+        if k.dim() != 5 or v.shape != k.shape or v.dtype != k.dtype:
+            _bad(where, "k and v must be [layers][pages][page_tokens][Hkv][Dh] and alike")
+        if any(a != b for a, b, n in zip(k.stride(), v.stride(), k.shape) if n > 1):
+            _bad(where, "k and v must have the same strides")
+        if k.stride(4) != 1:
+            _bad(where, "the last dim of k and v must be contiguous")
+        if not k.is_cuda:
+            _bad(where, "k must be a device tensor")
+        self.device = k.device
+        fp8 = k.dtype == torch.float8_e4m3fn
+        s = FmKvCache()
+        s.k = _tensor(k, where, "k", (torch.bfloat16, torch.float8_e4m3fn), self.device)
+        s.v = _tensor(v, where, "v", (k.dtype,), self.device)
+        s.fmt = FMT_FP8 if fp8 else FMT_BF16
+        s.layers, s.pages, s.page_tokens, s.Hkv, s.Dh = k.shape
+        s.layer_stride, s.page_stride, s.token_stride, s.head_stride = k.stride()[:4]
+        if fp8:
+            for name, x in (("k_scale", k_scale), ("v_scale", v_scale)):
+                if x is None or not x.is_contiguous() or x.numel() != s.layers:
+                    _bad(where, f"an FP8 cache needs {name}: float32 [layers], contiguous")
+                setattr(s, name, _tensor(x, where, name, (torch.float32,), self.device))
+        if table.dim() != 2 or not table.is_contiguous() or lens.numel() != table.shape[0]:
+            _bad(where, "table must be [seqs][max pages] contiguous and lens [seqs]")
+        s.seqs, s.table_stride = table.shape
+        s.table = _ints(table, where, "table", self.device, table.numel())
+        s.lens = _ints(lens, where, "lens", self.device, s.seqs)
+        if refs is not None:
+            s.refs = _ints(refs, where, "refs", self.device, s.pages)
+        self.struct = s
+        self.addr = ctypes.addressof(s)
+        self.k, self.v, self.table, self.lens, self.refs = k, v, table, lens, refs
+        self.k_scale, self.v_scale = k_scale, v_scale
+
+
+class KvBatch:
+    """The new tokens of a step (fm_kv_batch): start int32 [n + 1], tokens rows of the packed arrays, bounds on an
+    entry's new tokens and on the sequences' lengths, seq int32 [n] (None: entry i is sequence i)."""
+
+    def __init__(self, start, tokens: int, max_tokens: int, max_len: int, seq=None):
+        n = start.numel() - 1
+        if n < 0:
+            _bad("KvBatch", "start must have at least one element")
+        self.device = start.device
+        s = FmKvBatch()
+        s.start = _ints(start, "KvBatch", "start", self.device, 1)
+        if seq is not None:
+            s.seq = _ints(seq, "KvBatch", "seq", self.device, n)
+        s.n, s.tokens, s.max_tokens, s.max_len = n, int(tokens), int(max_tokens), int(max_len)
+        self.struct = s
+        self.addr = ctypes.addressof(s)
+        self.start, self.seq, self.tokens = start, seq, int(tokens)
+
+
+def rope_table(rotary_dim: int, theta: float = 10000.0, scaling: int = ROPE_PLAIN, factor: float = 1.0,
+               original_len: float = 0.0, beta_fast: float = 32.0, beta_slow: float = 1.0):
+    """(frequencies in turns per position * 2^64 as a host uint64 array [rotary_dim / 2], factor on cos and sin)."""
+    c = FmRopeConfig(int(rotary_dim), int(scaling), float(theta), float(factor), float(original_len), float(beta_fast),
+                     float(beta_slow))
+    freq = np.zeros(max(int(rotary_dim), 0) // 2, dtype=np.uint64)
+    mag = ctypes.c_float()
+    _check(load().fm_rope_table(ctypes.addressof(c), freq.ctypes.data, ctypes.addressof(mag)), "fm_rope_table")
+    return freq, mag.value
+
+
+class Rope:
+    """Rotary positions: the device table of rope_table and the layout of the pairs."""
+
+    def __init__(self, rotary_dim: int, theta: float = 10000.0, half: bool = True, scaling: int = ROPE_PLAIN,
+                 factor: float = 1.0, original_len: float = 0.0, beta_fast: float = 32.0, beta_slow: float = 1.0,
+                 device="cuda"):
+        import torch
+        freq, mag = rope_table(rotary_dim, theta, scaling, factor, original_len, beta_fast, beta_slow)
+        self.freq = torch.from_numpy(freq.view(np.int64)).to(device)
+        self.device = self.freq.device
+        self.struct = FmRope(self.freq.data_ptr(), int(rotary_dim), ROPE_HALF if half else ROPE_INTERLEAVED, mag)
+        self.addr = ctypes.addressof(self.struct)
+
+
+def refresh_prefix_pages(p: int, tok_begin: int, tok_end: int, cache: KvCache, seq: int, seq_tok: int = 0, stream=None):
+    _check(load().refresh_prefix_pages(p, tok_begin, tok_end, cache.addr, seq, seq_tok,
+                                       _here(cache.device, stream, "refresh_prefix_pages")), "refresh_prefix_pages", p)
+
+
+def kv_workspace_size(cache: KvCache, n: int = 0) -> int:
+    """Bytes of workspace of kv_reserve for n sequences and of kv_compact (n = 0)."""
+    b = ctypes.c_size_t()
+    _check(load().fm_kv_workspace_size(cache.addr, n, ctypes.byref(b)), "fm_kv_workspace_size")
+    return b.value
+
+
+def _workspace(ws, where: str, device):
+    if ws is None:
+        return None, 0
+    if ws.device != device or not ws.is_contiguous():
+        _bad(where, "the workspace must be a contiguous tensor on the cache's device")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def kv_reserve(cache: KvCache, seq, count, status, workspace, stream=None):
+    """Room for count[i] more tokens of sequence seq[i]; status int32 [2] on the device."""
+    d, n, w = cache.device, seq.numel(), "fm_kv_reserve"
+    ws, nb = _workspace(workspace, w, d)
+    _check(load().fm_kv_reserve(cache.addr, _ints(seq, w, "seq", d, n), _ints(count, w, "count", d, n), n,
+                                _ints(status, w, "status", d, 2), ws, nb, _here(d, stream, w)), w)
+
+
+def kv_fork(cache: KvCache, src, dst, status, stream=None):
+    """The empty sequence dst[i] names the pages of src[i]."""
+    d, n, w = cache.device, src.numel(), "fm_kv_fork"
+    _check(load().fm_kv_fork(cache.addr, _ints(src, w, "src", d, n), _ints(dst, w, "dst", d, n), n,
+                             _ints(status, w, "status", d, 2), _here(d, stream, w)), w)
+
+
+def kv_release(cache: KvCache, seq, status, keep=None, stream=None):
+    """Cut sequence seq[i] back to keep[i] tokens (None: to none)."""
+    d, n, w = cache.device, seq.numel(), "fm_kv_release"
+    _check(load().fm_kv_release(cache.addr, _ints(seq, w, "seq", d, n),
+                                None if keep is None else _ints(keep, w, "keep", d, n), n,
+                                _ints(status, w, "status", d, 2), _here(d, stream, w)), w)
+
+
+def kv_compact(cache: KvCache, status, workspace, stream=None):
+    """Move the live pages to the front of the pool."""
+    d, w = cache.device, "fm_kv_compact"
+    ws, nb = _workspace(workspace, w, d)
+    _check(load().fm_kv_compact(cache.addr, _ints(status, w, "status", d, 2), ws, nb, _here(d, stream, w)), w)
+
+
+def rope_append(cache: KvCache, layer: int, batch: KvBatch, rope: Rope, q, k, v, q_out, positions=None, stream=None):
+    """Rotate q [tokens][H][Dh] into q_out and k [tokens][Hkv][Dh] into the pages, store v there (all bfloat16; q and
+    q_out None: keys and values only)."""
+    import torch
+    d, w, s = cache.device, "fm_rope_append", cache.struct
+    bf, T = (torch.bfloat16,), batch.tokens
+    if batch.device != d or rope.device != d:
+        _bad(w, "the cache, the batch and the rotary table must be on one device")
+    H, qp, qs, op, os_ = 0, None, 0, None, 0
+    if q is not None:
+        H = q.shape[1]
+        qp, qs = _rows(q, w, "q", bf, d, (T, H, s.Dh))
+        op, os_ = _rows(q_out, w, "q_out", bf, d, (T, H, s.Dh))
+    kp, ks = _rows(k, w, "k", bf, d, (T, s.Hkv, s.Dh))
+    vp, vs = _rows(v, w, "v", bf, d, (T, s.Hkv, s.Dh))
+    _check(load().fm_rope_append(cache.addr, layer, batch.addr, rope.addr, qp, qs, H, kp, ks, vp, vs, op, os_,
+                                 None if positions is None else _ints(positions, w, "positions", d, T),
+                                 _here(d, stream, w)), w)
+
+
+def paged_attention_workspace_size(cache: KvCache, batch: KvBatch, H: int) -> int:
+    b = ctypes.c_size_t()
+    _check(load().fm_paged_attention_workspace_size(cache.addr, batch.addr, H, ctypes.byref(b)),
+           "fm_paged_attention_workspace_size")
+    return b.value
+
+
+def paged_attention(cache: KvCache, layer: int, batch: KvBatch, q, out, workspace=None, scale: float | None = None,
+                    causal: bool = True, window: int = 0, stream=None):
+    """Attention of q [tokens][H][Dh] (bfloat16) over the batch's sequences into out; scale None: 1 / sqrt(Dh)."""
+    import torch
+    d, w, s = cache.device, "fm_paged_attention", cache.struct
+    bf, T, H = (torch.bfloat16,), batch.tokens, q.shape[1]
+    if batch.device != d:
+        _bad(w, "the cache and the batch must be on one device")
+    qp, qs = _rows(q, w, "q", bf, d, (T, H, s.Dh))
+    op, os_ = _rows(out, w, "out", bf, d, (T, H, s.Dh))
+    ws, nb = _workspace(workspace, w, d)
+    _check(load().fm_paged_attention(cache.addr, layer, batch.addr, qp, qs, H,
+                                     s.Dh ** -0.5 if scale is None else float(scale), int(bool(causal)), int(window),
+                                     op, os_, ws, nb, _here(d, stream, w)), w)
+
+
+def norm_quant(x, r, gamma, eps: float, x_out, codes, scales, block: int = 0, stream=None):
+    """x [T][d] (float32 or bfloat16) + r (bfloat16 or None) -> x_out (or None), E4M3 codes (float8_e4m3fn or uint8)
+    of its RMS norm times gamma (float32 [d] or None) and their scales, per row (block 0) or per 128 columns."""
+    import torch
+    w, d = "fm_norm_quant", x.device
+    if not x.is_cuda:
+        _bad(w, "x must be a device tensor")
+    T, cols = x.shape
+    xp, xs = _rows(x, w, "x", (torch.float32, torch.bfloat16), d, (T, cols))
+    rp, rs = (None, 0) if r is None else _rows(r, w, "r", (torch.bfloat16,), d, (T, cols))
+    op, os_ = (None, 0) if x_out is None else _rows(x_out, w, "x_out", (x.dtype,), d, (T, cols))
+    gp = None
+    if gamma is not None:
+        gp = _tensor(gamma, w, "gamma", (torch.float32,), d, (cols,))
+        if not gamma.is_contiguous():
+            _bad(w, "gamma must be contiguous")
+    cp = _tensor(codes, w, "codes", (torch.float8_e4m3fn, torch.uint8), d, (T, cols))
+    sp = _tensor(scales, w, "scales", (torch.float32,), d)
+    if not codes.is_contiguous() or not scales.is_contiguous() or scales.numel() != T * (-(-cols // 128) if block else 1):
+        _bad(w, "codes and scales must be contiguous, scales [T] or [T][ceil(d / 128)]")
+    _check(load().fm_norm_quant(xp, xs, int(x.dtype == torch.float32), rp, rs, gp, T, cols, float(eps), op, os_, cp, sp,
+                                int(block), _here(d, stream, w)), w)
+
+
 # ---------------------------------------------------------------- convenience owner
 
 class DeviceWeights:
@@ -559,6 +861,10 @@ class Policy:
 
     def refresh_prefix(self, b, e, k, v, stream=None):
         refresh_prefix(self.handle, b, e, k, v, stream)
+
+    def refresh_prefix_pages(self, b, e, cache, seq, seq_tok=0, stream=None):
+        """Prefix rows [b, e) from tokens [seq_tok, seq_tok + e - b) of a cache's sequence."""
+        refresh_prefix_pages(self.handle, b, e, cache, seq, seq_tok, stream)
 
     def buffer(self, name: str, dtype=None, shape=None):
         """Zero-copy torch view of a named persistent buffer (a session's shared

@@ -1,0 +1,886 @@
+// The paged prefix cache: its bookkeeping on the device (fm_kv_reserve, fm_kv_fork, fm_kv_release, fm_kv_compact),
+// the rotary positions fused with the store of new keys and values (fm_rope_append), and the way from a sequence's
+// pages into a policy's persistent prefix (prefix_from_pages_launch).
+//
+// Bookkeeping. A sequence is a row of the page table and a length; `refs` counts the rows that name a page, 0 = free.
+// All of it lives on the device, so a serving step (fork, reserve, append, attend, release) needs no host round trip
+// and can be captured into a graph. Calls are all or nothing: every entry is validated before anything is written,
+// and the two status words say why a call did nothing. Free pages are taken lowest index first, so the result of a
+// call depends on its arguments alone. No kernel here waits on another CTA except through a cluster barrier.
+
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+#include <cstring>
+#include <mutex>
+
+#include "kv.h"
+#include "ptx.cuh"
+
+namespace fm {
+
+namespace {
+
+constexpr int kBookThreads = 1024;
+constexpr int kMaxEntries = 1024;   // sequences of one bookkeeping call: one thread each
+constexpr int kForkCluster = 8;
+
+// Device view of the bookkeeping.
+struct Book {
+  int32_t *table, *lens, *refs;
+  int seqs, table_stride, pages, page, shift;
+};
+
+// Device view of the pools, in 16-byte units.
+struct Pool {
+  uint4 *k, *v;
+  int64_t layer, pg, tok, head;   // strides
+  int layers, Hkv, chunks;        // chunks: 16-byte units of a row
+  int heads_inner;                // heads vary faster than tokens in memory
+};
+
+__host__ __device__ constexpr int up(int a, int b) { return (a + b - 1) / b; }
+
+// Exclusive sum over the block (1024 threads); *total receives the sum. Every thread calls it.
+__device__ __forceinline__ int block_exclusive(int v, int* warp_sums, int* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();   // warp_sums may still be read from an earlier call
+  if (lane == 31) warp_sums[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    int s = warp_sums[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += y;
+    }
+    warp_sums[lane] = s;
+  }
+  __syncthreads();
+  *total = warp_sums[31];
+  return (warp ? warp_sums[warp - 1] : 0) + x - v;
+}
+
+// Calls f(page, live) in ascending order within a warp's contiguous share of [0, pages); 32 pages a step, coalesced.
+template <typename F>
+__device__ __forceinline__ void for_warp_pages(const Book& b, F f) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int share = up(up(b.pages, 32), kBookThreads / 32) * 32;
+  const int lo = min(b.pages, warp * share), hi = min(b.pages, lo + share);
+  for (int p0 = lo; p0 < hi; p0 += 128) {
+    int r[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int pg = p0 + u * 32 + lane;
+      r[u] = pg < hi ? b.refs[pg] : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int pg = p0 + u * 32 + lane;
+      if (p0 + u * 32 < hi) f(pg, pg < hi, r[u]);   // warp-uniform
+    }
+  }
+}
+
+struct Copy {
+  int src, dst, rows;
+};
+
+// fm_kv_reserve. One CTA: the whole decision needs the order of the entries, and its work is a few hundred bytes an
+// entry plus one pass over refs (2200 pages: about 2 us); a second kernel copies the shared last pages on all SMs.
+__global__ void __launch_bounds__(kBookThreads) reserve_kernel(Book b, const int32_t* seq, const int32_t* count, int n,
+                                                               int32_t* status, Copy* copies, int32_t* fresh) {
+  __shared__ int s_seq[kMaxEntries], s_last[kMaxEntries], s_off[kMaxEntries], s_sums[32], s_bad;
+  pdl_trigger();
+  pdl_wait();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) s_bad = 0;
+  __syncthreads();
+  int s = -1 - tid, len = 0, add = 0, last = -1, last_refs = 0, bad = 0;
+  if (tid < n) {
+    s = seq[tid];
+    add = count[tid];
+    if (s < 0 || s >= b.seqs || add < 0) {
+      bad = FM_KV_BAD_ENTRY;
+    } else {
+      len = b.lens[s];
+      const int64_t room = static_cast<int64_t>(b.table_stride) * b.page;
+      if (len < 0 || len > room) {
+        bad = FM_KV_BAD_ENTRY;
+      } else if (len + static_cast<int64_t>(add) > room) {
+        bad = FM_KV_ROW_FULL;
+      } else if (add > 0 && (len & (b.page - 1))) {
+        last = b.table[static_cast<int64_t>(s) * b.table_stride + (len >> b.shift)];
+        if (last < 0 || last >= b.pages || (last_refs = b.refs[last]) < 1) {
+          bad = FM_KV_BAD_ENTRY;
+          last = -1;
+        }
+      }
+    }
+    s_seq[tid] = s;
+    s_last[tid] = last;
+  }
+  __syncthreads();
+  int earlier = 0;   // entries before this one that share its last page
+  for (int j = 0; j < tid && tid < n; ++j) {
+    if (s_seq[j] == s) bad |= FM_KV_BAD_ENTRY;
+    earlier += last >= 0 && s_last[j] == last;
+  }
+  const bool copied = last >= 0 && last_refs - earlier > 1;
+  const int have = (len >> b.shift) + ((len & (b.page - 1)) != 0);
+  const int end = len + add;
+  const int want = (end >> b.shift) + ((end & (b.page - 1)) != 0);
+  const int need = bad || tid >= n ? 0 : want - have + copied;
+  if (bad) atomicOr(&s_bad, bad);
+  int total = 0;
+  const int off = block_exclusive(need, s_sums, &total);
+  if (tid < n) s_off[tid] = off;
+  // free pages: every warp counts its share, then writes its ranks below `total`
+  int mine = 0;
+  for_warp_pages(b, [&](int, bool in, int refs) { mine += __popc(__ballot_sync(0xffffffffu, in && refs == 0)); });
+  int all_free = 0;
+  int rank = block_exclusive(lane == 0 ? mine : 0, s_sums, &all_free);
+  rank = __shfl_sync(0xffffffffu, rank, 0);
+  const int why = s_bad;
+  if (why || total > all_free) {   // the same in every thread
+    if (tid < n) copies[tid].rows = 0;
+    if (tid == 0) {
+      status[0] = why ? why : FM_KV_NO_PAGES;
+      status[1] = why ? 0 : total - all_free;
+    }
+    return;
+  }
+  if (rank < total)
+    for_warp_pages(b, [&](int pg, bool in, int refs) {
+      const unsigned m = __ballot_sync(0xffffffffu, in && refs == 0);
+      const int at = rank + __popc(m & ((1u << lane) - 1));
+      if (in && refs == 0 && at < total) fresh[at] = pg;
+      rank += __popc(m);
+    });
+  __syncthreads();
+  // the entries' changes: a copied page first, then the pages of the new tokens in order
+  if (tid < n) {
+    copies[tid].rows = copied ? len & (b.page - 1) : 0;
+    if (copied) {
+      const int to = fresh[off];
+      copies[tid].src = last;
+      copies[tid].dst = to;
+      b.table[static_cast<int64_t>(s) * b.table_stride + (len >> b.shift)] = to;
+      b.refs[to] = 1;
+      atomicSub(&b.refs[last], 1);
+    }
+    b.lens[s] = end;
+    s_last[tid] = copied;
+  }
+  __syncthreads();
+  for (int i = warp; i < n; i += kBookThreads / 32) {
+    const int si = s_seq[i], e = b.lens[si], c = count[i], l = e - c;
+    const int h = (l >> b.shift) + ((l & (b.page - 1)) != 0), w = (e >> b.shift) + ((e & (b.page - 1)) != 0);
+    const int base = s_off[i] + s_last[i];
+    for (int x = lane; x < w - h; x += 32) {
+      const int pg = fresh[base + x];
+      b.table[static_cast<int64_t>(si) * b.table_stride + h + x] = pg;
+      b.refs[pg] = 1;
+    }
+  }
+  if (tid == 0) {
+    status[0] = 0;
+    status[1] = total;
+  }
+}
+
+// Copies `rows` tokens of page src to page dst of one layer, K and V, 16 bytes a thread; four loads in flight.
+__device__ __forceinline__ void copy_rows(const Pool& p, int layer, int src, int dst, int rows) {
+  const int per_row = p.Hkv * p.chunks;
+  const int total = rows * per_row;
+  const int64_t base = layer * p.layer;
+  for (int x0 = threadIdx.x; x0 < total; x0 += blockDim.x * 2) {
+    uint4 a[2], d[2];
+    int64_t at[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int x = x0 + u * blockDim.x;
+      if (x >= total) continue;
+      const int c = x % p.chunks, y = x / p.chunks;
+      const int tok = p.heads_inner ? y / p.Hkv : y % rows, head = p.heads_inner ? y % p.Hkv : y / rows;
+      at[u] = base + tok * p.tok + head * p.head + c;
+      a[u] = p.k[at[u] + src * p.pg];
+      d[u] = p.v[at[u] + src * p.pg];
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      if (x0 + u * blockDim.x >= total) continue;
+      p.k[at[u] + dst * p.pg] = a[u];
+      p.v[at[u] + dst * p.pg] = d[u];
+    }
+  }
+}
+
+// The shared last pages of a reserve call: one CTA per entry and layer.
+__global__ void __launch_bounds__(256) copy_shared_kernel(Pool p, const Copy* copies) {
+  pdl_trigger();
+  pdl_wait();
+  const Copy c = copies[blockIdx.x];
+  if (c.rows > 0) copy_rows(p, blockIdx.y, c.src, c.dst, c.rows);
+}
+
+// fm_kv_fork (kFork) and fm_kv_release: one cluster; every CTA validates all entries before the cluster barrier, and
+// none is changed before every CTA has. The CTAs then take the entries in turn.
+template <bool kFork>
+__global__ void __launch_bounds__(kBookThreads)
+    share_kernel(Book b, const int32_t* seq, const int32_t* other, int n, int32_t* status) {
+  __shared__ int s_seq[kMaxEntries], s_oth[kMaxEntries], s_len[kMaxEntries], s_bad;
+  pdl_trigger();
+  pdl_wait();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) s_bad = 0;
+  __syncthreads();
+  int bad = 0, s = -1 - tid, o = 0;
+  if (tid < n) {
+    s = seq[tid];
+    o = other ? other[tid] : 0;
+    int len = 0;
+    const int64_t room = static_cast<int64_t>(b.table_stride) * b.page;
+    if (s < 0 || s >= b.seqs || (kFork && (o < 0 || o >= b.seqs)) || (!kFork && o < 0)) {
+      bad = FM_KV_BAD_ENTRY;
+    } else {
+      len = b.lens[s];
+      if (len < 0 || len > room || (kFork && b.lens[o] != 0)) bad = FM_KV_BAD_ENTRY;
+    }
+    s_seq[tid] = s;
+    s_oth[tid] = o;
+    s_len[tid] = len;
+  }
+  __syncthreads();
+  // fork: a target appears once and is no source; release: a sequence appears once
+  for (int j = 0; j < n && tid < n; ++j) {
+    if (kFork ? (s_seq[j] == o || (j != tid && s_oth[j] == o)) : (j != tid && s_seq[j] == s)) bad = FM_KV_BAD_ENTRY;
+  }
+  if (bad) atomicOr(&s_bad, bad);
+  __syncthreads();
+  const int why = s_bad;
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  const int rank = static_cast<int>(cluster_rank());
+  if (rank == 0 && tid == 0) {
+    status[0] = why;
+    status[1] = 0;
+  }
+  if (why) return;
+  // warps take (entry, part of its row); a row's unused places are -1 and copied like the rest
+  for (int i = rank * (kBookThreads / 32) + warp; i < n * 4; i += kForkCluster * (kBookThreads / 32)) {
+    const int e = i >> 2, part = i & 3;
+    const int64_t row = static_cast<int64_t>(s_seq[e]) * b.table_stride;
+    if (kFork) {
+      const int64_t to = static_cast<int64_t>(s_oth[e]) * b.table_stride;
+      for (int x = part * 32 + lane; x < b.table_stride; x += 128) {
+        const int pg = b.table[row + x];
+        b.table[to + x] = pg;
+        if (pg >= 0 && pg < b.pages) atomicAdd(&b.refs[pg], 1);
+      }
+      if (part == 0 && lane == 0) b.lens[s_oth[e]] = s_len[e];
+    } else {
+      const int len = s_len[e], keep = min(len, s_oth[e]);
+      const int lo = (keep >> b.shift) + ((keep & (b.page - 1)) != 0);
+      for (int x = lo + part * 32 + lane; x < b.table_stride; x += 128) {
+        const int pg = b.table[row + x];
+        if (pg >= 0 && pg < b.pages) atomicSub(&b.refs[pg], 1);
+        b.table[row + x] = -1;
+      }
+      if (part == 0 && lane == 0) b.lens[s_seq[e]] = keep;
+    }
+  }
+}
+
+// fm_kv_compact, the plan: live pages from n_live on move, in order, into the free ones below n_live, in order.
+// head: [0] n_live, [1] moves; src, dst: the moves; map: the new place of every page from n_live on (-1: free).
+__global__ void __launch_bounds__(kBookThreads) compact_plan_kernel(Book b, int32_t* status, int32_t* head, int32_t* src,
+                                                                    int32_t* dst, int32_t* map) {
+  __shared__ int s_sums[32];
+  pdl_trigger();
+  pdl_wait();
+  const int tid = threadIdx.x, lane = tid & 31;
+  int mine = 0;
+  for_warp_pages(b, [&](int, bool in, int refs) { mine += __popc(__ballot_sync(0xffffffffu, in && refs > 0)); });
+  int n_live = 0;
+  block_exclusive(lane == 0 ? mine : 0, s_sums, &n_live);
+  int above = 0, below = 0;
+  for_warp_pages(b, [&](int pg, bool in, int refs) {
+    above += __popc(__ballot_sync(0xffffffffu, in && refs > 0 && pg >= n_live));
+    below += __popc(__ballot_sync(0xffffffffu, in && refs <= 0 && pg < n_live));
+  });
+  int moves = 0, holes = 0;
+  int ra = __shfl_sync(0xffffffffu, block_exclusive(lane == 0 ? above : 0, s_sums, &moves), 0);
+  int rb = __shfl_sync(0xffffffffu, block_exclusive(lane == 0 ? below : 0, s_sums, &holes), 0);
+  for_warp_pages(b, [&](int pg, bool in, int refs) {
+    const bool a = in && refs > 0 && pg >= n_live, h = in && refs <= 0 && pg < n_live;
+    const unsigned ma = __ballot_sync(0xffffffffu, a), mh = __ballot_sync(0xffffffffu, h);
+    const unsigned under = (1u << lane) - 1;
+    if (a) src[ra + __popc(ma & under)] = pg;
+    if (h) dst[rb + __popc(mh & under)] = pg;
+    if (in && pg >= n_live && !a) map[pg] = -1;
+    ra += __popc(ma);
+    rb += __popc(mh);
+  });
+  __syncthreads();   // moves == holes: as many live pages above n_live as free ones below
+  for (int i = tid; i < moves; i += kBookThreads) {
+    const int from = src[i], to = dst[i];
+    map[from] = to;
+    b.refs[to] = b.refs[from];
+    b.refs[from] = 0;
+  }
+  if (tid == 0) {
+    head[0] = n_live;
+    head[1] = moves;
+    status[0] = 0;
+    status[1] = moves;
+  }
+}
+
+// The moves (sources and targets are disjoint) and the table's new page numbers.
+__global__ void __launch_bounds__(256) compact_move_kernel(Pool p, Book b, const int32_t* head, const int32_t* src,
+                                                           const int32_t* dst, const int32_t* map) {
+  pdl_trigger();
+  pdl_wait();
+  const int n_live = head[0], moves = head[1];
+  const int64_t items = static_cast<int64_t>(moves) * p.layers;
+  for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
+    const int m = static_cast<int>(i % moves);
+    copy_rows(p, static_cast<int>(i / moves), src[m], dst[m], b.page);
+  }
+  const int64_t cells = static_cast<int64_t>(b.seqs) * b.table_stride;
+  for (int64_t x = blockIdx.x * 256ll + threadIdx.x; x < cells; x += gridDim.x * 256ll) {
+    const int pg = b.table[x];
+    if (pg >= n_live && pg < b.pages) b.table[x] = map[pg];
+  }
+}
+
+// ---------------------------------------------------------------- rotary positions and the store
+
+struct AppendParams {
+  const __nv_bfloat16 *q, *k, *v;
+  __nv_bfloat16* q_out;
+  int64_t qs, ks, vs, os;   // elements between tokens
+  const int32_t *start, *seq, *lens, *table, *positions;
+  const uint64_t* freq;     // turns per position * 2^64 of each pair
+  float mag;
+  int rot, interleaved;
+  int tokens, max_tokens, seqs, table_stride, pages, page, shift;
+  int H, Hkv, Dh;
+  int groups, per;          // head groups of a token, heads of a group
+  void *kc, *vc;            // this layer
+  int64_t pg, tok, head;    // strides in elements
+  const float *k_scale, *v_scale;
+  int* err;
+};
+
+__device__ __forceinline__ uint32_t bf2(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ void unpack8(uint4 u, float* f) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ uint4 pack8(const float* f) {
+  return make_uint4(bf2(f[0], f[1]), bf2(f[2], f[3]), bf2(f[4], f[5]), bf2(f[6], f[7]));
+}
+__device__ __forceinline__ uint2 codes8(const float* f, float rs) {
+  uint32_t w[2] = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    const uint32_t c = __nv_cvt_float2_to_fp8x2(make_float2(f[i] * rs, f[i + 1] * rs), __NV_SATFINITE, __NV_E4M3);
+    w[i >> 2] |= c << (8 * (i & 2));
+  }
+  return make_uint2(w[0], w[1]);
+}
+
+// One thread: 16 elements (two 8-element chunks that hold whole pairs) of `per` heads of one token; the angles are
+// computed once for all of them. An angle is a fraction of a turn in 64-bit fixed point: position * freq modulo 2^64
+// drops whole turns exactly, at any position, without double precision. grid.y is the entry of the batch.
+template <bool F8>
+__global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
+  pdl_trigger();
+  const int units = p.Dh / 16;
+  const int64_t x = blockIdx.x * 256ll + threadIdx.x;
+  const int unit = static_cast<int>(x % units);
+  const int64_t y = x / units;
+  const int grp = static_cast<int>(y % p.groups);
+  const int64_t within = y / p.groups;
+  const int entry = blockIdx.y;
+  // chunks of this unit (in 8 elements): a rotated pair of chunks, or two that pass through
+  const int rot_units = p.rot / 16;
+  const bool turned = unit < rot_units;
+  const int c0 = turned && !p.interleaved ? unit : 2 * unit, c1 = turned && !p.interleaved ? unit + rot_units : 2 * unit + 1;
+  pdl_wait();
+  uint64_t f[8];
+  if (turned) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = __ldg(p.freq + unit * 8 + i);
+  }
+  const int begin = __ldg(p.start + entry), nq = __ldg(p.start + entry + 1) - begin;
+  const int sid = p.seq ? __ldg(p.seq + entry) : entry;
+  bool bad = begin < 0 || nq < 0 || begin > p.tokens || nq > p.tokens - begin || sid < 0 || sid >= p.seqs;
+  const int len = bad ? 0 : __ldg(p.lens + sid);
+  const bool over = bad || nq > p.max_tokens || len < nq || len > p.table_stride * static_cast<int64_t>(p.page);
+  if (over && x == 0) atomicOr(p.err, kErrBadBatch);
+  if (bad || within >= nq) return;
+  const int64_t token = begin + within;
+  const int64_t pos = static_cast<int64_t>(len) - nq + within;   // place in the sequence
+  int page = -1;
+  if (pos >= 0 && (pos >> p.shift) < p.table_stride)
+    page = __ldg(p.table + static_cast<int64_t>(sid) * p.table_stride + (pos >> p.shift));
+  if (page >= p.pages) page = -1;
+  if (page < 0 && unit == 0 && grp == 0) atomicOr(p.err, kErrBadBatch);
+  const int h0 = grp * p.per, h1 = min(h0 + p.per, p.H + 2 * p.Hkv);
+  float cs[8], sn[8];
+  if (turned && h0 < p.H + p.Hkv) {
+    const int64_t at = p.positions ? __ldg(p.positions + token) : pos;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      // the fraction of a turn as a signed 32-bit number: half turns in [-1, 1) for sincospif
+      const uint64_t turn = f[i] * static_cast<uint64_t>(at) + (1ull << 31);
+      sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f, &sn[i], &cs[i]);
+      cs[i] *= p.mag;
+      sn[i] *= p.mag;
+    }
+  }
+  const float rk = F8 ? 1.0f / __ldg(p.k_scale) : 1.0f, rv = F8 ? 1.0f / __ldg(p.v_scale) : 1.0f;
+  const int64_t cell = static_cast<int64_t>(page) * p.pg + (pos & (p.page - 1)) * p.tok;
+  for (int h = h0; h < h1; h += 2) {
+    uint4 in[2][2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {   // two heads' loads in flight
+      const int hh = h + u;
+      if (hh >= h1) continue;
+      const __nv_bfloat16* src = hh < p.H           ? p.q + token * p.qs + static_cast<int64_t>(hh) * p.Dh
+                                 : hh < p.H + p.Hkv ? p.k + token * p.ks + static_cast<int64_t>(hh - p.H) * p.Dh
+                                                    : p.v + token * p.vs + static_cast<int64_t>(hh - p.H - p.Hkv) * p.Dh;
+      in[u][0] = reinterpret_cast<const uint4*>(src)[c0];
+      in[u][1] = reinterpret_cast<const uint4*>(src)[c1];
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int hh = h + u;
+      if (hh >= h1) continue;
+      float a[8], b[8];
+      unpack8(in[u][0], a);
+      unpack8(in[u][1], b);
+      const bool is_v = hh >= p.H + p.Hkv;
+      if (turned && !is_v) {
+        if (p.interleaved) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float a0 = a[2 * i], a1 = a[2 * i + 1], b0 = b[2 * i], b1 = b[2 * i + 1];
+            a[2 * i] = a0 * cs[i] - a1 * sn[i];
+            a[2 * i + 1] = a1 * cs[i] + a0 * sn[i];
+            b[2 * i] = b0 * cs[4 + i] - b1 * sn[4 + i];
+            b[2 * i + 1] = b1 * cs[4 + i] + b0 * sn[4 + i];
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float x0 = a[i], x1 = b[i];
+            a[i] = x0 * cs[i] - x1 * sn[i];
+            b[i] = x1 * cs[i] + x0 * sn[i];
+          }
+        }
+      }
+      if (hh < p.H) {
+        uint4* dst = reinterpret_cast<uint4*>(p.q_out + token * p.os + static_cast<int64_t>(hh) * p.Dh);
+        dst[c0] = pack8(a);
+        dst[c1] = pack8(b);
+      } else if (page >= 0) {
+        const int64_t at = cell + static_cast<int64_t>(is_v ? hh - p.H - p.Hkv : hh - p.H) * p.head;
+        if constexpr (F8) {
+          uint2* dst = reinterpret_cast<uint2*>(static_cast<uint8_t*>(is_v ? p.vc : p.kc) + at);
+          const float rs = is_v ? rv : rk;
+          dst[c0] = codes8(a, rs);
+          dst[c1] = codes8(b, rs);
+        } else {
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(is_v ? p.vc : p.kc) + at);
+          dst[c0] = pack8(a);
+          dst[c1] = pack8(b);
+        }
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- pages -> a policy's prefix
+
+struct PrefixParams {
+  const uint8_t *k, *v;
+  int f8;
+  int64_t layer, pg, tok, head;   // bytes
+  const float *k_scale, *v_scale;
+  const int32_t *table, *lens;
+  int seq, seq_tok, rows, table_stride, pages, page, shift, Hkv, Dh;
+  __nv_bfloat16 *kcache, *vt;
+  int P, p_pad, tok_begin;
+  int* err;
+};
+
+constexpr int kPrefixTile = 64;
+
+// 16-bit values of 8 elements of a page row.
+__device__ __forceinline__ uint4 row_chunk(const uint8_t* row, int c, int f8, float scale) {
+  if (!f8) return reinterpret_cast<const uint4*>(row)[c];
+  const uint2 u = reinterpret_cast<const uint2*>(row)[c];
+  float f[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t w = i < 4 ? u.x : u.y;
+    const __half_raw h = __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>((w >> (8 * (i & 3))) & 0xff), __NV_E4M3);
+    f[i] = __half2float(__half(h)) * scale;
+  }
+  return pack8(f);
+}
+
+// One CTA: 64 tokens of one layer and head; keys are copied, values turned through shared memory so that both the
+// reads (rows) and the writes (16 bytes along the tokens where a whole group lies inside) are wide.
+__global__ void __launch_bounds__(256) prefix_kernel(const PrefixParams p) {
+  extern __shared__ uint16_t s_v[];   // [64][Dh + 2]
+  const int layer = blockIdx.z, g = blockIdx.y, t0 = blockIdx.x * kPrefixTile;
+  const int len = p.lens[p.seq];
+  const int chunks = p.Dh / 8, pitch = p.Dh + 2;
+  const float ks = p.f8 ? p.k_scale[layer] : 1.f, vs = p.f8 ? p.v_scale[layer] : 1.f;
+  for (int x = threadIdx.x; x < kPrefixTile * chunks; x += 256) {
+    const int r = x / chunks, c = x % chunks, t = t0 + r;
+    if (t >= p.rows) break;
+    const int64_t pos = static_cast<int64_t>(p.seq_tok) + t;
+    int page = -1;
+    if (pos < len && (pos >> p.shift) < p.table_stride)
+      page = p.table[static_cast<int64_t>(p.seq) * p.table_stride + (pos >> p.shift)];
+    if (page >= p.pages) page = -1;
+    uint4 k = make_uint4(0, 0, 0, 0), v = k;
+    if (page >= 0) {
+      const int64_t off = layer * p.layer + page * p.pg + (pos & (p.page - 1)) * p.tok + g * p.head;
+      k = row_chunk(p.k + off, c, p.f8, ks);
+      v = row_chunk(p.v + off, c, p.f8, vs);
+    } else if (c == 0) {
+      atomicOr(p.err, kErrBadBatch);
+    }
+    reinterpret_cast<uint4*>(p.kcache + ((static_cast<int64_t>(layer) * p.P + p.tok_begin + t) * p.Hkv + g) * p.Dh)[c] = k;
+    uint32_t* d = reinterpret_cast<uint32_t*>(s_v + r * pitch + c * 8);
+    d[0] = v.x, d[1] = v.y, d[2] = v.z, d[3] = v.w;
+  }
+  __syncthreads();
+  const int n = min(kPrefixTile, p.rows - t0);
+  for (int x = threadIdx.x; x < kPrefixTile * p.Dh; x += 256) {
+    const int r = x % kPrefixTile, d = x / kPrefixTile;
+    if (r < n)
+      reinterpret_cast<uint16_t*>(p.vt)[((static_cast<int64_t>(layer) * p.Hkv + g) * p.Dh + d) * p.p_pad + p.tok_begin +
+                                        t0 + r] = s_v[r * pitch + d];
+  }
+}
+
+int shift_of(int page) {
+  int s = 0;
+  while ((1 << s) < page) ++s;
+  return s;
+}
+
+Book book_of(const fm_kv_cache& c) {
+  return Book{c.table, c.lens, c.refs, c.seqs, c.table_stride, c.pages, c.page_tokens, shift_of(c.page_tokens)};
+}
+
+Pool pool_of(const fm_kv_cache& c) {
+  const int eb = c.fmt == FM_FMT_FP8 ? 1 : 2, per = 16 / eb;
+  Pool p;
+  p.k = static_cast<uint4*>(c.k);
+  p.v = static_cast<uint4*>(c.v);
+  p.layer = c.layer_stride / per;
+  p.pg = c.page_stride / per;
+  p.tok = c.token_stride / per;
+  p.head = c.head_stride / per;
+  p.layers = c.layers;
+  p.Hkv = c.Hkv;
+  p.chunks = c.Dh / per;
+  p.heads_inner = c.Hkv > 1 && c.head_stride < c.token_stride;
+  return p;
+}
+
+size_t align16(size_t v) { return (v + 15) / 16 * 16; }
+// Workspace: n copy records, then max(pages for a reserve's free list, the compaction's lists: head, src, dst, map).
+size_t kv_workspace(const fm_kv_cache& c, int n) {
+  return align16(n * sizeof(Copy)) + align16((4 + 3 * static_cast<size_t>(c.pages)) * sizeof(int32_t));
+}
+
+int page_call_check(const fm_kv_cache* c, int n, const void* status) {
+  const int st = kv_check(c);
+  if (st != FM_OK) return st;
+  if (!c->refs || !status) return record_error(FM_ERR_INVALID_ARG, "NULL argument");
+  if (n < 0 || n > kMaxEntries) return record_error(FM_ERR_SHAPE, "a call takes 0 to 1024 sequences");
+  return FM_OK;
+}
+
+int workspace_check(const fm_kv_cache& c, int n, const void* ws, size_t bytes) {
+  if (!ws) return record_error(FM_ERR_INVALID_ARG, "workspace is NULL");
+  if (reinterpret_cast<uintptr_t>(ws) % 16) return record_error(FM_ERR_ALIGN, "workspace not 16-byte aligned");
+  if (bytes < kv_workspace(c, n)) return record_error(FM_ERR_WORKSPACE, "workspace smaller than fm_kv_workspace_size()");
+  return FM_OK;
+}
+
+int done(cudaError_t e) { return e == cudaSuccess ? FM_OK : record_error(FM_ERR_CUDA, cudaGetErrorString(e)); }
+
+LaunchOpts opts(void* stream) {
+  LaunchOpts o;
+  o.stream = static_cast<cudaStream_t>(stream);
+  o.pdl = true;
+  return o;
+}
+
+template <bool kFork>
+int share(const fm_kv_cache* c, const int32_t* seq, const int32_t* other, int n, int32_t* status, void* stream) {
+  LaunchOpts o = opts(stream);
+  o.cluster = dim3(kForkCluster, 1, 1);
+  return done(launch(share_kernel<kFork>, dim3(kForkCluster), dim3(kBookThreads), 0, o, book_of(*c), seq, other, n, status));
+}
+
+}  // namespace
+
+int kv_check(const fm_kv_cache* c) {
+  if (!c || !c->k || !c->v || !c->table || !c->lens) return record_error(FM_ERR_INVALID_ARG, "NULL argument");
+  if (c->fmt != FM_FMT_BF16 && c->fmt != FM_FMT_FP8) return record_error(FM_ERR_INVALID_ARG, "cache format must be BF16 or FP8");
+  if (c->fmt == FM_FMT_FP8 && (!c->k_scale || !c->v_scale))
+    return record_error(FM_ERR_INVALID_ARG, "an FP8 cache needs its k_scale and v_scale");
+  if (c->layers < 1 || c->pages < 1 || c->Hkv < 1 || c->seqs < 1 || c->table_stride < 1)
+    return record_error(FM_ERR_SHAPE, "layers, pages, Hkv, seqs and table_stride must be positive");
+  if (c->page_tokens < 16 || c->page_tokens > 256 || (c->page_tokens & (c->page_tokens - 1)))
+    return record_error(FM_ERR_SHAPE, "page_tokens must be 16, 32, 64, 128 or 256");
+  if (c->Dh < 16 || c->Dh > 256 || c->Dh % 16) return record_error(FM_ERR_SHAPE, "Dh must be a multiple of 16 up to 256");
+  if (c->layers > 65535 || c->Hkv > 65535 || c->pages > (1 << 30))
+    return record_error(FM_ERR_SHAPE, "layers and Hkv up to 65535, pages up to 2^30");
+  if (static_cast<int64_t>(c->table_stride) * c->page_tokens > INT32_MAX)
+    return record_error(FM_ERR_SHAPE, "table_stride * page_tokens exceeds 2^31 - 1 tokens");
+  if (reinterpret_cast<uintptr_t>(c->k) % 16 || reinterpret_cast<uintptr_t>(c->v) % 16)
+    return record_error(FM_ERR_ALIGN, "k and v must be 16-byte aligned");
+  // rows must not overlap: each stride (of an extent above 1) spans all that is inside of it
+  const int eb = c->fmt == FM_FMT_FP8 ? 1 : 2;
+  struct { int64_t stride, extent; } d[4] = {{c->token_stride, c->page_tokens}, {c->head_stride, c->Hkv},
+                                             {c->page_stride, c->pages}, {c->layer_stride, c->layers}};
+  std::sort(d, d + 4, [](const auto& a, const auto& b) { return a.stride < b.stride; });
+  int64_t span = c->Dh;
+  for (const auto& x : d) {
+    if (x.extent == 1) continue;
+    if (x.stride * eb % 16) return record_error(FM_ERR_SHAPE, "cache strides must be multiples of 16 bytes");
+    if (x.stride < span || x.stride > (int64_t(1) << 39)) return record_error(FM_ERR_SHAPE, "cache strides overlap or are too large");
+    span += x.stride * (x.extent - 1);
+  }
+  return FM_OK;
+}
+
+int kv_batch_check(const fm_kv_cache* c, const fm_kv_batch* b) {
+  if (!b) return record_error(FM_ERR_INVALID_ARG, "NULL batch");
+  if (b->n < 0 || b->tokens < 0 || b->max_tokens < 0 || b->max_len < 0)
+    return record_error(FM_ERR_SHAPE, "a batch's counts must not be negative");
+  if (b->n > 65535) return record_error(FM_ERR_SHAPE, "a batch takes up to 65535 entries");
+  if (b->n > 0 && !b->start) return record_error(FM_ERR_INVALID_ARG, "the batch has no start");
+  if (b->n > 0 && !b->seq && b->n > c->seqs)
+    return record_error(FM_ERR_SHAPE, "without seq, entry i is sequence i: n must not exceed the cache's seqs");
+  return FM_OK;
+}
+
+cudaError_t prefix_from_pages_launch(const fm_kv_cache& c, int seq, int seq_tok, int rows, __nv_bfloat16* kcache,
+                                     __nv_bfloat16* vtcache, int P, int p_pad, int tok_begin, int* err, cudaStream_t st) {
+  const int eb = c.fmt == FM_FMT_FP8 ? 1 : 2;
+  PrefixParams p;
+  p.k = static_cast<const uint8_t*>(c.k);
+  p.v = static_cast<const uint8_t*>(c.v);
+  p.f8 = eb == 1;
+  p.layer = c.layer_stride * eb;
+  p.pg = c.page_stride * eb;
+  p.tok = c.token_stride * eb;
+  p.head = c.head_stride * eb;
+  p.k_scale = c.k_scale;
+  p.v_scale = c.v_scale;
+  p.table = c.table;
+  p.lens = c.lens;
+  p.seq = seq;
+  p.seq_tok = seq_tok;
+  p.rows = rows;
+  p.table_stride = c.table_stride;
+  p.pages = c.pages;
+  p.page = c.page_tokens;
+  p.shift = shift_of(c.page_tokens);
+  p.Hkv = c.Hkv;
+  p.Dh = c.Dh;
+  p.kcache = kcache;
+  p.vt = vtcache;
+  p.P = P;
+  p.p_pad = p_pad;
+  p.tok_begin = tok_begin;
+  p.err = err;
+  LaunchOpts o;
+  o.stream = st;
+  return launch(prefix_kernel, dim3(up(rows, kPrefixTile), c.Hkv, c.layers), dim3(256),
+                static_cast<size_t>(kPrefixTile) * (c.Dh + 2) * 2, o, p);
+}
+
+}  // namespace fm
+
+using namespace fm;
+
+extern "C" int fm_kv_workspace_size(const fm_kv_cache* c, int n, size_t* bytes) {
+  if (!bytes) return record_error(FM_ERR_INVALID_ARG, "bytes is NULL");
+  const int st = kv_check(c);
+  if (st != FM_OK) return st;
+  if (n < 0 || n > kMaxEntries) return record_error(FM_ERR_SHAPE, "a call takes 0 to 1024 sequences");
+  *bytes = kv_workspace(*c, n);
+  return FM_OK;
+}
+
+extern "C" int fm_kv_reserve(const fm_kv_cache* c, const int32_t* seq, const int32_t* count, int n, int32_t* status,
+                             void* workspace, size_t workspace_bytes, void* stream) {
+  int st = page_call_check(c, n, status);
+  if (st != FM_OK) return st;
+  if (n > 0 && (!seq || !count)) return record_error(FM_ERR_INVALID_ARG, "NULL argument");
+  st = workspace_check(*c, n, workspace, workspace_bytes);
+  if (st != FM_OK) return st;
+  Copy* copies = static_cast<Copy*>(workspace);
+  int32_t* fresh = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + align16(n * sizeof(Copy)));
+  const LaunchOpts o = opts(stream);
+  cudaError_t e = launch(reserve_kernel, dim3(1), dim3(kBookThreads), 0, o, book_of(*c), seq, count, n, status, copies, fresh);
+  if (e == cudaSuccess && n > 0)
+    e = launch(copy_shared_kernel, dim3(n, c->layers), dim3(256), 0, o, pool_of(*c), static_cast<const Copy*>(copies));
+  return done(e);
+}
+
+extern "C" int fm_kv_fork(const fm_kv_cache* c, const int32_t* src, const int32_t* dst, int n, int32_t* status, void* stream) {
+  const int st = page_call_check(c, n, status);
+  if (st != FM_OK) return st;
+  if (n > 0 && (!src || !dst)) return record_error(FM_ERR_INVALID_ARG, "NULL argument");
+  return share<true>(c, src, dst, n, status, stream);
+}
+
+extern "C" int fm_kv_release(const fm_kv_cache* c, const int32_t* seq, const int32_t* keep, int n, int32_t* status,
+                             void* stream) {
+  const int st = page_call_check(c, n, status);
+  if (st != FM_OK) return st;
+  if (n > 0 && !seq) return record_error(FM_ERR_INVALID_ARG, "NULL argument");
+  return share<false>(c, seq, keep, n, status, stream);
+}
+
+extern "C" int fm_kv_compact(const fm_kv_cache* c, int32_t* status, void* workspace, size_t workspace_bytes, void* stream) {
+  int st = page_call_check(c, 0, status);
+  if (st != FM_OK) return st;
+  st = workspace_check(*c, 0, workspace, workspace_bytes);
+  if (st != FM_OK) return st;
+  int32_t* head = static_cast<int32_t*>(workspace);
+  int32_t *src = head + 4, *dst = src + c->pages, *map = dst + c->pages;
+  const LaunchOpts o = opts(stream);
+  cudaError_t e = launch(compact_plan_kernel, dim3(1), dim3(kBookThreads), 0, o, book_of(*c), status, head, src, dst, map);
+  if (e == cudaSuccess)
+    e = launch(compact_move_kernel, dim3(152 * 8), dim3(256), 0, o, pool_of(*c), book_of(*c), static_cast<const int32_t*>(head),
+               static_cast<const int32_t*>(src), static_cast<const int32_t*>(dst), static_cast<const int32_t*>(map));
+  return done(e);
+}
+
+extern "C" int fm_rope_table(const fm_rope_config* r, uint64_t* freq, float* magnitude) {
+  if (!r || !freq || !magnitude) return record_error(FM_ERR_INVALID_ARG, "NULL argument");
+  if (r->rotary_dim < 16 || r->rotary_dim > 256 || r->rotary_dim % 16)
+    return record_error(FM_ERR_SHAPE, "rotary_dim must be a multiple of 16 up to 256");
+  if (!(r->theta > 1.0) || !std::isfinite(r->theta)) return record_error(FM_ERR_INVALID_ARG, "theta must exceed 1");
+  if (r->scaling < FM_ROPE_PLAIN || r->scaling > FM_ROPE_BY_PARTS) return record_error(FM_ERR_INVALID_ARG, "unknown scaling");
+  if (r->scaling != FM_ROPE_PLAIN && (!(r->factor >= 1.0) || !std::isfinite(r->factor)))
+    return record_error(FM_ERR_INVALID_ARG, "factor must be at least 1");
+  const double two_pi = 6.283185307179586476925286766559;
+  const int d = r->rotary_dim;
+  double theta = r->theta;
+  if (r->scaling == FM_ROPE_BASE) theta *= std::pow(r->factor, d / (d - 2.0));
+  double lo = 0, hi = 0;
+  if (r->scaling == FM_ROPE_BY_PARTS) {
+    if (!(r->original_len >= 1.0) || !std::isfinite(r->original_len) || !(r->beta_slow > 0.0) || !(r->beta_fast > r->beta_slow) ||
+        !std::isfinite(r->beta_fast))
+      return record_error(FM_ERR_INVALID_ARG, "by-parts scaling needs original_len >= 1 and beta_fast > beta_slow > 0");
+    const auto where = [&](double turns) { return d * std::log(r->original_len / (turns * two_pi)) / (2 * std::log(theta)); };
+    lo = std::max(std::floor(where(r->beta_fast)), 0.0);
+    hi = std::min(std::ceil(where(r->beta_slow)), d - 1.0);
+  }
+  for (int i = 0; i < d / 2; ++i) {
+    double f = std::pow(theta, -2.0 * i / d);
+    if (r->scaling == FM_ROPE_LINEAR) f /= r->factor;
+    if (r->scaling == FM_ROPE_BY_PARTS) {
+      const double t = std::min(1.0, std::max(0.0, (i - lo) / std::max(hi - lo, 0.001)));
+      f = f / r->factor * t + f * (1 - t);
+    }
+    // turns per position, below 0.16; 2^64 of them rounded to whole numbers (a double holds 53 bits of it)
+    freq[i] = static_cast<uint64_t>(std::ldexp(f / two_pi, 64) + 0.5);
+  }
+  *magnitude = r->scaling == FM_ROPE_BY_PARTS ? static_cast<float>(0.1 * std::log(r->factor) + 1.0) : 1.0f;
+  return FM_OK;
+}
+
+extern "C" int fm_rope_append(const fm_kv_cache* c, int layer, const fm_kv_batch* b, const fm_rope* rope, const uint16_t* q,
+                              int64_t q_stride, int H, const uint16_t* k, int64_t k_stride, const uint16_t* v,
+                              int64_t v_stride, uint16_t* q_out, int64_t q_out_stride, const int32_t* positions,
+                              void* stream) {
+  int st = kv_check(c);
+  if (st == FM_OK) st = kv_batch_check(c, b);
+  if (st != FM_OK) return st;
+  if (!rope) return record_error(FM_ERR_INVALID_ARG, "NULL argument");
+  if (layer < 0 || layer >= c->layers) return record_error(FM_ERR_INVALID_ARG, "layer out of range");
+  if (rope->rotary_dim < 0 || rope->rotary_dim > c->Dh || rope->rotary_dim % 16)
+    return record_error(FM_ERR_SHAPE, "rotary_dim must be a multiple of 16 up to Dh");
+  if (rope->rotary_dim > 0 && !rope->freq) return record_error(FM_ERR_INVALID_ARG, "the rotary table is NULL");
+  if (rope->layout != FM_ROPE_HALF && rope->layout != FM_ROPE_INTERLEAVED)
+    return record_error(FM_ERR_INVALID_ARG, "unknown rotary layout");
+  if (!std::isfinite(rope->magnitude)) return record_error(FM_ERR_INVALID_ARG, "magnitude must be finite");
+  if (H < 0 || H > 65535) return record_error(FM_ERR_SHAPE, "H must be 0 to 65535");
+  if (b->n == 0 || b->tokens == 0 || b->max_tokens == 0) return FM_OK;
+  if (!k || !v || (H > 0 && (!q || !q_out))) return record_error(FM_ERR_INVALID_ARG, "NULL argument");
+  const int64_t kv_row = static_cast<int64_t>(c->Hkv) * c->Dh, q_row = static_cast<int64_t>(H) * c->Dh;
+  if (k_stride < kv_row || v_stride < kv_row || k_stride % 8 || v_stride % 8 ||
+      (H > 0 && (q_stride < q_row || q_out_stride < q_row || q_stride % 8 || q_out_stride % 8)))
+    return record_error(FM_ERR_SHAPE, "token strides must be multiples of 8 elements and hold the token's heads");
+  for (const void* x : {static_cast<const void*>(k), static_cast<const void*>(v), static_cast<const void*>(q),
+                        static_cast<const void*>(q_out)})
+    if (reinterpret_cast<uintptr_t>(x) % 16) return record_error(FM_ERR_ALIGN, "q, k, v and q_out must be 16-byte aligned");
+  int* err = standalone_error_word();
+  if (!err) return record_error(FM_ERR_CUDA, "no error word on the current device");
+  const bool f8 = c->fmt == FM_FMT_FP8;
+  const int eb = f8 ? 1 : 2;
+  AppendParams p = {};
+  p.q = reinterpret_cast<const __nv_bfloat16*>(q);
+  p.k = reinterpret_cast<const __nv_bfloat16*>(k);
+  p.v = reinterpret_cast<const __nv_bfloat16*>(v);
+  p.q_out = reinterpret_cast<__nv_bfloat16*>(q_out);
+  p.qs = q_stride, p.ks = k_stride, p.vs = v_stride, p.os = q_out_stride;
+  p.start = b->start, p.seq = b->seq, p.lens = c->lens, p.table = c->table, p.positions = positions;
+  p.freq = rope->freq;
+  p.mag = rope->magnitude;
+  p.rot = rope->rotary_dim;
+  p.interleaved = rope->layout == FM_ROPE_INTERLEAVED;
+  p.tokens = b->tokens, p.max_tokens = b->max_tokens, p.seqs = c->seqs, p.table_stride = c->table_stride;
+  p.pages = c->pages, p.page = c->page_tokens, p.shift = shift_of(c->page_tokens);
+  p.H = H, p.Hkv = c->Hkv, p.Dh = c->Dh;
+  p.kc = static_cast<uint8_t*>(c->k) + layer * c->layer_stride * eb;
+  p.vc = static_cast<uint8_t*>(c->v) + layer * c->layer_stride * eb;
+  p.pg = c->page_stride, p.tok = c->token_stride, p.head = c->head_stride;
+  p.k_scale = f8 ? c->k_scale + layer : nullptr;
+  p.v_scale = f8 ? c->v_scale + layer : nullptr;
+  p.err = err;
+  // heads per thread: the angles are shared by more heads the more tokens there are to fill the GPU with
+  const int heads = H + 2 * c->Hkv, units = c->Dh / 16;
+  const int64_t all = static_cast<int64_t>(b->tokens) * units * heads;
+  p.per = 2;
+  while (p.per < 8 && all / (p.per * 2) >= 152 * 2048) p.per *= 2;
+  p.groups = up(heads, p.per);
+  const int64_t threads = static_cast<int64_t>(b->max_tokens) * p.groups * units;
+  if ((threads + 255) / 256 > INT32_MAX) return record_error(FM_ERR_SHAPE, "max_tokens x heads is too large for one call");
+  return done(launch(f8 ? append_kernel<true> : append_kernel<false>, dim3(static_cast<unsigned>((threads + 255) / 256), b->n),
+                     dim3(256), 0, opts(stream), p));
+}

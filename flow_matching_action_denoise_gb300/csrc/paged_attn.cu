@@ -1,0 +1,901 @@
+// Attention of a chunk of new tokens over a paged cache (fm_paged_attention).
+//
+//   o[t, h] = sum_j p_j v_j,  p = softmax_j(scale q[t, h] . k_j),  key j of the token's sequence with
+//   j < len, j <= pos(t) where causal, j > pos(t) - window where a window is set; a row without keys is zero.
+//
+// Work layout. The G = H / Hkv query heads of a KV head are stacked with the tokens into rows
+// R = token * G + head, so that a key tile is read once for all of them. A CTA takes up to 256 rows of one
+// entry and KV head and walks its keys in tiles of 128; S = Q K^T and O += P V run on tcgen05 tensor cores
+// (M = 128) with both accumulators and P in tensor memory, one pass with the running maximum and sum.
+// Two softmax warpgroups share the CTA. With more than 128 rows each owns a 128-row tile and both use every
+// key tile (`pair`); with up to 128 rows they own alternate key tiles of the same rows and merge at the end
+// (`alt`), so that single tokens keep two tiles in flight. While one warpgroup exponentiates, the tensor cores
+// work for the other. A long key axis with few rows is cut into splits of whole tiles, one CTA each, whose
+// (max, sum, O) go to the workspace and are joined in split order by combine_kernel.
+//
+// Pages. One warp reads the page table and moves every page's rows by TMA straight into the swizzled tile the
+// tensor cores read: values stay [token][head dim] and are read as an MN-major operand, so the cache needs no
+// transpose. Pages outside the sequence are loaded from behind the pool's end, which TMA fills with zeros; the
+// values behind the length inside the last page are zeroed in shared memory, since 0 * NaN is NaN.
+//
+// E4M3 cache. Two warps expand the codes to f16 (exact) into the same tile layout; q is scaled per row by a power
+// of two that puts its largest element in [2^14, 2^15) and held in f16 (bf16's 8 significant bits are kept down to
+// 2^-28 of that largest element), p is held in f16, so no rounding is coarser than for a 16-bit cache.
+//
+// Rounding: scores, statistics, P V sums and the splits' join are fp32; P is rounded to bf16 (f16 for the E4M3
+// cache), the operand type of the second product; the output is rounded once to bf16. The running maximum moves
+// only when it grows by more than 2^8 (in the exponent: 8), which makes rescaling O rare; the final division makes
+// the result independent of that reference.
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+
+#include "internal.h"
+#include "kv.h"
+#include "ptx.cuh"
+
+namespace fm {
+
+namespace {
+
+constexpr int kTileRows = 128;    // rows of a query tile (MMA M) and keys of a key tile
+constexpr int kThreads = 384;     // 8 softmax warps, MMA warp, TMA warp, 2 expanding warps
+constexpr int kMmaWarp = 8, kTmaWarp = 9, kCvtWarp = 10;
+constexpr int kSmemLimit = 226 * 1024;
+constexpr int kMaxRing = 8;
+constexpr float kGrow = 8.0f;     // the running maximum moves when it grows by more than this power of two
+constexpr uint32_t kCtlBytes = 512;
+
+struct AttnParams {
+  const __nv_bfloat16* q;
+  __nv_bfloat16* out;
+  int64_t q_stride, out_stride;   // elements between tokens
+  const int32_t* start;
+  const int32_t* seq;
+  const int32_t* lens;
+  const int32_t* table;
+  int n, tokens, max_tokens, seqs, table_stride, pages, page, page_shift;
+  int H, Hkv, G;
+  int causal, window;
+  float scale_log2;               // scale * log2(e)
+  const float* k_scale;
+  const float* v_scale;
+  int alt, splits, split_tiles;
+  int ring, raw_ring;
+  float* part_o;                  // [splits][tokens * H][Dh]
+  float2* part_ml;                // [splits][tokens * H] (log2 maximum, sum)
+  int* err;
+};
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2,
+                                            int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
+      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// Matrix descriptor of an MN-major operand in 128-byte-swizzled rows: rows along K (8-row groups 1024 bytes
+// apart), 64 elements of MN per row, further blocks of 64 `block_bytes` apart.
+__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t saddr, uint32_t block_bytes) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(block_bytes >> 4) << 16;
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+
+__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, float* v) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tadd.rn.f32x2 w, x, y;\n\t"
+      "mov.b64 {%0, %1}, w;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+template <bool kF16>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+  if constexpr (kF16) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  } else {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+}
+
+__device__ __forceinline__ uint32_t swz(int r, int c) {   // 16-byte chunk c of row r of a 128-byte-row tile
+  return static_cast<uint32_t>(r * 128 + ((c ^ (r & 7)) << 4));
+}
+
+struct Ctl {   // shared-memory control block
+  uint64_t full[kMaxRing], empty[kMaxRing], rfull[kMaxRing], rempty[kMaxRing];
+  uint64_t q_ready, s_full[2], p_full[2], o_done[2], drain;
+  uint32_t tmem;
+};
+static_assert(sizeof(Ctl) <= kCtlBytes, "control block");
+
+template <int DH, bool F8>
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tm_k,
+                      const __grid_constant__ CUtensorMap tm_v) {
+  constexpr int kHalves = DH / 64;                      // 128-byte blocks of a 16-bit row
+  constexpr uint32_t kTileBytes = kTileRows * DH * 2;   // a 16-bit tile
+  constexpr uint32_t kRawBytes = kTileRows * DH;        // a tile of E4M3 codes
+  constexpr uint32_t kBlock = kTileRows * 128;          // one 128-byte-row block
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int q_tiles = p.alt ? 1 : 2;
+  uint8_t* sq = smem;
+  uint8_t* sring = sq + q_tiles * kTileBytes;
+  uint8_t* sraw = sring + p.ring * kTileBytes;
+  Ctl& c = *reinterpret_cast<Ctl*>(sraw + (F8 ? p.raw_ring * kRawBytes : 0u));
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int row_block = gridDim.x - 1 - blockIdx.x;     // the rows with most keys (causal) start first
+  const int g = blockIdx.y;
+  const int entry = blockIdx.z / p.splits, split = blockIdx.z % p.splits;
+  const int block_rows = q_tiles * kTileRows;
+
+  if (tid == 0) {
+    for (int i = 0; i < kMaxRing; ++i) {
+      mbar_init(&c.full[i], F8 ? 2 : 1);
+      mbar_init(&c.empty[i], 1);
+      mbar_init(&c.rfull[i], 1);
+      mbar_init(&c.rempty[i], 2);
+    }
+    mbar_init(&c.q_ready, 8);
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&c.s_full[t], 1);
+      mbar_init(&c.p_full[t], 4);
+      mbar_init(&c.o_done[t], 1);
+    }
+    mbar_init(&c.drain, 1);
+    fence_mbar_init();
+  }
+  if (warp == kTmaWarp && lane == 0) {
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  pdl_wait();
+
+  // ---- the entry, its rows and its keys (the same in every thread)
+  int begin = __ldg(p.start + entry), nq = __ldg(p.start + entry + 1) - begin;
+  const int sid = p.seq ? __ldg(p.seq + entry) : entry;
+  bool bad = begin < 0 || nq < 0 || begin > p.tokens || nq > p.tokens - begin || sid < 0 || sid >= p.seqs;
+  int len = 0;
+  if (!bad) {
+    len = __ldg(p.lens + sid);
+    bad = len < 0 || len > p.table_stride * static_cast<int64_t>(p.page);
+    if (bad) len = 0;
+  } else {
+    nq = 0;
+  }
+  if ((bad || nq > p.max_tokens) && tid == 0 && row_block == 0 && g == 0 && split == 0) atomicOr(p.err, kErrBadBatch);
+  const int64_t rows = static_cast<int64_t>(nq) * p.G;
+  const int64_t row0 = static_cast<int64_t>(row_block) * block_rows;
+  if (row0 >= rows) return;   // before TMEM is taken, the same for the whole CTA
+
+  const int past = len - nq;   // pos(token) = past + token
+  auto key_end = [&](int64_t row) {   // one past the last key of a row
+    const int pos = past + static_cast<int>(row / p.G);
+    return pos < 0 ? 0 : (p.causal ? min(pos + 1, len) : len);
+  };
+  auto key_begin = [&](int64_t row) {
+    const int pos = past + static_cast<int>(row / p.G);
+    return p.window > 0 && pos >= p.window ? pos - p.window + 1 : 0;
+  };
+  const int64_t last_row = min(rows, row0 + block_rows) - 1;
+  const int hi_all = key_end(last_row);
+  int t_lo = key_begin(row0) / kTileRows;
+  int t_hi = (hi_all + kTileRows - 1) / kTileRows;
+  if (p.splits > 1) {
+    t_lo += split * p.split_tiles;
+    if (split < p.splits - 1) t_hi = min(t_hi, t_lo + p.split_tiles);   // the last one takes what is left
+  }
+  const int nt = max(0, t_hi - t_lo);   // key tiles of this CTA
+  int n_of[2];
+  if (p.alt) {
+    n_of[0] = (nt + 1) / 2;
+    n_of[1] = nt / 2;
+  } else {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int64_t lr = min(rows, row0 + (t + 1) * kTileRows) - 1;
+      n_of[t] = lr < row0 + t * kTileRows
+                    ? 0
+                    : max(0, min(t_hi, (key_end(lr) + kTileRows - 1) / kTileRows) - t_lo);
+    }
+  }
+  // Key tiles that some tile uses, and the tiles of each: n_of[0] <= n_of[1] except where tile 1 has no rows.
+  const int n_keys = p.alt ? nt : max(n_of[0], n_of[1]);
+
+  if (warp == kMmaWarp) {
+    tmem_alloc(&c.tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_trigger();   // after TMEM is held
+  const uint32_t tmem = c.tmem;
+  const uint32_t ring_a = smem_u32(sring), raw_a = smem_u32(sraw), q_a = smem_u32(sq);
+
+  if (warp < 8) {
+    // ================================================= softmax warpgroups
+    const int t = warp >> 2, wq = warp & 3;
+    const int r = wq * 32 + lane;
+    const int64_t row = row0 + (p.alt ? 0 : t * kTileRows) + r;
+    const bool live = row < rows;
+    const bool warp_live = row - lane < rows;
+    float c_row = p.scale_log2;
+    {   // ---- the query row into its swizzled tile (alternate tiles: the first warpgroup writes it)
+      const int64_t token = begin + row / p.G;
+      const int head = g * p.G + static_cast<int>(row % p.G);
+      const uint4* src = reinterpret_cast<const uint4*>(p.q + token * p.q_stride + static_cast<int64_t>(head) * DH);
+      const bool store = !p.alt || t == 0;
+      uint4 v[DH / 8];
+#pragma unroll
+      for (int i = 0; i < DH / 8; ++i) v[i] = live ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+      if constexpr (F8) {
+        uint32_t top = 0;   // largest |q| of the row as bf16 bits
+#pragma unroll
+        for (int i = 0; i < DH / 8; ++i) {
+          const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
+        }
+        // scale by 2^(14 - exponent): exact, and the inverse goes into the scores' factor
+        const int ex = static_cast<int>(top >> 7);   // biased exponent (0: zero or subnormal; 255: not finite)
+        const int sh = ex == 0 || ex == 255 ? 0 : min(max(141 - ex, -100), 100);   // 127 + 14 - ex
+        const float up = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
+        c_row *= __uint_as_float(static_cast<uint32_t>(127 - sh) << 23) * __ldg(p.k_scale);
+#pragma unroll
+        for (int i = 0; i < DH / 8; ++i) {
+          uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            w[e] = pack16<true>(__uint_as_float(w[e] << 16) * up, __uint_as_float(w[e] & 0xffff0000u) * up);
+          v[i] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+      if (store) {
+        const uint32_t base = q_a + (p.alt ? 0 : t * kTileBytes);
+#pragma unroll
+        for (int i = 0; i < DH / 8; ++i) st_shared_v4(base + (i >> 3) * kBlock + swz(r, i & 7), v[i]);
+        fence_async_smem();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&c.q_ready);
+    }
+    const int my_end = live ? key_end(row) : 0, my_begin = live ? key_begin(row) : 0;
+    const uint32_t t_lane = tmem + (static_cast<uint32_t>(wq * 32) << 16);
+    const uint32_t t_s = t_lane + t * 128, t_o = t_lane + 256 + t * 128;
+    const int n = n_of[t];
+    float m = -INFINITY;   // the reference maximum, in score units
+    float2 sum2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+    bool ok = true;
+    for (int i = 0; i < n; ++i) {
+      ok = mbar_wait(&c.s_full[t], i & 1);
+      if (!ok) break;
+      tc_fence_after();
+      __syncwarp();
+      if (warp_live) {
+        const int k0 = (t_lo + (p.alt ? 2 * i + t : i)) * kTileRows;
+        float s[128];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) tmem_ld32_async(t_s + b * 32, s + b * 32);
+        tmem_wait_ld();
+        const int lo = my_begin - k0, hi = my_end - k0;
+        if (__any_sync(0xffffffffu, lo > 0 || hi < kTileRows)) {
+#pragma unroll
+          for (int e = 0; e < 128; ++e) s[e] = e >= lo && e < hi ? s[e] : -INFINITY;
+        }
+        float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+        for (int e = 4; e < 128; e += 8) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            mx[j] = e + 4 + j < 128 ? fmaxf(fmaxf(mx[j], s[e + j]), s[e + 4 + j]) : fmaxf(mx[j], s[e + j]);
+        }
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        const bool grow = top > -INFINITY && !((top - m) * c_row <= kGrow);
+        if (__any_sync(0xffffffffu, grow)) {
+          float f = 1.0f;
+          if (grow) {
+            f = ex2_approx((m - top) * c_row);   // 0 for a row's first keys
+            m = top;
+            sum2[0].x *= f, sum2[0].y *= f, sum2[1].x *= f, sum2[1].y *= f;
+          }
+          // the tile's P V product before this one has completed: S was issued after it
+          if (i > 0) {
+#pragma unroll
+            for (int b = 0; b < DH; b += 16) {
+              float o[16];
+              tmem_ld16(t_o + b, o);
+              uint32_t w[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e] * f);
+              tmem_st16(t_o + b, w);
+            }
+            tmem_wait_st();
+          }
+        }
+        // f16 probabilities are held 2^6 larger: their subnormals begin that much lower
+        const float off = (F8 ? 6.0f : 0.0f) - (m > -INFINITY ? m * c_row : 0.0f);
+        const float2 c2 = make_float2(c_row, c_row), off2 = make_float2(off, off);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t w[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const int k = half * 64 + 2 * e;
+            float2 x = fma2(make_float2(s[k], s[k + 1]), c2, off2);
+            x.x = ex2_approx(x.x);
+            x.y = ex2_approx(x.y);
+            sum2[e & 1] = add2(sum2[e & 1], x);
+            w[e] = pack16<F8>(x.x, x.y);
+          }
+          tmem_st32(t_s + half * 32, w);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&c.p_full[t]);
+    }
+    const float2 st = add2(sum2[0], sum2[1]);
+    float sum = st.x + st.y;
+    float m2 = m > -INFINITY ? m * c_row : -INFINITY;   // log2 units
+    // ---- the end: O complete, joined across the warpgroups (alternate tiles), stored
+    if (p.alt) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        if (n_of[u] > 0) ok = mbar_wait(&c.o_done[u], 0) && ok;
+    } else if (n > 0) {
+      ok = mbar_wait(&c.o_done[t], 0) && ok;
+    }
+    tc_fence_after();
+    __syncwarp();
+    if (!ok) {
+      if (lane == 0) atomicOr(p.err, kErrPipelineTimeout);
+    }
+    const float vs = F8 ? __ldg(p.v_scale) : 1.0f;
+    const int64_t orow = (begin + row / p.G) * p.H + g * p.G + row % p.G;   // [token][head]
+    float* stage = reinterpret_cast<float*>(sring);                        // [128][DH], chunks swizzled by row
+    float2* stage_ml = reinterpret_cast<float2*>(sring + kTileRows * DH * 4);
+    if (p.alt) {
+      if (t == 1 && warp_live) {
+        stage_ml[r] = make_float2(m2, sum);
+#pragma unroll
+        for (int b = 0; b < DH; b += 16) {
+          float o[16];
+          if (n > 0)
+            tmem_ld16(t_o + b, o);
+          else
+            for (int e = 0; e < 16; ++e) o[e] = 0.f;
+#pragma unroll
+          for (int e = 0; e < 16; e += 4)
+            *reinterpret_cast<float4*>(stage + r * DH + ((((b + e) >> 2) ^ (r & 7)) << 2)) =
+                make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+        }
+      }
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+    }
+    if ((!p.alt || t == 0) && warp_live) {
+      float w0 = 1.0f, w1 = 0.0f;
+      if (p.alt) {
+        const float2 b = stage_ml[r];
+        const float top = fmaxf(m2, b.x);
+        w0 = m2 > -INFINITY ? ex2_approx(m2 - top) : 0.f;
+        w1 = b.x > -INFINITY ? ex2_approx(b.x - top) : 0.f;
+        sum = sum * w0 + b.y * w1;
+        m2 = top;
+      }
+      if (p.splits > 1) {
+        const int64_t at = static_cast<int64_t>(split) * p.tokens * p.H + orow;
+        if (live) p.part_ml[at] = make_float2(m2, sum);
+        w0 *= vs;
+        w1 *= vs;
+      } else {
+        const float inv = sum == 0.f ? 0.f : vs / sum;
+        w0 *= inv;
+        w1 *= inv;
+      }
+      if (p.splits == 1 || nt > 0) {
+#pragma unroll
+        for (int b = 0; b < DH; b += 16) {
+          float o[16];
+          if (n > 0)
+            tmem_ld16(t_o + b, o);
+          else
+            for (int e = 0; e < 16; ++e) o[e] = 0.f;
+          if (p.alt) {
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+              const float4 x = *reinterpret_cast<const float4*>(stage + r * DH + ((((b + e) >> 2) ^ (r & 7)) << 2));
+              o[e] = o[e] * w0 + x.x * w1;
+              o[e + 1] = o[e + 1] * w0 + x.y * w1;
+              o[e + 2] = o[e + 2] * w0 + x.z * w1;
+              o[e + 3] = o[e + 3] * w0 + x.w * w1;
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] *= w0;
+          }
+          if (live) {
+            if (p.splits > 1) {
+              float4* dst = reinterpret_cast<float4*>(
+                  p.part_o + (static_cast<int64_t>(split) * p.tokens * p.H + orow) * DH + b);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            } else {
+              uint4* dst = reinterpret_cast<uint4*>(p.out + (begin + row / p.G) * p.out_stride +
+                                                    (g * p.G + row % p.G) * DH + b);
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                dst[e] = make_uint4(pack16<false>(o[8 * e], o[8 * e + 1]), pack16<false>(o[8 * e + 2], o[8 * e + 3]),
+                                    pack16<false>(o[8 * e + 4], o[8 * e + 5]), pack16<false>(o[8 * e + 6], o[8 * e + 7]));
+            }
+          }
+        }
+      }
+    }
+  } else if (warp == kMmaWarp) {
+    // ================================================= tensor cores
+    // f32 accumulate; bf16 operands (code 1) or f16 (code 0); bit 16: the second operand MN-major
+    constexpr uint32_t fmt = F8 ? 0u : ((1u << 7) | (1u << 10));
+    constexpr uint32_t id_s = (1u << 4) | fmt | ((128u >> 3) << 17) | ((128u >> 4) << 24);
+    constexpr uint32_t id_o = (1u << 4) | fmt | (1u << 16) | ((static_cast<uint32_t>(DH) >> 3) << 17) | ((128u >> 4) << 24);
+    // the last key tile's values behind the length (inside its last page) are zeroed here (16-bit cache)
+    const int tail_tile = len % kTileRows ? len / kTileRows - t_lo : -1;
+    bool ok = mbar_wait(&c.q_ready, 0);
+    auto key_tile = [&](int t, int i) { return p.alt ? 2 * i + t : i; };
+    auto last_user = [&](int t, int j) { return p.alt || t == 1 || j >= n_of[1]; };
+    auto first_user = [&](int t, int j) { return p.alt || t == 0 || j >= n_of[0]; };
+    auto scores = [&](int t, int i) {
+      const int j = key_tile(t, i), item = 2 * j, b = item % p.ring;
+      if (!mbar_wait(&c.full[b], (item / p.ring) & 1)) return false;
+      tc_fence_after();
+      if (lane == 0) {
+        const uint32_t qa = q_a + (p.alt ? 0 : t * kTileBytes), ka = ring_a + b * kTileBytes;
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            tc_mma<false>(tmem + t * 128, sw128_kmajor_desc(qa + h * kBlock + k * 32),
+                          sw128_kmajor_desc(ka + h * kBlock + k * 32), id_s, (h | k) ? 1u : 0u);
+        if (last_user(t, j)) tc_commit(&c.empty[b]);
+        tc_commit(&c.s_full[t]);
+      }
+      __syncwarp();
+      return true;
+    };
+    auto values = [&](int t, int i) {
+      const int j = key_tile(t, i), item = 2 * j + 1, b = item % p.ring;
+      if (!mbar_wait(&c.full[b], (item / p.ring) & 1)) return false;
+      if (!F8 && j == tail_tile && first_user(t, j)) {
+        const int r0 = len % kTileRows;
+        for (int x = lane; x < (kTileRows - r0) * 8 * kHalves; x += 32)
+          st_shared_v4(ring_a + b * kTileBytes + (x % kHalves) * kBlock + r0 * 128 + (x / kHalves) * 16,
+                       make_uint4(0, 0, 0, 0));
+        fence_async_smem();
+        __syncwarp();
+      }
+      if (!mbar_wait(&c.p_full[t], i & 1)) return false;
+      tc_fence_after();
+      if (lane == 0) {
+        const uint32_t va = ring_a + b * kTileBytes;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          tc_mma_ts<false>(tmem + 256 + t * 128, tmem + t * 128 + k * 8, sw128_mnmajor_desc(va + k * 2048, kBlock), id_o,
+                           (i | k) ? 1u : 0u);
+        if (last_user(t, j)) tc_commit(&c.empty[b]);
+        if (i == n_of[t] - 1) tc_commit(&c.o_done[t]);
+      }
+      __syncwarp();
+      return true;
+    };
+    const int n_max = max(n_of[0], n_of[1]);
+    for (int t = 0; t < 2 && ok; ++t)
+      if (n_of[t] > 0) ok = scores(t, 0);
+    for (int i = 0; i < n_max && ok; ++i)
+      for (int t = 0; t < 2 && ok; ++t) {
+        if (i >= n_of[t]) continue;
+        ok = values(t, i);
+        if (ok && i + 1 < n_of[t]) ok = scores(t, i + 1);
+      }
+    if (!ok) {   // a wait ran out: let what was issued finish before the CTA leaves
+      if (lane == 0) {
+        atomicOr(p.err, kErrPipelineTimeout);
+        tc_commit(&c.drain);
+      }
+      __syncwarp();
+      mbar_wait(&c.drain, 0);
+    }
+  } else if (warp == kTmaWarp) {
+    // ================================================= page table and TMA
+    const int rows_box = min(p.page, kTileRows), boxes = kTileRows / rows_box;   // boxes of a tile
+    const int part = lane % boxes, half = lane / boxes;                          // this lane's box and block
+    const bool active = lane < boxes * (F8 ? 1 : kHalves);
+    const int32_t* trow = p.table + static_cast<int64_t>(sid) * p.table_stride;
+    auto page_of = [&](int j) {   // the page of this lane's box of key tile j; the pool's end where there is none
+      const int key = (t_lo + j) * kTileRows + part * rows_box;
+      if (!active || key >= len) return p.pages;
+      const int pg = __ldg(trow + (key >> p.page_shift));
+      if (pg < 0 || pg >= p.pages) {
+        atomicOr(p.err, kErrBadBatch);
+        return p.pages;
+      }
+      return pg;
+    };
+    const int nb = F8 ? p.raw_ring : p.ring;
+    uint64_t* full = F8 ? c.rfull : c.full;
+    uint64_t* empty = F8 ? c.rempty : c.empty;
+    const uint32_t base = F8 ? raw_a : ring_a;
+    constexpr uint32_t bytes = F8 ? kRawBytes : kTileBytes;
+    int pg = n_keys > 0 ? page_of(0) : 0;
+    bool ok = true;
+    int issued = 0;
+    for (int j = 0; j < n_keys && ok; ++j) {
+      const int row_in = ((t_lo + j) * kTileRows + part * rows_box) & (p.page - 1);
+      const int next = j + 1 < n_keys ? page_of(j + 1) : 0;
+      for (int kv = 0; kv < 2 && ok; ++kv) {
+        const int item = 2 * j + kv, b = item % nb;
+        if (item >= nb) ok = mbar_wait(&empty[b], (item / nb - 1) & 1);
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(&full[b], bytes);
+        __syncwarp();
+        if (active) {
+          const uint32_t dst = base + b * bytes + (F8 ? part * rows_box * DH : half * kBlock + part * rows_box * 128);
+          tma_load_4d(dst, kv ? &tm_v : &tm_k, &full[b], half * 64, row_in, g, pg);
+        }
+        ++issued;
+      }
+      pg = next;
+    }
+    if (!ok) {   // the copies in flight land before the CTA leaves
+      if (lane == 0) atomicOr(p.err, kErrPipelineTimeout);
+      for (int item = max(0, issued - nb); item < issued; ++item) mbar_wait(&full[item % nb], (item / nb) & 1);
+    }
+  } else if (F8) {
+    // ================================================= E4M3 codes -> f16 tiles
+    const int ct = tid - kCvtWarp * 32;   // 0..63
+    constexpr int kChunks = DH / 16;      // 16-code chunks of a row
+    bool ok = true;
+    for (int item = 0; item < 2 * n_keys && ok; ++item) {
+      const int rb = item % p.raw_ring, b = item % p.ring;
+      ok = mbar_wait(&c.rfull[rb], (item / p.raw_ring) & 1);
+      if (ok && item >= p.ring) ok = mbar_wait(&c.empty[b], (item / p.ring - 1) & 1);
+      if (!ok) break;
+      const int valid = len - (t_lo + (item >> 1)) * kTileRows;   // rows of the tile inside the length
+      const uint4* src = reinterpret_cast<const uint4*>(sraw + rb * kRawBytes);
+      const uint32_t dst = ring_a + b * kTileBytes;
+#pragma unroll 4
+      for (int x = ct; x < kTileRows * kChunks; x += 64) {
+        const int r = x / kChunks, ch = x % kChunks;
+        const uint4 v = r < valid ? src[x] : make_uint4(0, 0, 0, 0);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        uint32_t h[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w[e] & 0xffffu), __NV_E4M3);
+          const __half2_raw hi = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w[e] >> 16), __NV_E4M3);
+          h[2 * e] = static_cast<uint32_t>(lo.x) | (static_cast<uint32_t>(lo.y) << 16);
+          h[2 * e + 1] = static_cast<uint32_t>(hi.x) | (static_cast<uint32_t>(hi.y) << 16);
+        }
+        // the two halves of the row write their chunks in opposite orders: eight lanes, eight bank groups
+        const uint32_t at = dst + (ch >> 2) * kBlock;
+        const int c0 = (ch & 3) * 2, odd = (ch >> 2) & 1;
+        const uint4 a = make_uint4(h[0], h[1], h[2], h[3]), d = make_uint4(h[4], h[5], h[6], h[7]);
+        st_shared_v4(at + swz(r, c0 + odd), odd ? d : a);
+        st_shared_v4(at + swz(r, c0 + 1 - odd), odd ? a : d);
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&c.full[b]);
+        mbar_arrive(&c.rempty[rb]);
+      }
+    }
+    if (!ok && lane == 0) atomicOr(p.err, kErrPipelineTimeout);
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the splits of every (token, head) row in split order: a warp per row.
+template <int DH>
+__global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ part_o, const float2* __restrict__ part_ml,
+                                                      int splits, int tokens, int H, const int32_t* __restrict__ start,
+                                                      int n, __nv_bfloat16* __restrict__ out, int64_t out_stride) {
+  pdl_wait();
+  const int64_t rows = static_cast<int64_t>(tokens) * H;
+  const int64_t row = blockIdx.x * 8ll + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (row >= rows) return;
+  const int token = static_cast<int>(row / H);
+  if (token < __ldg(start) || token >= __ldg(start + n)) return;   // rows of no entry keep what they hold
+  float top = -INFINITY;
+  for (int s = lane; s < splits; s += 32) top = fmaxf(top, part_ml[s * rows + row].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  constexpr int kPer = DH / 32;
+  float acc[kPer] = {};
+  float sum = 0.f;
+  for (int s0 = 0; s0 < splits; s0 += 32) {
+    float w = 0.f, l = 0.f;
+    if (s0 + lane < splits) {
+      const float2 ml = part_ml[(s0 + lane) * rows + row];
+      w = ml.x > -INFINITY ? exp2f(ml.x - top) : 0.f;
+      l = ml.y * w;
+    }
+    const int cnt = min(32, splits - s0);
+#pragma unroll 4
+    for (int i = 0; i < cnt; ++i) {
+      const float wi = __shfl_sync(0xffffffffu, w, i);
+      sum += __shfl_sync(0xffffffffu, l, i);
+      if (wi == 0.f) continue;
+      const float* src = part_o + ((s0 + i) * rows + row) * DH + lane * kPer;
+      if constexpr (kPer == 4) {
+        const float4 v = *reinterpret_cast<const float4*>(src);
+        acc[0] += wi * v.x, acc[1] += wi * v.y, acc[2] += wi * v.z, acc[3] += wi * v.w;
+      } else {
+        const float2 v = *reinterpret_cast<const float2*>(src);
+        acc[0] += wi * v.x, acc[1] += wi * v.y;
+      }
+    }
+  }
+  const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+  __nv_bfloat16* dst = out + token * out_stride + (row % H) * DH + lane * kPer;
+  if constexpr (kPer == 4)
+    *reinterpret_cast<uint2*>(dst) = make_uint2(pack16<false>(acc[0] * inv, acc[1] * inv), pack16<false>(acc[2] * inv, acc[3] * inv));
+  else
+    *reinterpret_cast<uint32_t*>(dst) = pack16<false>(acc[0] * inv, acc[1] * inv);
+}
+
+// Rows of one KV head's page block as a TMA source: (head dim, token, head, page).
+bool kv_tmap(CUtensorMap* map, const fm_kv_cache& c, const void* base) {
+  const bool f8 = c.fmt == FM_FMT_FP8;
+  const uint64_t eb = f8 ? 1 : 2;
+  const uint64_t dims[4] = {static_cast<uint64_t>(c.Dh), static_cast<uint64_t>(c.page_tokens),
+                            static_cast<uint64_t>(c.Hkv), static_cast<uint64_t>(c.pages)};
+  // the stride of an extent of one is never used: any legal value
+  const auto stride = [&](int64_t s, int extent) { return (extent == 1 ? c.Dh : s) * eb; };
+  const uint64_t strides[3] = {stride(c.token_stride, c.page_tokens), stride(c.head_stride, c.Hkv),
+                               stride(c.page_stride, c.pages)};
+  const uint32_t box[4] = {static_cast<uint32_t>(f8 ? c.Dh : 64),
+                           static_cast<uint32_t>(std::min(c.page_tokens, kTileRows)), 1, 1};
+  return make_tmap_4d(map, base, static_cast<int>(eb), dims, strides, box, !f8);
+}
+
+struct Plan {
+  int alt, splits, split_tiles, ring, raw_ring;
+  size_t smem;
+};
+
+int sm_count() {
+  static std::atomic<int> cached[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+    cudaGetLastError();
+    return 152;
+  }
+  int v = cached[dev].load(std::memory_order_relaxed);
+  if (v) return v;
+  if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || v <= 0) {
+    cudaGetLastError();
+    v = 152;
+  }
+  cached[dev].store(v, std::memory_order_relaxed);
+  return v;
+}
+
+// The variant for a batch: by its bounds and the number of SMs alone, so that the workspace query and the launch agree.
+Plan plan_of(const fm_kv_cache& c, const fm_kv_batch& b, int H) {
+  Plan pl;
+  const int64_t rows = static_cast<int64_t>(b.max_tokens) * (H / c.Hkv);
+  pl.alt = rows <= kTileRows;
+  const size_t tile = static_cast<size_t>(kTileRows) * c.Dh * 2;
+  const size_t q = tile * (pl.alt ? 1 : 2);
+  const size_t room = kSmemLimit - kCtlBytes - q;
+  if (c.fmt == FM_FMT_FP8) {
+    pl.ring = 4;
+    pl.raw_ring = static_cast<int>(std::min<size_t>(kMaxRing, (room - pl.ring * tile) / (tile / 2)));
+  } else {
+    pl.ring = static_cast<int>(std::min<size_t>(kMaxRing, room / tile));
+    pl.raw_ring = 0;
+  }
+  pl.smem = 1024 + q + pl.ring * tile + pl.raw_ring * (tile / 2) + kCtlBytes;
+  const int64_t block_rows = pl.alt ? kTileRows : 2 * kTileRows;
+  const int64_t units = (rows + block_rows - 1) / block_rows * c.Hkv * b.n;
+  const int tiles = std::max(1, (b.max_len + kTileRows - 1) / kTileRows);
+  const int sms = sm_count();
+  int64_t want = units > 0 ? (2 * sms + units - 1) / units : 1;
+  if (units >= sms) want = 1;
+  const int min_tiles = pl.alt ? 2 : 4;
+  int64_t splits = std::max<int64_t>(1, std::min<int64_t>(want, tiles / min_tiles));
+  pl.split_tiles = static_cast<int>((tiles + splits - 1) / splits);
+  // a window's first key lies inside a tile: one tile more than the bound's count can be touched
+  pl.splits = splits == 1 ? 1 : (tiles + pl.split_tiles - 1) / pl.split_tiles;
+  return pl;
+}
+
+template <int DH, bool F8>
+cudaError_t configure_one() {
+  return cudaFuncSetAttribute(paged_attn_kernel<DH, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              kSmemLimit + 1024);
+}
+
+cudaError_t configure() {
+  cudaError_t e = configure_one<64, false>();
+  if (e == cudaSuccess) e = configure_one<128, false>();
+  if (e == cudaSuccess) e = configure_one<64, true>();
+  if (e == cudaSuccess) e = configure_one<128, true>();
+  return e;
+}
+
+int check(const fm_kv_cache* c, const fm_kv_batch* b, int H) {
+  int st = kv_check(c);
+  if (st == FM_OK) st = kv_batch_check(c, b);
+  if (st != FM_OK) return st;
+  if (H <= 0 || H % c->Hkv) return record_error(FM_ERR_SHAPE, "H must be a positive multiple of the cache's Hkv");
+  if (c->Dh != 64 && c->Dh != 128) return record_error(FM_ERR_SHAPE, "attention takes head dims of 64 or 128");
+  if (c->page_tokens > 256) return record_error(FM_ERR_SHAPE, "attention takes pages of 16 to 256 tokens");
+  const int64_t rows = static_cast<int64_t>(b->max_tokens) * (H / c->Hkv);
+  if (rows > (int64_t(1) << 30)) return record_error(FM_ERR_SHAPE, "max_tokens * H / Hkv exceeds 2^30");
+  const Plan pl = plan_of(*c, *b, H);
+  if (c->Hkv > 65535 || static_cast<int64_t>(b->n) * pl.splits > 65535)
+    return record_error(FM_ERR_SHAPE, "too many entries for one call (entries x splits and Hkv up to 65535)");
+  return FM_OK;
+}
+
+size_t workspace(const Plan& pl, const fm_kv_cache& c, const fm_kv_batch& b, int H) {
+  if (pl.splits == 1) return 0;
+  return static_cast<size_t>(pl.splits) * b.tokens * H * (c.Dh * sizeof(float) + sizeof(float2));
+}
+
+}  // namespace
+
+}  // namespace fm
+
+extern "C" int fm_paged_attention_workspace_size(const fm_kv_cache* c, const fm_kv_batch* b, int H, size_t* bytes) {
+  if (!bytes) return fm::record_error(FM_ERR_INVALID_ARG, "bytes is NULL");
+  const int st = fm::check(c, b, H);
+  if (st != FM_OK) return st;
+  *bytes = b->n && b->tokens ? fm::workspace(fm::plan_of(*c, *b, H), *c, *b, H) : 0;
+  return FM_OK;
+}
+
+extern "C" int fm_paged_attention(const fm_kv_cache* c, int layer, const fm_kv_batch* b, const uint16_t* q,
+                                  int64_t q_stride, int H, float scale, int causal, int window, uint16_t* out,
+                                  int64_t out_stride, void* workspace, size_t workspace_bytes, void* stream) {
+  using namespace fm;
+  const int st = check(c, b, H);
+  if (st != FM_OK) return st;
+  if (layer < 0 || layer >= c->layers) return record_error(FM_ERR_INVALID_ARG, "layer out of range");
+  if (!(scale > 0.f) || !std::isfinite(scale)) return record_error(FM_ERR_INVALID_ARG, "scale must be positive and finite");
+  if (window < 0) return record_error(FM_ERR_INVALID_ARG, "window must be 0 (none) or positive");
+  if (b->n == 0 || b->tokens == 0 || b->max_tokens == 0) return FM_OK;
+  if (!q || !out) return record_error(FM_ERR_INVALID_ARG, "NULL argument");
+  const int64_t row = static_cast<int64_t>(H) * c->Dh;
+  if (q_stride < row || out_stride < row || q_stride % 8 || out_stride % 8)
+    return record_error(FM_ERR_SHAPE, "token strides must be multiples of 8 elements and hold H * Dh");
+  if (reinterpret_cast<uintptr_t>(q) % 16 || reinterpret_cast<uintptr_t>(out) % 16)
+    return record_error(FM_ERR_ALIGN, "q and out must be 16-byte aligned");
+  const Plan pl = plan_of(*c, *b, H);
+  const size_t need = fm::workspace(pl, *c, *b, H);
+  if (need) {
+    if (!workspace) return record_error(FM_ERR_INVALID_ARG, "workspace is NULL");
+    if (reinterpret_cast<uintptr_t>(workspace) % 16) return record_error(FM_ERR_ALIGN, "workspace not 16-byte aligned");
+    if (workspace_bytes < need)
+      return record_error(FM_ERR_WORKSPACE, "workspace smaller than fm_paged_attention_workspace_size()");
+  }
+  const bool f8 = c->fmt == FM_FMT_FP8;
+  const int64_t off = layer * c->layer_stride * (f8 ? 1 : 2);
+  CUtensorMap tk, tv;
+  if (!kv_tmap(&tk, *c, static_cast<const uint8_t*>(c->k) + off) || !kv_tmap(&tv, *c, static_cast<const uint8_t*>(c->v) + off))
+    return record_error(FM_ERR_CUDA, "cuTensorMapEncodeTiled (cache pages) failed");
+  int* err = standalone_error_word();
+  if (!err) return record_error(FM_ERR_CUDA, "no error word on the current device");
+  cudaError_t e = configure_once(4, configure);
+  if (e != cudaSuccess) return record_error(FM_ERR_CUDA, cudaGetErrorString(e));
+  AttnParams p = {};
+  p.q = reinterpret_cast<const __nv_bfloat16*>(q);
+  p.out = reinterpret_cast<__nv_bfloat16*>(out);
+  p.q_stride = q_stride;
+  p.out_stride = out_stride;
+  p.start = b->start;
+  p.seq = b->seq;
+  p.lens = c->lens;
+  p.table = c->table;
+  p.n = b->n;
+  p.tokens = b->tokens;
+  p.max_tokens = b->max_tokens;
+  p.seqs = c->seqs;
+  p.table_stride = c->table_stride;
+  p.pages = c->pages;
+  p.page = c->page_tokens;
+  while ((1 << p.page_shift) < c->page_tokens) ++p.page_shift;
+  p.H = H;
+  p.Hkv = c->Hkv;
+  p.G = H / c->Hkv;
+  p.causal = causal != 0;
+  p.window = window;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.k_scale = f8 ? c->k_scale + layer : nullptr;
+  p.v_scale = f8 ? c->v_scale + layer : nullptr;
+  p.alt = pl.alt;
+  p.splits = pl.splits;
+  p.split_tiles = pl.split_tiles;
+  p.ring = pl.ring;
+  p.raw_ring = pl.raw_ring;
+  p.part_o = static_cast<float*>(workspace);
+  p.part_ml = reinterpret_cast<float2*>(p.part_o + static_cast<size_t>(pl.splits) * b->tokens * H * c->Dh);
+  p.err = err;
+  const int64_t rows = static_cast<int64_t>(b->max_tokens) * p.G;
+  const int64_t block_rows = pl.alt ? kTileRows : 2 * kTileRows;
+  LaunchOpts o;
+  o.stream = static_cast<cudaStream_t>(stream);
+  o.pdl = true;
+  const dim3 grid(static_cast<unsigned>((rows + block_rows - 1) / block_rows), static_cast<unsigned>(c->Hkv),
+                  static_cast<unsigned>(b->n * pl.splits));
+  auto kernel = c->Dh == 128 ? (f8 ? paged_attn_kernel<128, true> : paged_attn_kernel<128, false>)
+                             : (f8 ? paged_attn_kernel<64, true> : paged_attn_kernel<64, false>);
+  e = launch(kernel, grid, dim3(kThreads), pl.smem, o, p, tk, tv);
+  if (e == cudaSuccess && pl.splits > 1) {
+    const int64_t blocks = (static_cast<int64_t>(b->tokens) * H + 7) / 8;
+    auto join = c->Dh == 128 ? combine_kernel<128> : combine_kernel<64>;
+    e = launch(join, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, o, static_cast<const float*>(p.part_o),
+               static_cast<const float2*>(p.part_ml), pl.splits, b->tokens, H, b->start, b->n, p.out, out_stride);
+  }
+  return e == cudaSuccess ? FM_OK : record_error(FM_ERR_CUDA, cudaGetErrorString(e));
+}

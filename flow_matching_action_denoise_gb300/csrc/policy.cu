@@ -16,6 +16,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <atomic>
 #include <chrono>
 #include <cstdio>
 #include <cstring>
@@ -24,6 +25,7 @@
 #include <vector>
 
 #include "internal.h"
+#include "kv.h"
 
 using fm::LaunchOpts;
 
@@ -851,6 +853,19 @@ int check_ptrs(const fm_weights* w, int L, bool given, std::string* why) {
 
 namespace fm {
 
+int* standalone_error_word() {
+  static std::atomic<int*> cached[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
+  int* w = cached[dev].load(std::memory_order_acquire);
+  if (w) return w;
+  void* addr = nullptr;
+  if (cudaGetSymbolAddress(&addr, fm_standalone_err) != cudaSuccess) return nullptr;
+  w = static_cast<int*>(addr);
+  cached[dev].store(w, std::memory_order_release);
+  return w;
+}
+
 int record_error(int status, const char* why) { return fail(nullptr, status, why); }
 
 int gemm_consumer_scratch_bytes(int M, int N, int K, int fmt, int s, size_t* bytes, const char** why) {
@@ -1199,6 +1214,27 @@ int refresh_prefix(fm_policy* p, int tok_begin, int tok_end, const uint16_t* k, 
   return FM_OK;
 }
 
+int refresh_prefix_pages(fm_policy* p, int tok_begin, int tok_end, const fm_kv_cache* cache, int seq, int seq_tok,
+                         void* stream) {
+  if (!p) return fail(p, FM_ERR_INVALID_ARG, "NULL policy");
+  const int st = fm::kv_check(cache);
+  if (st != FM_OK) return fail(p, st, g_last_error);
+  const fm_config& c = p->cfg;
+  if (tok_begin < 0 || tok_end > c.P || tok_begin >= tok_end) return fail(p, FM_ERR_SHAPE, "bad token range");
+  if (cache->layers != c.L || cache->Hkv != c.Hkv || cache->Dh != c.Dh)
+    return fail(p, FM_ERR_SHAPE, "the cache's layers, Hkv and Dh must be the policy's");
+  const int rows = tok_end - tok_begin;
+  if (seq < 0 || seq >= cache->seqs) return fail(p, FM_ERR_INVALID_ARG, "sequence out of range");
+  if (seq_tok < 0 || seq_tok > cache->table_stride * static_cast<int64_t>(cache->page_tokens) - rows)
+    return fail(p, FM_ERR_SHAPE, "the tokens lie outside the sequence's table row");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  FM_CUDA(p, fm::prefix_from_pages_launch(*cache, seq, seq_tok, rows, p->at<__nv_bfloat16>(p->ly.kcache),
+                                          p->at<__nv_bfloat16>(p->ly.vcache), c.P, (c.P + 7) / 8 * 8, tok_begin,
+                                          p->errw(), s));
+  if (p->dv.attn_fp8) FM_CUDA(p, requant_prefix(p, tok_begin, tok_end, s));
+  return FM_OK;
+}
+
 uint64_t steady_ns() {
   return static_cast<uint64_t>(std::chrono::duration_cast<std::chrono::nanoseconds>(
                                    std::chrono::steady_clock::now().time_since_epoch())
@@ -1411,7 +1447,9 @@ int fm_device_status(fm_policy* p, void* stream, int* word) {
   FM_CUDA(p, cudaMemsetAsync(p->errw(), 0, sizeof w, s));
   FM_CUDA(p, cudaStreamSynchronize(s));
   *word = w;
-  return w ? fail(p, FM_ERR_DEVICE, "a kernel abandoned a bounded wait") : FM_OK;
+  return w ? fail(p, FM_ERR_DEVICE,
+                  w & fm::kErrPipelineTimeout ? "a kernel abandoned a bounded wait"
+                                              : "a prefix row was read from a token without a page") : FM_OK;
 }
 
 int fm_standalone_status(void* stream, int* word) {
@@ -1430,7 +1468,10 @@ int fm_standalone_status(void* stream, int* word) {
   }
   FM_CUDA(nullptr, cudaStreamSynchronize(s));
   *word = got[0] | got[1];
-  return *word ? fail(nullptr, FM_ERR_DEVICE, "a standalone kernel abandoned a bounded wait") : FM_OK;
+  return *word ? fail(nullptr, FM_ERR_DEVICE,
+                      *word & fm::kErrPipelineTimeout ? "a standalone kernel abandoned a bounded wait"
+                                                      : "a paged batch left its bounds or met a token without a page")
+               : FM_OK;
 }
 
 int fm_named_buffer(const fm_policy* p, const char* name, void** ptr, size_t* bytes) {

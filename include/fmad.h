@@ -232,6 +232,18 @@ int set_prefix_kv(fm_policy* p, const uint16_t* k, const uint16_t* v, void* stre
 int refresh_prefix(fm_policy* p, int tok_begin, int tok_end, const uint16_t* k,
                    const uint16_t* v, void* stream);
 
+/* refresh_prefix whose rows come from a paged cache (see fm_kv_cache below): prefix rows
+ * [tok_begin, tok_end) of every layer from tokens [seq_tok, seq_tok + tok_end - tok_begin)
+ * of sequence `seq` (a row of the cache's table). The cache has the policy's L layers, Hkv
+ * and Dh (FM_ERR_SHAPE otherwise); an FP8 cache is dequantised with its scales and rounded
+ * to bf16. A token at or behind the sequence's length, or without a page, gives a zero row
+ * and sets bit 2 of the policy's error word (fm_device_status). Asynchronous.
+ * Source: news article "FlashRT-PAI", section "It optimises the relay" (selective
+ * refresh of the image-dependent state). */
+struct fm_kv_cache;
+int refresh_prefix_pages(fm_policy* p, int tok_begin, int tok_end, const struct fm_kv_cache* cache, int seq,
+                         int seq_tok, void* stream);
+
 /* One decision: S Euler steps from the noise (t = 1) to the action chunk (t = 0).
  * noise: device fp32 [M][A], or NULL to start from the policy's noise/action
  * buffer as it stands (e.g. after restore_state). actions: device fp32 [M][A]
@@ -331,13 +343,15 @@ int fm_session_fork(fm_policy* base, const void* capsule, size_t bytes, int caps
 
 /* Synchronise `stream`, read and clear the device error word. Returns FM_OK, or
  * FM_ERR_DEVICE with *word = the bits a kernel set when it abandoned a bounded
- * wait (1 = TMA/MMA pipeline wait expired). */
+ * wait (1 = TMA/MMA pipeline wait expired) or met a token without a page (2, see
+ * refresh_prefix_pages). */
 int fm_device_status(fm_policy* p, void* stream, int* word);
 
 /* Error word of the policy-free building blocks (fm_test_skinny_gemm, fm_gemm_consumer,
- * fm_gemm_consumer_noalloc): synchronise `stream`, read and clear the bits their kernels
+ * fm_gemm_consumer_noalloc, fm_rope_append, fm_paged_attention): synchronise `stream`, read and clear the bits their kernels
  * set when they abandoned a bounded wait on the current device. Returns FM_OK, or
- * FM_ERR_DEVICE with *word = the bits (1 = TMA/MMA pipeline wait expired); the outputs of
+ * FM_ERR_DEVICE with *word = the bits (1 = TMA/MMA pipeline wait expired, 2 = a paged
+ * batch outside its bounds or a token without a page); the outputs of
  * the calls since the previous check are then not to be trusted. Those entry points are
  * asynchronous, so they cannot report this themselves. */
 int fm_standalone_status(void* stream, int* word);
@@ -562,6 +576,176 @@ int fm_test_consumer(const float* partials, int nparts, int M, int N, const floa
  * x_in, x_out device fp32 [M][d]; q_out device [M][d] codes (fp8 or bf16). */
 int fm_test_layer(fm_policy* p, const float* x_in, int layer, int step, float* x_out,
                   void* q_out, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The paged prefix cache: what fills the prefix that a policy attends to. A model
+ * that reads images and instructions runs its layers as fm_norm_quant -> projection
+ * -> fm_rope_append -> fm_paged_attention -> projection over a cache whose sequences
+ * grow, share and return pages (fm_kv_reserve, fm_kv_fork, fm_kv_release,
+ * fm_kv_compact), and refresh_prefix_pages hands a sequence to a policy.
+ *
+ * All state is caller-owned device memory and all work is stream-ordered, with no
+ * host round trip: a step can be captured into a CUDA graph. Calls that change one
+ * cache, and calls that use one workspace, must be ordered by the caller (one stream,
+ * or events); captured graphs that share a workspace must not run at once.
+ * ------------------------------------------------------------------------- */
+
+/* A cache: K and V pools of `layers` layers x `pages` pages of `page_tokens` tokens x Hkv
+ * heads x Dh elements, and its bookkeeping. Dh elements of a row are contiguous; the other
+ * strides (elements, the same in K and V) may be in any order as long as rows do not
+ * overlap. Preconditions (FM_ERR_SHAPE unless noted):
+ *   fmt BF16 or FP8 (FM_ERR_INVALID_ARG); page_tokens 16, 32, 64, 128 or 256; Dh a multiple
+ *   of 16 up to 256; layers, Hkv <= 65535; pages <= 2^30; strides of extents above one
+ *   multiples of 16 bytes; k, v 16-byte aligned (FM_ERR_ALIGN); table_stride * page_tokens
+ *   < 2^31.
+ * An FP8 cache holds E4M3 codes, value = code * k_scale[layer] (v_scale for V).
+ * A sequence is a row of the table: its page numbers in order, -1 behind them, and its
+ * length in lens. refs counts the rows that name a page (0 = free); the fm_kv_* calls need
+ * it, the others take NULL. Start with table = -1, lens = 0, refs = 0. */
+typedef struct fm_kv_cache {
+  void* k;
+  void* v;
+  int fmt;
+  int layers, pages, page_tokens, Hkv, Dh;
+  int64_t layer_stride, page_stride, token_stride, head_stride;
+  const float* k_scale;   /* device fp32 [layers], FP8 only */
+  const float* v_scale;
+  int32_t* table;         /* device [seqs][table_stride] */
+  int32_t* lens;          /* device [seqs] */
+  int32_t* refs;          /* device [pages] */
+  int seqs, table_stride;
+} fm_kv_cache;
+
+/* The new tokens of a step, packed: entry i has rows [start[i], start[i + 1]) of the packed
+ * arrays and is the end of sequence seq[i] (NULL: sequence i): with new = start[i + 1] -
+ * start[i], its row j is the token at position lens[seq[i]] - new + j. So lens already
+ * counts the new tokens (fm_kv_reserve adds them). Rows that belong to no entry are neither
+ * read nor written. max_tokens bounds every entry's new tokens (more: bit 2 of the error
+ * word, and the rows behind it are not computed); max_len is the length that the work is
+ * divided for (a longer sequence is right, only slower). 0 <= n <= 65535. */
+typedef struct fm_kv_batch {
+  const int32_t* start;   /* device [n + 1] */
+  const int32_t* seq;     /* device [n] or NULL */
+  int n;
+  int tokens;             /* rows of the packed arrays */
+  int max_tokens;
+  int max_len;
+} fm_kv_batch;
+
+/* Bits of status[0] of the fm_kv_* calls; 0 = done. status[1]: pages taken
+ * (fm_kv_reserve; with FM_KV_NO_PAGES the pages that were missing) or moved (fm_kv_compact),
+ * else 0. A call that reports a bit has changed nothing. */
+enum {
+  FM_KV_NO_PAGES = 1,    /* too few free pages */
+  FM_KV_BAD_ENTRY = 2,   /* a sequence out of range, named twice where it may be named once,
+                            a negative count, a fork target that is not empty or is also a
+                            source, or bookkeeping that contradicts itself */
+  FM_KV_ROW_FULL = 4     /* a sequence would outgrow its table row */
+};
+
+/* Bytes of workspace for fm_kv_reserve of n sequences and for fm_kv_compact (n = 0). */
+int fm_kv_workspace_size(const fm_kv_cache* c, int n, size_t* bytes);
+
+/* Make room for count[i] more tokens at the end of sequence seq[i] (device int32 [n], no
+ * sequence twice, n <= 1024): lens grows by the counts, pages are taken lowest free index
+ * first, entry by entry. Where the last page is begun and shared, the first entry that
+ * would write to it gets a copy of its tokens (all layers) in a page taken before the
+ * entry's others; the last of a page's users keeps the page. All entries or none. status:
+ * device int32 [2]. workspace: device, 16-byte aligned. Asynchronous. */
+int fm_kv_reserve(const fm_kv_cache* c, const int32_t* seq, const int32_t* count, int n, int32_t* status,
+                  void* workspace, size_t workspace_bytes, void* stream);
+
+/* Sequence dst[i] (empty, named once, no source of the call) becomes a fork of src[i]: it
+ * names the same pages, no token is copied. A source may be named many times. n <= 1024.
+ * All or none. Asynchronous. */
+int fm_kv_fork(const fm_kv_cache* c, const int32_t* src, const int32_t* dst, int n, int32_t* status, void* stream);
+
+/* Cut sequence seq[i] back to its first keep[i] tokens (NULL: 0, the sequence becomes
+ * empty; more than its length: no change): pages that no row names any more are free
+ * again. n <= 1024, no sequence twice. All or none. Asynchronous. */
+int fm_kv_release(const fm_kv_cache* c, const int32_t* seq, const int32_t* keep, int n, int32_t* status, void* stream);
+
+/* Draw the pool together: with n_live pages in use, those at n_live and above move in
+ * ascending order into the free ones below it, in ascending order; K, V (all layers),
+ * table and refs follow. Afterwards pages [n_live, pages) are free. Asynchronous. */
+int fm_kv_compact(const fm_kv_cache* c, int32_t* status, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Rotary positions. Pair i of a head turns by position * f_i: with FM_ROPE_HALF the elements
+ * (i, i + rotary_dim / 2), with FM_ROPE_INTERLEAVED (2i, 2i + 1); elements from rotary_dim
+ * on pass unchanged. f_i = theta^(-2 i / rotary_dim), scaled for long contexts by
+ *   FM_ROPE_LINEAR    f_i / factor (positions squeezed);
+ *   FM_ROPE_BASE      theta replaced by theta * factor^(rotary_dim / (rotary_dim - 2));
+ *   FM_ROPE_BY_PARTS  f_i kept where the pair turns more than beta_fast times within
+ *                     original_len, f_i / factor where less than beta_slow, a linear ramp
+ *                     over i between, and cos and sin multiplied by 0.1 ln(factor) + 1
+ *                     (Peng et al., "YaRN", 2023). */
+enum { FM_ROPE_HALF = 0, FM_ROPE_INTERLEAVED = 1 };
+enum { FM_ROPE_PLAIN = 0, FM_ROPE_LINEAR = 1, FM_ROPE_BASE = 2, FM_ROPE_BY_PARTS = 3 };
+typedef struct fm_rope_config {
+  int rotary_dim;   /* a multiple of 16, 16..256 */
+  int scaling;      /* FM_ROPE_* */
+  double theta;     /* > 1 */
+  double factor;    /* >= 1, unused by FM_ROPE_PLAIN */
+  double original_len, beta_fast, beta_slow;   /* FM_ROPE_BY_PARTS */
+} fm_rope_config;
+
+/* The frequencies as turns per position times 2^64 (HOST uint64 [rotary_dim / 2]; upload
+ * them once) and the factor on cos and sin. Whole turns then vanish modulo 2^64, so an angle
+ * is exact to 2^-52 turns per position of frequency error at any position. Host call. */
+int fm_rope_table(const fm_rope_config* r, uint64_t* freq, float* magnitude);
+
+typedef struct fm_rope {
+  const uint64_t* freq;   /* device [rotary_dim / 2], from fm_rope_table */
+  int rotary_dim;         /* a multiple of 16 up to Dh; 0: no rotation */
+  int layout;             /* FM_ROPE_HALF or FM_ROPE_INTERLEAVED */
+  float magnitude;
+} fm_rope;
+
+/* Rotate the batch's queries into q_out and its keys into the cache's pages, and store its
+ * values there: q [tokens][H][Dh], k, v [tokens][Hkv][Dh], q_out like q, all bf16 with
+ * `stride` elements between tokens (a multiple of 8; parts of one merged projection output
+ * do); q_out may be q. H = 0 stores keys and values only. The pages must exist
+ * (fm_kv_reserve); pages of an FP8 cache receive E4M3(x * fp32(1 / scale)), saturated.
+ * positions: NULL, or device int32 [tokens] that replaces the positions in the angles (not
+ * the places in the cache). A token without a page sets bit 2 of fm_standalone_status and
+ * is not stored. Asynchronous. */
+int fm_rope_append(const fm_kv_cache* c, int layer, const fm_kv_batch* b, const fm_rope* rope, const uint16_t* q,
+                   int64_t q_stride, int H, const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride,
+                   uint16_t* q_out, int64_t q_out_stride, const int32_t* positions, void* stream);
+
+/* Bytes of workspace for fm_paged_attention (0 where the keys are not split); depends on the
+ * cache's Dh, Hkv and format, the batch's counts and H only. */
+int fm_paged_attention_workspace_size(const fm_kv_cache* c, const fm_kv_batch* b, int H, size_t* bytes);
+
+/* Attention of the batch's tokens over their sequences' pages (their own included):
+ *   out[t][h] = sum_j p_j v_j,  p = softmax_j(scale * q[t][h] . k_j)
+ * over keys j < lens, j <= position(t) if causal != 0, j > position(t) - window if
+ * window > 0; query head h reads KV head h / (H / Hkv). Tokens at negative positions, and
+ * any row without keys, give zeros. q, out: device bf16 [tokens][H][Dh], `stride` elements
+ * between tokens (a multiple of 8); out must not overlap q. Dh 64 or 128; H a multiple of
+ * Hkv; scale > 0. Softmax and sums in fp32, probabilities rounded to bf16 (f16 with an FP8
+ * cache). What a page holds behind its sequence's length does not matter, even NaN; the
+ * keys and values before it must be finite (a NaN there reaches every row whose key tile
+ * holds it, masked or not). A token without a page counts as a zero key and value and sets
+ * bit 2 of fm_standalone_status. workspace: device, 16-byte aligned. Asynchronous. */
+int fm_paged_attention(const fm_kv_cache* c, int layer, const fm_kv_batch* b, const uint16_t* q, int64_t q_stride, int H,
+                       float scale, int causal, int window, uint16_t* out, int64_t out_stride, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
+/* Residual addition + RMS norm + E4M3 with scales taken from the data:
+ *   s = x + r (r NULL: x);  x_out = s (unless NULL);
+ *   y = s / sqrt(mean(s^2) + eps) * gamma (gamma NULL: 1);
+ *   scale = max|y| / 448 over the row (block 0) or over each 128 columns (block 128, the
+ *   last block may be shorter);  codes = E4M3(y / scale), 0 where scale is 0.
+ * x, x_out: device [T][d], fp32 if x_f32 else bf16; r device bf16 [T][d]; `stride` elements
+ * between rows (multiples of 8); x_out may be x. gamma device fp32 [d]; codes device uint8
+ * [T][d] contiguous: a GEMM operand; scales device fp32 [T] or [T][ceil(d / 128)]. d a
+ * multiple of 16 up to 16384. Statistics in fp32 from the unrounded s. Asynchronous.
+ * Source: blog post, "Static quantisation" (the fused residual, norm and FP8 convert), here
+ * with scales from the data for activations that have not been calibrated. */
+int fm_norm_quant(const void* x, int64_t x_stride, int x_f32, const uint16_t* r, int64_t r_stride, const float* gamma,
+                  int T, int d, float eps, void* x_out, int64_t x_out_stride, uint8_t* codes, float* scales, int block,
+                  void* stream);
 
 #ifdef __cplusplus
 }
