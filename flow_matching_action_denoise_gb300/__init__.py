@@ -548,43 +548,64 @@ def _bad(where: str, why: str):
     raise FmError(1, where, why)
 
 
-def _tensor(x, where: str, name: str, dtypes, device, shape=None):
-    """x's address after checking what the C side cannot see: the type, the device and the shape (None: any extent)."""
+# The checks of what the C side cannot see (type, device, shape, contiguity). A serving step makes these calls by the
+# thousand, so each check is a few attribute reads and the reason is worked out only after one has failed.
+
+def _check_tensor(x, where: str, name: str, dtypes, dev: int, shape=None):
     if x.dtype not in dtypes:
         _bad(where, f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {x.dtype}")
-    if x.device != device:
-        _bad(where, f"{name} is on {x.device}, expected {device}")
-    if shape is not None and (x.dim() != len(shape) or any(a is not None and a != b for a, b in zip(shape, x.shape))):
+    if x.get_device() != dev:
+        _bad(where, f"{name} is on {x.device}, expected cuda:{dev}")
+    if shape is not None and tuple(x.shape) != shape:
         _bad(where, f"{name} must have shape {shape}, got {tuple(x.shape)}")
+
+
+def _heads(x, where: str, name: str, dtype, dev: int, rows: int, heads: int, dim: int):
+    """(address, elements between rows) of x [rows][heads][dim] whose rows are contiguous."""
+    if x.dtype is not dtype or x.get_device() != dev or x.shape != (rows, heads, dim):
+        _check_tensor(x, where, name, (dtype,), dev, (rows, heads, dim))
+    s0, s1, s2 = x.stride()
+    if (s2 != 1 and dim != 1) or (s1 != dim and heads != 1):
+        _bad(where, f"{name}: a row's elements must be contiguous")
+    return x.data_ptr(), s0 if rows > 1 else heads * dim
+
+
+def _rows(x, where: str, name: str, dtype, dev: int, rows: int, cols: int):
+    """(address, elements between rows) of x [rows][cols] whose rows are contiguous."""
+    if x.dtype is not dtype or x.get_device() != dev or x.shape != (rows, cols):
+        _check_tensor(x, where, name, (dtype,), dev, (rows, cols))
+    s0, s1 = x.stride()
+    if s1 != 1 and cols != 1:
+        _bad(where, f"{name}: a row's elements must be contiguous")
+    return x.data_ptr(), s0 if rows > 1 else cols
+
+
+def _ints(x, where: str, name: str, dev: int, count: int):
+    import torch
+    if x.dtype is not torch.int32 or x.get_device() != dev:
+        _check_tensor(x, where, name, (torch.int32,), dev)
+    if not x.is_contiguous() or x.numel() < count:
+        _bad(where, f"{name} must be contiguous with at least {count} elements")
     return x.data_ptr()
 
 
-def _rows(x, where: str, name: str, dtypes, device, shape):
-    """(address, elements between rows) of x [rows][heads][dim] or [rows][dim] with the rows' own elements contiguous."""
-    ptr = _tensor(x, where, name, dtypes, device, shape)
-    inner = 1
-    for size, stride in zip(reversed(x.shape[1:]), reversed(x.stride()[1:])):
-        if size != 1 and stride != inner:
-            _bad(where, f"{name}: a row's elements must be contiguous")
-        inner *= size
-    return ptr, (x.stride(0) if x.shape[0] > 1 else inner)
-
-
-def _ints(x, where: str, name: str, device, count: int):
+def _here(dev: int, stream, where: str):
+    """The stream to use on device `dev`: the given one, or that device's current one. The library works on the
+    current device, so the two must agree."""
     import torch
-    ptr = _tensor(x, where, name, (torch.int32,), device)
-    if not x.is_contiguous() or x.numel() < count:
-        _bad(where, f"{name} must be contiguous with at least {count} elements")
-    return ptr
+    if torch._C._cuda_getDevice() != dev:
+        _bad(where, f"the tensors are on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)   # current_stream(dev).cuda_stream without its Python objects
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
-def _here(device, stream, where: str):
-    """The stream to use on `device`: the given one, or that device's current one. The library works on the current
-    device, so the two must agree."""
-    import torch
-    if torch.cuda.current_device() != device.index:
-        _bad(where, f"the tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
-    return _stream(stream)
+def _workspace(ws, where: str, dev: int):
+    if ws is None:
+        return None, 0
+    if ws.get_device() != dev or not ws.is_contiguous():
+        _bad(where, "the workspace must be a contiguous tensor on the cache's device")
+    return ws.data_ptr(), ws.nbytes
 
 
 class KvCache:
@@ -606,11 +627,12 @@ class KvCache:
             _bad(where, "the last dim of k and v must be contiguous")
         if not k.is_cuda:
             _bad(where, "k must be a device tensor")
-        self.device = k.device
+        self.device, self.dev = k.device, k.get_device()
         fp8 = k.dtype == torch.float8_e4m3fn
         s = FmKvCache()
-        s.k = _tensor(k, where, "k", (torch.bfloat16, torch.float8_e4m3fn), self.device)
-        s.v = _tensor(v, where, "v", (k.dtype,), self.device)
+        _check_tensor(k, where, "k", (torch.bfloat16, torch.float8_e4m3fn), self.dev)
+        _check_tensor(v, where, "v", (k.dtype,), self.dev)
+        s.k, s.v = k.data_ptr(), v.data_ptr()
         s.fmt = FMT_FP8 if fp8 else FMT_BF16
         s.layers, s.pages, s.page_tokens, s.Hkv, s.Dh = k.shape
         s.layer_stride, s.page_stride, s.token_stride, s.head_stride = k.stride()[:4]
@@ -618,16 +640,18 @@ class KvCache:
             for name, x in (("k_scale", k_scale), ("v_scale", v_scale)):
                 if x is None or not x.is_contiguous() or x.numel() != s.layers:
                     _bad(where, f"an FP8 cache needs {name}: float32 [layers], contiguous")
-                setattr(s, name, _tensor(x, where, name, (torch.float32,), self.device))
+                _check_tensor(x, where, name, (torch.float32,), self.dev)
+                setattr(s, name, x.data_ptr())
         if table.dim() != 2 or not table.is_contiguous() or lens.numel() != table.shape[0]:
             _bad(where, "table must be [seqs][max pages] contiguous and lens [seqs]")
         s.seqs, s.table_stride = table.shape
-        s.table = _ints(table, where, "table", self.device, table.numel())
-        s.lens = _ints(lens, where, "lens", self.device, s.seqs)
+        s.table = _ints(table, where, "table", self.dev, table.numel())
+        s.lens = _ints(lens, where, "lens", self.dev, s.seqs)
         if refs is not None:
-            s.refs = _ints(refs, where, "refs", self.device, s.pages)
+            s.refs = _ints(refs, where, "refs", self.dev, s.pages)
         self.struct = s
         self.addr = ctypes.addressof(s)
+        self.Hkv, self.Dh = s.Hkv, s.Dh
         self.k, self.v, self.table, self.lens, self.refs = k, v, table, lens, refs
         self.k_scale, self.v_scale = k_scale, v_scale
 
@@ -640,11 +664,11 @@ class KvBatch:
         n = start.numel() - 1
         if n < 0:
             _bad("KvBatch", "start must have at least one element")
-        self.device = start.device
+        self.device, self.dev = start.device, start.get_device()
         s = FmKvBatch()
-        s.start = _ints(start, "KvBatch", "start", self.device, 1)
+        s.start = _ints(start, "KvBatch", "start", self.dev, 1)
         if seq is not None:
-            s.seq = _ints(seq, "KvBatch", "seq", self.device, n)
+            s.seq = _ints(seq, "KvBatch", "seq", self.dev, n)
         s.n, s.tokens, s.max_tokens, s.max_len = n, int(tokens), int(max_tokens), int(max_len)
         self.struct = s
         self.addr = ctypes.addressof(s)
@@ -671,14 +695,14 @@ class Rope:
         import torch
         freq, mag = rope_table(rotary_dim, theta, scaling, factor, original_len, beta_fast, beta_slow)
         self.freq = torch.from_numpy(freq.view(np.int64)).to(device)
-        self.device = self.freq.device
+        self.device, self.dev = self.freq.device, self.freq.get_device()
         self.struct = FmRope(self.freq.data_ptr(), int(rotary_dim), ROPE_HALF if half else ROPE_INTERLEAVED, mag)
         self.addr = ctypes.addressof(self.struct)
 
 
 def refresh_prefix_pages(p: int, tok_begin: int, tok_end: int, cache: KvCache, seq: int, seq_tok: int = 0, stream=None):
     _check(load().refresh_prefix_pages(p, tok_begin, tok_end, cache.addr, seq, seq_tok,
-                                       _here(cache.device, stream, "refresh_prefix_pages")), "refresh_prefix_pages", p)
+                                       _here(cache.dev, stream, "refresh_prefix_pages")), "refresh_prefix_pages", p)
 
 
 def kv_workspace_size(cache: KvCache, n: int = 0) -> int:
@@ -688,62 +712,63 @@ def kv_workspace_size(cache: KvCache, n: int = 0) -> int:
     return b.value
 
 
-def _workspace(ws, where: str, device):
-    if ws is None:
-        return None, 0
-    if ws.device != device or not ws.is_contiguous():
-        _bad(where, "the workspace must be a contiguous tensor on the cache's device")
-    return ws.data_ptr(), ws.numel() * ws.element_size()
-
-
 def kv_reserve(cache: KvCache, seq, count, status, workspace, stream=None):
     """Room for count[i] more tokens of sequence seq[i]; status int32 [2] on the device."""
-    d, n, w = cache.device, seq.numel(), "fm_kv_reserve"
+    d, n, w = cache.dev, seq.numel(), "fm_kv_reserve"
     ws, nb = _workspace(workspace, w, d)
-    _check(load().fm_kv_reserve(cache.addr, _ints(seq, w, "seq", d, n), _ints(count, w, "count", d, n), n,
-                                _ints(status, w, "status", d, 2), ws, nb, _here(d, stream, w)), w)
+    st = (_lib or load()).fm_kv_reserve(cache.addr, _ints(seq, w, "seq", d, n), _ints(count, w, "count", d, n), n,
+                                        _ints(status, w, "status", d, 2), ws, nb, _here(d, stream, w))
+    if st:
+        _check(st, w)
 
 
 def kv_fork(cache: KvCache, src, dst, status, stream=None):
     """The empty sequence dst[i] names the pages of src[i]."""
-    d, n, w = cache.device, src.numel(), "fm_kv_fork"
-    _check(load().fm_kv_fork(cache.addr, _ints(src, w, "src", d, n), _ints(dst, w, "dst", d, n), n,
-                             _ints(status, w, "status", d, 2), _here(d, stream, w)), w)
+    d, n, w = cache.dev, src.numel(), "fm_kv_fork"
+    st = (_lib or load()).fm_kv_fork(cache.addr, _ints(src, w, "src", d, n), _ints(dst, w, "dst", d, n), n,
+                                     _ints(status, w, "status", d, 2), _here(d, stream, w))
+    if st:
+        _check(st, w)
 
 
 def kv_release(cache: KvCache, seq, status, keep=None, stream=None):
     """Cut sequence seq[i] back to keep[i] tokens (None: to none)."""
-    d, n, w = cache.device, seq.numel(), "fm_kv_release"
-    _check(load().fm_kv_release(cache.addr, _ints(seq, w, "seq", d, n),
-                                None if keep is None else _ints(keep, w, "keep", d, n), n,
-                                _ints(status, w, "status", d, 2), _here(d, stream, w)), w)
+    d, n, w = cache.dev, seq.numel(), "fm_kv_release"
+    st = (_lib or load()).fm_kv_release(cache.addr, _ints(seq, w, "seq", d, n),
+                                        None if keep is None else _ints(keep, w, "keep", d, n), n,
+                                        _ints(status, w, "status", d, 2), _here(d, stream, w))
+    if st:
+        _check(st, w)
 
 
 def kv_compact(cache: KvCache, status, workspace, stream=None):
     """Move the live pages to the front of the pool."""
-    d, w = cache.device, "fm_kv_compact"
+    d, w = cache.dev, "fm_kv_compact"
     ws, nb = _workspace(workspace, w, d)
-    _check(load().fm_kv_compact(cache.addr, _ints(status, w, "status", d, 2), ws, nb, _here(d, stream, w)), w)
+    st = (_lib or load()).fm_kv_compact(cache.addr, _ints(status, w, "status", d, 2), ws, nb, _here(d, stream, w))
+    if st:
+        _check(st, w)
 
 
 def rope_append(cache: KvCache, layer: int, batch: KvBatch, rope: Rope, q, k, v, q_out, positions=None, stream=None):
     """Rotate q [tokens][H][Dh] into q_out and k [tokens][Hkv][Dh] into the pages, store v there (all bfloat16; q and
     q_out None: keys and values only)."""
     import torch
-    d, w, s = cache.device, "fm_rope_append", cache.struct
-    bf, T = (torch.bfloat16,), batch.tokens
-    if batch.device != d or rope.device != d:
+    d, w, bf, T, Hkv, Dh = cache.dev, "fm_rope_append", torch.bfloat16, batch.tokens, cache.Hkv, cache.Dh
+    if batch.dev != d or rope.dev != d:
         _bad(w, "the cache, the batch and the rotary table must be on one device")
     H, qp, qs, op, os_ = 0, None, 0, None, 0
     if q is not None:
         H = q.shape[1]
-        qp, qs = _rows(q, w, "q", bf, d, (T, H, s.Dh))
-        op, os_ = _rows(q_out, w, "q_out", bf, d, (T, H, s.Dh))
-    kp, ks = _rows(k, w, "k", bf, d, (T, s.Hkv, s.Dh))
-    vp, vs = _rows(v, w, "v", bf, d, (T, s.Hkv, s.Dh))
-    _check(load().fm_rope_append(cache.addr, layer, batch.addr, rope.addr, qp, qs, H, kp, ks, vp, vs, op, os_,
-                                 None if positions is None else _ints(positions, w, "positions", d, T),
-                                 _here(d, stream, w)), w)
+        qp, qs = _heads(q, w, "q", bf, d, T, H, Dh)
+        op, os_ = _heads(q_out, w, "q_out", bf, d, T, H, Dh)
+    kp, ks = _heads(k, w, "k", bf, d, T, Hkv, Dh)
+    vp, vs = _heads(v, w, "v", bf, d, T, Hkv, Dh)
+    st = (_lib or load()).fm_rope_append(cache.addr, layer, batch.addr, rope.addr, qp, qs, H, kp, ks, vp, vs, op, os_,
+                                         None if positions is None else _ints(positions, w, "positions", d, T),
+                                         _here(d, stream, w))
+    if st:
+        _check(st, w)
 
 
 def paged_attention_workspace_size(cache: KvCache, batch: KvBatch, H: int) -> int:
@@ -757,40 +782,49 @@ def paged_attention(cache: KvCache, layer: int, batch: KvBatch, q, out, workspac
                     causal: bool = True, window: int = 0, stream=None):
     """Attention of q [tokens][H][Dh] (bfloat16) over the batch's sequences into out; scale None: 1 / sqrt(Dh)."""
     import torch
-    d, w, s = cache.device, "fm_paged_attention", cache.struct
-    bf, T, H = (torch.bfloat16,), batch.tokens, q.shape[1]
-    if batch.device != d:
+    d, w, bf, T, H, Dh = cache.dev, "fm_paged_attention", torch.bfloat16, batch.tokens, q.shape[1], cache.Dh
+    if batch.dev != d:
         _bad(w, "the cache and the batch must be on one device")
-    qp, qs = _rows(q, w, "q", bf, d, (T, H, s.Dh))
-    op, os_ = _rows(out, w, "out", bf, d, (T, H, s.Dh))
+    qp, qs = _heads(q, w, "q", bf, d, T, H, Dh)
+    op, os_ = _heads(out, w, "out", bf, d, T, H, Dh)
     ws, nb = _workspace(workspace, w, d)
-    _check(load().fm_paged_attention(cache.addr, layer, batch.addr, qp, qs, H,
-                                     s.Dh ** -0.5 if scale is None else float(scale), int(bool(causal)), int(window),
-                                     op, os_, ws, nb, _here(d, stream, w)), w)
+    st = (_lib or load()).fm_paged_attention(cache.addr, layer, batch.addr, qp, qs, H,
+                                             Dh ** -0.5 if scale is None else scale, 1 if causal else 0, window, op, os_,
+                                             ws, nb, _here(d, stream, w))
+    if st:
+        _check(st, w)
 
 
 def norm_quant(x, r, gamma, eps: float, x_out, codes, scales, block: int = 0, stream=None):
     """x [T][d] (float32 or bfloat16) + r (bfloat16 or None) -> x_out (or None), E4M3 codes (float8_e4m3fn or uint8)
     of its RMS norm times gamma (float32 [d] or None) and their scales, per row (block 0) or per 128 columns."""
     import torch
-    w, d = "fm_norm_quant", x.device
-    if not x.is_cuda:
+    w, d, f32 = "fm_norm_quant", x.get_device(), torch.float32
+    if d < 0:
         _bad(w, "x must be a device tensor")
     T, cols = x.shape
-    xp, xs = _rows(x, w, "x", (torch.float32, torch.bfloat16), d, (T, cols))
-    rp, rs = (None, 0) if r is None else _rows(r, w, "r", (torch.bfloat16,), d, (T, cols))
-    op, os_ = (None, 0) if x_out is None else _rows(x_out, w, "x_out", (x.dtype,), d, (T, cols))
+    xt = x.dtype
+    if xt is not f32 and xt is not torch.bfloat16:
+        _bad(w, f"x must be float32 or bfloat16, got {xt}")
+    xp, xs = _rows(x, w, "x", xt, d, T, cols)
+    rp, rs = (None, 0) if r is None else _rows(r, w, "r", torch.bfloat16, d, T, cols)
+    op, os_ = (None, 0) if x_out is None else _rows(x_out, w, "x_out", xt, d, T, cols)
     gp = None
     if gamma is not None:
-        gp = _tensor(gamma, w, "gamma", (torch.float32,), d, (cols,))
-        if not gamma.is_contiguous():
+        if gamma.dtype is not f32 or gamma.get_device() != d or gamma.shape != (cols,) or not gamma.is_contiguous():
+            _check_tensor(gamma, w, "gamma", (f32,), d, (cols,))
             _bad(w, "gamma must be contiguous")
-    cp = _tensor(codes, w, "codes", (torch.float8_e4m3fn, torch.uint8), d, (T, cols))
-    sp = _tensor(scales, w, "scales", (torch.float32,), d)
+        gp = gamma.data_ptr()
+    if codes.get_device() != d or codes.shape != (T, cols) or codes.dtype not in (torch.float8_e4m3fn, torch.uint8):
+        _check_tensor(codes, w, "codes", (torch.float8_e4m3fn, torch.uint8), d, (T, cols))
+    if scales.dtype is not f32 or scales.get_device() != d:
+        _check_tensor(scales, w, "scales", (f32,), d)
     if not codes.is_contiguous() or not scales.is_contiguous() or scales.numel() != T * (-(-cols // 128) if block else 1):
         _bad(w, "codes and scales must be contiguous, scales [T] or [T][ceil(d / 128)]")
-    _check(load().fm_norm_quant(xp, xs, int(x.dtype == torch.float32), rp, rs, gp, T, cols, float(eps), op, os_, cp, sp,
-                                int(block), _here(d, stream, w)), w)
+    st = (_lib or load()).fm_norm_quant(xp, xs, 1 if xt is f32 else 0, rp, rs, gp, T, cols, eps, op, os_,
+                                        codes.data_ptr(), scales.data_ptr(), block, _here(d, stream, w))
+    if st:
+        _check(st, w)
 
 
 # ---------------------------------------------------------------- convenience owner

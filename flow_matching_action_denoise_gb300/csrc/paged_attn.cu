@@ -44,8 +44,11 @@ namespace fm {
 namespace {
 
 constexpr int kTileRows = 128;    // rows of a query tile (MMA M) and keys of a key tile
-constexpr int kThreads = 384;     // 8 softmax warps, MMA warp, TMA warp, 2 expanding warps
-constexpr int kMmaWarp = 8, kTmaWarp = 9, kCvtWarp = 10;
+constexpr int kMmaWarp = 8, kTmaWarp = 9, kCvtWarp = 12, kCvtWarps = 4;
+// Warpgroups: two softmax, one with the MMA and the TMA warp, and with an E4M3 cache one that expands codes. Registers
+// move to the softmax warpgroups, which keep 128 scores each: 384 x 168 = 256 x 216 + 128 x 72, 512 x 128 = 256 x 192 +
+// 256 x 64.
+constexpr int threads_of(bool f8) { return f8 ? 512 : 384; }
 constexpr int kSmemLimit = 226 * 1024;
 constexpr int kMaxRing = 8;
 constexpr float kGrow = 8.0f;     // the running maximum moves when it grows by more than this power of two
@@ -70,6 +73,36 @@ struct AttnParams {
   float* part_o;                  // [splits][tokens * H][Dh]
   float2* part_ml;                // [splits][tokens * H] (log2 maximum, sum)
   int* err;
+};
+
+// True once the phase with the given parity has completed; false after 2^22 polls (each of which the hardware suspends
+// for a while: seconds, far beyond any legitimate wait). Reading a clock between the polls cost more than the wait.
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity) {
+#pragma unroll 1
+  for (int i = 0; i < (1 << 22); ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  return false;
+}
+
+// One lane of a converged warp. Unlike a comparison with a lane number it tells the compiler that a single lane is
+// active: tcgen05 instructions take their operands from the warp's uniform registers, and under a plain branch each
+// MMA took about 100 cycles to issue (operands collected lane by lane), longer than it runs.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t pred = 0;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\t@p mov.s32 %0, 1;\n}" : "+r"(pred));
+  return pred != 0;
+}
+
+// Position in a ring of buffers: the buffer and the parity of its barrier's phase.
+struct Ring {
+  int b = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next(int n) {
+    if (++b == n) {
+      b = 0;
+      phase ^= 1;
+    }
+  }
 };
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2,
@@ -153,13 +186,13 @@ __device__ __forceinline__ uint32_t swz(int r, int c) {   // 16-byte chunk c of 
 
 struct Ctl {   // shared-memory control block
   uint64_t full[kMaxRing], empty[kMaxRing], rfull[kMaxRing], rempty[kMaxRing];
-  uint64_t q_ready, s_full[2], p_full[2], o_done[2], drain;
+  uint64_t q_ready, s_full[2], p_full[2][2], o_done[2], drain;
   uint32_t tmem;
 };
 static_assert(sizeof(Ctl) <= kCtlBytes, "control block");
 
 template <int DH, bool F8>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(threads_of(F8), 1)
     paged_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v) {
   constexpr int kHalves = DH / 64;                      // 128-byte blocks of a 16-bit row
@@ -182,15 +215,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     for (int i = 0; i < kMaxRing; ++i) {
-      mbar_init(&c.full[i], F8 ? 2 : 1);
+      mbar_init(&c.full[i], F8 ? kCvtWarps : 1);
       mbar_init(&c.empty[i], 1);
       mbar_init(&c.rfull[i], 1);
-      mbar_init(&c.rempty[i], 2);
+      mbar_init(&c.rempty[i], kCvtWarps);
     }
     mbar_init(&c.q_ready, 8);
     for (int t = 0; t < 2; ++t) {
       mbar_init(&c.s_full[t], 1);
-      mbar_init(&c.p_full[t], 4);
+      mbar_init(&c.p_full[t][0], 4);
+      mbar_init(&c.p_full[t][1], 4);
       mbar_init(&c.o_done[t], 1);
     }
     mbar_init(&c.drain, 1);
@@ -215,20 +249,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     nq = 0;
   }
   if ((bad || nq > p.max_tokens) && tid == 0 && row_block == 0 && g == 0 && split == 0) atomicOr(p.err, kErrBadBatch);
-  const int64_t rows = static_cast<int64_t>(nq) * p.G;
-  const int64_t row0 = static_cast<int64_t>(row_block) * block_rows;
+  const int rows = nq > p.max_tokens ? p.max_tokens * p.G : nq * p.G;   // <= 2^30
+  const int row0 = row_block * block_rows;
   if (row0 >= rows) return;   // before TMEM is taken, the same for the whole CTA
 
   const int past = len - nq;   // pos(token) = past + token
-  auto key_end = [&](int64_t row) {   // one past the last key of a row
-    const int pos = past + static_cast<int>(row / p.G);
+  auto key_end = [&](int row) {   // one past the last key of a row
+    const int pos = past + row / p.G;
     return pos < 0 ? 0 : (p.causal ? min(pos + 1, len) : len);
   };
-  auto key_begin = [&](int64_t row) {
-    const int pos = past + static_cast<int>(row / p.G);
+  auto key_begin = [&](int row) {
+    const int pos = past + row / p.G;
     return p.window > 0 && pos >= p.window ? pos - p.window + 1 : 0;
   };
-  const int64_t last_row = min(rows, row0 + block_rows) - 1;
+  const int last_row = min(rows, row0 + block_rows) - 1;
   const int hi_all = key_end(last_row);
   int t_lo = key_begin(row0) / kTileRows;
   int t_hi = (hi_all + kTileRows - 1) / kTileRows;
@@ -244,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      const int64_t lr = min(rows, row0 + (t + 1) * kTileRows) - 1;
+      const int lr = min(rows, row0 + (t + 1) * kTileRows) - 1;
       n_of[t] = lr < row0 + t * kTileRows
                     ? 0
                     : max(0, min(t_hi, (key_end(lr) + kTileRows - 1) / kTileRows) - t_lo);
@@ -264,162 +298,196 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = c.tmem;
   const uint32_t ring_a = smem_u32(sring), raw_a = smem_u32(sraw), q_a = smem_u32(sq);
 
+  // one instruction for a whole warpgroup
+  if (warp < 8) {
+    if constexpr (F8)
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    else
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+  } else {
+    if constexpr (F8)
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    else
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+  }
+
   if (warp < 8) {
     // ================================================= softmax warpgroups
     const int t = warp >> 2, wq = warp & 3;
     const int r = wq * 32 + lane;
-    const int64_t row = row0 + (p.alt ? 0 : t * kTileRows) + r;
+    const int tile_row0 = row0 + (p.alt ? 0 : t * kTileRows);
+    const int row = tile_row0 + r;
     const bool live = row < rows;
     const bool warp_live = row - lane < rows;
+    constexpr int kRowChunks = DH / 8;          // 16-byte chunks of a 16-bit row
+    constexpr int kStep = 32 / kRowChunks;      // rows a warp moves at a time
+    // this lane's rows of the warp's 32 (cooperative moves: kRowChunks lanes a row), as offsets of [token][head]
+    const int lane_row = lane / kRowChunks, lane_chunk = lane % kRowChunks;
     float c_row = p.scale_log2;
-    {   // ---- the query row into its swizzled tile (alternate tiles: the first warpgroup writes it)
-      const int64_t token = begin + row / p.G;
-      const int head = g * p.G + static_cast<int>(row % p.G);
-      const uint4* src = reinterpret_cast<const uint4*>(p.q + token * p.q_stride + static_cast<int64_t>(head) * DH);
-      const bool store = !p.alt || t == 0;
-      uint4 v[DH / 8];
+    {   // ---- the query rows into their swizzled tile; of one tile for both warpgroups each takes every other step
+      const uint32_t base = q_a + (p.alt ? 0 : t * kTileBytes);
+      constexpr int kSteps = 32 / kStep;
+      uint4 v[kSteps];
 #pragma unroll
-      for (int i = 0; i < DH / 8; ++i) v[i] = live ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-      if constexpr (F8) {
-        uint32_t top = 0;   // largest |q| of the row as bf16 bits
+      for (int i = 0; i < kSteps; ++i) {
+        const int rr = wq * 32 + i * kStep + lane_row, R = tile_row0 + rr;
+        v[i] = make_uint4(0, 0, 0, 0);
+        if (R < rows && (F8 || !p.alt || (i & 1) == t)) {
+          const int token = R / p.G, head = g * p.G + R % p.G;
+          v[i] = __ldg(reinterpret_cast<const uint4*>(p.q + (begin + token) * p.q_stride + head * DH) + lane_chunk);
+        }
+      }
 #pragma unroll
-        for (int i = 0; i < DH / 8; ++i) {
-          const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+      for (int i = 0; i < kSteps; ++i) {
+        const int rr = wq * 32 + i * kStep + lane_row;
+        if constexpr (F8) {
+          uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+          uint32_t top = 0;   // largest |q| of the row as bf16 bits
 #pragma unroll
           for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
-        }
-        // scale by 2^(14 - exponent): exact, and the inverse goes into the scores' factor
-        const int ex = static_cast<int>(top >> 7);   // biased exponent (0: zero or subnormal; 255: not finite)
-        const int sh = ex == 0 || ex == 255 ? 0 : min(max(141 - ex, -100), 100);   // 127 + 14 - ex
-        const float up = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
-        c_row *= __uint_as_float(static_cast<uint32_t>(127 - sh) << 23) * __ldg(p.k_scale);
 #pragma unroll
-        for (int i = 0; i < DH / 8; ++i) {
-          uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+          for (int o = kRowChunks / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+          // scale by 2^(14 - exponent): exact, and the inverse goes into the scores' factor
+          const int ex = static_cast<int>(top >> 7);   // biased exponent (0: zero or subnormal; 255: not finite)
+          const int sh = ex == 0 || ex == 255 ? 0 : min(max(141 - ex, -100), 100);   // 127 + 14 - ex
+          const float up = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
+          // the lane that owns this row's scores keeps the factor
+          const int from = (lane - i * kStep) * kRowChunks;
+          const float down = __shfl_sync(0xffffffffu, __uint_as_float(static_cast<uint32_t>(127 - sh) << 23), from & 31);
+          if (from >= 0 && from < 32) c_row *= down * __ldg(p.k_scale);
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             w[e] = pack16<true>(__uint_as_float(w[e] << 16) * up, __uint_as_float(w[e] & 0xffff0000u) * up);
           v[i] = make_uint4(w[0], w[1], w[2], w[3]);
         }
+        if (!p.alt || (i & 1) == t) st_shared_v4(base + (lane_chunk >> 3) * kBlock + swz(rr, lane_chunk & 7), v[i]);
       }
-      if (store) {
-        const uint32_t base = q_a + (p.alt ? 0 : t * kTileBytes);
-#pragma unroll
-        for (int i = 0; i < DH / 8; ++i) st_shared_v4(base + (i >> 3) * kBlock + swz(r, i & 7), v[i]);
-        fence_async_smem();
-      }
+      fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&c.q_ready);
     }
-    const int my_end = live ? key_end(row) : 0, my_begin = live ? key_begin(row) : 0;
+    // rows behind the last one need no mask: what they compute is not used
+    const int my_end = live ? key_end(row) : 0x7fffffff, my_begin = live ? key_begin(row) : 0;
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(wq * 32) << 16);
     const uint32_t t_s = t_lane + t * 128, t_o = t_lane + 256 + t * 128;
     const int n = n_of[t];
-    float m = -INFINITY;   // the reference maximum, in score units
-    float2 sum2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+    float m = -INFINITY;                    // the reference maximum, in score units
+    float m_grow = -INFINITY;               // a maximum above this moves it
+    constexpr float kShift = F8 ? 6.0f : 0.0f;   // f16 probabilities are held 2^6 larger: subnormals begin lower
+    float off = kShift;                     // -m in log2 units
+    const float grow_by = kGrow / c_row;
+    float2 sum2[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
     bool ok = true;
     for (int i = 0; i < n; ++i) {
-      ok = mbar_wait(&c.s_full[t], i & 1);
+      ok = wait_for(&c.s_full[t], i & 1);
       if (!ok) break;
       tc_fence_after();
       __syncwarp();
-      if (warp_live) {
-        const int k0 = (t_lo + (p.alt ? 2 * i + t : i)) * kTileRows;
-        float s[128];
+      if (!warp_live) {
+        if (lane == 0) {
+          mbar_arrive(&c.p_full[t][0]);
+          mbar_arrive(&c.p_full[t][1]);
+        }
+        continue;
+      }
+      const int k0 = (t_lo + (p.alt ? 2 * i + t : i)) * kTileRows;
+      float s[128];
+      // the next 32 columns are on their way while the maximum of the last ones is taken
+      const int lo = my_begin - k0, hi = my_end - k0;
+      const bool edge = __any_sync(0xffffffffu, lo > 0 || hi < kTileRows);
+      tmem_ld32_async(t_s, s);
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int b = 0; b < 4; ++b) tmem_ld32_async(t_s + b * 32, s + b * 32);
+      for (int b = 0; b < 4; ++b) {
         tmem_wait_ld();
-        const int lo = my_begin - k0, hi = my_end - k0;
-        if (__any_sync(0xffffffffu, lo > 0 || hi < kTileRows)) {
+        if (b < 3) tmem_ld32_async(t_s + (b + 1) * 32, s + (b + 1) * 32);
+        if (edge) {
 #pragma unroll
-          for (int e = 0; e < 128; ++e) s[e] = e >= lo && e < hi ? s[e] : -INFINITY;
+          for (int e = b * 32; e < b * 32 + 32; ++e) s[e] = e >= lo && e < hi ? s[e] : -INFINITY;
         }
-        float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-        for (int e = 4; e < 128; e += 8) {
+        for (int e = b * 32; e < b * 32 + 32; e += 8) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            mx[j] = e + 4 + j < 128 ? fmaxf(fmaxf(mx[j], s[e + j]), s[e + 4 + j]) : fmaxf(mx[j], s[e + j]);
+          for (int j = 0; j < 4; ++j) mx[j] = fmaxf(fmaxf(mx[j], s[e + j]), s[e + 4 + j]);
         }
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        const bool grow = top > -INFINITY && !((top - m) * c_row <= kGrow);
-        if (__any_sync(0xffffffffu, grow)) {
-          float f = 1.0f;
-          if (grow) {
-            f = ex2_approx((m - top) * c_row);   // 0 for a row's first keys
-            m = top;
-            sum2[0].x *= f, sum2[0].y *= f, sum2[1].x *= f, sum2[1].y *= f;
+      }
+      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+      const bool grow = top > m_grow;
+      if (__any_sync(0xffffffffu, grow)) {
+        float f = 1.0f;
+        if (grow) {
+          f = ex2_approx((m - top) * c_row);   // 0 for a row's first keys
+          m = top;
+          m_grow = top + grow_by;
+          off = kShift - m * c_row;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) sum2[j].x *= f, sum2[j].y *= f;
+        }
+        // the P V product of the tile before has completed: these scores were issued after it
+        if (i > 0) {
+#pragma unroll 1
+          for (int b = 0; b < DH; b += 16) {
+            float o[16];
+            tmem_ld16(t_o + b, o);
+            uint32_t w[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e] * f);
+            tmem_st16(t_o + b, w);
           }
-          // the tile's P V product before this one has completed: S was issued after it
-          if (i > 0) {
-#pragma unroll
-            for (int b = 0; b < DH; b += 16) {
-              float o[16];
-              tmem_ld16(t_o + b, o);
-              uint32_t w[16];
-#pragma unroll
-              for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e] * f);
-              tmem_st16(t_o + b, w);
-            }
-            tmem_wait_st();
-          }
         }
-        // f16 probabilities are held 2^6 larger: their subnormals begin that much lower
-        const float off = (F8 ? 6.0f : 0.0f) - (m > -INFINITY ? m * c_row : 0.0f);
-        const float2 c2 = make_float2(c_row, c_row), off2 = make_float2(off, off);
+      }
+      const float2 c2 = make_float2(c_row, c_row), off2 = make_float2(off, off);
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t w[32];
+      for (int half = 0; half < 2; ++half) {   // the first 64 keys' product starts while the others are exponentiated
+        uint32_t w[32];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const int k = half * 64 + 2 * e;
-            float2 x = fma2(make_float2(s[k], s[k + 1]), c2, off2);
-            x.x = ex2_approx(x.x);
-            x.y = ex2_approx(x.y);
-            sum2[e & 1] = add2(sum2[e & 1], x);
-            w[e] = pack16<F8>(x.x, x.y);
-          }
-          tmem_st32(t_s + half * 32, w);
+        for (int e = 0; e < 32; ++e) {
+          const int k = half * 64 + 2 * e;
+          const float2 x = fma2(make_float2(s[k], s[k + 1]), c2, off2);
+          s[k] = ex2_approx(x.x);
+          s[k + 1] = ex2_approx(x.y);
+          w[e] = pack16<F8>(s[k], s[k + 1]);
         }
+        tmem_st32(t_s + half * 32, w);
         tmem_wait_st();
         tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&c.p_full[t][half]);
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&c.p_full[t]);
+      // the sum is off the path of the tensor cores
+#pragma unroll
+      for (int e = 0; e < 128; e += 8) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sum2[j] = add2(sum2[j], make_float2(s[e + 2 * j], s[e + 2 * j + 1]));
+      }
     }
-    const float2 st = add2(sum2[0], sum2[1]);
+    const float2 st = add2(add2(sum2[0], sum2[1]), add2(sum2[2], sum2[3]));
     float sum = st.x + st.y;
     float m2 = m > -INFINITY ? m * c_row : -INFINITY;   // log2 units
     // ---- the end: O complete, joined across the warpgroups (alternate tiles), stored
     if (p.alt) {
 #pragma unroll
       for (int u = 0; u < 2; ++u)
-        if (n_of[u] > 0) ok = mbar_wait(&c.o_done[u], 0) && ok;
+        if (n_of[u] > 0) ok = wait_for(&c.o_done[u], 0) && ok;
     } else if (n > 0) {
-      ok = mbar_wait(&c.o_done[t], 0) && ok;
+      ok = wait_for(&c.o_done[t], 0) && ok;
     }
     tc_fence_after();
     __syncwarp();
-    if (!ok) {
-      if (lane == 0) atomicOr(p.err, kErrPipelineTimeout);
-    }
+    if (!ok && lane == 0) atomicOr(p.err, kErrPipelineTimeout);
     const float vs = F8 ? __ldg(p.v_scale) : 1.0f;
-    const int64_t orow = (begin + row / p.G) * p.H + g * p.G + row % p.G;   // [token][head]
-    float* stage = reinterpret_cast<float*>(sring);                        // [128][DH], chunks swizzled by row
-    float2* stage_ml = reinterpret_cast<float2*>(sring + kTileRows * DH * 4);
+    float* join = reinterpret_cast<float*>(sring);                        // [128][DH], chunks swizzled by row
+    float2* join_ml = reinterpret_cast<float2*>(sring + kTileRows * DH * 4);
     if (p.alt) {
       if (t == 1 && warp_live) {
-        stage_ml[r] = make_float2(m2, sum);
-#pragma unroll
+        join_ml[r] = make_float2(m2, sum);
+#pragma unroll 1
         for (int b = 0; b < DH; b += 16) {
-          float o[16];
-          if (n > 0)
-            tmem_ld16(t_o + b, o);
-          else
-            for (int e = 0; e < 16; ++e) o[e] = 0.f;
+          float o[16] = {};
+          if (n > 0) tmem_ld16(t_o + b, o);
 #pragma unroll
           for (int e = 0; e < 16; e += 4)
-            *reinterpret_cast<float4*>(stage + r * DH + ((((b + e) >> 2) ^ (r & 7)) << 2)) =
+            *reinterpret_cast<float4*>(join + r * DH + ((((b + e) >> 2) ^ (r & 7)) << 2)) =
                 make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
         }
       }
@@ -428,16 +496,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     if ((!p.alt || t == 0) && warp_live) {
       float w0 = 1.0f, w1 = 0.0f;
       if (p.alt) {
-        const float2 b = stage_ml[r];
+        const float2 b = join_ml[r];
         const float top = fmaxf(m2, b.x);
         w0 = m2 > -INFINITY ? ex2_approx(m2 - top) : 0.f;
         w1 = b.x > -INFINITY ? ex2_approx(b.x - top) : 0.f;
         sum = sum * w0 + b.y * w1;
         m2 = top;
       }
+      const int64_t split_row = static_cast<int64_t>(split) * p.tokens * p.H;
       if (p.splits > 1) {
-        const int64_t at = static_cast<int64_t>(split) * p.tokens * p.H + orow;
-        if (live) p.part_ml[at] = make_float2(m2, sum);
+        if (live) p.part_ml[split_row + static_cast<int64_t>(begin + row / p.G) * p.H + g * p.G + row % p.G] = make_float2(m2, sum);
         w0 *= vs;
         w1 *= vs;
       } else {
@@ -445,18 +513,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         w0 *= inv;
         w1 *= inv;
       }
-      if (p.splits == 1 || nt > 0) {
-#pragma unroll
-        for (int b = 0; b < DH; b += 16) {
-          float o[16];
-          if (n > 0)
-            tmem_ld16(t_o + b, o);
-          else
-            for (int e = 0; e < 16; ++e) o[e] = 0.f;
+      // TMEM gives a lane one row: rows are staged in the query tile's 32 rows of this warp (its last reader has
+      // completed) and leave kRowChunks lanes a row, whole 16-byte chunks. fp32 shares take two passes.
+      const uint32_t stage = q_a + (p.alt ? 0 : t * kTileBytes) + wq * 32 * DH * 2;
+      const int passes = p.splits > 1 ? 2 : 1;
+      for (int pass = 0; pass < passes && (p.splits == 1 || nt > 0); ++pass) {
+        const int dims = DH / passes, d0 = pass * dims;
+#pragma unroll 1
+        for (int b = 0; b < dims; b += 16) {
+          float o[16] = {};
+          if (n > 0) tmem_ld16(t_o + d0 + b, o);
           if (p.alt) {
 #pragma unroll
             for (int e = 0; e < 16; e += 4) {
-              const float4 x = *reinterpret_cast<const float4*>(stage + r * DH + ((((b + e) >> 2) ^ (r & 7)) << 2));
+              const float4 x = *reinterpret_cast<const float4*>(join + r * DH + ((((d0 + b + e) >> 2) ^ (r & 7)) << 2));
               o[e] = o[e] * w0 + x.x * w1;
               o[e + 1] = o[e + 1] * w0 + x.y * w1;
               o[e + 2] = o[e + 2] * w0 + x.z * w1;
@@ -466,22 +536,35 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int e = 0; e < 16; ++e) o[e] *= w0;
           }
-          if (live) {
-            if (p.splits > 1) {
-              float4* dst = reinterpret_cast<float4*>(
-                  p.part_o + (static_cast<int64_t>(split) * p.tokens * p.H + orow) * DH + b);
+          if (p.splits > 1) {
 #pragma unroll
-              for (int e = 0; e < 4; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-            } else {
-              uint4* dst = reinterpret_cast<uint4*>(p.out + (begin + row / p.G) * p.out_stride +
-                                                    (g * p.G + row % p.G) * DH + b);
+            for (int e = 0; e < 16; e += 4)
+              st_shared_v4(stage + lane * (DH * 2) + ((((b + e) >> 2) ^ (lane & 7)) << 4),
+                           make_uint4(__float_as_uint(o[e]), __float_as_uint(o[e + 1]), __float_as_uint(o[e + 2]),
+                                      __float_as_uint(o[e + 3])));
+          } else {
 #pragma unroll
-              for (int e = 0; e < 2; ++e)
-                dst[e] = make_uint4(pack16<false>(o[8 * e], o[8 * e + 1]), pack16<false>(o[8 * e + 2], o[8 * e + 3]),
-                                    pack16<false>(o[8 * e + 4], o[8 * e + 5]), pack16<false>(o[8 * e + 6], o[8 * e + 7]));
-            }
+            for (int e = 0; e < 16; e += 8)
+              st_shared_v4(stage + lane * (DH * 2) + ((((b + e) >> 3) ^ (lane & 7)) << 4),
+                           make_uint4(pack16<false>(o[e], o[e + 1]), pack16<false>(o[e + 2], o[e + 3]),
+                                      pack16<false>(o[e + 4], o[e + 5]), pack16<false>(o[e + 6], o[e + 7])));
           }
         }
+        __syncwarp();
+#pragma unroll 4
+        for (int i = 0; i < 32; i += kStep) {
+          const int rr = i + lane_row, R = tile_row0 + wq * 32 + rr;
+          const uint4 x = *reinterpret_cast<const uint4*>(sq + (p.alt ? 0 : t * kTileBytes) + wq * 32 * DH * 2 + rr * (DH * 2) +
+                                                          ((lane_chunk ^ (rr & 7)) << 4));
+          if (R < rows) {
+            const int token = begin + R / p.G, head = g * p.G + R % p.G;
+            if (p.splits > 1)
+              reinterpret_cast<uint4*>(p.part_o + (split_row + static_cast<int64_t>(token) * p.H + head) * DH + d0)[lane_chunk] = x;
+            else
+              reinterpret_cast<uint4*>(p.out + token * p.out_stride + head * DH)[lane_chunk] = x;
+          }
+        }
+        __syncwarp();
       }
     }
   } else if (warp == kMmaWarp) {
@@ -492,51 +575,62 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t id_o = (1u << 4) | fmt | (1u << 16) | ((static_cast<uint32_t>(DH) >> 3) << 17) | ((128u >> 4) << 24);
     // the last key tile's values behind the length (inside its last page) are zeroed here (16-bit cache)
     const int tail_tile = len % kTileRows ? len / kTileRows - t_lo : -1;
-    bool ok = mbar_wait(&c.q_ready, 0);
-    auto key_tile = [&](int t, int i) { return p.alt ? 2 * i + t : i; };
-    auto last_user = [&](int t, int j) { return p.alt || t == 1 || j >= n_of[1]; };
-    auto first_user = [&](int t, int j) { return p.alt || t == 0 || j >= n_of[0]; };
+    bool ok = wait_for(&c.q_ready, 0);
+    // Buffers alternate between the keys and the values of the key tiles in order. Tile t walks its own key tiles:
+    // all of them, or every other one. ks, vs: the next keys' and values' place in the ring of each t.
+    Ring ks[2], vs[2];
+    const int step = p.alt ? 4 : 2;
+    vs[0].next(p.ring), vs[1].next(p.ring);
+    if (p.alt) {
+      ks[1].next(p.ring), ks[1].next(p.ring);
+      vs[1].next(p.ring), vs[1].next(p.ring);
+    }
     auto scores = [&](int t, int i) {
-      const int j = key_tile(t, i), item = 2 * j, b = item % p.ring;
-      if (!mbar_wait(&c.full[b], (item / p.ring) & 1)) return false;
+      Ring& k = ks[t];
+      if (!wait_for(&c.full[k.b], k.phase)) return false;
       tc_fence_after();
-      if (lane == 0) {
-        const uint32_t qa = q_a + (p.alt ? 0 : t * kTileBytes), ka = ring_a + b * kTileBytes;
+      if (elect_one()) {
+        const uint64_t qd = sw128_kmajor_desc(q_a + (p.alt ? 0 : t * kTileBytes)), kd = sw128_kmajor_desc(ring_a + k.b * kTileBytes);
 #pragma unroll
         for (int h = 0; h < kHalves; ++h)
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            tc_mma<false>(tmem + t * 128, sw128_kmajor_desc(qa + h * kBlock + k * 32),
-                          sw128_kmajor_desc(ka + h * kBlock + k * 32), id_s, (h | k) ? 1u : 0u);
-        if (last_user(t, j)) tc_commit(&c.empty[b]);
+          for (int x = 0; x < 4; ++x)   // descriptor addresses count 16 bytes
+            tc_mma<false>(tmem + t * 128, qd + ((h * kBlock + x * 32) >> 4), kd + ((h * kBlock + x * 32) >> 4), id_s, (h | x) ? 1u : 0u);
+        if (p.alt || t == 1 || i >= n_of[1]) tc_commit(&c.empty[k.b]);   // the keys' last user
         tc_commit(&c.s_full[t]);
       }
       __syncwarp();
+      for (int x = 0; x < step; ++x) k.next(p.ring);
       return true;
     };
     auto values = [&](int t, int i) {
-      const int j = key_tile(t, i), item = 2 * j + 1, b = item % p.ring;
-      if (!mbar_wait(&c.full[b], (item / p.ring) & 1)) return false;
-      if (!F8 && j == tail_tile && first_user(t, j)) {
+      Ring& v = vs[t];
+      if (!wait_for(&c.full[v.b], v.phase)) return false;
+      if (!F8 && (p.alt ? 2 * i + t : i) == tail_tile && (p.alt || t == 0 || i >= n_of[0])) {   // by its first user
         const int r0 = len % kTileRows;
         for (int x = lane; x < (kTileRows - r0) * 8 * kHalves; x += 32)
-          st_shared_v4(ring_a + b * kTileBytes + (x % kHalves) * kBlock + r0 * 128 + (x / kHalves) * 16,
+          st_shared_v4(ring_a + v.b * kTileBytes + (x % kHalves) * kBlock + r0 * 128 + (x / kHalves) * 16,
                        make_uint4(0, 0, 0, 0));
         fence_async_smem();
         __syncwarp();
       }
-      if (!mbar_wait(&c.p_full[t], i & 1)) return false;
-      tc_fence_after();
-      if (lane == 0) {
-        const uint32_t va = ring_a + b * kTileBytes;
+      const uint64_t vd = sw128_mnmajor_desc(ring_a + v.b * kTileBytes, kBlock);
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          tc_mma_ts<false>(tmem + 256 + t * 128, tmem + t * 128 + k * 8, sw128_mnmajor_desc(va + k * 2048, kBlock), id_o,
-                           (i | k) ? 1u : 0u);
-        if (last_user(t, j)) tc_commit(&c.empty[b]);
-        if (i == n_of[t] - 1) tc_commit(&c.o_done[t]);
+      for (int half = 0; half < 2; ++half) {
+        if (!wait_for(&c.p_full[t][half], i & 1)) return false;
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int x = half * 4; x < half * 4 + 4; ++x)
+            tc_mma_ts<false>(tmem + 256 + t * 128, tmem + t * 128 + x * 8, vd + ((x * 2048) >> 4), id_o, (i | x) ? 1u : 0u);
+          if (half == 1) {
+            if (p.alt || t == 1 || i >= n_of[1]) tc_commit(&c.empty[v.b]);
+            if (i == n_of[t] - 1) tc_commit(&c.o_done[t]);
+          }
+        }
+        __syncwarp();
       }
-      __syncwarp();
+      for (int x = 0; x < step; ++x) v.next(p.ring);
       return true;
     };
     const int n_max = max(n_of[0], n_of[1]);
@@ -549,12 +643,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok && i + 1 < n_of[t]) ok = scores(t, i + 1);
       }
     if (!ok) {   // a wait ran out: let what was issued finish before the CTA leaves
-      if (lane == 0) {
+      if (elect_one()) {
         atomicOr(p.err, kErrPipelineTimeout);
         tc_commit(&c.drain);
       }
       __syncwarp();
-      mbar_wait(&c.drain, 0);
+      wait_for(&c.drain, 0);
     }
   } else if (warp == kTmaWarp) {
     // ================================================= page table and TMA
@@ -580,42 +674,46 @@ __global__ void __launch_bounds__(kThreads, 1)
     int pg = n_keys > 0 ? page_of(0) : 0;
     bool ok = true;
     int issued = 0;
+    Ring at;
     for (int j = 0; j < n_keys && ok; ++j) {
       const int row_in = ((t_lo + j) * kTileRows + part * rows_box) & (p.page - 1);
       const int next = j + 1 < n_keys ? page_of(j + 1) : 0;
       for (int kv = 0; kv < 2 && ok; ++kv) {
-        const int item = 2 * j + kv, b = item % nb;
-        if (item >= nb) ok = mbar_wait(&empty[b], (item / nb - 1) & 1);
+        if (issued >= nb) ok = wait_for(&empty[at.b], at.phase ^ 1);
         if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(&full[b], bytes);
+        if (lane == 0) mbar_arrive_expect_tx(&full[at.b], bytes);
         __syncwarp();
         if (active) {
-          const uint32_t dst = base + b * bytes + (F8 ? part * rows_box * DH : half * kBlock + part * rows_box * 128);
-          tma_load_4d(dst, kv ? &tm_v : &tm_k, &full[b], half * 64, row_in, g, pg);
+          const uint32_t dst = base + at.b * bytes + (F8 ? part * rows_box * DH : half * kBlock + part * rows_box * 128);
+          tma_load_4d(dst, kv ? &tm_v : &tm_k, &full[at.b], half * 64, row_in, g, pg);
         }
+        __syncwarp();
         ++issued;
+        at.next(nb);
       }
       pg = next;
     }
     if (!ok) {   // the copies in flight land before the CTA leaves
       if (lane == 0) atomicOr(p.err, kErrPipelineTimeout);
-      for (int item = max(0, issued - nb); item < issued; ++item) mbar_wait(&full[item % nb], (item / nb) & 1);
+      for (int item = max(0, issued - nb); item < issued; ++item) wait_for(&full[item % nb], (item / nb) & 1);
     }
-  } else if (F8) {
+  } else if (F8 && warp >= kCvtWarp) {
     // ================================================= E4M3 codes -> f16 tiles
-    const int ct = tid - kCvtWarp * 32;   // 0..63
+    const int ct = tid - kCvtWarp * 32;
+    constexpr int kCvtThreads = kCvtWarps * 32;
     constexpr int kChunks = DH / 16;      // 16-code chunks of a row
     bool ok = true;
-    for (int item = 0; item < 2 * n_keys && ok; ++item) {
-      const int rb = item % p.raw_ring, b = item % p.ring;
-      ok = mbar_wait(&c.rfull[rb], (item / p.raw_ring) & 1);
-      if (ok && item >= p.ring) ok = mbar_wait(&c.empty[b], (item / p.ring - 1) & 1);
+    Ring raw, out;
+    for (int item = 0; item < 2 * n_keys && ok; ++item, raw.next(p.raw_ring), out.next(p.ring)) {
+      const int rb = raw.b, b = out.b;
+      ok = wait_for(&c.rfull[rb], raw.phase);
+      if (ok && item >= p.ring) ok = wait_for(&c.empty[b], out.phase ^ 1);
       if (!ok) break;
       const int valid = len - (t_lo + (item >> 1)) * kTileRows;   // rows of the tile inside the length
       const uint4* src = reinterpret_cast<const uint4*>(sraw + rb * kRawBytes);
       const uint32_t dst = ring_a + b * kTileBytes;
 #pragma unroll 4
-      for (int x = ct; x < kTileRows * kChunks; x += 64) {
+      for (int x = ct; x < kTileRows * kChunks; x += kCvtThreads) {
         const int r = x / kChunks, ch = x % kChunks;
         const uint4 v = r < valid ? src[x] : make_uint4(0, 0, 0, 0);
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -890,7 +988,7 @@ extern "C" int fm_paged_attention(const fm_kv_cache* c, int layer, const fm_kv_b
                   static_cast<unsigned>(b->n * pl.splits));
   auto kernel = c->Dh == 128 ? (f8 ? paged_attn_kernel<128, true> : paged_attn_kernel<128, false>)
                              : (f8 ? paged_attn_kernel<64, true> : paged_attn_kernel<64, false>);
-  e = launch(kernel, grid, dim3(kThreads), pl.smem, o, p, tk, tv);
+  e = launch(kernel, grid, dim3(threads_of(f8)), pl.smem, o, p, tk, tv);
   if (e == cudaSuccess && pl.splits > 1) {
     const int64_t blocks = (static_cast<int64_t>(b->tokens) * H + 7) / 8;
     auto join = c->Dh == 128 ? combine_kernel<128> : combine_kernel<64>;
