@@ -44,9 +44,10 @@ namespace fm {
 namespace {
 
 constexpr int kTileRows = 128;    // rows of a query tile (MMA M) and keys of a key tile
-constexpr int kMmaWarp = 8, kTmaWarp = 9, kCvtWarp = 12, kCvtWarps = 4;
-// Warpgroups: two softmax, one with the MMA and the TMA warp, and with an E4M3 cache one that expands codes. Registers
-// move to the softmax warpgroups, which keep 128 scores each: 384 x 168 = 256 x 216 + 128 x 72, 512 x 128 = 256 x 192 +
+// Warp roles behind the eight softmax warps: an MMA warp for each tile (one alone spent its time issuing: 16 MMAs, five
+// waits and four commits a tile in sequence), TMA, the tail's zeros, and with an E4M3 cache four that expand codes.
+constexpr int kMmaWarp = 8, kTmaWarp = 10, kTailWarp = 11, kCvtWarp = 12, kCvtWarps = 4;
+// Registers move to the softmax warpgroups, which keep 128 scores each: 384 x 168 = 256 x 216 + 128 x 72, 512 x 128 = 256 x 192 +
 // 256 x 64.
 constexpr int threads_of(bool f8) { return f8 ? 512 : 384; }
 constexpr int kSmemLimit = 226 * 1024;
@@ -186,7 +187,7 @@ __device__ __forceinline__ uint32_t swz(int r, int c) {   // 16-byte chunk c of 
 
 struct Ctl {   // shared-memory control block
   uint64_t full[kMaxRing], empty[kMaxRing], rfull[kMaxRing], rempty[kMaxRing];
-  uint64_t q_ready, s_full[2], p_full[2][2], o_done[2], drain;
+  uint64_t q_ready, s_full[2], p_full[2], o_done[2], turn[2], tail, drain[2];
   uint32_t tmem;
 };
 static_assert(sizeof(Ctl) <= kCtlBytes, "control block");
@@ -213,26 +214,30 @@ __global__ void __launch_bounds__(threads_of(F8), 1)
   const int entry = blockIdx.z / p.splits, split = blockIdx.z % p.splits;
   const int block_rows = q_tiles * kTileRows;
 
-  if (tid == 0) {
-    for (int i = 0; i < kMaxRing; ++i) {
-      mbar_init(&c.full[i], F8 ? kCvtWarps : 1);
-      mbar_init(&c.empty[i], 1);
-      mbar_init(&c.rfull[i], 1);
-      mbar_init(&c.rempty[i], kCvtWarps);
+  if (warp == kTmaWarp) {   // this warp's first copies start before the CTA meets
+    if (elect_one()) {
+      for (int i = 0; i < kMaxRing; ++i) {
+        mbar_init(&c.full[i], F8 ? kCvtWarps : 1);
+        mbar_init(&c.empty[i], p.alt ? 1 : 2);   // a key tile has one user, or both
+        mbar_init(&c.rfull[i], 1);
+        mbar_init(&c.rempty[i], kCvtWarps);
+      }
+      mbar_init(&c.q_ready, 8);
+      for (int t = 0; t < 2; ++t) {
+        mbar_init(&c.s_full[t], 1);
+        mbar_init(&c.p_full[t], 4);
+        mbar_init(&c.o_done[t], 1);
+      }
+      mbar_init(&c.turn[0], 1);
+      mbar_init(&c.turn[1], 1);
+      mbar_init(&c.tail, 1);
+      mbar_init(&c.drain[0], 1);
+      mbar_init(&c.drain[1], 1);
+      fence_mbar_init();
+      tma_prefetch_desc(&tm_k);
+      tma_prefetch_desc(&tm_v);
     }
-    mbar_init(&c.q_ready, 8);
-    for (int t = 0; t < 2; ++t) {
-      mbar_init(&c.s_full[t], 1);
-      mbar_init(&c.p_full[t][0], 4);
-      mbar_init(&c.p_full[t][1], 4);
-      mbar_init(&c.o_done[t], 1);
-    }
-    mbar_init(&c.drain, 1);
-    fence_mbar_init();
-  }
-  if (warp == kTmaWarp && lane == 0) {
-    tma_prefetch_desc(&tm_k);
-    tma_prefetch_desc(&tm_v);
+    __syncwarp();
   }
   pdl_wait();
 
@@ -286,18 +291,110 @@ __global__ void __launch_bounds__(threads_of(F8), 1)
   }
   // Key tiles that some tile uses, and the tiles of each: n_of[0] <= n_of[1] except where tile 1 has no rows.
   const int n_keys = p.alt ? nt : max(n_of[0], n_of[1]);
+  const int tail_tile = len % kTileRows ? len / kTileRows - t_lo : -1;   // the tile that the length ends in
 
-  if (warp == kMmaWarp) {
+  const uint32_t ring_a = smem_u32(sring), raw_a = smem_u32(sraw), q_a = smem_u32(sq);
+
+  // ---- the TMA warp's copies: one call moves the next key or value tile, a box for the rows of each page (at most
+  // 128) and each 128-byte block.
+  const int rows_box = min(p.page, kTileRows), boxes = kTileRows / rows_box;
+  const int ring_n = F8 ? p.raw_ring : p.ring;
+  uint64_t* const ring_full = F8 ? c.rfull : c.full;
+  uint64_t* const ring_empty = F8 ? c.rempty : c.empty;
+  constexpr uint32_t ring_bytes = F8 ? kRawBytes : kTileBytes;
+  auto page_of = [&](int j) {   // lane x: the page of box x of key tile j; the pool's end where there is none
+    const int key = (t_lo + j) * kTileRows + lane * rows_box;
+    if (lane >= boxes || key >= len || j >= n_keys) return p.pages;
+    const int pg = __ldg(p.table + static_cast<int64_t>(sid) * p.table_stride + (key >> p.page_shift));
+    if (pg < 0 || pg >= p.pages) {
+      atomicOr(p.err, kErrBadBatch);
+      return p.pages;
+    }
+    return pg;
+  };
+  int copy_next = 0, copy_page = 0, copy_page_after = 0;
+  Ring copy_at;
+  auto copy_one = [&](bool first) {   // first: into a buffer that nothing has used
+    const int j = copy_next >> 1, kv = copy_next & 1;
+    if (kv == 0) {
+      copy_page = copy_page_after;
+      copy_page_after = page_of(j + 1);   // on its way while this tile's copies wait for their buffers
+    }
+    if (!first && copy_next >= ring_n && !wait_for(&ring_empty[copy_at.b], copy_at.phase ^ 1)) return false;
+    if (lane == 0) mbar_arrive_expect_tx(&ring_full[copy_at.b], ring_bytes);
+    __syncwarp();
+    // one lane issues all boxes: lanes that issue their own would be taken one after the other at twice the cost
+    const CUtensorMap* map = kv ? &tm_v : &tm_k;
+    const uint32_t dst = (F8 ? raw_a : ring_a) + copy_at.b * ring_bytes;
+    for (int x = 0; x < boxes; ++x) {
+      const int pg = __shfl_sync(0xffffffffu, copy_page, x);
+      const int row_in = ((t_lo + j) * kTileRows + x * rows_box) & (p.page - 1);
+      if (elect_one()) {
+        if constexpr (F8) {
+          tma_load_4d(dst + x * rows_box * DH, map, &ring_full[copy_at.b], 0, row_in, g, pg);
+        } else {
+#pragma unroll
+          for (int h = 0; h < kHalves; ++h)
+            tma_load_4d(dst + h * kBlock + x * rows_box * 128, map, &ring_full[copy_at.b], h * 64, row_in, g, pg);
+        }
+      }
+      __syncwarp();
+    }
+    ++copy_next;
+    copy_at.next(ring_n);
+    return true;
+  };
+
+  // ---- the softmax warps' query rows: kRowChunks lanes a row, kStep rows a warp at a time
+  constexpr int kRowChunks = DH / 8;          // 16-byte chunks of a 16-bit row
+  constexpr int kStep = 32 / kRowChunks;
+  constexpr int kSteps = 32 / kStep;
+  const int t_of = (warp >> 2) & 1, wq = warp & 3;
+  const int tile_row0 = row0 + (p.alt ? 0 : t_of * kTileRows);
+  const int lane_row = lane / kRowChunks, lane_chunk = lane % kRowChunks;
+  // Walks the token and the head of a lane's rows, a division for the first only. G comes in opaque, so that nothing
+  // of a walk is kept in registers for the next one.
+  struct Walk {
+    int tok, head, step_tok, step_head, G;
+    __device__ __forceinline__ Walk(int row, int group) : G(group) {
+      asm volatile("" : "+r"(G));
+      tok = row / G;
+      head = row - tok * G;
+      step_tok = kStep / G;
+      step_head = kStep - step_tok * G;
+    }
+    __device__ __forceinline__ void next() {
+      tok += step_tok;
+      head += step_head;
+      if (head >= G) {
+        head -= G;
+        ++tok;
+      }
+    }
+  };
+  uint4 qv[kSteps];
+  if (warp < 8) {
+    const __nv_bfloat16* q0 = p.q + begin * p.q_stride + g * p.G * DH + lane_chunk * 8;
+    Walk at(tile_row0 + wq * 32 + lane_row, p.G);
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      const int R = tile_row0 + wq * 32 + i * kStep + lane_row;
+      qv[i] = make_uint4(0, 0, 0, 0);
+      if (R < rows && (F8 || !p.alt || (i & 1) == t_of)) qv[i] = __ldg(reinterpret_cast<const uint4*>(q0 + at.tok * p.q_stride + at.head * DH));
+      at.next();
+    }
+  } else if (warp == kMmaWarp) {
     tmem_alloc(&c.tmem, 512);
     tmem_relinquish();
+  } else if (warp == kTmaWarp) {
+    copy_page_after = page_of(0);
+    while (copy_next < min(ring_n, 2 * n_keys)) copy_one(true);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   pdl_trigger();   // after TMEM is held
   const uint32_t tmem = c.tmem;
-  const uint32_t ring_a = smem_u32(sring), raw_a = smem_u32(sraw), q_a = smem_u32(sq);
-
   // one instruction for a whole warpgroup
   if (warp < 8) {
     if constexpr (F8)
@@ -313,35 +410,19 @@ __global__ void __launch_bounds__(threads_of(F8), 1)
 
   if (warp < 8) {
     // ================================================= softmax warpgroups
-    const int t = warp >> 2, wq = warp & 3;
+    const int t = t_of;
     const int r = wq * 32 + lane;
-    const int tile_row0 = row0 + (p.alt ? 0 : t * kTileRows);
     const int row = tile_row0 + r;
     const bool live = row < rows;
     const bool warp_live = row - lane < rows;
-    constexpr int kRowChunks = DH / 8;          // 16-byte chunks of a 16-bit row
-    constexpr int kStep = 32 / kRowChunks;      // rows a warp moves at a time
-    // this lane's rows of the warp's 32 (cooperative moves: kRowChunks lanes a row), as offsets of [token][head]
-    const int lane_row = lane / kRowChunks, lane_chunk = lane % kRowChunks;
     float c_row = p.scale_log2;
     {   // ---- the query rows into their swizzled tile; of one tile for both warpgroups each takes every other step
       const uint32_t base = q_a + (p.alt ? 0 : t * kTileBytes);
-      constexpr int kSteps = 32 / kStep;
-      uint4 v[kSteps];
-#pragma unroll
-      for (int i = 0; i < kSteps; ++i) {
-        const int rr = wq * 32 + i * kStep + lane_row, R = tile_row0 + rr;
-        v[i] = make_uint4(0, 0, 0, 0);
-        if (R < rows && (F8 || !p.alt || (i & 1) == t)) {
-          const int token = R / p.G, head = g * p.G + R % p.G;
-          v[i] = __ldg(reinterpret_cast<const uint4*>(p.q + (begin + token) * p.q_stride + head * DH) + lane_chunk);
-        }
-      }
 #pragma unroll
       for (int i = 0; i < kSteps; ++i) {
         const int rr = wq * 32 + i * kStep + lane_row;
         if constexpr (F8) {
-          uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+          uint32_t w[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
           uint32_t top = 0;   // largest |q| of the row as bf16 bits
 #pragma unroll
           for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
@@ -358,9 +439,9 @@ __global__ void __launch_bounds__(threads_of(F8), 1)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             w[e] = pack16<true>(__uint_as_float(w[e] << 16) * up, __uint_as_float(w[e] & 0xffff0000u) * up);
-          v[i] = make_uint4(w[0], w[1], w[2], w[3]);
+          qv[i] = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        if (!p.alt || (i & 1) == t) st_shared_v4(base + (lane_chunk >> 3) * kBlock + swz(rr, lane_chunk & 7), v[i]);
+        if (!p.alt || (i & 1) == t) st_shared_v4(base + (lane_chunk >> 3) * kBlock + swz(rr, lane_chunk & 7), qv[i]);
       }
       fence_async_smem();
       __syncwarp();
@@ -384,33 +465,28 @@ __global__ void __launch_bounds__(threads_of(F8), 1)
       tc_fence_after();
       __syncwarp();
       if (!warp_live) {
-        if (lane == 0) {
-          mbar_arrive(&c.p_full[t][0]);
-          mbar_arrive(&c.p_full[t][1]);
-        }
+        if (lane == 0) mbar_arrive(&c.p_full[t]);
         continue;
       }
       const int k0 = (t_lo + (p.alt ? 2 * i + t : i)) * kTileRows;
       float s[128];
-      // the next 32 columns are on their way while the maximum of the last ones is taken
       const int lo = my_begin - k0, hi = my_end - k0;
       const bool edge = __any_sync(0xffffffffu, lo > 0 || hi < kTileRows);
-      tmem_ld32_async(t_s, s);
-      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        tmem_wait_ld();
-        if (b < 3) tmem_ld32_async(t_s + (b + 1) * 32, s + (b + 1) * 32);
-        if (edge) {
+      for (int b = 0; b < 4; ++b) tmem_ld32_async(t_s + b * 32, s + b * 32);
+      tmem_wait_ld();
+      if (edge) {
 #pragma unroll
-          for (int e = b * 32; e < b * 32 + 32; ++e) s[e] = e >= lo && e < hi ? s[e] : -INFINITY;
-        }
-#pragma unroll
-        for (int e = b * 32; e < b * 32 + 32; e += 8) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) mx[j] = fmaxf(fmaxf(mx[j], s[e + j]), s[e + 4 + j]);
-        }
+        for (int e = 0; e < 128; ++e) s[e] = e >= lo && e < hi ? s[e] : -INFINITY;
       }
+      float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+      for (int e = 4; e < 124; e += 8) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) mx[j] = fmaxf(fmaxf(mx[j], s[e + j]), s[e + 4 + j]);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) mx[j] = fmaxf(mx[j], s[124 + j]);
       const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
       const bool grow = top > m_grow;
       if (__any_sync(0xffffffffu, grow)) {
@@ -437,23 +513,26 @@ __global__ void __launch_bounds__(threads_of(F8), 1)
         }
       }
       const float2 c2 = make_float2(c_row, c_row), off2 = make_float2(off, off);
+      auto probabilities = [&](int from, int pairs, uint32_t* w) {
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {   // the first 64 keys' product starts while the others are exponentiated
-        uint32_t w[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const int k = half * 64 + 2 * e;
+        for (int e = 0; e < pairs; ++e) {
+          const int k = from + 2 * e;
           const float2 x = fma2(make_float2(s[k], s[k + 1]), c2, off2);
           s[k] = ex2_approx(x.x);
           s[k + 1] = ex2_approx(x.y);
           w[e] = pack16<F8>(s[k], s[k + 1]);
         }
-        tmem_st32(t_s + half * 32, w);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&c.p_full[t][half]);
+      };
+#pragma unroll
+      for (int part = 0; part < 2; ++part) {
+        uint32_t w[32];
+        probabilities(part * 64, 32, w);
+        tmem_st32(t_s + part * 32, w);
       }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&c.p_full[t]);
       // the sum is off the path of the tensor cores
 #pragma unroll
       for (int e = 0; e < 128; e += 8) {
@@ -478,18 +557,24 @@ __global__ void __launch_bounds__(threads_of(F8), 1)
     const float vs = F8 ? __ldg(p.v_scale) : 1.0f;
     float* join = reinterpret_cast<float*>(sring);                        // [128][DH], chunks swizzled by row
     float2* join_ml = reinterpret_cast<float2*>(sring + kTileRows * DH * 4);
+    float o[DH];
+    auto load_o = [&]() {   // this row's sums
+      if (n > 0) {
+#pragma unroll
+        for (int b = 0; b < DH; b += 32) tmem_ld32_async(t_o + b, o + b);
+        tmem_wait_ld();
+      } else {
+#pragma unroll
+        for (int e = 0; e < DH; ++e) o[e] = 0.f;
+      }
+    };
     if (p.alt) {
       if (t == 1 && warp_live) {
         join_ml[r] = make_float2(m2, sum);
-#pragma unroll 1
-        for (int b = 0; b < DH; b += 16) {
-          float o[16] = {};
-          if (n > 0) tmem_ld16(t_o + b, o);
+        load_o();
 #pragma unroll
-          for (int e = 0; e < 16; e += 4)
-            *reinterpret_cast<float4*>(join + r * DH + ((((b + e) >> 2) ^ (r & 7)) << 2)) =
-                make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-        }
+        for (int e = 0; e < DH; e += 4)
+          *reinterpret_cast<float4*>(join + r * DH + (((e >> 2) ^ (r & 7)) << 2)) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
       }
       asm volatile("bar.sync 1, 256;" ::: "memory");
     }
@@ -516,183 +601,205 @@ __global__ void __launch_bounds__(threads_of(F8), 1)
       // TMEM gives a lane one row: rows are staged in the query tile's 32 rows of this warp (its last reader has
       // completed) and leave kRowChunks lanes a row, whole 16-byte chunks. fp32 shares take two passes.
       const uint32_t stage = q_a + (p.alt ? 0 : t * kTileBytes) + wq * 32 * DH * 2;
-      const int passes = p.splits > 1 ? 2 : 1;
-      for (int pass = 0; pass < passes && (p.splits == 1 || nt > 0); ++pass) {
-        const int dims = DH / passes, d0 = pass * dims;
-#pragma unroll 1
-        for (int b = 0; b < dims; b += 16) {
-          float o[16] = {};
-          if (n > 0) tmem_ld16(t_o + d0 + b, o);
-          if (p.alt) {
+      load_o();
+      if (p.alt) {
 #pragma unroll
-            for (int e = 0; e < 16; e += 4) {
-              const float4 x = *reinterpret_cast<const float4*>(join + r * DH + ((((d0 + b + e) >> 2) ^ (r & 7)) << 2));
-              o[e] = o[e] * w0 + x.x * w1;
-              o[e + 1] = o[e + 1] * w0 + x.y * w1;
-              o[e + 2] = o[e + 2] * w0 + x.z * w1;
-              o[e + 3] = o[e + 3] * w0 + x.w * w1;
-            }
-          } else {
+        for (int e = 0; e < DH; e += 4) {
+          const float4 x = *reinterpret_cast<const float4*>(join + r * DH + (((e >> 2) ^ (r & 7)) << 2));
+          o[e] = o[e] * w0 + x.x * w1;
+          o[e + 1] = o[e + 1] * w0 + x.y * w1;
+          o[e + 2] = o[e + 2] * w0 + x.z * w1;
+          o[e + 3] = o[e + 3] * w0 + x.w * w1;
+        }
+      } else {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] *= w0;
+        for (int e = 0; e < DH; ++e) o[e] *= w0;
+      }
+      const int passes = p.splits == 1 ? 1 : nt > 0 ? 2 : 0;
+#pragma unroll
+      for (int pass = 0; pass < 2; ++pass) {
+        if (pass >= passes) break;
+        const int d0 = pass * (DH / 2);
+        if (p.splits > 1) {
+#pragma unroll
+          for (int e = 0; e < DH / 2; e += 4) {
+            const int k = pass * (DH / 2) + e;
+            st_shared_v4(stage + lane * (DH * 2) + (((e >> 2) ^ (lane & 7)) << 4),
+                         make_uint4(__float_as_uint(o[k]), __float_as_uint(o[k + 1]), __float_as_uint(o[k + 2]),
+                                    __float_as_uint(o[k + 3])));
           }
-          if (p.splits > 1) {
+        } else {
 #pragma unroll
-            for (int e = 0; e < 16; e += 4)
-              st_shared_v4(stage + lane * (DH * 2) + ((((b + e) >> 2) ^ (lane & 7)) << 4),
-                           make_uint4(__float_as_uint(o[e]), __float_as_uint(o[e + 1]), __float_as_uint(o[e + 2]),
-                                      __float_as_uint(o[e + 3])));
-          } else {
-#pragma unroll
-            for (int e = 0; e < 16; e += 8)
-              st_shared_v4(stage + lane * (DH * 2) + ((((b + e) >> 3) ^ (lane & 7)) << 4),
-                           make_uint4(pack16<false>(o[e], o[e + 1]), pack16<false>(o[e + 2], o[e + 3]),
-                                      pack16<false>(o[e + 4], o[e + 5]), pack16<false>(o[e + 6], o[e + 7])));
-          }
+          for (int e = 0; e < DH; e += 8)
+            st_shared_v4(stage + lane * (DH * 2) + (((e >> 3) ^ (lane & 7)) << 4),
+                         make_uint4(pack16<false>(o[e], o[e + 1]), pack16<false>(o[e + 2], o[e + 3]),
+                                    pack16<false>(o[e + 4], o[e + 5]), pack16<false>(o[e + 6], o[e + 7])));
         }
         __syncwarp();
+        Walk at(tile_row0 + wq * 32 + lane_row, p.G);
 #pragma unroll 4
         for (int i = 0; i < 32; i += kStep) {
           const int rr = i + lane_row, R = tile_row0 + wq * 32 + rr;
           const uint4 x = *reinterpret_cast<const uint4*>(sq + (p.alt ? 0 : t * kTileBytes) + wq * 32 * DH * 2 + rr * (DH * 2) +
                                                           ((lane_chunk ^ (rr & 7)) << 4));
           if (R < rows) {
-            const int token = begin + R / p.G, head = g * p.G + R % p.G;
             if (p.splits > 1)
-              reinterpret_cast<uint4*>(p.part_o + (split_row + static_cast<int64_t>(token) * p.H + head) * DH + d0)[lane_chunk] = x;
+              reinterpret_cast<uint4*>(p.part_o + (split_row + static_cast<int64_t>(begin + at.tok) * p.H + g * p.G + at.head) * DH + d0)[lane_chunk] = x;
             else
-              reinterpret_cast<uint4*>(p.out + token * p.out_stride + head * DH)[lane_chunk] = x;
+              reinterpret_cast<uint4*>(p.out + (begin + at.tok) * p.out_stride + (g * p.G + at.head) * DH)[lane_chunk] = x;
           }
+          at.next();
         }
         __syncwarp();
       }
     }
-  } else if (warp == kMmaWarp) {
-    // ================================================= tensor cores
+  } else if (warp < kTmaWarp) {
+    // ================================================= tensor cores, a warp for each tile
     // f32 accumulate; bf16 operands (code 1) or f16 (code 0); bit 16: the second operand MN-major
     constexpr uint32_t fmt = F8 ? 0u : ((1u << 7) | (1u << 10));
     constexpr uint32_t id_s = (1u << 4) | fmt | ((128u >> 3) << 17) | ((128u >> 4) << 24);
     constexpr uint32_t id_o = (1u << 4) | fmt | (1u << 16) | ((static_cast<uint32_t>(DH) >> 3) << 17) | ((128u >> 4) << 24);
-    // the last key tile's values behind the length (inside its last page) are zeroed here (16-bit cache)
-    const int tail_tile = len % kTileRows ? len / kTileRows - t_lo : -1;
-    bool ok = wait_for(&c.q_ready, 0);
-    // Buffers alternate between the keys and the values of the key tiles in order. Tile t walks its own key tiles:
-    // all of them, or every other one. ks, vs: the next keys' and values' place in the ring of each t.
-    Ring ks[2], vs[2];
+    const int t = warp - kMmaWarp;
+    const int n = n_of[t];
+    const uint32_t t_s = tmem + t * 128, t_o = tmem + 256 + t * 128;
+    // Buffers alternate between the keys and the values of the key tiles in order. Tile t walks all of them, or every
+    // other one. ks, vs: the next keys' and values' place in the ring.
     const int step = p.alt ? 4 : 2;
-    vs[0].next(p.ring), vs[1].next(p.ring);
-    if (p.alt) {
-      ks[1].next(p.ring), ks[1].next(p.ring);
-      vs[1].next(p.ring), vs[1].next(p.ring);
+    Ring ks, vs;
+    vs.next(p.ring);
+    if (p.alt && t == 1) {
+      for (int x = 0; x < 2; ++x) {
+        ks.next(p.ring);
+        vs.next(p.ring);
+      }
     }
-    auto scores = [&](int t, int i) {
-      Ring& k = ks[t];
-      if (!wait_for(&c.full[k.b], k.phase)) return false;
+    const int tail_i = tail_tile < 0 ? -1 : (p.alt ? ((tail_tile & 1) == t ? tail_tile >> 1 : -1) : tail_tile);
+    const uint64_t qd = sw128_kmajor_desc(q_a + (p.alt ? 0 : t * kTileBytes));
+    bool ok = wait_for(&c.q_ready, 0);
+    auto scores = [&](uint64_t kd) {
+#pragma unroll
+      for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+        for (int x = 0; x < 4; ++x)   // descriptor addresses count 16 bytes
+          tc_mma<false>(t_s, qd + ((h * kBlock + x * 32) >> 4), kd + ((h * kBlock + x * 32) >> 4), id_s, (h | x) ? 1u : 0u);
+    };
+    auto advance = [&](Ring& r) {
+      for (int x = 0; x < step; ++x) r.next(p.ring);
+    };
+    if (n > 0) {
+      ok = ok && wait_for(&c.full[ks.b], ks.phase);
       tc_fence_after();
-      if (elect_one()) {
-        const uint64_t qd = sw128_kmajor_desc(q_a + (p.alt ? 0 : t * kTileBytes)), kd = sw128_kmajor_desc(ring_a + k.b * kTileBytes);
-#pragma unroll
-        for (int h = 0; h < kHalves; ++h)
-#pragma unroll
-          for (int x = 0; x < 4; ++x)   // descriptor addresses count 16 bytes
-            tc_mma<false>(tmem + t * 128, qd + ((h * kBlock + x * 32) >> 4), kd + ((h * kBlock + x * 32) >> 4), id_s, (h | x) ? 1u : 0u);
-        if (p.alt || t == 1 || i >= n_of[1]) tc_commit(&c.empty[k.b]);   // the keys' last user
+      const uint64_t kd = sw128_kmajor_desc(ring_a + ks.b * kTileBytes);
+      if (ok && elect_one()) {
+        scores(kd);
         tc_commit(&c.s_full[t]);
+        tc_commit(&c.empty[ks.b]);
       }
       __syncwarp();
-      for (int x = 0; x < step; ++x) k.next(p.ring);
-      return true;
-    };
-    auto values = [&](int t, int i) {
-      Ring& v = vs[t];
-      if (!wait_for(&c.full[v.b], v.phase)) return false;
-      if (!F8 && (p.alt ? 2 * i + t : i) == tail_tile && (p.alt || t == 0 || i >= n_of[0])) {   // by its first user
-        const int r0 = len % kTileRows;
-        for (int x = lane; x < (kTileRows - r0) * 8 * kHalves; x += 32)
-          st_shared_v4(ring_a + v.b * kTileBytes + (x % kHalves) * kBlock + r0 * 128 + (x / kHalves) * 16,
-                       make_uint4(0, 0, 0, 0));
-        fence_async_smem();
-        __syncwarp();
-      }
-      const uint64_t vd = sw128_mnmajor_desc(ring_a + v.b * kTileBytes, kBlock);
+      advance(ks);
+    }
+    // The two warps take turns on the tensor cores, a batch of P V and the next scores each: interleaved, both tiles'
+    // products would end late and both warpgroups would then exponentiate at the same time. Everything a batch needs
+    // is waited for before its turn, and the turn passes on before the commits, so that the queue of MMAs never drains.
+    const int rounds = max(n_of[0], n_of[1]);
+    for (int i = 0; i < rounds && ok; ++i) {
+      const bool mine = i < n, more = i + 1 < n;
+      if (mine)
+        ok = wait_for(&c.full[vs.b], vs.phase) && (F8 || i != tail_i || wait_for(&c.tail, 0)) &&
+             (F8 || !more || wait_for(&c.full[ks.b], ks.phase)) && wait_for(&c.p_full[t], i & 1);
+      const uint64_t vd = sw128_mnmajor_desc(ring_a + vs.b * kTileBytes, kBlock);
+      const uint64_t kd = sw128_kmajor_desc(ring_a + ks.b * kTileBytes);
+      ok = ok && wait_for(&c.turn[t], t == 0 ? (i & 1) ^ 1 : i & 1);
+      if (!ok) break;
+      tc_fence_after();
+      auto products = [&]() {
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        if (!wait_for(&c.p_full[t][half], i & 1)) return false;
-        tc_fence_after();
-        if (elect_one()) {
-#pragma unroll
-          for (int x = half * 4; x < half * 4 + 4; ++x)
-            tc_mma_ts<false>(tmem + 256 + t * 128, tmem + t * 128 + x * 8, vd + ((x * 2048) >> 4), id_o, (i | x) ? 1u : 0u);
-          if (half == 1) {
-            if (p.alt || t == 1 || i >= n_of[1]) tc_commit(&c.empty[v.b]);
-            if (i == n_of[t] - 1) tc_commit(&c.o_done[t]);
-          }
+        for (int x = 0; x < 8; ++x) tc_mma_ts<false>(t_o, t_s + x * 8, vd + ((x * 2048) >> 4), id_o, (i | x) ? 1u : 0u);
+      };
+      if constexpr (F8) {
+        // codes are expanded into four buffers only: the values' is given back before the next keys are waited for
+        if (mine && elect_one()) {
+          products();
+          if (!more) tc_commit(&c.o_done[t]);
+          tc_commit(&c.empty[vs.b]);
         }
         __syncwarp();
+        if (more) {
+          ok = wait_for(&c.full[ks.b], ks.phase);
+          if (!ok) break;
+          tc_fence_after();
+        }
+        if (elect_one()) {
+          if (more) scores(kd);
+          mbar_arrive(&c.turn[t ^ 1]);
+          if (more) {
+            tc_commit(&c.s_full[t]);
+            tc_commit(&c.empty[ks.b]);
+          }
+        }
+      } else if (elect_one()) {
+        if (mine) {
+          products();
+          if (more) scores(kd);
+        }
+        mbar_arrive(&c.turn[t ^ 1]);
+        if (mine) {
+          if (more) {
+            tc_commit(&c.s_full[t]);
+            tc_commit(&c.empty[ks.b]);
+          } else {
+            tc_commit(&c.o_done[t]);
+          }
+          tc_commit(&c.empty[vs.b]);
+        }
       }
-      for (int x = 0; x < step; ++x) v.next(p.ring);
-      return true;
-    };
-    const int n_max = max(n_of[0], n_of[1]);
-    for (int t = 0; t < 2 && ok; ++t)
-      if (n_of[t] > 0) ok = scores(t, 0);
-    for (int i = 0; i < n_max && ok; ++i)
-      for (int t = 0; t < 2 && ok; ++t) {
-        if (i >= n_of[t]) continue;
-        ok = values(t, i);
-        if (ok && i + 1 < n_of[t]) ok = scores(t, i + 1);
+      __syncwarp();
+      if (mine) advance(vs);
+      if (more) advance(ks);
+      if (!mine && !p.alt) {   // a key tile that only the other one uses waits for this one's release all the same
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          Ring& at = kv ? vs : ks;
+          ok = ok && wait_for(&c.full[at.b], at.phase);
+          if (ok && lane == 0) mbar_arrive(&c.empty[at.b]);
+          at.next(p.ring);
+          at.next(p.ring);
+        }
       }
+    }
     if (!ok) {   // a wait ran out: let what was issued finish before the CTA leaves
       if (elect_one()) {
         atomicOr(p.err, kErrPipelineTimeout);
-        tc_commit(&c.drain);
+        tc_commit(&c.drain[t]);
       }
       __syncwarp();
-      wait_for(&c.drain, 0);
+      wait_for(&c.drain[t], 0);
+    }
+  } else if (warp == kTailWarp) {
+    // ================================================= the last key tile's values behind the length (16-bit cache)
+    if (!F8 && tail_tile >= 0 && tail_tile < n_keys) {
+      // every phase of its buffer in turn: a parity alone does not tell them apart
+      const int item = 2 * tail_tile + 1, b = item % p.ring;
+      bool ok = true;
+      for (int ph = 0; ph <= item / p.ring && ok; ++ph) ok = wait_for(&c.full[b], ph & 1);
+      if (ok) {
+        const int r0 = len % kTileRows;
+        for (int x = lane; x < (kTileRows - r0) * 8 * kHalves; x += 32)
+          st_shared_v4(ring_a + b * kTileBytes + (x % kHalves) * kBlock + r0 * 128 + (x / kHalves) * 16,
+                       make_uint4(0, 0, 0, 0));
+        fence_async_smem();
+      } else if (lane == 0) {
+        atomicOr(p.err, kErrPipelineTimeout);
+      }
+      __syncwarp();
+      if (ok && lane == 0) mbar_arrive(&c.tail);
     }
   } else if (warp == kTmaWarp) {
     // ================================================= page table and TMA
-    const int rows_box = min(p.page, kTileRows), boxes = kTileRows / rows_box;   // boxes of a tile
-    const int part = lane % boxes, half = lane / boxes;                          // this lane's box and block
-    const bool active = lane < boxes * (F8 ? 1 : kHalves);
-    const int32_t* trow = p.table + static_cast<int64_t>(sid) * p.table_stride;
-    auto page_of = [&](int j) {   // the page of this lane's box of key tile j; the pool's end where there is none
-      const int key = (t_lo + j) * kTileRows + part * rows_box;
-      if (!active || key >= len) return p.pages;
-      const int pg = __ldg(trow + (key >> p.page_shift));
-      if (pg < 0 || pg >= p.pages) {
-        atomicOr(p.err, kErrBadBatch);
-        return p.pages;
-      }
-      return pg;
-    };
-    const int nb = F8 ? p.raw_ring : p.ring;
-    uint64_t* full = F8 ? c.rfull : c.full;
-    uint64_t* empty = F8 ? c.rempty : c.empty;
-    const uint32_t base = F8 ? raw_a : ring_a;
-    constexpr uint32_t bytes = F8 ? kRawBytes : kTileBytes;
-    int pg = n_keys > 0 ? page_of(0) : 0;
     bool ok = true;
-    int issued = 0;
-    Ring at;
-    for (int j = 0; j < n_keys && ok; ++j) {
-      const int row_in = ((t_lo + j) * kTileRows + part * rows_box) & (p.page - 1);
-      const int next = j + 1 < n_keys ? page_of(j + 1) : 0;
-      for (int kv = 0; kv < 2 && ok; ++kv) {
-        if (issued >= nb) ok = wait_for(&empty[at.b], at.phase ^ 1);
-        if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(&full[at.b], bytes);
-        __syncwarp();
-        if (active) {
-          const uint32_t dst = base + at.b * bytes + (F8 ? part * rows_box * DH : half * kBlock + part * rows_box * 128);
-          tma_load_4d(dst, kv ? &tm_v : &tm_k, &full[at.b], half * 64, row_in, g, pg);
-        }
-        __syncwarp();
-        ++issued;
-        at.next(nb);
-      }
-      pg = next;
-    }
+    while (copy_next < 2 * n_keys && ok) ok = copy_one(false);
+    const int issued = copy_next, nb = ring_n;
+    uint64_t* full = ring_full;
     if (!ok) {   // the copies in flight land before the CTA leaves
       if (lane == 0) atomicOr(p.err, kErrPipelineTimeout);
       for (int item = max(0, issued - nb); item < issued; ++item) wait_for(&full[item % nb], (item / nb) & 1);
@@ -702,6 +809,12 @@ __global__ void __launch_bounds__(threads_of(F8), 1)
     const int ct = tid - kCvtWarp * 32;
     constexpr int kCvtThreads = kCvtWarps * 32;
     constexpr int kChunks = DH / 16;      // 16-code chunks of a row
+    constexpr int kRowStep = kCvtThreads / kChunks;   // a multiple of 8: a thread's swizzle is the same in all its rows
+    // this thread's rows cr, cr + kRowStep, ...; the two halves of a row write their two chunks in opposite orders, so
+    // that eight lanes reach eight bank groups
+    const int cr = ct / kChunks, ch = ct % kChunks, odd = (ch >> 2) & 1;
+    const uint32_t dst = (ch >> 2) * kBlock;
+    const uint32_t place0 = swz(cr, (ch & 3) * 2 + odd), place1 = swz(cr, (ch & 3) * 2 + 1 - odd);
     bool ok = true;
     Ring raw, out;
     for (int item = 0; item < 2 * n_keys && ok; ++item, raw.next(p.raw_ring), out.next(p.ring)) {
@@ -710,13 +823,18 @@ __global__ void __launch_bounds__(threads_of(F8), 1)
       if (ok && item >= p.ring) ok = wait_for(&c.empty[b], out.phase ^ 1);
       if (!ok) break;
       const int valid = len - (t_lo + (item >> 1)) * kTileRows;   // rows of the tile inside the length
-      const uint4* src = reinterpret_cast<const uint4*>(sraw + rb * kRawBytes);
-      const uint32_t dst = ring_a + b * kTileBytes;
-#pragma unroll 4
-      for (int x = ct; x < kTileRows * kChunks; x += kCvtThreads) {
-        const int r = x / kChunks, ch = x % kChunks;
-        const uint4 v = r < valid ? src[x] : make_uint4(0, 0, 0, 0);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      const uint4* src = reinterpret_cast<const uint4*>(sraw + rb * kRawBytes) + ct;
+      constexpr int kIter = kTileRows / kRowStep;
+      uint4 v[kIter];
+#pragma unroll
+      for (int x = 0; x < kIter; ++x) v[x] = src[x * kCvtThreads];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&c.rempty[rb]);
+      const uint32_t at = ring_a + b * kTileBytes + dst;
+#pragma unroll
+      for (int x = 0; x < kIter; ++x) {
+        if (cr + x * kRowStep >= valid) v[x] = make_uint4(0, 0, 0, 0);
+        const uint32_t w[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
         uint32_t h[8];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -725,19 +843,13 @@ __global__ void __launch_bounds__(threads_of(F8), 1)
           h[2 * e] = static_cast<uint32_t>(lo.x) | (static_cast<uint32_t>(lo.y) << 16);
           h[2 * e + 1] = static_cast<uint32_t>(hi.x) | (static_cast<uint32_t>(hi.y) << 16);
         }
-        // the two halves of the row write their chunks in opposite orders: eight lanes, eight bank groups
-        const uint32_t at = dst + (ch >> 2) * kBlock;
-        const int c0 = (ch & 3) * 2, odd = (ch >> 2) & 1;
         const uint4 a = make_uint4(h[0], h[1], h[2], h[3]), d = make_uint4(h[4], h[5], h[6], h[7]);
-        st_shared_v4(at + swz(r, c0 + odd), odd ? d : a);
-        st_shared_v4(at + swz(r, c0 + 1 - odd), odd ? a : d);
+        st_shared_v4(at + x * kRowStep * 128 + place0, odd ? d : a);
+        st_shared_v4(at + x * kRowStep * 128 + place1, odd ? a : d);
       }
       fence_async_smem();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&c.full[b]);
-        mbar_arrive(&c.rempty[rb]);
-      }
+      if (lane == 0) mbar_arrive(&c.full[b]);
     }
     if (!ok && lane == 0) atomicOr(p.err, kErrPipelineTimeout);
   }
