@@ -13,7 +13,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libfmad.so")
 SOURCES = ["gemm.cu", "gemm_nvfp4.cu", "attn.cu", "rowops.cu", "ofuse.cu", "policy.cu", "noalloc.cu", "handoff.cu",
-           "paged_attn.cu", "kv.cu", "normq.cu"]
+           "paged_attn.cu", "paged_decode.cu", "kv.cu", "normq.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

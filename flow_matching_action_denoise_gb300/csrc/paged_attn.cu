@@ -37,6 +37,7 @@
 
 #include "internal.h"
 #include "kv.h"
+#include "paged.cuh"
 #include "ptx.cuh"
 
 namespace fm {
@@ -52,67 +53,7 @@ constexpr int kMmaWarp = 8, kTmaWarp = 10, kTailWarp = 11, kCvtWarp = 12, kCvtWa
 constexpr int threads_of(bool f8) { return f8 ? 512 : 384; }
 constexpr int kSmemLimit = 226 * 1024;
 constexpr int kMaxRing = 8;
-constexpr float kGrow = 8.0f;     // the running maximum moves when it grows by more than this power of two
 constexpr uint32_t kCtlBytes = 512;
-
-struct AttnParams {
-  const __nv_bfloat16* q;
-  __nv_bfloat16* out;
-  int64_t q_stride, out_stride;   // elements between tokens
-  const int32_t* start;
-  const int32_t* seq;
-  const int32_t* lens;
-  const int32_t* table;
-  int n, tokens, max_tokens, seqs, table_stride, pages, page, page_shift;
-  int H, Hkv, G;
-  int causal, window;
-  float scale_log2;               // scale * log2(e)
-  const float* k_scale;
-  const float* v_scale;
-  int alt, splits, split_tiles;
-  int ring, raw_ring;
-  float* part_o;                  // [splits][tokens * H][Dh]
-  float2* part_ml;                // [splits][tokens * H] (log2 maximum, sum)
-  int* err;
-};
-
-// True once the phase with the given parity has completed; false after 2^22 polls (each of which the hardware suspends
-// for a while: seconds, far beyond any legitimate wait). Reading a clock between the polls cost more than the wait.
-__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity) {
-#pragma unroll 1
-  for (int i = 0; i < (1 << 22); ++i)
-    if (mbar_try_wait(bar, parity)) return true;
-  return false;
-}
-
-// One lane of a converged warp. Unlike a comparison with a lane number it tells the compiler that a single lane is
-// active: tcgen05 instructions take their operands from the warp's uniform registers, and under a plain branch each
-// MMA took about 100 cycles to issue (operands collected lane by lane), longer than it runs.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t pred = 0;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\t@p mov.s32 %0, 1;\n}" : "+r"(pred));
-  return pred != 0;
-}
-
-// Position in a ring of buffers: the buffer and the parity of its barrier's phase.
-struct Ring {
-  int b = 0;
-  uint32_t phase = 0;
-  __device__ __forceinline__ void next(int n) {
-    if (++b == n) {
-      b = 0;
-      phase ^= 1;
-    }
-  }
-};
-
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2,
-                                            int c3) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
-      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
-      : "memory");
-}
 
 // Matrix descriptor of an MN-major operand in 128-byte-swizzled rows: rows along K (8-row groups 1024 bytes
 // apart), 64 elements of MN per row, further blocks of 64 `block_bytes` apart.
@@ -168,17 +109,6 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
       : "=f"(d.x), "=f"(d.y)
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
-}
-
-template <bool kF16>
-__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
-  if constexpr (kF16) {
-    const __half2 v = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&v);
-  } else {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&v);
-  }
 }
 
 __device__ __forceinline__ uint32_t swz(int r, int c) {   // 16-byte chunk c of row r of a 128-byte-row tile
@@ -242,31 +172,15 @@ __global__ void __launch_bounds__(threads_of(F8), 1)
   pdl_wait();
 
   // ---- the entry, its rows and its keys (the same in every thread)
-  int begin = __ldg(p.start + entry), nq = __ldg(p.start + entry + 1) - begin;
-  const int sid = p.seq ? __ldg(p.seq + entry) : entry;
-  bool bad = begin < 0 || nq < 0 || begin > p.tokens || nq > p.tokens - begin || sid < 0 || sid >= p.seqs;
-  int len = 0;
-  if (!bad) {
-    len = __ldg(p.lens + sid);
-    bad = len < 0 || len > p.table_stride * static_cast<int64_t>(p.page);
-    if (bad) len = 0;
-  } else {
-    nq = 0;
-  }
-  if ((bad || nq > p.max_tokens) && tid == 0 && row_block == 0 && g == 0 && split == 0) atomicOr(p.err, kErrBadBatch);
-  const int rows = nq > p.max_tokens ? p.max_tokens * p.G : nq * p.G;   // <= 2^30
+  const Entry en = entry_of(p, entry, tid == 0 && row_block == 0 && g == 0 && split == 0);
+  const int begin = en.begin, nq = en.nq, len = en.len, sid = en.sid;
+  const int rows = min(nq, p.max_tokens) * p.G;   // <= 2^30
   const int row0 = row_block * block_rows;
   if (row0 >= rows) return;   // before TMEM is taken, the same for the whole CTA
 
-  const int past = len - nq;   // pos(token) = past + token
-  auto key_end = [&](int row) {   // one past the last key of a row
-    const int pos = past + row / p.G;
-    return pos < 0 ? 0 : (p.causal ? min(pos + 1, len) : len);
-  };
-  auto key_begin = [&](int row) {
-    const int pos = past + row / p.G;
-    return p.window > 0 && pos >= p.window ? pos - p.window + 1 : 0;
-  };
+  const int past = len - nq;   // position of token i: past + i
+  auto key_end = [&](int row) { return last_key(p, past + row / p.G, len); };
+  auto key_begin = [&](int row) { return first_key(p, past + row / p.G); };
   const int last_row = min(rows, row0 + block_rows) - 1;
   const int hi_all = key_end(last_row);
   int t_lo = key_begin(row0) / kTileRows;
@@ -913,7 +827,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ 
 }
 
 // Rows of one KV head's page block as a TMA source: (head dim, token, head, page).
-bool kv_tmap(CUtensorMap* map, const fm_kv_cache& c, const void* base) {
+bool kv_tmap(CUtensorMap* map, const fm_kv_cache& c, const void* base, bool decode) {
   const bool f8 = c.fmt == FM_FMT_FP8;
   const uint64_t eb = f8 ? 1 : 2;
   const uint64_t dims[4] = {static_cast<uint64_t>(c.Dh), static_cast<uint64_t>(c.page_tokens),
@@ -923,13 +837,15 @@ bool kv_tmap(CUtensorMap* map, const fm_kv_cache& c, const void* base) {
   const uint64_t strides[3] = {stride(c.token_stride, c.page_tokens), stride(c.head_stride, c.Hkv),
                                stride(c.page_stride, c.pages)};
   const uint32_t box[4] = {static_cast<uint32_t>(f8 ? c.Dh : 64),
-                           static_cast<uint32_t>(std::min(c.page_tokens, kTileRows)), 1, 1};
-  return make_tmap_4d(map, base, static_cast<int>(eb), dims, strides, box, !f8);
+                           static_cast<uint32_t>(std::min(c.page_tokens, decode ? kDecodeKeys : kTileRows)), 1, 1};
+  // codes that are expanded in shared memory lie there in plain rows, all else is read by matrix instructions
+  const int swizzle = f8 ? (decode ? c.Dh : 0) : 128;
+  return make_tmap_4d(map, base, static_cast<int>(eb), dims, strides, box, swizzle);
 }
 
 struct Plan {
-  int alt, splits, split_tiles, ring, raw_ring;
-  size_t smem;
+  int decode, alt, splits, split_tiles, ring, raw_ring;
+  size_t smem, workspace;
 };
 
 int sm_count() {
@@ -949,33 +865,71 @@ int sm_count() {
   return v;
 }
 
-// The variant for a batch: by its bounds and the number of SMs alone, so that the workspace query and the launch agree.
-Plan plan_of(const fm_kv_cache& c, const fm_kv_batch& b, int H) {
-  Plan pl;
+// The number of splits of a batch's keys. window 0: the one that the workspace is sized for.
+int splits_of(const fm_kv_cache& c, const fm_kv_batch& b, int H, int window) {
   const int64_t rows = static_cast<int64_t>(b.max_tokens) * (H / c.Hkv);
-  pl.alt = rows <= kTileRows;
-  const size_t tile = static_cast<size_t>(kTileRows) * c.Dh * 2;
-  const size_t q = tile * (pl.alt ? 1 : 2);
-  const size_t room = kSmemLimit - kCtlBytes - q;
-  if (c.fmt == FM_FMT_FP8) {
-    pl.ring = 4;
-    pl.raw_ring = static_cast<int>(std::min<size_t>(kMaxRing, (room - pl.ring * tile) / (tile / 2)));
-  } else {
-    pl.ring = static_cast<int>(std::min<size_t>(kMaxRing, room / tile));
-    pl.raw_ring = 0;
-  }
-  pl.smem = 1024 + q + pl.ring * tile + pl.raw_ring * (tile / 2) + kCtlBytes;
-  const int64_t block_rows = pl.alt ? kTileRows : 2 * kTileRows;
-  const int64_t units = (rows + block_rows - 1) / block_rows * c.Hkv * b.n;
-  const int tiles = std::max(1, (b.max_len + kTileRows - 1) / kTileRows);
   const int sms = sm_count();
-  int64_t want = units > 0 ? (2 * sms + units - 1) / units : 1;
-  if (units >= sms) want = 1;
-  const int min_tiles = pl.alt ? 2 : 4;
-  int64_t splits = std::max<int64_t>(1, std::min<int64_t>(want, tiles / min_tiles));
-  pl.split_tiles = static_cast<int>((tiles + splits - 1) / splits);
-  // a window's first key lies inside a tile: one tile more than the bound's count can be touched
-  pl.splits = splits == 1 ? 1 : (tiles + pl.split_tiles - 1) / pl.split_tiles;
+  const bool f8 = c.fmt == FM_FMT_FP8;
+  int64_t keys = std::max(1, b.max_len);
+  if (window > 0) keys = std::min<int64_t>(keys, static_cast<int64_t>(window) + b.max_tokens);
+  if (rows <= kDecodeRows) {
+    // splits of at least two tiles until about four CTAs an SM are under way (their rings keep HBM busy; more only
+    // cost their start). Up to 8 are a cluster and need no workspace.
+    const int64_t units = static_cast<int64_t>(c.Hkv) * std::max(1, b.n);
+    const int64_t tiles = (keys + kDecodeKeys - 1) / kDecodeKeys + (window > 0);
+    const int64_t want = std::max<int64_t>(1, std::min<int64_t>((4 * sms) / units, (tiles + 1) / 2));
+    if (want > 8 && want < 24) return 8;   // a second kernel pays for three times the CTAs
+    return static_cast<int>(std::min<int64_t>(want, 256));
+  }
+  // One CTA an SM: waves x (start and end + tiles x time of a tile), in units of 0.1 us as measured, with the join of
+  // splits (a kernel, and every share written and read) added. The number of splits with the least of it.
+  const bool alt = rows <= kTileRows;
+  const int64_t block_rows = alt ? kTileRows : 2 * kTileRows;
+  const int64_t units = std::max<int64_t>(1, (rows + block_rows - 1) / block_rows * c.Hkv * b.n);
+  const int64_t tiles = (keys + kTileRows - 1) / kTileRows + (window > 0);
+  const int64_t fixed = f8 ? 85 : 70, each = alt ? (f8 ? 15 : 8) : (f8 ? 18 : 14);
+  int64_t best = 0, splits = 1;
+  for (int64_t s = 1; s <= std::min<int64_t>(64, std::max<int64_t>(1, tiles / 2)); ++s) {
+    const int64_t waves = (units * s + sms - 1) / sms;
+    const int64_t shares = s * b.tokens * H * c.Dh * 8;   // bytes, at 4 TB/s: 4e5 bytes in 0.1 us
+    const int64_t cost = waves * (fixed + (tiles + s - 1) / s * each) + (s > 1 ? 25 + shares / 400000 : 0);
+    if (s == 1 || cost < best) {
+      best = cost;
+      splits = s;
+    }
+  }
+  return static_cast<int>(splits);
+}
+
+// The variant for a batch, by its bounds and the number of SMs alone. A window, which the workspace query does not
+// know, only lowers the number of splits.
+Plan plan_of(const fm_kv_cache& c, const fm_kv_batch& b, int H, int window) {
+  Plan pl = {};
+  const int64_t rows = static_cast<int64_t>(b.max_tokens) * (H / c.Hkv);
+  pl.splits = splits_of(c, b, H, 0);
+  int64_t keys = std::max(1, b.max_len);
+  if (window > 0) {
+    pl.splits = std::min(pl.splits, splits_of(c, b, H, window));
+    keys = std::min<int64_t>(keys, static_cast<int64_t>(window) + b.max_tokens);
+  }
+  pl.decode = rows <= kDecodeRows;
+  if (!pl.decode) {
+    pl.alt = rows <= kTileRows;
+    const int64_t tiles = (keys + kTileRows - 1) / kTileRows + (window > 0);
+    pl.split_tiles = static_cast<int>((tiles + pl.splits - 1) / pl.splits);
+    const size_t tile = static_cast<size_t>(kTileRows) * c.Dh * 2;
+    const size_t q = tile * (pl.alt ? 1 : 2);
+    const size_t room = kSmemLimit - kCtlBytes - q;
+    if (c.fmt == FM_FMT_FP8) {
+      pl.ring = 4;
+      pl.raw_ring = static_cast<int>(std::min<size_t>(kMaxRing, (room - pl.ring * tile) / (tile / 2)));
+    } else {
+      pl.ring = static_cast<int>(std::min<size_t>(kMaxRing, room / tile));
+    }
+    pl.smem = 1024 + q + pl.ring * tile + pl.raw_ring * (tile / 2) + kCtlBytes;
+  }
+  if (pl.splits > (pl.decode ? 8 : 1))
+    pl.workspace = static_cast<size_t>(pl.splits) * b.tokens * H * (c.Dh * sizeof(float) + sizeof(float2));
   return pl;
 }
 
@@ -990,6 +944,7 @@ cudaError_t configure() {
   if (e == cudaSuccess) e = configure_one<128, false>();
   if (e == cudaSuccess) e = configure_one<64, true>();
   if (e == cudaSuccess) e = configure_one<128, true>();
+  if (e == cudaSuccess) e = decode_configure();
   return e;
 }
 
@@ -1002,15 +957,10 @@ int check(const fm_kv_cache* c, const fm_kv_batch* b, int H) {
   if (c->page_tokens > 256) return record_error(FM_ERR_SHAPE, "attention takes pages of 16 to 256 tokens");
   const int64_t rows = static_cast<int64_t>(b->max_tokens) * (H / c->Hkv);
   if (rows > (int64_t(1) << 30)) return record_error(FM_ERR_SHAPE, "max_tokens * H / Hkv exceeds 2^30");
-  const Plan pl = plan_of(*c, *b, H);
+  const Plan pl = plan_of(*c, *b, H, 0);
   if (c->Hkv > 65535 || static_cast<int64_t>(b->n) * pl.splits > 65535)
     return record_error(FM_ERR_SHAPE, "too many entries for one call (entries x splits and Hkv up to 65535)");
   return FM_OK;
-}
-
-size_t workspace(const Plan& pl, const fm_kv_cache& c, const fm_kv_batch& b, int H) {
-  if (pl.splits == 1) return 0;
-  return static_cast<size_t>(pl.splits) * b.tokens * H * (c.Dh * sizeof(float) + sizeof(float2));
 }
 
 }  // namespace
@@ -1021,7 +971,7 @@ extern "C" int fm_paged_attention_workspace_size(const fm_kv_cache* c, const fm_
   if (!bytes) return fm::record_error(FM_ERR_INVALID_ARG, "bytes is NULL");
   const int st = fm::check(c, b, H);
   if (st != FM_OK) return st;
-  *bytes = b->n && b->tokens ? fm::workspace(fm::plan_of(*c, *b, H), *c, *b, H) : 0;
+  *bytes = b->n && b->tokens ? fm::plan_of(*c, *b, H, 0).workspace : 0;
   return FM_OK;
 }
 
@@ -1041,8 +991,8 @@ extern "C" int fm_paged_attention(const fm_kv_cache* c, int layer, const fm_kv_b
     return record_error(FM_ERR_SHAPE, "token strides must be multiples of 8 elements and hold H * Dh");
   if (reinterpret_cast<uintptr_t>(q) % 16 || reinterpret_cast<uintptr_t>(out) % 16)
     return record_error(FM_ERR_ALIGN, "q and out must be 16-byte aligned");
-  const Plan pl = plan_of(*c, *b, H);
-  const size_t need = fm::workspace(pl, *c, *b, H);
+  const Plan pl = plan_of(*c, *b, H, window);
+  const size_t need = pl.workspace;
   if (need) {
     if (!workspace) return record_error(FM_ERR_INVALID_ARG, "workspace is NULL");
     if (reinterpret_cast<uintptr_t>(workspace) % 16) return record_error(FM_ERR_ALIGN, "workspace not 16-byte aligned");
@@ -1052,7 +1002,8 @@ extern "C" int fm_paged_attention(const fm_kv_cache* c, int layer, const fm_kv_b
   const bool f8 = c->fmt == FM_FMT_FP8;
   const int64_t off = layer * c->layer_stride * (f8 ? 1 : 2);
   CUtensorMap tk, tv;
-  if (!kv_tmap(&tk, *c, static_cast<const uint8_t*>(c->k) + off) || !kv_tmap(&tv, *c, static_cast<const uint8_t*>(c->v) + off))
+  if (!kv_tmap(&tk, *c, static_cast<const uint8_t*>(c->k) + off, pl.decode) ||
+      !kv_tmap(&tv, *c, static_cast<const uint8_t*>(c->v) + off, pl.decode))
     return record_error(FM_ERR_CUDA, "cuTensorMapEncodeTiled (cache pages) failed");
   int* err = standalone_error_word();
   if (!err) return record_error(FM_ERR_CUDA, "no error word on the current device");
@@ -1088,20 +1039,26 @@ extern "C" int fm_paged_attention(const fm_kv_cache* c, int layer, const fm_kv_b
   p.split_tiles = pl.split_tiles;
   p.ring = pl.ring;
   p.raw_ring = pl.raw_ring;
-  p.part_o = static_cast<float*>(workspace);
-  p.part_ml = reinterpret_cast<float2*>(p.part_o + static_cast<size_t>(pl.splits) * b->tokens * H * c->Dh);
+  if (need) {
+    p.part_o = static_cast<float*>(workspace);
+    p.part_ml = reinterpret_cast<float2*>(p.part_o + static_cast<size_t>(pl.splits) * b->tokens * H * c->Dh);
+  }
   p.err = err;
   const int64_t rows = static_cast<int64_t>(b->max_tokens) * p.G;
   const int64_t block_rows = pl.alt ? kTileRows : 2 * kTileRows;
   LaunchOpts o;
   o.stream = static_cast<cudaStream_t>(stream);
   o.pdl = true;
-  const dim3 grid(static_cast<unsigned>((rows + block_rows - 1) / block_rows), static_cast<unsigned>(c->Hkv),
-                  static_cast<unsigned>(b->n * pl.splits));
-  auto kernel = c->Dh == 128 ? (f8 ? paged_attn_kernel<128, true> : paged_attn_kernel<128, false>)
-                             : (f8 ? paged_attn_kernel<64, true> : paged_attn_kernel<64, false>);
-  e = launch(kernel, grid, dim3(threads_of(f8)), pl.smem, o, p, tk, tv);
-  if (e == cudaSuccess && pl.splits > 1) {
+  if (pl.decode) {
+    e = decode_launch(p, c->Dh, f8, tk, tv, o);
+  } else {
+    const dim3 grid(static_cast<unsigned>((rows + block_rows - 1) / block_rows), static_cast<unsigned>(c->Hkv),
+                    static_cast<unsigned>(b->n * pl.splits));
+    auto kernel = c->Dh == 128 ? (f8 ? paged_attn_kernel<128, true> : paged_attn_kernel<128, false>)
+                               : (f8 ? paged_attn_kernel<64, true> : paged_attn_kernel<64, false>);
+    e = launch(kernel, grid, dim3(threads_of(f8)), pl.smem, o, p, tk, tv);
+  }
+  if (e == cudaSuccess && need) {
     const int64_t blocks = (static_cast<int64_t>(b->tokens) * H + 7) / 8;
     auto join = c->Dh == 128 ? combine_kernel<128> : combine_kernel<64>;
     e = launch(join, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, o, static_cast<const float*>(p.part_o),
