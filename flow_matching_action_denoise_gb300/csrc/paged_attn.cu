@@ -29,7 +29,6 @@
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
-#include <cuda_fp8.h>
 
 #include <algorithm>
 #include <atomic>
@@ -751,12 +750,7 @@ __global__ void __launch_bounds__(threads_of(F8), 1)
         const uint32_t w[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
         uint32_t h[8];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w[e] & 0xffffu), __NV_E4M3);
-          const __half2_raw hi = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w[e] >> 16), __NV_E4M3);
-          h[2 * e] = static_cast<uint32_t>(lo.x) | (static_cast<uint32_t>(lo.y) << 16);
-          h[2 * e + 1] = static_cast<uint32_t>(hi.x) | (static_cast<uint32_t>(hi.y) << 16);
-        }
+        for (int e = 0; e < 4; ++e) expand4(w[e], h[2 * e], h[2 * e + 1]);
         const uint4 a = make_uint4(h[0], h[1], h[2], h[3]), d = make_uint4(h[4], h[5], h[6], h[7]);
         st_shared_v4(at + x * kRowStep * 128 + place0, odd ? d : a);
         st_shared_v4(at + x * kRowStep * 128 + place1, odd ? a : d);
@@ -776,48 +770,61 @@ __global__ void __launch_bounds__(threads_of(F8), 1)
   }
 }
 
-// Joins the splits of every (token, head) row in split order: a warp per row.
+// Joins the splits of every (token, head) row: `warps` (1, 2, 4 or 8, a power of two) of a CTA's eight share a row, each
+// every warps-th split, and are summed in warp order.
 template <int DH>
 __global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ part_o, const float2* __restrict__ part_ml,
-                                                      int splits, int tokens, int H, const int32_t* __restrict__ start,
-                                                      int n, __nv_bfloat16* __restrict__ out, int64_t out_stride) {
-  pdl_wait();
-  const int64_t rows = static_cast<int64_t>(tokens) * H;
-  const int64_t row = blockIdx.x * 8ll + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (row >= rows) return;
-  const int token = static_cast<int>(row / H);
-  if (token < __ldg(start) || token >= __ldg(start + n)) return;   // rows of no entry keep what they hold
-  float top = -INFINITY;
-  for (int s = lane; s < splits; s += 32) top = fmaxf(top, part_ml[s * rows + row].x);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                                                      int splits, int warps, int tokens, int H,
+                                                      const int32_t* __restrict__ start, int n,
+                                                      __nv_bfloat16* __restrict__ out, int64_t out_stride) {
   constexpr int kPer = DH / 32;
+  __shared__ float s_acc[8][DH];
+  __shared__ float s_sum[8];
+  pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t rows = static_cast<int64_t>(tokens) * H;
+  const int64_t row = (blockIdx.x * 8ll + warp) / warps;
+  const int sub = warp & (warps - 1);
+  const int token = static_cast<int>(row / H);
+  // rows of no entry keep what they hold
+  const bool live = row < rows && token >= __ldg(start) && token < __ldg(start + n);
   float acc[kPer] = {};
   float sum = 0.f;
-  for (int s0 = 0; s0 < splits; s0 += 32) {
-    float w = 0.f, l = 0.f;
-    if (s0 + lane < splits) {
-      const float2 ml = part_ml[(s0 + lane) * rows + row];
-      w = ml.x > -INFINITY ? exp2f(ml.x - top) : 0.f;
-      l = ml.y * w;
-    }
-    const int cnt = min(32, splits - s0);
+  if (live) {
+    float top = -INFINITY;
+    for (int s = lane; s < splits; s += 32) top = fmaxf(top, part_ml[s * rows + row].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
 #pragma unroll 4
-    for (int i = 0; i < cnt; ++i) {
-      const float wi = __shfl_sync(0xffffffffu, w, i);
-      sum += __shfl_sync(0xffffffffu, l, i);
-      if (wi == 0.f) continue;
-      const float* src = part_o + ((s0 + i) * rows + row) * DH + lane * kPer;
+    for (int s = sub; s < splits; s += warps) {
+      const float2 ml = part_ml[s * rows + row];   // one address for the warp
+      if (!(ml.x > -INFINITY)) continue;
+      const float w = exp2f(ml.x - top);
+      sum += ml.y * w;
+      const float* src = part_o + (s * rows + row) * DH + lane * kPer;
       if constexpr (kPer == 4) {
         const float4 v = *reinterpret_cast<const float4*>(src);
-        acc[0] += wi * v.x, acc[1] += wi * v.y, acc[2] += wi * v.z, acc[3] += wi * v.w;
+        acc[0] += w * v.x, acc[1] += w * v.y, acc[2] += w * v.z, acc[3] += w * v.w;
       } else {
         const float2 v = *reinterpret_cast<const float2*>(src);
-        acc[0] += wi * v.x, acc[1] += wi * v.y;
+        acc[0] += w * v.x, acc[1] += w * v.y;
       }
     }
   }
+  if (warps > 1) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) s_acc[warp][lane * kPer + i] = acc[i];
+    if (lane == 0) s_sum[warp] = sum;
+    __syncthreads();
+    if (sub == 0) {
+      for (int w = 1; w < warps; ++w) {
+        sum += s_sum[warp + w];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) acc[i] += s_acc[warp + w][lane * kPer + i];
+      }
+    }
+  }
+  if (!live || sub) return;
   const float inv = sum == 0.f ? 0.f : 1.0f / sum;
   __nv_bfloat16* dst = out + token * out_stride + (row % H) * DH + lane * kPer;
   if constexpr (kPer == 4)
@@ -1059,10 +1066,13 @@ extern "C" int fm_paged_attention(const fm_kv_cache* c, int layer, const fm_kv_b
     e = launch(kernel, grid, dim3(threads_of(f8)), pl.smem, o, p, tk, tv);
   }
   if (e == cudaSuccess && need) {
-    const int64_t blocks = (static_cast<int64_t>(b->tokens) * H + 7) / 8;
+    // a warp takes up to four splits where there are few rows (256 splits of 8 rows took 45 us with a warp a row)
+    int warps = 1;
+    while (warps < 8 && pl.splits > 4 * warps) warps *= 2;
+    const int64_t blocks = (static_cast<int64_t>(b->tokens) * H * warps + 7) / 8;
     auto join = c->Dh == 128 ? combine_kernel<128> : combine_kernel<64>;
     e = launch(join, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, o, static_cast<const float*>(p.part_o),
-               static_cast<const float2*>(p.part_ml), pl.splits, b->tokens, H, b->start, b->n, p.out, out_stride);
+               static_cast<const float2*>(p.part_ml), pl.splits, warps, b->tokens, H, b->start, b->n, p.out, out_stride);
   }
   return e == cudaSuccess ? FM_OK : record_error(FM_ERR_CUDA, cudaGetErrorString(e));
 }

@@ -1,22 +1,25 @@
 // Attention over a paged cache for up to 16 stacked rows (tokens x query heads of a KV head): single tokens.
 //
 // Bound by reading the cache. A CTA takes one entry, KV head and split of its keys: a warp moves tiles of 64 keys by
-// TMA into a three-stage ring, four warps take 16 keys each of every tile. Rows are the M of m16n8k16 tensor core
-// instructions, so that keys and values pass from shared memory straight into the fragments of one warp: the big
-// tensor cores would fill an eighth of their 128 rows and need E4M3 codes expanded in shared memory first (32 KB of
-// codes became 192 KB of traffic there: 1.5 us a 128-key tile and SM, against 0.7 us at which HBM delivers them).
-// Here codes are expanded in registers (exact, to f16). Every warp keeps its own running maximum, sum and O; the four
-// are joined in shared memory, the splits of a key axis by their cluster through distributed shared memory (up to 8
-// splits: no workspace, no second kernel), more through the workspace.
+// TMA into a three-stage ring, four warps take 16 keys each of every tile. Keys and head dims are the M = 16 of
+// m16n8k16 tensor core instructions and the stacked rows their N, eight or sixteen: S^T = K Q^T, O^T = V^T P^T. So keys
+// and values pass from shared memory straight into the fragments of one warp, and eight rows cost no padding (rows as
+// M = 16 took twice the instructions and registers for eight). The big tensor cores would fill a sixteenth of their
+// 128 rows and need E4M3 codes expanded in shared memory first: 32 KB of codes became 192 KB of traffic there, 1.2 us a
+// 128-key tile and SM against 0.7 us at which HBM delivers them. Here codes are expanded in registers (exact, to f16).
+// Every warp keeps its own running maximum, sum and O; the four are joined in shared memory, the splits of a key axis by
+// their cluster through distributed shared memory (up to 8 splits: no workspace, no second kernel), more through the
+// workspace.
 //
-// E4M3 fragments. A 16-byte row piece holds 16 codes. Keys (n) x head dims (k): a lane's word is four consecutive dims
+// E4M3 fragments. A 16-byte row piece holds 16 codes. Keys (M) x head dims (K): a lane's word is four consecutive dims
 // of one key, taken as k pairs (2t, 2t + 1) and (2t + 8, 2t + 9); the query's fragments use the same order of dims, so
-// the products meet. Values: the transposed load gives a lane [key, key + 1] x [dim, dim + 1], two byte permutations
-// make the pairs of keys of an even and of an odd dim: the two n tiles of a 16-dim piece are its even and its odd dims.
+// the products meet. Values: the transposed load gives a lane [key, key + 1] x [dim, dim + 1], a byte permutation makes
+// the pairs of keys of an even and of an odd dim: rows g and g + 8 of a 16-dim piece are its dims 2g and 2g + 1.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
-#include <cuda_fp8.h>
+
+#include <type_traits>
 
 #include "kv.h"
 #include "paged.cuh"
@@ -41,6 +44,12 @@ __device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
                : "r"(addr)
                : "memory");
 }
+// The 8 x 8 matrix of 16-bit elements that the warp holds, transposed.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
 template <bool kF16>
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   if constexpr (kF16)
@@ -52,12 +61,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// Two E4M3 codes (the low 16 bits) as f16 values.
-__device__ __forceinline__ uint32_t expand2(uint32_t codes) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(codes & 0xffffu), __NV_E4M3);
-  return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
-}
-
 // Byte offset of 16-byte piece c of row r in a tile of `row_bytes` rows (64: 64-byte swizzle, 128: 128-byte).
 template <int kRowBytes>
 __device__ __forceinline__ uint32_t piece(int r, int c) {
@@ -67,8 +70,9 @@ __device__ __forceinline__ uint32_t piece(int r, int c) {
     return static_cast<uint32_t>(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
 }
 
-template <int DH, bool F8>
-__global__ void __launch_bounds__(kThreads, 3)
+// NT: row tiles of eight.
+template <int DH, bool F8, int NT>
+__global__ void __launch_bounds__(kThreads, NT == 1 ? (F8 ? 4 : 2) : (F8 ? 3 : 2))
     decode_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
   constexpr int kRowBytes = F8 ? DH : 128;                 // bytes of a row in a block
   constexpr int kBlocks = F8 ? 1 : DH / 64;
@@ -90,7 +94,7 @@ __global__ void __launch_bounds__(kThreads, 3)
   pdl_trigger();
   pdl_wait();
   const Entry en = entry_of(p, blockIdx.z, tid == 0 && g == 0 && split == 0);
-  const int rows = min(min(en.nq, p.max_tokens) * p.G, kDecodeRows);
+  const int rows = min(min(en.nq, p.max_tokens) * p.G, 8 * NT);
   if (rows == 0) return;   // the same in the whole cluster
   const int past = en.len - en.nq;
   const int lo_all = first_key(p, past), hi_all = last_key(p, past + (rows - 1) / p.G, en.len);
@@ -101,12 +105,20 @@ __global__ void __launch_bounds__(kThreads, 3)
   const int nt = max(0, min(per, first + all - t_lo));
   __syncthreads();
 
-  const int q4 = lane & 3, r0 = lane >> 2;   // this lane's rows r0 and r0 + 8, its quarter of a row
-  float o[DH / 8][4];
+  // this lane's key (dim) g of eight, its quarter t of a row; its stacked rows are 8 x + 2 t and + 1
+  const int q4 = lane & 3, g8 = lane >> 2;
+  float o[NT][DH / 16][4];
 #pragma unroll
-  for (int i = 0; i < DH / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-  float m[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
-  float c_row[2] = {p.scale_log2, p.scale_log2};
+  for (int x = 0; x < NT; ++x)
+#pragma unroll
+    for (int i = 0; i < DH / 16; ++i) o[x][i][0] = o[x][i][1] = o[x][i][2] = o[x][i][3] = 0.f;
+  float m[2 * NT], sum[2 * NT], c_row[2 * NT];
+#pragma unroll
+  for (int u = 0; u < 2 * NT; ++u) {
+    m[u] = -INFINITY;
+    sum[u] = 0.f;
+    c_row[u] = p.scale_log2;
+  }
   bool ok = true;
   if (warp == kWarps) {
     // ================================================= page table and TMA
@@ -152,10 +164,10 @@ __global__ void __launch_bounds__(kThreads, 3)
     }
   } else {
     // ================================================= 16 keys of every tile
-    uint32_t qf[DH / 16][4];
+    uint32_t qf[NT][DH / 16][2];   // row 8 x + g
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {   // rows r0, r0 + 8
-      const int row = r0 + 8 * u;
+    for (int x = 0; x < NT; ++x) {
+      const int row = 8 * x + g8;
       const bool live = row < rows;
       const int tok = row / p.G, head = row - tok * p.G;
       const __nv_bfloat16* src = p.q + static_cast<int64_t>(en.begin + tok) * p.q_stride + (g * p.G + head) * DH;
@@ -163,11 +175,11 @@ __global__ void __launch_bounds__(kThreads, 3)
       for (int c = 0; c < DH / 16; ++c) {
         if constexpr (F8) {   // dims 16 c + 4 t .. + 3
           const uint2 v = live ? __ldg(reinterpret_cast<const uint2*>(src + c * 16 + q4 * 4)) : make_uint2(0, 0);
-          qf[c][u] = v.x;
-          qf[c][2 + u] = v.y;
+          qf[x][c][0] = v.x;
+          qf[x][c][1] = v.y;
         } else {
-          qf[c][u] = live ? __ldg(reinterpret_cast<const uint32_t*>(src + c * 16 + q4 * 2)) : 0u;
-          qf[c][2 + u] = live ? __ldg(reinterpret_cast<const uint32_t*>(src + c * 16 + q4 * 2 + 8)) : 0u;
+          qf[x][c][0] = live ? __ldg(reinterpret_cast<const uint32_t*>(src + c * 16 + q4 * 2)) : 0u;
+          qf[x][c][1] = live ? __ldg(reinterpret_cast<const uint32_t*>(src + c * 16 + q4 * 2 + 8)) : 0u;
         }
       }
       if constexpr (F8) {
@@ -176,35 +188,43 @@ __global__ void __launch_bounds__(kThreads, 3)
 #pragma unroll
         for (int c = 0; c < DH / 16; ++c)
 #pragma unroll
-          for (int x = 0; x < 2; ++x) top = max(top, max(qf[c][u + 2 * x] & 0x7fffu, (qf[c][u + 2 * x] >> 16) & 0x7fffu));
+          for (int y = 0; y < 2; ++y) top = max(top, max(qf[x][c][y] & 0x7fffu, (qf[x][c][y] >> 16) & 0x7fffu));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
         const int ex = static_cast<int>(top >> 7);
         const int sh = ex == 0 || ex == 255 ? 0 : min(max(141 - ex, -100), 100);
         const float up = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
-        c_row[u] *= __uint_as_float(static_cast<uint32_t>(127 - sh) << 23) * __ldg(p.k_scale);
+        const float down = __uint_as_float(static_cast<uint32_t>(127 - sh) << 23) * __ldg(p.k_scale);
+        // the scores' lanes own rows 2 t, 2 t + 1 of the eight
+#pragma unroll
+        for (int u = 0; u < 2; ++u) c_row[2 * x + u] *= __shfl_sync(0xffffffffu, down, (2 * q4 + u) * 4);
 #pragma unroll
         for (int c = 0; c < DH / 16; ++c)
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const uint32_t w = qf[c][u + 2 * x];
-            qf[c][u + 2 * x] = pack16<true>(__uint_as_float(w << 16) * up, __uint_as_float(w & 0xffff0000u) * up);
+          for (int y = 0; y < 2; ++y) {
+            const uint32_t w = qf[x][c][y];
+            qf[x][c][y] = pack16<true>(__uint_as_float(w << 16) * up, __uint_as_float(w & 0xffff0000u) * up);
           }
       }
     }
-    int my_lo[2], my_hi[2];
+    int my_lo[2 * NT], my_hi[2 * NT];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int row = r0 + 8 * u, pos = past + row / p.G;
+    for (int u = 0; u < 2 * NT; ++u) {
+      const int row = 8 * (u >> 1) + 2 * q4 + (u & 1), pos = past + row / p.G;
       my_lo[u] = row < rows ? first_key(p, pos) : 0;
       my_hi[u] = row < rows ? last_key(p, pos, en.len) : hi_all;
     }
     constexpr float kShift = F8 ? 6.0f : 0.0f;   // f16 probabilities are held 2^6 larger: subnormals begin lower
-    float off[2] = {kShift, kShift}, m_grow[2] = {-INFINITY, -INFINITY};
-    const float grow_by[2] = {kGrow / c_row[0], kGrow / c_row[1]};
+    float off[2 * NT], m_grow[2 * NT];
+#pragma unroll
+    for (int u = 0; u < 2 * NT; ++u) {
+      off[u] = kShift;
+      m_grow[u] = -INFINITY;
+    }
     // this lane's row of the matrices that ldmatrix moves: keys, and values transposed
-    const int k_row = warp * 16 + (lane >> 4) * 8 + (lane & 7), k_sub = (lane >> 3) & 1;
-    const int v_row = warp * 16 + ((lane >> 3) & 1) * 8 + (lane & 7), v_sub = lane >> 4;
+    const int k_row = warp * 16 + ((lane >> 3) & 1) * 8 + (lane & 7), k_sub = lane >> 4;
+    const int v_row = warp * 16 + (lane >> 4) * 8 + (lane & 7), v_sub = (lane >> 3) & 1;
+    const int f_row = warp * 16 + ((lane >> 3) & 1) * 8 + (lane & 7), f_sub = lane >> 4;   // E4M3 values
     Ring at;
     for (int j = 0; j < nt; ++j) {
       ok = wait_for(&full[at.b], at.phase);
@@ -212,100 +232,117 @@ __global__ void __launch_bounds__(kThreads, 3)
       const uint32_t kt = smem_u32(smem) + at.b * 2 * kTile, vt = kt + kTile;
       const int k0 = (t_lo + j) * kDecodeKeys + warp * 16;
       if (k0 < hi_all && k0 + 16 > lo_all) {
-        float s[2][4] = {};
+        float s[NT][4] = {};
         if constexpr (F8) {
 #pragma unroll
           for (int c = 0; c < DH / 32; ++c) {
-            uint32_t r[4];   // keys 0-7 and 8-15 (r[0..1], r[2..3]) of two 16-dim pieces
+            uint32_t r[4];   // keys 0-7 and 8-15 of piece 2c, the same of piece 2c + 1
             ldsm4(r, kt + piece<kRowBytes>(k_row, 2 * c + k_sub));
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              mma16816<true>(s[0], qf[2 * c + x], expand2(r[x]), expand2(r[x] >> 16));
-              mma16816<true>(s[1], qf[2 * c + x], expand2(r[2 + x]), expand2(r[2 + x] >> 16));
+            for (int y = 0; y < 2; ++y) {
+              uint32_t a[4];
+              expand4(r[2 * y], a[0], a[2]);
+              expand4(r[2 * y + 1], a[1], a[3]);
+#pragma unroll
+              for (int x = 0; x < NT; ++x) mma16816<true>(s[x], a, qf[x][2 * c + y][0], qf[x][2 * c + y][1]);
             }
           }
         } else {
 #pragma unroll
           for (int c = 0; c < DH / 16; ++c) {
-            uint32_t r[4];
-            ldsm4(r, kt + (c >> 2) * kBlock + piece<128>(k_row, 2 * (c & 3) + k_sub));
-            mma16816<false>(s[0], qf[c], r[0], r[1]);
-            mma16816<false>(s[1], qf[c], r[2], r[3]);
+            uint32_t a[4];
+            ldsm4(a, kt + (c >> 2) * kBlock + piece<128>(k_row, 2 * (c & 3) + k_sub));
+#pragma unroll
+            for (int x = 0; x < NT; ++x) mma16816<false>(s[x], a, qf[x][c][0], qf[x][c][1]);
           }
         }
-        // s[x][0..1]: row r0, keys 8 x + 2 t, + 1; s[x][2..3]: row r0 + 8
-        const bool edge = k0 + 16 > my_hi[0] || k0 + 16 > my_hi[1] || k0 < my_lo[0] || k0 < my_lo[1];
+        // s[x][0..1]: key g, rows 2 t, 2 t + 1 of tile x; s[x][2..3]: key g + 8
+        bool edge = false, grow = false;
+#pragma unroll
+        for (int u = 0; u < 2 * NT; ++u) edge |= k0 + 16 > my_hi[u] || k0 < my_lo[u];
         if (__any_sync(0xffffffffu, edge)) {
 #pragma unroll
-          for (int x = 0; x < 2; ++x)
+          for (int u = 0; u < 2 * NT; ++u)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int key = k0 + 8 * x + 2 * q4 + (e & 1);
-              s[x][e] = key >= my_lo[e >> 1] && key < my_hi[e >> 1] ? s[x][e] : -INFINITY;
+            for (int y = 0; y < 2; ++y) {
+              const int key = k0 + 8 * y + g8;
+              float& v = s[u >> 1][2 * y + (u & 1)];
+              v = key >= my_lo[u] && key < my_hi[u] ? v : -INFINITY;
             }
         }
-        float top[2];
-        bool grow = false;
+        float top[2 * NT];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          top[u] = fmaxf(fmaxf(s[0][2 * u], s[0][2 * u + 1]), fmaxf(s[1][2 * u], s[1][2 * u + 1]));
-          top[u] = fmaxf(top[u], __shfl_xor_sync(0xffffffffu, top[u], 1));
-          top[u] = fmaxf(top[u], __shfl_xor_sync(0xffffffffu, top[u], 2));
+        for (int u = 0; u < 2 * NT; ++u) {
+          top[u] = fmaxf(s[u >> 1][u & 1], s[u >> 1][2 + (u & 1)]);
           grow |= top[u] > m_grow[u];
         }
+        // the maximum over the keys is needed only where one of them moves it
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
+          for (int u = 0; u < 2 * NT; ++u) {
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) top[u] = fmaxf(top[u], __shfl_xor_sync(0xffffffffu, top[u], d));
             if (!(top[u] > m_grow[u])) continue;
             const float f = ex2_approx((m[u] - top[u]) * c_row[u]);   // 0 for a row's first keys
             m[u] = top[u];
-            m_grow[u] = top[u] + grow_by[u];
+            m_grow[u] = top[u] + kGrow / c_row[u];
             off[u] = kShift - m[u] * c_row[u];
             sum[u] *= f;
 #pragma unroll
-            for (int i = 0; i < DH / 8; ++i) {
-              o[i][2 * u] *= f;
-              o[i][2 * u + 1] *= f;
+            for (int i = 0; i < DH / 16; ++i) {
+              o[u >> 1][i][u & 1] *= f;
+              o[u >> 1][i][2 + (u & 1)] *= f;
             }
           }
         }
+        uint32_t pf[NT][2];   // keys 2 t, 2 t + 1 (and + 8) of row g
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
+        for (int x = 0; x < NT; ++x) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            s[x][e] = ex2_approx(fmaf(s[x][e], c_row[e >> 1], off[e >> 1]));
-            sum[e >> 1] += s[x][e];
+            const int u = 2 * x + (e & 1);
+            s[x][e] = ex2_approx(fmaf(s[x][e], c_row[u], off[u]));
+            sum[u] += s[x][e];
           }
-        const uint32_t pf[4] = {pack16<F8>(s[0][0], s[0][1]), pack16<F8>(s[0][2], s[0][3]), pack16<F8>(s[1][0], s[1][1]),
-                                pack16<F8>(s[1][2], s[1][3])};
+          pf[x][0] = transpose8x8(pack16<F8>(s[x][0], s[x][1]));
+          pf[x][1] = transpose8x8(pack16<F8>(s[x][2], s[x][3]));
+        }
         // values behind the length may be anything, and 0 * NaN is NaN: masks of the pairs of keys (2t, 2t + 1) and + 8
-        const int in = en.len - k0 - 2 * q4;   // keys of the length from this lane's first one on
-        if constexpr (F8) {
+        auto products = [&](auto tail) {
+          constexpr bool kTail = decltype(tail)::value;
+          const int in = en.len - k0 - 2 * q4;   // keys of the length from this lane's first one on
           const uint32_t k0m = in >= 2 ? 0xffffffffu : in == 1 ? 0x0000ffffu : 0u;
           const uint32_t k8m = in >= 10 ? 0xffffffffu : in == 9 ? 0x0000ffffu : 0u;
+          if constexpr (F8) {
 #pragma unroll
-          for (int c = 0; c < DH / 32; ++c) {
-            uint32_t r[4];   // keys 0-7, 8-15 of piece 2c, the same of piece 2c + 1
-            ldsm4_t(r, vt + piece<kRowBytes>(v_row, 2 * c + v_sub));
+            for (int c = 0; c < DH / 32; ++c) {
+              uint32_t r[4];   // keys 0-7, 8-15 of piece 2c, the same of piece 2c + 1
+              ldsm4_t(r, vt + piece<kRowBytes>(f_row, 2 * c + f_sub));
+              if constexpr (kTail) r[0] &= k0m, r[1] &= k8m, r[2] &= k0m, r[3] &= k8m;
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const uint32_t a = r[2 * x] & k0m, b = r[2 * x + 1] & k8m;
-              const int i = (2 * c + x) * 2;
-              mma16816<true>(o[i], pf, expand2(__byte_perm(a, 0, 0x4420)), expand2(__byte_perm(b, 0, 0x4420)));
-              mma16816<true>(o[i + 1], pf, expand2(__byte_perm(a, 0, 0x4431)), expand2(__byte_perm(b, 0, 0x4431)));
+              for (int y = 0; y < 2; ++y) {
+                uint32_t a[4];   // dims 2 g and 2 g + 1, keys (2t, 2t + 1) and + 8
+                expand4(__byte_perm(r[2 * y], 0, 0x3120), a[0], a[1]);
+                expand4(__byte_perm(r[2 * y + 1], 0, 0x3120), a[2], a[3]);
+#pragma unroll
+                for (int x = 0; x < NT; ++x) mma16816<true>(o[x][2 * c + y], a, pf[x][0], pf[x][1]);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < DH / 16; ++c) {
+              uint32_t a[4];   // keys 0-7 of pieces 2c, 2c + 1, keys 8-15 of them
+              ldsm4_t(a, vt + (c >> 2) * kBlock + piece<128>(v_row, 2 * (c & 3) + v_sub));
+              if constexpr (kTail) a[0] &= k0m, a[1] &= k0m, a[2] &= k8m, a[3] &= k8m;
+#pragma unroll
+              for (int x = 0; x < NT; ++x) mma16816<false>(o[x][c], a, pf[x][0], pf[x][1]);
             }
           }
-        } else {
-          const uint32_t k0m = in >= 2 ? 0xffffffffu : in == 1 ? 0x0000ffffu : 0u;
-          const uint32_t k8m = in >= 10 ? 0xffffffffu : in == 9 ? 0x0000ffffu : 0u;
-#pragma unroll
-          for (int c = 0; c < DH / 16; ++c) {
-            uint32_t r[4];
-            ldsm4_t(r, vt + (c >> 2) * kBlock + piece<128>(v_row, 2 * (c & 3) + v_sub));
-            mma16816<false>(o[2 * c], pf, r[0] & k0m, r[1] & k8m);
-            mma16816<false>(o[2 * c + 1], pf, r[2] & k0m, r[3] & k8m);
-          }
-        }
+        };
+        if (k0 + 16 > en.len)
+          products(std::true_type{});
+        else
+          products(std::false_type{});
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[at.b]);
@@ -315,27 +352,26 @@ __global__ void __launch_bounds__(kThreads, 3)
   }
   __syncthreads();   // every tile has been used: the ring holds the warps' sums now
 
-  // ---- join the four warps: [warp][row][DH] sums, then the CTA's [row][DH]
+  // ---- join the four warps: [warp][row] sums, then the CTA's [row][DH]. Rows lie 8 floats apart in the banks.
+  constexpr int kPitch = DH + 8;
   float* sums = reinterpret_cast<float*>(smem);
-  float* cta = sums + kWarps * kDecodeRows * DH;
+  float* cta = sums + kWarps * 8 * NT * kPitch;
   if (warp < kWarps) {
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
+    for (int u = 0; u < 2 * NT; ++u) {
       float l = sum[u];
-      l += __shfl_xor_sync(0xffffffffu, l, 1);
-      l += __shfl_xor_sync(0xffffffffu, l, 2);
-      const int row = r0 + 8 * u;
-      if (q4 == 0) s_ml[warp][row] = make_float2(m[u] > -INFINITY ? m[u] * c_row[u] : -INFINITY, l);
-      float* dst = sums + (warp * kDecodeRows + row) * DH;
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+      const int row = 8 * (u >> 1) + 2 * q4 + (u & 1);
+      if (g8 == 0) s_ml[warp][row] = make_float2(m[u] > -INFINITY ? m[u] * c_row[u] : -INFINITY, l);
+      float* dst = sums + (warp * 8 * NT + row) * kPitch;
 #pragma unroll
       for (int c = 0; c < DH / 16; ++c) {
-        // E4M3: tiles 2c, 2c + 1 are the even and odd dims of a piece: a lane's four are consecutive
         if constexpr (F8) {
-          *reinterpret_cast<float4*>(dst + c * 16 + q4 * 4) =
-              make_float4(o[2 * c][2 * u], o[2 * c + 1][2 * u], o[2 * c][2 * u + 1], o[2 * c + 1][2 * u + 1]);
+          *reinterpret_cast<float2*>(dst + c * 16 + 2 * g8) = make_float2(o[u >> 1][c][u & 1], o[u >> 1][c][2 + (u & 1)]);
         } else {
-          *reinterpret_cast<float2*>(dst + c * 16 + q4 * 2) = make_float2(o[2 * c][2 * u], o[2 * c][2 * u + 1]);
-          *reinterpret_cast<float2*>(dst + c * 16 + 8 + q4 * 2) = make_float2(o[2 * c + 1][2 * u], o[2 * c + 1][2 * u + 1]);
+          dst[c * 16 + g8] = o[u >> 1][c][u & 1];
+          dst[c * 16 + 8 + g8] = o[u >> 1][c][2 + (u & 1)];
         }
       }
     }
@@ -355,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 3)
     for (int w = 0; w < kWarps; ++w) {
       const float2 ml = s_ml[w][row];
       const float f = ml.x > -INFINITY ? ex2_approx(ml.x - top) : 0.f;
-      const float4 v = *reinterpret_cast<const float4*>(sums + (w * kDecodeRows + row) * DH + d);
+      const float4 v = *reinterpret_cast<const float4*>(sums + (w * 8 * NT + row) * kPitch + d);
       l += ml.y * f;
       acc.x += v.x * f, acc.y += v.y * f, acc.z += v.z * f, acc.w += v.w * f;
     }
@@ -413,31 +449,42 @@ __global__ void __launch_bounds__(kThreads, 3)
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-template <int DH, bool F8>
+template <int DH, bool F8, int NT>
 constexpr size_t smem_bytes() {
   const size_t ring = static_cast<size_t>(kStages) * 2 * kDecodeKeys * DH * (F8 ? 1 : 2);
-  const size_t join = static_cast<size_t>(kWarps + 1) * kDecodeRows * DH * 4;
+  const size_t join = static_cast<size_t>(8 * NT) * (kWarps * (DH + 8) + DH) * 4;
   return 1024 + (ring > join ? ring : join);
 }
 
-template <int DH, bool F8>
+template <int DH, bool F8, int NT>
 cudaError_t configure_one() {
-  return cudaFuncSetAttribute(decode_kernel<DH, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              static_cast<int>(smem_bytes<DH, F8>()));
+  return cudaFuncSetAttribute(decode_kernel<DH, F8, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              static_cast<int>(smem_bytes<DH, F8, NT>()));
+}
+
+template <int DH, bool F8, int NT>
+cudaError_t run(const AttnParams& p, const CUtensorMap& tk, const CUtensorMap& tv, const LaunchOpts& o) {
+  return launch(decode_kernel<DH, F8, NT>, dim3(p.splits, p.Hkv, p.n), dim3(kThreads), smem_bytes<DH, F8, NT>(), o, p, tk, tv);
 }
 
 template <int DH, bool F8>
-cudaError_t run(const AttnParams& p, const CUtensorMap& tk, const CUtensorMap& tv, const LaunchOpts& o) {
-  return launch(decode_kernel<DH, F8>, dim3(p.splits, p.Hkv, p.n), dim3(kThreads), smem_bytes<DH, F8>(), o, p, tk, tv);
+cudaError_t run_rows(const AttnParams& p, const CUtensorMap& tk, const CUtensorMap& tv, const LaunchOpts& o) {
+  return p.max_tokens * p.G <= 8 ? run<DH, F8, 1>(p, tk, tv, o) : run<DH, F8, 2>(p, tk, tv, o);
+}
+
+template <int DH, bool F8>
+cudaError_t configure_rows() {
+  const cudaError_t e = configure_one<DH, F8, 1>();
+  return e == cudaSuccess ? configure_one<DH, F8, 2>() : e;
 }
 
 }  // namespace
 
 cudaError_t decode_configure() {
-  cudaError_t e = configure_one<64, false>();
-  if (e == cudaSuccess) e = configure_one<128, false>();
-  if (e == cudaSuccess) e = configure_one<64, true>();
-  if (e == cudaSuccess) e = configure_one<128, true>();
+  cudaError_t e = configure_rows<64, false>();
+  if (e == cudaSuccess) e = configure_rows<128, false>();
+  if (e == cudaSuccess) e = configure_rows<64, true>();
+  if (e == cudaSuccess) e = configure_rows<128, true>();
   return e;
 }
 
@@ -445,8 +492,8 @@ cudaError_t decode_launch(const AttnParams& p, int Dh, bool f8, const CUtensorMa
                           const LaunchOpts& opts) {
   LaunchOpts o = opts;
   if (p.splits > 1 && !p.part_o) o.cluster = dim3(p.splits, 1, 1);
-  if (Dh == 128) return f8 ? run<128, true>(p, tk, tv, o) : run<128, false>(p, tk, tv, o);
-  return f8 ? run<64, true>(p, tk, tv, o) : run<64, false>(p, tk, tv, o);
+  if (Dh == 128) return f8 ? run_rows<128, true>(p, tk, tv, o) : run_rows<128, false>(p, tk, tv, o);
+  return f8 ? run_rows<64, true>(p, tk, tv, o) : run_rows<64, false>(p, tk, tv, o);
 }
 
 }  // namespace fm
