@@ -39,6 +39,7 @@ constexpr int kDecodeKeys = 64;   // keys of a tile
 cudaError_t decode_launch(const AttnParams& p, int Dh, bool f8, const CUtensorMap& tk, const CUtensorMap& tv,
                           const LaunchOpts& o);
 cudaError_t decode_configure();
+int decode_resident(int Dh, bool f8, int rows);   // CTAs of it on an SM at once
 
 // An entry of the batch; one that is out of range has no tokens and no keys.
 struct Entry {

@@ -880,13 +880,16 @@ int splits_of(const fm_kv_cache& c, const fm_kv_batch& b, int H, int window) {
   int64_t keys = std::max(1, b.max_len);
   if (window > 0) keys = std::min<int64_t>(keys, static_cast<int64_t>(window) + b.max_tokens);
   if (rows <= kDecodeRows) {
-    // splits of at least two tiles until about four CTAs an SM are under way (their rings keep HBM busy; more only
-    // cost their start). Up to 8 are a cluster and need no workspace.
+    // As many CTAs as are resident at once: a second wave costs more than longer splits (64 units of 4096 keys: 25 us
+    // in 256 CTAs, 31 us in 384). Splits of at least two tiles up to 8, which join in their cluster; beyond, where a
+    // second kernel joins them, of at least four (32768 keys of one unit: 11.6 us in 64 splits, 20.7 us in 256), and
+    // only where 8 would be long (4096 keys of one unit: 8.3 us in 8, 7.7 us in 24; 2000: 7.4 us in 8, 7.5 us in 16).
     const int64_t units = static_cast<int64_t>(c.Hkv) * std::max(1, b.n);
     const int64_t tiles = (keys + kDecodeKeys - 1) / kDecodeKeys + (window > 0);
-    const int64_t want = std::max<int64_t>(1, std::min<int64_t>((4 * sms) / units, (tiles + 1) / 2));
-    if (want > 8 && want < 24) return 8;   // a second kernel pays for three times the CTAs
-    return static_cast<int>(std::min<int64_t>(want, 256));
+    const int64_t slots = std::max<int64_t>(1, static_cast<int64_t>(sms) * decode_resident(c.Dh, f8, static_cast<int>(rows)) / units);
+    const int64_t want = tiles > 40 ? std::min<int64_t>(std::min<int64_t>(slots, 64), (tiles + 3) / 4)
+                                    : std::min<int64_t>(std::min<int64_t>(slots, 8), (tiles + 1) / 2);
+    return static_cast<int>(std::max<int64_t>(1, want));
   }
   // One CTA an SM: waves x (start and end + tiles x time of a tile), in units of 0.1 us as measured, with the join of
   // splits (a kernel, and every share written and read) added. The number of splits with the least of it.

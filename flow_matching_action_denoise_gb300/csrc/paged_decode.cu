@@ -29,7 +29,12 @@ namespace fm {
 
 namespace {
 
-constexpr int kWarps = 4, kStages = 3;
+constexpr int kWarps = 4;
+constexpr int kDepth = 3;   // stages of the ring
+// CTAs an SM of a variant, by shared memory (16-bit tiles of 128 dims are 32 KB; two stages and three CTAs were slower:
+// 28 us against 25 us for 32 sequences of 4096 keys) and registers.
+template <int DH, bool F8, int NT>
+constexpr int kResident = NT == 1 ? (F8 || DH == 64 ? 4 : 2) : (F8 || DH == 64 ? 3 : 2);
 constexpr int kThreads = (kWarps + 1) * 32;
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
@@ -72,7 +77,7 @@ __device__ __forceinline__ uint32_t piece(int r, int c) {
 
 // NT: row tiles of eight.
 template <int DH, bool F8, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? (F8 ? 4 : 2) : (F8 ? 3 : 2))
+__global__ void __launch_bounds__(kThreads, kResident<DH, F8, NT>)
     decode_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
   constexpr int kRowBytes = F8 ? DH : 128;                 // bytes of a row in a block
   constexpr int kBlocks = F8 ? 1 : DH / 64;
@@ -80,12 +85,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? (F8 ? 4 : 2) : (F8 ? 3 : 2
   constexpr uint32_t kTile = kBlock * kBlocks;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ uint64_t full[kStages], empty[kStages];
+  __shared__ uint64_t full[kDepth], empty[kDepth];
   __shared__ float2 s_ml[kWarps + 1][kDecodeRows];         // (log2 maximum, sum) of each warp, and of the CTA
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int split = blockIdx.x, g = blockIdx.y;
   if (tid == 0) {
-    for (int i = 0; i < kStages; ++i) {
+    for (int i = 0; i < kDepth; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], kWarps);
     }
@@ -139,7 +144,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? (F8 ? 4 : 2) : (F8 ? 3 : 2
     for (; j < nt; ++j) {
       const int here = after;
       after = page_of(j + 1);
-      if (j >= kStages) ok = wait_for(&empty[at.b], at.phase ^ 1);
+      if (j >= kDepth) ok = wait_for(&empty[at.b], at.phase ^ 1);
       if (!ok) break;
       if (lane == 0) mbar_arrive_expect_tx(&full[at.b], 2 * kTile);
       __syncwarp();
@@ -156,11 +161,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? (F8 ? 4 : 2) : (F8 ? 3 : 2
         }
         __syncwarp();
       }
-      at.next(kStages);
+      at.next(kDepth);
     }
     if (!ok) {   // the copies in flight land before the CTA leaves
       if (lane == 0) atomicOr(p.err, kErrPipelineTimeout);
-      for (int x = max(0, j - kStages); x < j; ++x) wait_for(&full[x % kStages], (x / kStages) & 1);
+      for (int x = max(0, j - kDepth); x < j; ++x) wait_for(&full[x % kDepth], (x / kDepth) & 1);
     }
   } else {
     // ================================================= 16 keys of every tile
@@ -346,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? (F8 ? 4 : 2) : (F8 ? 3 : 2
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[at.b]);
-      at.next(kStages);
+      at.next(kDepth);
     }
     if (!ok && lane == 0) atomicOr(p.err, kErrPipelineTimeout);
   }
@@ -451,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? (F8 ? 4 : 2) : (F8 ? 3 : 2
 
 template <int DH, bool F8, int NT>
 constexpr size_t smem_bytes() {
-  const size_t ring = static_cast<size_t>(kStages) * 2 * kDecodeKeys * DH * (F8 ? 1 : 2);
+  const size_t ring = static_cast<size_t>(kDepth) * 2 * kDecodeKeys * DH * (F8 ? 1 : 2);
   const size_t join = static_cast<size_t>(8 * NT) * (kWarps * (DH + 8) + DH) * 4;
   return 1024 + (ring > join ? ring : join);
 }
@@ -486,6 +491,13 @@ cudaError_t decode_configure() {
   if (e == cudaSuccess) e = configure_rows<64, true>();
   if (e == cudaSuccess) e = configure_rows<128, true>();
   return e;
+}
+
+int decode_resident(int Dh, bool f8, int rows) {
+  if (Dh == 128) return rows <= 8 ? (f8 ? kResident<128, true, 1> : kResident<128, false, 1>)
+                                  : (f8 ? kResident<128, true, 2> : kResident<128, false, 2>);
+  return rows <= 8 ? (f8 ? kResident<64, true, 1> : kResident<64, false, 1>)
+                   : (f8 ? kResident<64, true, 2> : kResident<64, false, 2>);
 }
 
 cudaError_t decode_launch(const AttnParams& p, int Dh, bool f8, const CUtensorMap& tk, const CUtensorMap& tv,
