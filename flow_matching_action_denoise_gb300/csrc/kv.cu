@@ -34,12 +34,15 @@ struct Book {
   int seqs, table_stride, pages, page, shift;
 };
 
-// Device view of the pools, in 16-byte units.
+// Device view of the pools, in 16-byte units. The rows (token, head) of a page are taken as runs that are contiguous in
+// memory: one run of all rows where heads lie inside of tokens without gaps, a run of the tokens of each head where
+// tokens lie inside of heads, else a run a row.
+enum Runs { kRunAll, kRunHead, kRunRow };
 struct Pool {
   uint4 *k, *v;
   int64_t layer, pg, tok, head;   // strides
   int layers, Hkv, chunks;        // chunks: 16-byte units of a row
-  int heads_inner;                // heads vary faster than tokens in memory
+  Runs runs;
 };
 
 __host__ __device__ constexpr int up(int a, int b) { return (a + b - 1) / b; }
@@ -198,11 +201,14 @@ __global__ void __launch_bounds__(kBookThreads) reserve_kernel(Book b, const int
   }
 }
 
-// Copies `rows` tokens of page src to page dst of one layer, K and V, 16 bytes a thread; four loads in flight.
+// Copies `rows` tokens of page src to page dst of one layer, K and V, 16 bytes a thread, four loads in flight.
 __device__ __forceinline__ void copy_rows(const Pool& p, int layer, int src, int dst, int rows) {
-  const int per_row = p.Hkv * p.chunks;
-  const int total = rows * per_row;
   const int64_t base = layer * p.layer;
+  const uint4 *ks = p.k + base + src * p.pg, *vs = p.v + base + src * p.pg;
+  uint4 *kd = p.k + base + dst * p.pg, *vd = p.v + base + dst * p.pg;
+  const int len = p.runs == kRunAll ? rows * p.Hkv * p.chunks : p.runs == kRunHead ? rows * p.chunks : p.chunks;
+  const int runs = p.runs == kRunAll ? 1 : p.runs == kRunHead ? p.Hkv : rows * p.Hkv;
+  const int total = len * runs;
   for (int x0 = threadIdx.x; x0 < total; x0 += blockDim.x * 2) {
     uint4 a[2], d[2];
     int64_t at[2];
@@ -210,17 +216,19 @@ __device__ __forceinline__ void copy_rows(const Pool& p, int layer, int src, int
     for (int u = 0; u < 2; ++u) {
       const int x = x0 + u * blockDim.x;
       if (x >= total) continue;
-      const int c = x % p.chunks, y = x / p.chunks;
-      const int tok = p.heads_inner ? y / p.Hkv : y % rows, head = p.heads_inner ? y % p.Hkv : y / rows;
-      at[u] = base + tok * p.tok + head * p.head + c;
-      a[u] = p.k[at[u] + src * p.pg];
-      d[u] = p.v[at[u] + src * p.pg];
+      at[u] = x;
+      if (runs > 1) {
+        const int y = x / len, c = x - y * len;
+        at[u] = p.runs == kRunHead ? y * p.head + c : (y / p.Hkv) * p.tok + (y % p.Hkv) * p.head + c;
+      }
+      a[u] = __ldcs(ks + at[u]);
+      d[u] = __ldcs(vs + at[u]);
     }
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       if (x0 + u * blockDim.x >= total) continue;
-      p.k[at[u] + dst * p.pg] = a[u];
-      p.v[at[u] + dst * p.pg] = d[u];
+      kd[at[u]] = a[u];
+      vd[at[u]] = d[u];
     }
   }
 }
@@ -375,7 +383,7 @@ struct AppendParams {
   int rot, interleaved;
   int tokens, max_tokens, seqs, table_stride, pages, page, shift;
   int H, Hkv, Dh;
-  int groups, per;          // head groups of a token, heads of a group
+  int toks, groups;         // tokens of a CTA, threads that share the heads of a token
   void *kc, *vc;            // this layer
   int64_t pg, tok, head;    // strides in elements
   const float *k_scale, *v_scale;
@@ -407,114 +415,134 @@ __device__ __forceinline__ uint2 codes8(const float* f, float rs) {
   return make_uint2(w[0], w[1]);
 }
 
-// One thread: 16 elements (two 8-element chunks that hold whole pairs) of `per` heads of one token; the angles are
-// computed once for all of them. An angle is a fraction of a turn in 64-bit fixed point: position * freq modulo 2^64
-// drops whole turns exactly, at any position, without double precision. grid.y is the entry of the batch.
+// One CTA: `toks` tokens of an entry (grid.y), all heads. The angles of a token are computed once, a thread each, into
+// shared memory: computed by every thread for its own pairs they were a third of the kernel's instructions. An angle is
+// a fraction of a turn in 64-bit fixed point: position * freq modulo 2^64 drops whole turns exactly, at any position,
+// without double precision. One thread: 16 elements (two 8-element chunks that hold whole pairs) of every groups-th
+// head. Bound by HBM: q, k and v are read once and written once.
 template <bool F8>
 __global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
+  extern __shared__ float2 s_angle[];   // [toks][rot / 2] (cos, sin) times magnitude
   pdl_trigger();
-  const int units = p.Dh / 16;
-  const int64_t x = blockIdx.x * 256ll + threadIdx.x;
-  const int unit = static_cast<int>(x % units);
-  const int64_t y = x / units;
-  const int grp = static_cast<int>(y % p.groups);
-  const int64_t within = y / p.groups;
+  const int units = p.Dh / 16, pairs = p.rot / 2;
+  const int unit = threadIdx.x % units, tok = (threadIdx.x / units) % p.toks, grp = threadIdx.x / (units * p.toks);
   const int entry = blockIdx.y;
-  // chunks of this unit (in 8 elements): a rotated pair of chunks, or two that pass through
-  const int rot_units = p.rot / 16;
-  const bool turned = unit < rot_units;
-  const int c0 = turned && !p.interleaved ? unit : 2 * unit, c1 = turned && !p.interleaved ? unit + rot_units : 2 * unit + 1;
   pdl_wait();
-  uint64_t f[8];
-  if (turned) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = __ldg(p.freq + unit * 8 + i);
-  }
   const int begin = __ldg(p.start + entry), nq = __ldg(p.start + entry + 1) - begin;
   const int sid = p.seq ? __ldg(p.seq + entry) : entry;
-  bool bad = begin < 0 || nq < 0 || begin > p.tokens || nq > p.tokens - begin || sid < 0 || sid >= p.seqs;
+  const bool bad = begin < 0 || nq < 0 || begin > p.tokens || nq > p.tokens - begin || sid < 0 || sid >= p.seqs;
   const int len = bad ? 0 : __ldg(p.lens + sid);
   const bool over = bad || nq > p.max_tokens || len < nq || len > p.table_stride * static_cast<int64_t>(p.page);
-  if (over && x == 0) atomicOr(p.err, kErrBadBatch);
-  if (bad || within >= nq) return;
-  const int64_t token = begin + within;
-  const int64_t pos = static_cast<int64_t>(len) - nq + within;   // place in the sequence
+  if (over && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.err, kErrBadBatch);
+  const int first = blockIdx.x * p.toks;
+  if (bad || first >= nq) return;   // the same for the whole CTA
+  const int past = len - nq;
+  for (int x = threadIdx.x; x < p.toks * pairs; x += 256) {
+    const int i = x % pairs, w = first + x / pairs;
+    if (w >= nq) break;
+    const int64_t at = p.positions ? __ldg(p.positions + begin + w) : past + w;
+    // the fraction of a turn as a signed 32-bit number: half turns in [-1, 1) for sincospif
+    const uint64_t turn = __ldg(p.freq + i) * static_cast<uint64_t>(at) + (1ull << 31);
+    float2 a;
+    sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f, &a.y, &a.x);
+    s_angle[x] = make_float2(a.x * p.mag, a.y * p.mag);
+  }
+  const int within = first + tok;
+  const bool mine = grp < p.groups && within < nq;
+  const int64_t token = begin + static_cast<int64_t>(within);
+  const int64_t pos = static_cast<int64_t>(past) + within;   // place in the sequence
   int page = -1;
-  if (pos >= 0 && (pos >> p.shift) < p.table_stride)
+  if (mine && pos >= 0 && (pos >> p.shift) < p.table_stride)
     page = __ldg(p.table + static_cast<int64_t>(sid) * p.table_stride + (pos >> p.shift));
   if (page >= p.pages) page = -1;
-  if (page < 0 && unit == 0 && grp == 0) atomicOr(p.err, kErrBadBatch);
-  const int h0 = grp * p.per, h1 = min(h0 + p.per, p.H + 2 * p.Hkv);
-  float cs[8], sn[8];
-  if (turned && h0 < p.H + p.Hkv) {
-    const int64_t at = p.positions ? __ldg(p.positions + token) : pos;
+  if (mine && page < 0 && unit == 0 && grp == 0) atomicOr(p.err, kErrBadBatch);
+  __syncthreads();
+  if (!mine) return;
+  // chunks of this unit (in 8 elements): a rotated pair of chunks, or two that pass through
+  const int rot_units = p.rot / 16;
+  const bool turned = unit < rot_units, split = turned && !p.interleaved;
+  const int c0 = (split ? unit : 2 * unit) * 8, c1 = (split ? unit + rot_units : 2 * unit + 1) * 8;
+  float2 ang[8];
+  if (turned) {
+    const float4* src = reinterpret_cast<const float4*>(s_angle + tok * pairs + unit * 8);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      // the fraction of a turn as a signed 32-bit number: half turns in [-1, 1) for sincospif
-      const uint64_t turn = f[i] * static_cast<uint64_t>(at) + (1ull << 31);
-      sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f, &sn[i], &cs[i]);
-      cs[i] *= p.mag;
-      sn[i] *= p.mag;
+    for (int i = 0; i < 4; ++i) {
+      const float4 v = src[i];
+      ang[2 * i] = make_float2(v.x, v.y);
+      ang[2 * i + 1] = make_float2(v.z, v.w);
     }
   }
-  const float rk = F8 ? 1.0f / __ldg(p.k_scale) : 1.0f, rv = F8 ? 1.0f / __ldg(p.v_scale) : 1.0f;
-  const int64_t cell = static_cast<int64_t>(page) * p.pg + (pos & (p.page - 1)) * p.tok;
-  for (int h = h0; h < h1; h += 2) {
-    uint4 in[2][2];
+  auto turn = [&](float* a, float* b) {
+    if (!turned) return;
+    if (p.interleaved) {
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {   // two heads' loads in flight
-      const int hh = h + u;
-      if (hh >= h1) continue;
-      const __nv_bfloat16* src = hh < p.H           ? p.q + token * p.qs + static_cast<int64_t>(hh) * p.Dh
-                                 : hh < p.H + p.Hkv ? p.k + token * p.ks + static_cast<int64_t>(hh - p.H) * p.Dh
-                                                    : p.v + token * p.vs + static_cast<int64_t>(hh - p.H - p.Hkv) * p.Dh;
-      in[u][0] = reinterpret_cast<const uint4*>(src)[c0];
-      in[u][1] = reinterpret_cast<const uint4*>(src)[c1];
+      for (int i = 0; i < 4; ++i) {
+        const float a0 = a[2 * i], a1 = a[2 * i + 1], b0 = b[2 * i], b1 = b[2 * i + 1];
+        a[2 * i] = a0 * ang[i].x - a1 * ang[i].y;
+        a[2 * i + 1] = a1 * ang[i].x + a0 * ang[i].y;
+        b[2 * i] = b0 * ang[4 + i].x - b1 * ang[4 + i].y;
+        b[2 * i + 1] = b1 * ang[4 + i].x + b0 * ang[4 + i].y;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float x0 = a[i], x1 = b[i];
+        a[i] = x0 * ang[i].x - x1 * ang[i].y;
+        b[i] = x1 * ang[i].x + x0 * ang[i].y;
+      }
     }
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int hh = h + u;
-      if (hh >= h1) continue;
+  };
+  {   // ---- queries
+    const __nv_bfloat16* src = p.q + token * p.qs;
+    __nv_bfloat16* dst = p.q_out + token * p.os;
+#pragma unroll 4
+    for (int h = grp; h < p.H; h += p.groups) {
+      const uint4 u = __ldcs(reinterpret_cast<const uint4*>(src + h * p.Dh + c0)), w = __ldcs(reinterpret_cast<const uint4*>(src + h * p.Dh + c1));
+      if (!turned) {
+        *reinterpret_cast<uint4*>(dst + h * p.Dh + c0) = u;
+        *reinterpret_cast<uint4*>(dst + h * p.Dh + c1) = w;
+        continue;
+      }
       float a[8], b[8];
-      unpack8(in[u][0], a);
-      unpack8(in[u][1], b);
-      const bool is_v = hh >= p.H + p.Hkv;
-      if (turned && !is_v) {
-        if (p.interleaved) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float a0 = a[2 * i], a1 = a[2 * i + 1], b0 = b[2 * i], b1 = b[2 * i + 1];
-            a[2 * i] = a0 * cs[i] - a1 * sn[i];
-            a[2 * i + 1] = a1 * cs[i] + a0 * sn[i];
-            b[2 * i] = b0 * cs[4 + i] - b1 * sn[4 + i];
-            b[2 * i + 1] = b1 * cs[4 + i] + b0 * sn[4 + i];
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float x0 = a[i], x1 = b[i];
-            a[i] = x0 * cs[i] - x1 * sn[i];
-            b[i] = x1 * cs[i] + x0 * sn[i];
-          }
-        }
-      }
-      if (hh < p.H) {
-        uint4* dst = reinterpret_cast<uint4*>(p.q_out + token * p.os + static_cast<int64_t>(hh) * p.Dh);
-        dst[c0] = pack8(a);
-        dst[c1] = pack8(b);
-      } else if (page >= 0) {
-        const int64_t at = cell + static_cast<int64_t>(is_v ? hh - p.H - p.Hkv : hh - p.H) * p.head;
-        if constexpr (F8) {
-          uint2* dst = reinterpret_cast<uint2*>(static_cast<uint8_t*>(is_v ? p.vc : p.kc) + at);
-          const float rs = is_v ? rv : rk;
-          dst[c0] = codes8(a, rs);
-          dst[c1] = codes8(b, rs);
-        } else {
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(is_v ? p.vc : p.kc) + at);
-          dst[c0] = pack8(a);
-          dst[c1] = pack8(b);
-        }
-      }
+      unpack8(u, a);
+      unpack8(w, b);
+      turn(a, b);
+      *reinterpret_cast<uint4*>(dst + h * p.Dh + c0) = pack8(a);
+      *reinterpret_cast<uint4*>(dst + h * p.Dh + c1) = pack8(b);
+    }
+  }
+  if (page < 0) return;
+  // ---- keys and values
+  const int64_t cell = static_cast<int64_t>(page) * p.pg + (pos & (p.page - 1)) * p.tok;
+  const float rk = F8 ? 1.0f / __ldg(p.k_scale) : 1.0f, rv = F8 ? 1.0f / __ldg(p.v_scale) : 1.0f;
+  // heads go round the groups where the queries' left off, so that a small batch spreads over all of them
+  int h = grp - p.H % p.groups;
+  if (h < 0) h += p.groups;
+#pragma unroll 2
+  for (; h < 2 * p.Hkv; h += p.groups) {
+    const bool is_v = h >= p.Hkv;
+    const int hh = is_v ? h - p.Hkv : h;
+    const __nv_bfloat16* src = (is_v ? p.v + token * p.vs : p.k + token * p.ks) + hh * p.Dh;
+    const uint4 u = __ldcs(reinterpret_cast<const uint4*>(src + c0)), w = __ldcs(reinterpret_cast<const uint4*>(src + c1));
+    const int64_t at = cell + hh * p.head;
+    if (!F8 && (is_v || !turned)) {
+      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(is_v ? p.vc : p.kc) + at;
+      *reinterpret_cast<uint4*>(dst + c0) = u;
+      *reinterpret_cast<uint4*>(dst + c1) = w;
+      continue;
+    }
+    float a[8], b[8];
+    unpack8(u, a);
+    unpack8(w, b);
+    if (!is_v) turn(a, b);
+    if constexpr (F8) {
+      uint8_t* dst = static_cast<uint8_t*>(is_v ? p.vc : p.kc) + at;
+      *reinterpret_cast<uint2*>(dst + c0) = codes8(a, is_v ? rv : rk);
+      *reinterpret_cast<uint2*>(dst + c1) = codes8(b, is_v ? rv : rk);
+    } else {
+      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.kc) + at;
+      *reinterpret_cast<uint4*>(dst + c0) = pack8(a);
+      *reinterpret_cast<uint4*>(dst + c1) = pack8(b);
     }
   }
 }
@@ -609,7 +637,13 @@ Pool pool_of(const fm_kv_cache& c) {
   p.layers = c.layers;
   p.Hkv = c.Hkv;
   p.chunks = c.Dh / per;
-  p.heads_inner = c.Hkv > 1 && c.head_stride < c.token_stride;
+  const bool one = c.Hkv == 1;
+  if ((one || c.head_stride == c.Dh) && c.token_stride == static_cast<int64_t>(c.Hkv) * c.Dh)
+    p.runs = kRunAll;
+  else if (c.token_stride == c.Dh)
+    p.runs = kRunHead;
+  else
+    p.runs = kRunRow;
   return p;
 }
 
@@ -873,14 +907,13 @@ extern "C" int fm_rope_append(const fm_kv_cache* c, int layer, const fm_kv_batch
   p.k_scale = f8 ? c->k_scale + layer : nullptr;
   p.v_scale = f8 ? c->v_scale + layer : nullptr;
   p.err = err;
-  // heads per thread: the angles are shared by more heads the more tokens there are to fill the GPU with
-  const int heads = H + 2 * c->Hkv, units = c->Dh / 16;
-  const int64_t all = static_cast<int64_t>(b->tokens) * units * heads;
-  p.per = 2;
-  while (p.per < 8 && all / (p.per * 2) >= 152 * 2048) p.per *= 2;
-  p.groups = up(heads, p.per);
-  const int64_t threads = static_cast<int64_t>(b->max_tokens) * p.groups * units;
-  if ((threads + 255) / 256 > INT32_MAX) return record_error(FM_ERR_SHAPE, "max_tokens x heads is too large for one call");
-  return done(launch(f8 ? append_kernel<true> : append_kernel<false>, dim3(static_cast<unsigned>((threads + 255) / 256), b->n),
-                     dim3(256), 0, opts(stream), p));
+  // a token has Dh / 16 threads a head group; a CTA takes four tokens where there are enough to fill the GPU with, else
+  // one, whose heads then spread over more threads
+  const int units = c->Dh / 16;
+  p.toks = static_cast<int64_t>(b->tokens) >= 4 * 152 * 4 ? 4 : 1;
+  p.groups = 256 / (units * p.toks);
+  const int64_t blocks = up(b->max_tokens, p.toks);
+  if (b->n > 65535) return record_error(FM_ERR_SHAPE, "a batch takes up to 65535 entries");
+  return done(launch(f8 ? append_kernel<true> : append_kernel<false>, dim3(static_cast<unsigned>(blocks), b->n), dim3(256),
+                     sizeof(float2) * p.toks * (p.rot / 2), opts(stream), p));
 }

@@ -171,17 +171,19 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_quant_kernel(const
       const int v = lane + k * TPR;
       if (!live || v >= vecs) continue;
       const float scale = __fdiv_rn(p.block ? top[k] : row_top, 448.0f);
-      const float inv = 1.0f / scale;
+      if (scale > 1e-30f || !(scale == scale)) {
+        const float inv = __fdiv_rn(1.0f, scale);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[k][e] *= inv;
+      } else {   // the reciprocal may overflow; a zero scale (all zeros) gives zero codes
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[k][e] = scale > 0.f ? __fdiv_rn(x[k][e], scale) : 0.f;
+      }
       uint32_t w[2] = {0, 0};
 #pragma unroll
-      for (int e = 0; e < 8; e += 2) {
-        // a scale whose reciprocal overflows is divided by; a zero scale (all zeros) gives zero codes
-        const bool mul = scale > 1e-30f || !(scale == scale);
-        const float a = mul ? x[k][e] * inv : (scale > 0.f ? __fdiv_rn(x[k][e], scale) : 0.f);
-        const float b = mul ? x[k][e + 1] * inv : (scale > 0.f ? __fdiv_rn(x[k][e + 1], scale) : 0.f);
-        const uint32_t c = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-        w[e >> 2] |= c << (8 * (e & 2));
-      }
+      for (int e = 0; e < 8; e += 2)
+        w[e >> 2] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(x[k][e], x[k][e + 1]), __NV_SATFINITE, __NV_E4M3))
+                     << (8 * (e & 2));
       *reinterpret_cast<uint2*>(p.codes + row * p.d + v * 8) = make_uint2(w[0], w[1]);
       if (p.block) {
         if ((v & 15) == 0) p.scales[row * ((p.d + 127) / 128) + (v >> 4)] = scale;
