@@ -4,15 +4,14 @@
 //   code = E4M3(y / scale)
 //
 // Bound by HBM: x, r, the sum and the codes cross it once, a row stays in registers between its two reductions.
-// A row belongs to 32..512 threads, each with up to four 8-element vectors. Few rows take one vector a thread (the
-// latency of a row is its chain of loads and reductions); many rows take up to four, so that a warp keeps more bytes
-// in flight and fewer threads meet in a reduction. The CTAs are persistent: gamma is read once per CTA and stays in
-// registers. Sums and scales are fp32; s is rounded once to x's type when stored and the norm uses it unrounded.
+// A row belongs to 8..512 threads with one to four 8-element vectors each, all loads issued before the first reduction,
+// and a CTA of its own where it takes more than a warp, so that no row waits for another's reduction (CTAs of four rows in
+// step took 38 us for 12000 rows of 2048, now 28.8 us: 6.0 TB/s). Sums and scales are fp32; s is rounded once to x's
+// type when stored and the norm uses it unrounded.
 
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
-#include <algorithm>
 #include <cmath>
 
 #include "internal.h"
@@ -79,13 +78,12 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 template <int TPR, bool kMax>
 __device__ __forceinline__ float row_reduce(float v, float* red) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
+  for (int o = (TPR < 32 ? TPR : 32) / 2; o > 0; o >>= 1) {
     const float w = __shfl_xor_sync(0xffffffffu, v, o);
     v = kMax ? max_nan(v, w) : v + w;
   }
   if constexpr (TPR > 32) {
     const int warp = threadIdx.x >> 5;
-    __syncthreads();
     if ((threadIdx.x & 31) == 0) red[warp] = v;
     __syncthreads();
     const int first = warp / (TPR / 32) * (TPR / 32);
@@ -96,121 +94,136 @@ __device__ __forceinline__ float row_reduce(float v, float* red) {
   return v;
 }
 
+// A CTA: rows that fit a warp in groups of 256 threads, else one row, so that no row waits for another's barrier.
+__host__ __device__ constexpr int threads_of(int tpr) { return tpr > 32 ? tpr : 256; }
+
 template <int TPR, int NV, bool F32>
-__global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_quant_kernel(const NormParams p) {
-  constexpr int kThreads = TPR > 256 ? TPR : 256;
-  constexpr int kRows = kThreads / TPR;
+__global__ void __launch_bounds__(threads_of(TPR)) norm_quant_kernel(const NormParams p) {
+  constexpr int kThreads = threads_of(TPR);
   __shared__ float red[2][kThreads / 32];
   pdl_trigger();
-  const int lane = threadIdx.x % TPR, sub = threadIdx.x / TPR;
-  const int vecs = p.d / 8;
-  float gm[NV][8];
   pdl_wait();
+  const int lane = threadIdx.x % TPR;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (kThreads / TPR) + threadIdx.x / TPR;
+  const int vecs = p.d / 8;
+  const bool live = row < p.T;   // every thread of the CTA takes part in the reductions
+  float x[NV][8];
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     const int v = lane + k * TPR;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) gm[k][e] = 1.0f;
-    if (p.gamma && v < vecs) load8<true>(p.gamma, v * 8, gm[k]);
+    for (int e = 0; e < 8; ++e) x[k][e] = 0.f;
+    if (live && v < vecs) load8<F32>(p.x, row * p.xs + v * 8, x[k]);
   }
-  for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * kRows; row0 < p.T; row0 += static_cast<int64_t>(gridDim.x) * kRows) {
-    const int64_t row = row0 + sub;
-    const bool live = row < p.T;   // every thread of the CTA takes part in the reductions
-    float x[NV][8];
-    float ss = 0.f;
+  if (p.r) {
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int v = lane + k * TPR;
+      if (live && v < vecs) {
+        float r[8];
+        load8<false>(p.r, row * p.rs + v * 8, r);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[k][e] = 0.f;
-      if (live && v < vecs) load8<F32>(p.x, row * p.xs + v * 8, x[k]);
-    }
-    if (p.r) {
-#pragma unroll
-      for (int k = 0; k < NV; ++k) {
-        const int v = lane + k * TPR;
-        if (live && v < vecs) {
-          float r[8];
-          load8<false>(p.r, row * p.rs + v * 8, r);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[k][e] += r[e];
-        }
+        for (int e = 0; e < 8; ++e) x[k][e] += r[e];
       }
     }
+  }
+  float ss = 0.f;
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int v = lane + k * TPR;
-      if (p.x_out && live && v < vecs) store8<F32>(p.x_out, row * p.os + v * 8, x[k]);
+  for (int k = 0; k < NV; ++k) {
+    const int v = lane + k * TPR;
+    if (p.x_out && live && v < vecs) store8<F32>(p.x_out, row * p.os + v * 8, x[k]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(x[k][e], x[k][e], ss);
+    for (int e = 0; e < 8; ++e) ss = fmaf(x[k][e], x[k][e], ss);
+  }
+  const float rr = 1.0f / sqrtf(row_reduce<TPR, false>(ss, red[0]) / p.d + p.eps);
+  float top[NV];
+  float row_top = 0.f;
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    const int v = lane + k * TPR;
+    float g[8];
+    const bool has = p.gamma && v < vecs;
+    if (has) load8<true>(p.gamma, v * 8, g);
+    top[k] = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      x[k][e] *= has ? rr * g[e] : rr;
+      top[k] = max_nan(top[k], fabsf(x[k][e]));
     }
-    const float rr = 1.0f / sqrtf(row_reduce<TPR, false>(ss, red[0]) / p.d + p.eps);
-    float top[NV];
-    float row_top = 0.f;
+    row_top = max_nan(row_top, top[k]);
+  }
+  if (p.block) {
+    // 128 columns are 16 consecutive vectors: 16 aligned lanes (a row of 8 threads has at most 64 columns)
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      top[k] = 0.f;
+    for (int k = 0; k < NV; ++k)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        x[k][e] = x[k][e] * rr * gm[k][e];
-        top[k] = max_nan(top[k], fabsf(x[k][e]));
-      }
-      row_top = max_nan(row_top, top[k]);
+      for (int o = (TPR < 16 ? TPR : 16) / 2; o > 0; o >>= 1) top[k] = max_nan(top[k], __shfl_xor_sync(0xffffffffu, top[k], o));
+  } else {
+    row_top = row_reduce<TPR, true>(row_top, red[1]);
+  }
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    const int v = lane + k * TPR;
+    if (!live || v >= vecs) continue;
+    const float scale = __fdiv_rn(p.block ? top[k] : row_top, 448.0f);
+    if (scale > 1e-30f || !(scale == scale)) {
+      const float inv = __fdiv_rn(1.0f, scale);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[k][e] *= inv;
+    } else {   // the reciprocal may overflow; a zero scale (all zeros) gives zero codes
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[k][e] = scale > 0.f ? __fdiv_rn(x[k][e], scale) : 0.f;
     }
+    uint32_t w[2] = {0, 0};
+#pragma unroll
+    for (int e = 0; e < 8; e += 2)
+      w[e >> 2] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(x[k][e], x[k][e + 1]), __NV_SATFINITE, __NV_E4M3))
+                   << (8 * (e & 2));
+    *reinterpret_cast<uint2*>(p.codes + row * p.d + v * 8) = make_uint2(w[0], w[1]);
     if (p.block) {
-      // 128 columns are 16 consecutive vectors: 16 aligned lanes
-#pragma unroll
-      for (int k = 0; k < NV; ++k)
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) top[k] = max_nan(top[k], __shfl_xor_sync(0xffffffffu, top[k], o));
-    } else {
-      row_top = row_reduce<TPR, true>(row_top, red[1]);
-    }
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int v = lane + k * TPR;
-      if (!live || v >= vecs) continue;
-      const float scale = __fdiv_rn(p.block ? top[k] : row_top, 448.0f);
-      if (scale > 1e-30f || !(scale == scale)) {
-        const float inv = __fdiv_rn(1.0f, scale);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[k][e] *= inv;
-      } else {   // the reciprocal may overflow; a zero scale (all zeros) gives zero codes
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[k][e] = scale > 0.f ? __fdiv_rn(x[k][e], scale) : 0.f;
-      }
-      uint32_t w[2] = {0, 0};
-#pragma unroll
-      for (int e = 0; e < 8; e += 2)
-        w[e >> 2] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(x[k][e], x[k][e + 1]), __NV_SATFINITE, __NV_E4M3))
-                     << (8 * (e & 2));
-      *reinterpret_cast<uint2*>(p.codes + row * p.d + v * 8) = make_uint2(w[0], w[1]);
-      if (p.block) {
-        if ((v & 15) == 0) p.scales[row * ((p.d + 127) / 128) + (v >> 4)] = scale;
-      } else if (v == 0) {
-        p.scales[row] = scale;
-      }
+      if ((v & 15) == 0) p.scales[row * ((p.d + 127) / 128) + (v >> 4)] = scale;
+    } else if (v == 0) {
+      p.scales[row] = scale;
     }
   }
 }
 
 template <int TPR, int NV>
 cudaError_t run(const NormParams& p, bool f32, const LaunchOpts& o) {
-  constexpr int kThreads = TPR > 256 ? TPR : 256;
-  const int64_t blocks = (p.T + kThreads / TPR - 1) / (kThreads / TPR);
-  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(blocks, 152 * (2048 / kThreads))));
+  constexpr int kThreads = threads_of(TPR);
+  const dim3 grid(static_cast<unsigned>((p.T + kThreads / TPR - 1) / (kThreads / TPR)));
   return f32 ? launch(norm_quant_kernel<TPR, NV, true>, grid, dim3(kThreads), 0, o, p)
              : launch(norm_quant_kernel<TPR, NV, false>, grid, dim3(kThreads), 0, o, p);
 }
 
-template <int NV>
+template <int kRowVecs>
+cudaError_t many(const NormParams& p, bool f32, const LaunchOpts& o) {
+  return f32 ? run<kRowVecs / 2, 2>(p, true, o) : run<kRowVecs / 4, 4>(p, false, o);
+}
+
+// Threads of a row and vectors of a thread. Many rows: four 16-byte vectors of bf16, two 32-byte ones of fp32 (12000
+// rows of 2048, bf16: 28.8 us with 64 x 4, 30.5 with 128 x 2, 34 with 256 x 1, 52 with 32 x 8; fp32: 43 with 64 x 4,
+// 40.8 with 128 x 2). Fewer than fill the GPU that way: one vector (1000 rows of 2048: 3.8 us against 5.1).
 cudaError_t pick(const NormParams& p, bool f32, const LaunchOpts& o) {
   const int vecs = p.d / 8;
-  if (vecs <= 32 * NV) return run<32, NV>(p, f32, o);
-  if (vecs <= 64 * NV) return run<64, NV>(p, f32, o);
-  if (vecs <= 128 * NV) return run<128, NV>(p, f32, o);
-  if (vecs <= 256 * NV) return run<256, NV>(p, f32, o);
-  return run<512, NV>(p, f32, o);
+  if (vecs <= 8) return run<8, 1>(p, f32, o);
+  if (vecs <= 16) return run<16, 1>(p, f32, o);
+  if (static_cast<int64_t>(p.T) * vecs < 152 * 4096) {
+    if (vecs <= 32) return run<32, 1>(p, f32, o);
+    if (vecs <= 64) return run<64, 1>(p, f32, o);
+    if (vecs <= 128) return run<128, 1>(p, f32, o);
+    if (vecs <= 256) return run<256, 1>(p, f32, o);
+    if (vecs <= 512) return run<512, 1>(p, f32, o);
+    if (vecs <= 1024) return run<512, 2>(p, f32, o);
+    return run<512, 4>(p, f32, o);
+  }
+  if (vecs <= 32) return run<16, 2>(p, f32, o);
+  if (vecs <= 64) return run<32, 2>(p, f32, o);
+  if (vecs <= 128) return many<128>(p, f32, o);
+  if (vecs <= 256) return many<256>(p, f32, o);
+  if (vecs <= 512) return many<512>(p, f32, o);
+  if (vecs <= 1024) return many<1024>(p, f32, o);
+  return run<512, 4>(p, f32, o);
 }
 
 }  // namespace
@@ -237,12 +250,6 @@ extern "C" int fm_norm_quant(const void* x, int64_t x_stride, int x_f32, const u
   LaunchOpts o;
   o.stream = static_cast<cudaStream_t>(stream);
   o.pdl = true;
-  // few rows: one vector a thread (two for the longest rows); many: up to four
-  const bool few = static_cast<int64_t>(T) * (d / 8) < 152 * 1024;
-  cudaError_t e;
-  if (few && d <= 4096)
-    e = pick<1>(p, x_f32 != 0, o);
-  else
-    e = pick<4>(p, x_f32 != 0, o);
+  const cudaError_t e = pick(p, x_f32 != 0, o);
   return e == cudaSuccess ? FM_OK : record_error(FM_ERR_CUDA, cudaGetErrorString(e));
 }
