@@ -72,12 +72,19 @@ __device__ __forceinline__ int first_key(const AttnParams& p, int pos) {
   return p.window > 0 && pos >= p.window ? pos - p.window + 1 : 0;
 }
 
-// True once the phase with the given parity has completed; false after 2^22 polls (each of which the hardware suspends
-// for a while: seconds, far beyond any legitimate wait). Reading a clock between the polls cost more than the wait.
+// True once the phase with the given parity has completed; false after 2^18 polls, in each of which the hardware may
+// suspend the thread for 20 us: seconds at most, and far beyond any legitimate wait. No clock is read between the polls.
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity) {
 #pragma unroll 1
-  for (int i = 0; i < (1 << 22); ++i)
-    if (mbar_try_wait(bar, parity)) return true;
+  for (int i = 0; i < (1 << 18); ++i) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.b32 %0, 1, 0, p;\n}\n"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
+        : "memory");
+    if (done) return true;
+  }
   return false;
 }
 

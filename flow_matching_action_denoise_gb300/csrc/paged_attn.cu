@@ -52,7 +52,7 @@ constexpr int kMmaWarp = 8, kTmaWarp = 10, kTailWarp = 11, kCvtWarp = 12, kCvtWa
 constexpr int threads_of(bool f8) { return f8 ? 512 : 384; }
 constexpr int kSmemLimit = 226 * 1024;
 constexpr int kMaxRing = 8;
-constexpr uint32_t kCtlBytes = 512;
+constexpr uint32_t kCtlBytes = 1024;
 
 // Matrix descriptor of an MN-major operand in 128-byte-swizzled rows: rows along K (8-row groups 1024 bytes
 // apart), 64 elements of MN per row, further blocks of 64 `block_bytes` apart.
@@ -110,6 +110,11 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return d;
 }
 
+// 16 bytes from global to shared memory, or 16 zero bytes (src is not read then).
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool has) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(has ? 16 : 0) : "memory");
+}
+
 __device__ __forceinline__ uint32_t swz(int r, int c) {   // 16-byte chunk c of row r of a 128-byte-row tile
   return static_cast<uint32_t>(r * 128 + ((c ^ (r & 7)) << 4));
 }
@@ -118,6 +123,7 @@ struct Ctl {   // shared-memory control block
   uint64_t full[kMaxRing], empty[kMaxRing], rfull[kMaxRing], rempty[kMaxRing];
   uint64_t q_ready, s_full[2], p_full[2], o_done[2], turn[2], tail, drain[2];
   uint32_t tmem;
+  float q_factor[kTileRows];   // E4M3 cache, alternate tiles: the scores' factor of every query row
 };
 static_assert(sizeof(Ctl) <= kCtlBytes, "control block");
 
@@ -143,7 +149,11 @@ __global__ void __launch_bounds__(threads_of(F8), 1)
   const int entry = blockIdx.z / p.splits, split = blockIdx.z % p.splits;
   const int block_rows = q_tiles * kTileRows;
 
-  if (warp == kTmaWarp) {   // this warp's first copies start before the CTA meets
+  // the CTA meets once, before anything is known of its entry; each role then goes as soon as its own data are there
+  if (warp == kMmaWarp) {
+    tmem_alloc(&c.tmem, 512);
+    tmem_relinquish();
+  } else if (warp == kTmaWarp) {
     if (elect_one()) {
       for (int i = 0; i < kMaxRing; ++i) {
         mbar_init(&c.full[i], F8 ? kCvtWarps : 1);
@@ -175,7 +185,15 @@ __global__ void __launch_bounds__(threads_of(F8), 1)
   const int begin = en.begin, nq = en.nq, len = en.len, sid = en.sid;
   const int rows = min(nq, p.max_tokens) * p.G;   // <= 2^30
   const int row0 = row_block * block_rows;
-  if (row0 >= rows) return;   // before TMEM is taken, the same for the whole CTA
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_trigger();   // after TMEM is held
+  const uint32_t tmem = c.tmem;
+  if (row0 >= rows) {   // the same for the whole CTA
+    if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+    return;
+  }
 
   const int past = len - nq;   // position of token i: past + i
   auto key_end = [&](int row) { return last_key(p, past + row / p.G, len); };
@@ -227,13 +245,13 @@ __global__ void __launch_bounds__(threads_of(F8), 1)
   };
   int copy_next = 0, copy_page = 0, copy_page_after = 0;
   Ring copy_at;
-  auto copy_one = [&](bool first) {   // first: into a buffer that nothing has used
+  auto copy_one = [&]() {
     const int j = copy_next >> 1, kv = copy_next & 1;
     if (kv == 0) {
       copy_page = copy_page_after;
       copy_page_after = page_of(j + 1);   // on its way while this tile's copies wait for their buffers
     }
-    if (!first && copy_next >= ring_n && !wait_for(&ring_empty[copy_at.b], copy_at.phase ^ 1)) return false;
+    if (copy_next >= ring_n && !wait_for(&ring_empty[copy_at.b], copy_at.phase ^ 1)) return false;
     if (lane == 0) mbar_arrive_expect_tx(&ring_full[copy_at.b], ring_bytes);
     __syncwarp();
     // one lane issues all boxes: lanes that issue their own would be taken one after the other at twice the cost
@@ -265,49 +283,52 @@ __global__ void __launch_bounds__(threads_of(F8), 1)
   const int t_of = (warp >> 2) & 1, wq = warp & 3;
   const int tile_row0 = row0 + (p.alt ? 0 : t_of * kTileRows);
   const int lane_row = lane / kRowChunks, lane_chunk = lane % kRowChunks;
-  // Walks the token and the head of a lane's rows, a division for the first only. G comes in opaque, so that nothing
-  // of a walk is kept in registers for the next one.
+  // Walks a lane's rows (every kStep-th) in an array [token][head][DH] by additions alone; G comes in opaque, so that
+  // nothing of a walk is kept in registers for the next one. Elements are counted.
   struct Walk {
-    int tok, head, step_tok, step_head, G;
-    __device__ __forceinline__ Walk(int row, int group) : G(group) {
+    int64_t at, step, wrap;   // the row's place, the way to the next, and more where that is another token
+    int head, step_head, G;
+    __device__ __forceinline__ Walk(int row, int group, int64_t tok_stride, int64_t from) : G(group) {
       asm volatile("" : "+r"(G));
-      tok = row / G;
+      const int tok = row / G, step_tok = kStep / G;
       head = row - tok * G;
-      step_tok = kStep / G;
       step_head = kStep - step_tok * G;
+      at = from + tok * tok_stride + head * DH;
+      step = step_tok * tok_stride + step_head * DH;
+      wrap = tok_stride - static_cast<int64_t>(G) * DH;
     }
     __device__ __forceinline__ void next() {
-      tok += step_tok;
+      at += step;
       head += step_head;
       if (head >= G) {
         head -= G;
-        ++tok;
+        at += wrap;
       }
     }
   };
-  uint4 qv[kSteps];
-  if (warp < 8) {
-    const __nv_bfloat16* q0 = p.q + begin * p.q_stride + g * p.G * DH + lane_chunk * 8;
-    Walk at(tile_row0 + wq * 32 + lane_row, p.G);
+  // Byte offset of this lane's chunk of its i-th row inside a tile of 128-byte-row blocks (128-byte swizzle), and inside
+  // a warp's 32 staged rows of DH * 2 bytes: kStep is 2 or 4, so that all but i is the lane's own.
+  const uint32_t tile_lane = (lane_chunk >> 3) * kBlock + (wq * 32 + lane_row) * 128 + (((lane_chunk & 7) ^ lane_row) << 4);
+  const uint32_t stage_lane = lane_row * (DH * 2) + ((lane_chunk ^ lane_row) << 4);
+  auto tile_at = [&](int i) { return (tile_lane + i * kStep * 128) ^ (((i * kStep) & 7) << 4); };
+  auto stage_at = [&](int i) { return (stage_lane + i * kStep * (DH * 2)) ^ (((i * kStep) & 7) << 4); };
+  // What runs once a CTA: independent steps without divisions or clocks between them (as a loop of dependent ones the
+  // 16 copies took 3000 cycles to issue).
+  const uint32_t q_tile = q_a + (p.alt ? 0 : t_of * kTileBytes);
+  if (warp < 8) {   // the rows go to their place in the swizzled tile; of one tile each warpgroup takes every other step
+    Walk walk(tile_row0 + wq * 32 + lane_row, p.G, p.q_stride, begin * p.q_stride + g * p.G * DH + lane_chunk * 8);
+    const int left = rows - tile_row0 - wq * 32 - lane_row;   // rows from this lane's first one on
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
-      const int R = tile_row0 + wq * 32 + i * kStep + lane_row;
-      qv[i] = make_uint4(0, 0, 0, 0);
-      if (R < rows && (F8 || !p.alt || (i & 1) == t_of)) qv[i] = __ldg(reinterpret_cast<const uint4*>(q0 + at.tok * p.q_stride + at.head * DH));
-      at.next();
+      const bool has = i * kStep < left;
+      if (!p.alt || (i & 1) == t_of) cp_async16_or_zero(q_tile + tile_at(i), p.q + (has ? walk.at : 0), has);
+      walk.next();
     }
-  } else if (warp == kMmaWarp) {
-    tmem_alloc(&c.tmem, 512);
-    tmem_relinquish();
+    asm volatile("cp.async.commit_group;" ::: "memory");
   } else if (warp == kTmaWarp) {
     copy_page_after = page_of(0);
-    while (copy_next < min(ring_n, 2 * n_keys)) copy_one(true);
   }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  pdl_trigger();   // after TMEM is held
-  const uint32_t tmem = c.tmem;
+
   // one instruction for a whole warpgroup
   if (warp < 8) {
     if constexpr (F8)
@@ -328,38 +349,46 @@ __global__ void __launch_bounds__(threads_of(F8), 1)
     const int row = tile_row0 + r;
     const bool live = row < rows;
     const bool warp_live = row - lane < rows;
+    asm volatile("cp.async.wait_all;" ::: "memory");
     float c_row = p.scale_log2;
-    {   // ---- the query rows into their swizzled tile; of one tile for both warpgroups each takes every other step
-      const uint32_t base = q_a + (p.alt ? 0 : t * kTileBytes);
+    if constexpr (F8) {
+      // Every thread turns its own row into f16, scaled by 2^(14 - exponent of its largest element): exact, and the
+      // inverse goes into the scores' factor.
+      __syncwarp();
+      if (p.alt) asm volatile("bar.sync 1, 256;" ::: "memory");   // the other warpgroup's copies
+      if ((!p.alt || t == 0) && warp_live) {
+        uint4* mine = reinterpret_cast<uint4*>(sq + (p.alt ? 0 : t * kTileBytes) + r * 128);
+        uint4 v[kRowChunks];
+        uint32_t top = 0;   // largest |q| of the row as bf16 bits
 #pragma unroll
-      for (int i = 0; i < kSteps; ++i) {
-        const int rr = wq * 32 + i * kStep + lane_row;
-        if constexpr (F8) {
-          uint32_t w[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
-          uint32_t top = 0;   // largest |q| of the row as bf16 bits
+        for (int ch = 0; ch < kRowChunks; ++ch) {
+          v[ch] = mine[(ch >> 3) * (kBlock / 16) + ((ch & 7) ^ (r & 7))];
+          const uint32_t w[4] = {v[ch].x, v[ch].y, v[ch].z, v[ch].w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
+        }
+        const int ex = static_cast<int>(top >> 7);   // biased exponent (0: zero or subnormal; 255: not finite)
+        const int sh = ex == 0 || ex == 255 ? 0 : min(max(141 - ex, -100), 100);   // 127 + 14 - ex
+        const float up = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
+        c_row *= __uint_as_float(static_cast<uint32_t>(127 - sh) << 23) * __ldg(p.k_scale);
 #pragma unroll
-          for (int o = kRowChunks / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-          // scale by 2^(14 - exponent): exact, and the inverse goes into the scores' factor
-          const int ex = static_cast<int>(top >> 7);   // biased exponent (0: zero or subnormal; 255: not finite)
-          const int sh = ex == 0 || ex == 255 ? 0 : min(max(141 - ex, -100), 100);   // 127 + 14 - ex
-          const float up = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
-          // the lane that owns this row's scores keeps the factor
-          const int from = (lane - i * kStep) * kRowChunks;
-          const float down = __shfl_sync(0xffffffffu, __uint_as_float(static_cast<uint32_t>(127 - sh) << 23), from & 31);
-          if (from >= 0 && from < 32) c_row *= down * __ldg(p.k_scale);
+        for (int ch = 0; ch < kRowChunks; ++ch) {
+          uint32_t w[4] = {v[ch].x, v[ch].y, v[ch].z, v[ch].w};
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             w[e] = pack16<true>(__uint_as_float(w[e] << 16) * up, __uint_as_float(w[e] & 0xffff0000u) * up);
-          qv[i] = make_uint4(w[0], w[1], w[2], w[3]);
+          mine[(ch >> 3) * (kBlock / 16) + ((ch & 7) ^ (r & 7))] = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        if (!p.alt || (i & 1) == t) st_shared_v4(base + (lane_chunk >> 3) * kBlock + swz(rr, lane_chunk & 7), qv[i]);
       }
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&c.q_ready);
+      if (p.alt) {   // the other warpgroup's scores are of the same rows
+        if (t == 0) c.q_factor[r] = c_row;
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        c_row = c.q_factor[r];
+      }
     }
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&c.q_ready);
     // rows behind the last one need no mask: what they compute is not used
     const int my_end = live ? key_end(row) : 0x7fffffff, my_begin = live ? key_begin(row) : 0;
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(wq * 32) << 16);
@@ -470,24 +499,27 @@ __global__ void __launch_bounds__(threads_of(F8), 1)
     const float vs = F8 ? __ldg(p.v_scale) : 1.0f;
     float* join = reinterpret_cast<float*>(sring);                        // [128][DH], chunks swizzled by row
     float2* join_ml = reinterpret_cast<float2*>(sring + kTileRows * DH * 4);
-    float o[DH];
-    auto load_o = [&]() {   // this row's sums
+    auto load_o = [&](int b, float* o) {   // 32 of this row's sums
       if (n > 0) {
-#pragma unroll
-        for (int b = 0; b < DH; b += 32) tmem_ld32_async(t_o + b, o + b);
+        tmem_ld32_async(t_o + b, o);
         tmem_wait_ld();
       } else {
 #pragma unroll
-        for (int e = 0; e < DH; ++e) o[e] = 0.f;
+        for (int e = 0; e < 32; ++e) o[e] = 0.f;
       }
     };
     if (p.alt) {
       if (t == 1 && warp_live) {
         join_ml[r] = make_float2(m2, sum);
-        load_o();
+#pragma unroll 1
+        for (int b = 0; b < DH; b += 32) {
+          float o[32];
+          load_o(b, o);
 #pragma unroll
-        for (int e = 0; e < DH; e += 4)
-          *reinterpret_cast<float4*>(join + r * DH + (((e >> 2) ^ (r & 7)) << 2)) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<float4*>(join + r * DH + ((((b + e) >> 2) ^ (r & 7)) << 2)) =
+                make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+        }
       }
       asm volatile("bar.sync 1, 256;" ::: "memory");
     }
@@ -514,54 +546,59 @@ __global__ void __launch_bounds__(threads_of(F8), 1)
       // TMEM gives a lane one row: rows are staged in the query tile's 32 rows of this warp (its last reader has
       // completed) and leave kRowChunks lanes a row, whole 16-byte chunks. fp32 shares take two passes.
       const uint32_t stage = q_a + (p.alt ? 0 : t * kTileBytes) + wq * 32 * DH * 2;
-      load_o();
-      if (p.alt) {
-#pragma unroll
-        for (int e = 0; e < DH; e += 4) {
-          const float4 x = *reinterpret_cast<const float4*>(join + r * DH + (((e >> 2) ^ (r & 7)) << 2));
-          o[e] = o[e] * w0 + x.x * w1;
-          o[e + 1] = o[e + 1] * w0 + x.y * w1;
-          o[e + 2] = o[e + 2] * w0 + x.z * w1;
-          o[e + 3] = o[e + 3] * w0 + x.w * w1;
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < DH; ++e) o[e] *= w0;
-      }
       const int passes = p.splits == 1 ? 1 : nt > 0 ? 2 : 0;
+#pragma unroll 1
+      for (int pass = 0; pass < passes; ++pass) {
+        const int dims = p.splits == 1 ? DH : DH / 2, d0 = pass * dims;
+#pragma unroll 1
+        for (int b = 0; b < dims; b += 32) {
+          float o[32];
+          load_o(d0 + b, o);
+          if (p.alt) {
 #pragma unroll
-      for (int pass = 0; pass < 2; ++pass) {
-        if (pass >= passes) break;
-        const int d0 = pass * (DH / 2);
-        if (p.splits > 1) {
+            for (int e = 0; e < 32; e += 4) {
+              const float4 x = *reinterpret_cast<const float4*>(join + r * DH + ((((d0 + b + e) >> 2) ^ (r & 7)) << 2));
+              o[e] = o[e] * w0 + x.x * w1;
+              o[e + 1] = o[e + 1] * w0 + x.y * w1;
+              o[e + 2] = o[e + 2] * w0 + x.z * w1;
+              o[e + 3] = o[e + 3] * w0 + x.w * w1;
+            }
+          } else {
 #pragma unroll
-          for (int e = 0; e < DH / 2; e += 4) {
-            const int k = pass * (DH / 2) + e;
-            st_shared_v4(stage + lane * (DH * 2) + (((e >> 2) ^ (lane & 7)) << 4),
-                         make_uint4(__float_as_uint(o[k]), __float_as_uint(o[k + 1]), __float_as_uint(o[k + 2]),
-                                    __float_as_uint(o[k + 3])));
+            for (int e = 0; e < 32; ++e) o[e] *= w0;
           }
-        } else {
+          if (p.splits > 1) {
 #pragma unroll
-          for (int e = 0; e < DH; e += 8)
-            st_shared_v4(stage + lane * (DH * 2) + (((e >> 3) ^ (lane & 7)) << 4),
-                         make_uint4(pack16<false>(o[e], o[e + 1]), pack16<false>(o[e + 2], o[e + 3]),
-                                    pack16<false>(o[e + 4], o[e + 5]), pack16<false>(o[e + 6], o[e + 7])));
+            for (int e = 0; e < 32; e += 4)
+              st_shared_v4(stage + lane * (DH * 2) + ((((b + e) >> 2) ^ (lane & 7)) << 4),
+                           make_uint4(__float_as_uint(o[e]), __float_as_uint(o[e + 1]), __float_as_uint(o[e + 2]),
+                                      __float_as_uint(o[e + 3])));
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; e += 8)
+              st_shared_v4(stage + lane * (DH * 2) + ((((b + e) >> 3) ^ (lane & 7)) << 4),
+                           make_uint4(pack16<false>(o[e], o[e + 1]), pack16<false>(o[e + 2], o[e + 3]),
+                                      pack16<false>(o[e + 4], o[e + 5]), pack16<false>(o[e + 6], o[e + 7])));
+          }
         }
         __syncwarp();
-        Walk at(tile_row0 + wq * 32 + lane_row, p.G);
-#pragma unroll 4
-        for (int i = 0; i < 32; i += kStep) {
-          const int rr = i + lane_row, R = tile_row0 + wq * 32 + rr;
-          const uint4 x = *reinterpret_cast<const uint4*>(sq + (p.alt ? 0 : t * kTileBytes) + wq * 32 * DH * 2 + rr * (DH * 2) +
-                                                          ((lane_chunk ^ (rr & 7)) << 4));
-          if (R < rows) {
-            if (p.splits > 1)
-              reinterpret_cast<uint4*>(p.part_o + (split_row + static_cast<int64_t>(begin + at.tok) * p.H + g * p.G + at.head) * DH + d0)[lane_chunk] = x;
-            else
-              reinterpret_cast<uint4*>(p.out + (begin + at.tok) * p.out_stride + (g * p.G + at.head) * DH)[lane_chunk] = x;
+        const int left = rows - tile_row0 - wq * 32 - lane_row;
+        const uint8_t* staged = sq + (p.alt ? 0 : t * kTileBytes) + wq * 32 * DH * 2;
+        if (p.splits > 1) {   // shares: [split][token][head][DH], this pass's half of the dims
+          Walk walk(tile_row0 + wq * 32 + lane_row, p.G, static_cast<int64_t>(p.H) * DH,
+                    (split_row + static_cast<int64_t>(begin) * p.H + g * p.G) * DH + d0 + lane_chunk * 4);
+#pragma unroll
+          for (int i = 0; i < kSteps; ++i) {
+            if (i * kStep < left) *reinterpret_cast<uint4*>(p.part_o + walk.at) = *reinterpret_cast<const uint4*>(staged + stage_at(i));
+            walk.next();
           }
-          at.next();
+        } else {
+          Walk walk(tile_row0 + wq * 32 + lane_row, p.G, p.out_stride, begin * p.out_stride + g * p.G * DH + lane_chunk * 8);
+#pragma unroll
+          for (int i = 0; i < kSteps; ++i) {
+            if (i * kStep < left) *reinterpret_cast<uint4*>(p.out + walk.at) = *reinterpret_cast<const uint4*>(staged + stage_at(i));
+            walk.next();
+          }
         }
         __syncwarp();
       }
@@ -710,7 +747,7 @@ __global__ void __launch_bounds__(threads_of(F8), 1)
   } else if (warp == kTmaWarp) {
     // ================================================= page table and TMA
     bool ok = true;
-    while (copy_next < 2 * n_keys && ok) ok = copy_one(false);
+    while (copy_next < 2 * n_keys && ok) ok = copy_one();
     const int issued = copy_next, nb = ring_n;
     uint64_t* full = ring_full;
     if (!ok) {   // the copies in flight land before the CTA leaves
