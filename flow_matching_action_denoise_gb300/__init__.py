@@ -580,12 +580,15 @@ def _rows(x, where: str, name: str, dtype, dev: int, rows: int, cols: int):
     return x.data_ptr(), s0 if rows > 1 else cols
 
 
+_I32 = None   # torch.int32, once a cache or a batch exists
+
+
 def _ints(x, where: str, name: str, dev: int, count: int):
-    import torch
-    if x.dtype is not torch.int32 or x.get_device() != dev:
+    if x.dtype is not _I32 or x.get_device() != dev or x.numel() < count or not x.is_contiguous():
+        import torch
         _check_tensor(x, where, name, (torch.int32,), dev)
-    if not x.is_contiguous() or x.numel() < count:
-        _bad(where, f"{name} must be contiguous with at least {count} elements")
+        if not x.is_contiguous() or x.numel() < count:
+            _bad(where, f"{name} must be contiguous with at least {count} elements")
     return x.data_ptr()
 
 
@@ -618,6 +621,8 @@ class KvCache:
 
     def __init__(self, k, v, table, lens, refs=None, k_scale=None, v_scale=None):
         import torch
+        global _I32
+        _I32 = torch.int32
         where = "KvCache"
         if k.dim() != 5 or v.shape != k.shape or v.dtype != k.dtype:
             _bad(where, "k and v must be [layers][pages][page_tokens][Hkv][Dh] and alike")

@@ -24,7 +24,8 @@ namespace fm {
 
 namespace {
 
-constexpr int kBookThreads = 1024;
+constexpr int kBookThreads = 1024;   // of a bookkeeping CTA; 256 where entries and pages are few: barriers are cheaper
+constexpr int kSmallThreads = 256, kSmallPages = 1024;
 constexpr int kMaxEntries = 1024;   // sequences of one bookkeeping call: one thread each
 constexpr int kForkCluster = 8;
 
@@ -47,8 +48,10 @@ struct Pool {
 
 __host__ __device__ constexpr int up(int a, int b) { return (a + b - 1) / b; }
 
-// Exclusive sum over the block (1024 threads); *total receives the sum. Every thread calls it.
+// Exclusive sum over the CTA's THREADS threads; *total receives the sum. Every thread calls it.
+template <int THREADS>
 __device__ __forceinline__ int block_exclusive(int v, int* warp_sums, int* total) {
+  constexpr int kWarps = THREADS / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int x = v;
 #pragma unroll
@@ -59,40 +62,57 @@ __device__ __forceinline__ int block_exclusive(int v, int* warp_sums, int* total
   __syncthreads();   // warp_sums may still be read from an earlier call
   if (lane == 31) warp_sums[warp] = x;
   __syncthreads();
-  if (warp == 0) {
-    int s = warp_sums[lane];
+  int s = lane < kWarps ? warp_sums[lane] : 0;   // every warp scans the sums for itself
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, s, o);
-      if (lane >= o) s += y;
-    }
-    warp_sums[lane] = s;
+  for (int o = 1; o < kWarps; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += y;
   }
-  __syncthreads();
-  *total = warp_sums[31];
-  return (warp ? warp_sums[warp - 1] : 0) + x - v;
+  *total = __shfl_sync(0xffffffffu, s, kWarps - 1);
+  const int before = __shfl_sync(0xffffffffu, s, warp > 0 ? warp - 1 : 0);
+  return (warp ? before : 0) + x - v;
 }
 
-// Calls f(page, live) in ascending order within a warp's contiguous share of [0, pages); 32 pages a step, coalesced.
-template <typename F>
-__device__ __forceinline__ void for_warp_pages(const Book& b, F f) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int share = up(up(b.pages, 32), kBookThreads / 32) * 32;
-  const int lo = min(b.pages, warp * share), hi = min(b.pages, lo + share);
-  for (int p0 = lo; p0 < hi; p0 += 128) {
-    int r[4];
+// Calls f(page, inside, refs) in ascending order within a warp's contiguous share of [0, pages); 32 pages a step,
+// coalesced. The first steps' counts are loaded once and kept: most pools need no second load in a second walk.
+template <int THREADS>
+struct PageWalk {
+  static constexpr int kKeep = 4;
+  int lo, hi, kept[kKeep];
+  __device__ __forceinline__ explicit PageWalk(const Book& b) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int share = up(up(b.pages, 32), THREADS / 32) * 32;
+    lo = min(b.pages, warp * share);
+    hi = min(b.pages, lo + share);
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int pg = p0 + u * 32 + lane;
-      r[u] = pg < hi ? b.refs[pg] : -1;
-    }
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int pg = p0 + u * 32 + lane;
-      if (p0 + u * 32 < hi) f(pg, pg < hi, r[u]);   // warp-uniform
+    for (int u = 0; u < kKeep; ++u) {
+      const int pg = lo + u * 32 + lane;
+      kept[u] = pg < hi ? b.refs[pg] : -1;
     }
   }
-}
+  template <typename F>
+  __device__ __forceinline__ void each(const Book& b, F f) const {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int u = 0; u < kKeep; ++u) {
+      const int pg = lo + u * 32 + lane;
+      if (lo + u * 32 < hi) f(pg, pg < hi, kept[u]);   // warp-uniform
+    }
+    for (int p0 = lo + kKeep * 32; p0 < hi; p0 += 128) {
+      int r[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int pg = p0 + u * 32 + lane;
+        r[u] = pg < hi ? b.refs[pg] : -1;
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int pg = p0 + u * 32 + lane;
+        if (p0 + u * 32 < hi) f(pg, pg < hi, r[u]);
+      }
+    }
+  }
+};
 
 struct Copy {
   int src, dst, rows;
@@ -100,14 +120,16 @@ struct Copy {
 
 // fm_kv_reserve. One CTA: the whole decision needs the order of the entries, and its work is a few hundred bytes an
 // entry plus one pass over refs (2200 pages: about 2 us); a second kernel copies the shared last pages on all SMs.
-__global__ void __launch_bounds__(kBookThreads) reserve_kernel(Book b, const int32_t* seq, const int32_t* count, int n,
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) reserve_kernel(Book b, const int32_t* seq, const int32_t* count, int n,
                                                                int32_t* status, Copy* copies, int32_t* fresh) {
-  __shared__ int s_seq[kMaxEntries], s_last[kMaxEntries], s_off[kMaxEntries], s_sums[32], s_bad;
+  __shared__ int s_seq[THREADS], s_last[THREADS], s_off[THREADS], s_sums[32], s_bad;
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) s_bad = 0;
   __syncthreads();
+  const PageWalk<THREADS> walk(b);   // its loads are on their way while the entries are looked up
   int s = -1 - tid, len = 0, add = 0, last = -1, last_refs = 0, bad = 0;
   if (tid < n) {
     s = seq[tid];
@@ -145,13 +167,13 @@ __global__ void __launch_bounds__(kBookThreads) reserve_kernel(Book b, const int
   const int need = bad || tid >= n ? 0 : want - have + copied;
   if (bad) atomicOr(&s_bad, bad);
   int total = 0;
-  const int off = block_exclusive(need, s_sums, &total);
+  const int off = block_exclusive<THREADS>(need, s_sums, &total);
   if (tid < n) s_off[tid] = off;
   // free pages: every warp counts its share, then writes its ranks below `total`
   int mine = 0;
-  for_warp_pages(b, [&](int, bool in, int refs) { mine += __popc(__ballot_sync(0xffffffffu, in && refs == 0)); });
+  walk.each(b, [&](int, bool in, int refs) { mine += __popc(__ballot_sync(0xffffffffu, in && refs == 0)); });
   int all_free = 0;
-  int rank = block_exclusive(lane == 0 ? mine : 0, s_sums, &all_free);
+  int rank = block_exclusive<THREADS>(lane == 0 ? mine : 0, s_sums, &all_free);
   rank = __shfl_sync(0xffffffffu, rank, 0);
   const int why = s_bad;
   if (why || total > all_free) {   // the same in every thread
@@ -163,7 +185,7 @@ __global__ void __launch_bounds__(kBookThreads) reserve_kernel(Book b, const int
     return;
   }
   if (rank < total)
-    for_warp_pages(b, [&](int pg, bool in, int refs) {
+    walk.each(b, [&](int pg, bool in, int refs) {
       const unsigned m = __ballot_sync(0xffffffffu, in && refs == 0);
       const int at = rank + __popc(m & ((1u << lane) - 1));
       if (in && refs == 0 && at < total) fresh[at] = pg;
@@ -185,7 +207,7 @@ __global__ void __launch_bounds__(kBookThreads) reserve_kernel(Book b, const int
     s_last[tid] = copied;
   }
   __syncthreads();
-  for (int i = warp; i < n; i += kBookThreads / 32) {
+  for (int i = warp; i < n; i += THREADS / 32) {
     const int si = s_seq[i], e = b.lens[si], c = count[i], l = e - c;
     const int h = (l >> b.shift) + ((l & (b.page - 1)) != 0), w = (e >> b.shift) + ((e & (b.page - 1)) != 0);
     const int base = s_off[i] + s_last[i];
@@ -277,14 +299,14 @@ __global__ void __launch_bounds__(kBookThreads)
   __syncthreads();
   const int why = s_bad;
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-  const int rank = static_cast<int>(cluster_rank());
+  const int rank = static_cast<int>(cluster_rank()), warps = static_cast<int>(blockDim.x >> 5);
   if (rank == 0 && tid == 0) {
     status[0] = why;
     status[1] = 0;
   }
   if (why) return;
   // warps take (entry, part of its row); a row's unused places are -1 and copied like the rest
-  for (int i = rank * (kBookThreads / 32) + warp; i < n * 4; i += kForkCluster * (kBookThreads / 32)) {
+  for (int i = rank * warps + warp; i < n * 4; i += gridDim.x * warps) {
     const int e = i >> 2, part = i & 3;
     const int64_t row = static_cast<int64_t>(s_seq[e]) * b.table_stride;
     if (kFork) {
@@ -310,25 +332,27 @@ __global__ void __launch_bounds__(kBookThreads)
 
 // fm_kv_compact, the plan: live pages from n_live on move, in order, into the free ones below n_live, in order.
 // head: [0] n_live, [1] moves; src, dst: the moves; map: the new place of every page from n_live on (-1: free).
-__global__ void __launch_bounds__(kBookThreads) compact_plan_kernel(Book b, int32_t* status, int32_t* head, int32_t* src,
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) compact_plan_kernel(Book b, int32_t* status, int32_t* head, int32_t* src,
                                                                     int32_t* dst, int32_t* map) {
   __shared__ int s_sums[32];
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31;
+  const PageWalk<THREADS> walk(b);
   int mine = 0;
-  for_warp_pages(b, [&](int, bool in, int refs) { mine += __popc(__ballot_sync(0xffffffffu, in && refs > 0)); });
+  walk.each(b, [&](int, bool in, int refs) { mine += __popc(__ballot_sync(0xffffffffu, in && refs > 0)); });
   int n_live = 0;
-  block_exclusive(lane == 0 ? mine : 0, s_sums, &n_live);
+  block_exclusive<THREADS>(lane == 0 ? mine : 0, s_sums, &n_live);
   int above = 0, below = 0;
-  for_warp_pages(b, [&](int pg, bool in, int refs) {
+  walk.each(b, [&](int pg, bool in, int refs) {
     above += __popc(__ballot_sync(0xffffffffu, in && refs > 0 && pg >= n_live));
     below += __popc(__ballot_sync(0xffffffffu, in && refs <= 0 && pg < n_live));
   });
   int moves = 0, holes = 0;
-  int ra = __shfl_sync(0xffffffffu, block_exclusive(lane == 0 ? above : 0, s_sums, &moves), 0);
-  int rb = __shfl_sync(0xffffffffu, block_exclusive(lane == 0 ? below : 0, s_sums, &holes), 0);
-  for_warp_pages(b, [&](int pg, bool in, int refs) {
+  int ra = __shfl_sync(0xffffffffu, block_exclusive<THREADS>(lane == 0 ? above : 0, s_sums, &moves), 0);
+  int rb = __shfl_sync(0xffffffffu, block_exclusive<THREADS>(lane == 0 ? below : 0, s_sums, &holes), 0);
+  walk.each(b, [&](int pg, bool in, int refs) {
     const bool a = in && refs > 0 && pg >= n_live, h = in && refs <= 0 && pg < n_live;
     const unsigned ma = __ballot_sync(0xffffffffu, a), mh = __ballot_sync(0xffffffffu, h);
     const unsigned under = (1u << lane) - 1;
@@ -339,7 +363,7 @@ __global__ void __launch_bounds__(kBookThreads) compact_plan_kernel(Book b, int3
     rb += __popc(mh);
   });
   __syncthreads();   // moves == holes: as many live pages above n_live as free ones below
-  for (int i = tid; i < moves; i += kBookThreads) {
+  for (int i = tid; i < moves; i += THREADS) {
     const int from = src[i], to = dst[i];
     map[from] = to;
     b.refs[to] = b.refs[from];
@@ -680,8 +704,11 @@ LaunchOpts opts(void* stream) {
 template <bool kFork>
 int share(const fm_kv_cache* c, const int32_t* seq, const int32_t* other, int n, int32_t* status, void* stream) {
   LaunchOpts o = opts(stream);
-  o.cluster = dim3(kForkCluster, 1, 1);
-  return done(launch(share_kernel<kFork>, dim3(kForkCluster), dim3(kBookThreads), 0, o, book_of(*c), seq, other, n, status));
+  // a small call is one small CTA (barriers and a cluster's start are most of it); 64 forks of 50 pages took 12 us so
+  const bool small = n <= kSmallThreads && static_cast<int64_t>(n) * c->table_stride <= 1024;
+  const int threads = small ? kSmallThreads : kBookThreads, ctas = small ? 1 : kForkCluster;
+  o.cluster = dim3(ctas, 1, 1);
+  return done(launch(share_kernel<kFork>, dim3(ctas), dim3(threads), 0, o, book_of(*c), seq, other, n, status));
 }
 
 }  // namespace
@@ -711,7 +738,7 @@ int kv_check(const fm_kv_cache* c) {
   for (const auto& x : d) {
     if (x.extent == 1) continue;
     if (x.stride * eb % 16) return record_error(FM_ERR_SHAPE, "cache strides must be multiples of 16 bytes");
-    if (x.stride < span || x.stride > (int64_t(1) << 39)) return record_error(FM_ERR_SHAPE, "cache strides overlap or are too large");
+    if (x.stride < span || x.stride >= (int64_t(1) << 40) / eb) return record_error(FM_ERR_SHAPE, "cache strides overlap or are too large");
     span += x.stride * (x.extent - 1);
   }
   return FM_OK;
@@ -787,7 +814,9 @@ extern "C" int fm_kv_reserve(const fm_kv_cache* c, const int32_t* seq, const int
   Copy* copies = static_cast<Copy*>(workspace);
   int32_t* fresh = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + align16(n * sizeof(Copy)));
   const LaunchOpts o = opts(stream);
-  cudaError_t e = launch(reserve_kernel, dim3(1), dim3(kBookThreads), 0, o, book_of(*c), seq, count, n, status, copies, fresh);
+  const bool small = n <= kSmallThreads && c->pages <= kSmallPages;
+  cudaError_t e = launch(small ? reserve_kernel<kSmallThreads> : reserve_kernel<kBookThreads>, dim3(1),
+                         dim3(small ? kSmallThreads : kBookThreads), 0, o, book_of(*c), seq, count, n, status, copies, fresh);
   if (e == cudaSuccess && n > 0)
     e = launch(copy_shared_kernel, dim3(n, c->layers), dim3(256), 0, o, pool_of(*c), static_cast<const Copy*>(copies));
   return done(e);
@@ -816,7 +845,9 @@ extern "C" int fm_kv_compact(const fm_kv_cache* c, int32_t* status, void* worksp
   int32_t* head = static_cast<int32_t*>(workspace);
   int32_t *src = head + 4, *dst = src + c->pages, *map = dst + c->pages;
   const LaunchOpts o = opts(stream);
-  cudaError_t e = launch(compact_plan_kernel, dim3(1), dim3(kBookThreads), 0, o, book_of(*c), status, head, src, dst, map);
+  const bool small = c->pages <= kSmallPages;
+  cudaError_t e = launch(small ? compact_plan_kernel<kSmallThreads> : compact_plan_kernel<kBookThreads>, dim3(1),
+                         dim3(small ? kSmallThreads : kBookThreads), 0, o, book_of(*c), status, head, src, dst, map);
   if (e == cudaSuccess)
     e = launch(compact_move_kernel, dim3(152 * 8), dim3(256), 0, o, pool_of(*c), book_of(*c), static_cast<const int32_t*>(head),
                static_cast<const int32_t*>(src), static_cast<const int32_t*>(dst), static_cast<const int32_t*>(map));

@@ -72,19 +72,13 @@ __device__ __forceinline__ int first_key(const AttnParams& p, int pos) {
   return p.window > 0 && pos >= p.window ? pos - p.window + 1 : 0;
 }
 
-// True once the phase with the given parity has completed; false after 2^18 polls, in each of which the hardware may
-// suspend the thread for 20 us: seconds at most, and far beyond any legitimate wait. No clock is read between the polls.
+// True once the phase with the given parity has completed; false after 2^22 polls (the hardware suspends the thread in
+// each for a while): far beyond any legitimate wait. No clock is read between the polls, and no suspension time is
+// asked for: with 20 us the E4M3 variant took 285 us instead of 270 for 4096 tokens over 12288 keys.
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity) {
 #pragma unroll 1
-  for (int i = 0; i < (1 << 18); ++i) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.b32 %0, 1, 0, p;\n}\n"
-        : "=r"(done)
-        : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
-        : "memory");
-    if (done) return true;
-  }
+  for (int i = 0; i < (1 << 22); ++i)
+    if (mbar_try_wait(bar, parity)) return true;
   return false;
 }
 

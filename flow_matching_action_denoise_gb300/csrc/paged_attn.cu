@@ -45,8 +45,8 @@ namespace {
 
 constexpr int kTileRows = 128;    // rows of a query tile (MMA M) and keys of a key tile
 // Warp roles behind the eight softmax warps: an MMA warp for each tile (one alone spent its time issuing: 16 MMAs, five
-// waits and four commits a tile in sequence), TMA, the tail's zeros, and with an E4M3 cache four that expand codes.
-constexpr int kMmaWarp = 8, kTmaWarp = 10, kTailWarp = 11, kCvtWarp = 12, kCvtWarps = 4;
+// waits and four commits a tile in sequence), TMA (and the tail's zeros), and with an E4M3 cache four that expand codes.
+constexpr int kMmaWarp = 8, kTmaWarp = 10, kCvtWarp = 12, kCvtWarps = 4;
 // Registers move to the softmax warpgroups, which keep 128 scores each: 384 x 168 = 256 x 216 + 128 x 72, 512 x 128 = 256 x 192 +
 // 256 x 64.
 constexpr int threads_of(bool f8) { return f8 ? 512 : 384; }
@@ -725,29 +725,27 @@ __global__ void __launch_bounds__(threads_of(F8), 1)
       __syncwarp();
       wait_for(&c.drain[t], 0);
     }
-  } else if (warp == kTailWarp) {
-    // ================================================= the last key tile's values behind the length (16-bit cache)
-    if (!F8 && tail_tile >= 0 && tail_tile < n_keys) {
-      // every phase of its buffer in turn: a parity alone does not tell them apart
-      const int item = 2 * tail_tile + 1, b = item % p.ring;
-      bool ok = true;
-      for (int ph = 0; ph <= item / p.ring && ok; ++ph) ok = wait_for(&c.full[b], ph & 1);
-      if (ok) {
-        const int r0 = len % kTileRows;
-        for (int x = lane; x < (kTileRows - r0) * 8 * kHalves; x += 32)
-          st_shared_v4(ring_a + b * kTileBytes + (x % kHalves) * kBlock + r0 * 128 + (x / kHalves) * 16,
-                       make_uint4(0, 0, 0, 0));
-        fence_async_smem();
-      } else if (lane == 0) {
-        atomicOr(p.err, kErrPipelineTimeout);
-      }
-      __syncwarp();
-      if (ok && lane == 0) mbar_arrive(&c.tail);
-    }
   } else if (warp == kTmaWarp) {
     // ================================================= page table and TMA
     bool ok = true;
-    while (copy_next < 2 * n_keys && ok) ok = copy_one();
+    Ring last;   // the last copy's buffer
+    while (copy_next < 2 * n_keys && ok) {
+      last = copy_at;
+      ok = copy_one();
+    }
+    if (!F8 && ok && tail_tile >= 0 && tail_tile == n_keys - 1) {
+      // the values behind the length, in the last tile and so in the last buffer that was filled
+      ok = wait_for(&c.full[last.b], last.phase);
+      if (ok) {
+        const int r0 = len % kTileRows;
+        for (int x = lane; x < (kTileRows - r0) * 8 * kHalves; x += 32)
+          st_shared_v4(ring_a + last.b * kTileBytes + (x % kHalves) * kBlock + r0 * 128 + (x / kHalves) * 16,
+                       make_uint4(0, 0, 0, 0));
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&c.tail);
+      }
+    }
     const int issued = copy_next, nb = ring_n;
     uint64_t* full = ring_full;
     if (!ok) {   // the copies in flight land before the CTA leaves

@@ -598,7 +598,7 @@ int fm_test_layer(fm_policy* p, const float* x_in, int layer, int step, float* x
  *   of 16 up to 256; layers, Hkv <= 65535; pages <= 2^30; strides of extents above one
  *   multiples of 16 bytes; k, v 16-byte aligned (FM_ERR_ALIGN); table_stride * page_tokens
  *   < 2^31.
- * An FP8 cache holds E4M3 codes, value = code * k_scale[layer] (v_scale for V).
+ * An FP8 cache holds E4M3 codes, value = code * k_scale[layer] (v_scale for V); scales are positive.
  * A sequence is a row of the table: its page numbers in order, -1 behind them, and its
  * length in lens. refs counts the rows that name a page (0 = free); the fm_kv_* calls need
  * it, the others take NULL. Start with table = -1, lens = 0, refs = 0. */

@@ -176,7 +176,9 @@ def test_rope_table_values():
     turns = base / 2.0 ** 64 * 4096.0
     assert abs(mag - (0.1 * math.log(8) + 1)) < 1e-6
     assert np.allclose(ratio[turns > 32 * 1.4], 1) and np.allclose(ratio[turns < 1 / 1.4], 8) and (np.diff(ratio) > -1e-9).all()
-    assert np.array_equal(fmad.rope_table(64, 10000.0, fmad.ROPE_BY_PARTS, 1.0, 4096.0)[0], fmad.rope_table(64, 10000.0)[0])
+    # factor 1 mixes equal frequencies: three roundings of doubles, then whole numbers
+    same = fmad.rope_table(64, 10000.0, fmad.ROPE_BY_PARTS, 1.0, 4096.0)[0].astype(np.float64)
+    assert np.allclose(same, base, rtol=2.0 ** -51, atol=1.0)
 
 
 @pytest.mark.parametrize("args,status", [
