@@ -521,7 +521,7 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
     __nv_bfloat16* dst = p.q_out + token * p.os;
 #pragma unroll 4
     for (int h = grp; h < p.H; h += p.groups) {
-      const uint4 u = __ldcs(reinterpret_cast<const uint4*>(src + h * p.Dh + c0)), w = __ldcs(reinterpret_cast<const uint4*>(src + h * p.Dh + c1));
+      const uint4 u = *reinterpret_cast<const uint4*>(src + h * p.Dh + c0), w = *reinterpret_cast<const uint4*>(src + h * p.Dh + c1);
       if (!turned) {
         *reinterpret_cast<uint4*>(dst + h * p.Dh + c0) = u;
         *reinterpret_cast<uint4*>(dst + h * p.Dh + c1) = w;
@@ -547,7 +547,7 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
     const bool is_v = h >= p.Hkv;
     const int hh = is_v ? h - p.Hkv : h;
     const __nv_bfloat16* src = (is_v ? p.v + token * p.vs : p.k + token * p.ks) + hh * p.Dh;
-    const uint4 u = __ldcs(reinterpret_cast<const uint4*>(src + c0)), w = __ldcs(reinterpret_cast<const uint4*>(src + c1));
+    const uint4 u = *reinterpret_cast<const uint4*>(src + c0), w = *reinterpret_cast<const uint4*>(src + c1);
     const int64_t at = cell + hh * p.head;
     if (!F8 && (is_v || !turned)) {
       __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(is_v ? p.vc : p.kc) + at;
