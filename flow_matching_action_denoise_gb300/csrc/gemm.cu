@@ -28,7 +28,6 @@
 #include <atomic>
 
 #include "internal.h"
-#include "kv.h"
 #include "ptx.cuh"
 
 namespace fm {
@@ -682,19 +681,6 @@ bool make_tmap_kblocks(CUtensorMap* map, const void* base, int elem_bytes, uint6
   return r == CUDA_SUCCESS;
 }
 
-bool make_tmap_4d(CUtensorMap* map, const void* base, int elem_bytes, const uint64_t dims[4], const uint64_t strides[3],
-                  const uint32_t box[4], int swizzle) {
-  auto enc = tmap_encoder();
-  if (!enc) return false;
-  const CUtensorMapDataType dt = elem_bytes == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  const cuuint64_t d[4] = {dims[0], dims[1], dims[2], dims[3]}, s[3] = {strides[0], strides[1], strides[2]};
-  const cuuint32_t b[4] = {box[0], box[1], box[2], box[3]}, estr[4] = {1, 1, 1, 1};
-  return enc(map, dt, 4, const_cast<void*>(base), d, s, b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             swizzle == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : swizzle == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 int gemm_plan(int M, int N, int K, int fp8, int s, int cs, GemmShape* g, int tile) {
   if (M < 1 || M > 256 || N <= 0 || K <= 0 || N % 128 || K % 128) return FM_ERR_SHAPE;
   if (tile != kTileN && tile != kTileN / 2) return FM_ERR_SHAPE;
@@ -758,11 +744,11 @@ cudaError_t allow_max_dynamic_smem(const void* kernel, size_t* granted) {
 }
 
 cudaError_t configure_once(int family, cudaError_t (*fn)()) {
-  static std::atomic<uint64_t> done[5];
+  static std::atomic<uint64_t> done[4];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (family < 0 || family >= 5 || dev >= 64) return fn();
+  if (family < 0 || family >= 4 || dev >= 64) return fn();
   const uint64_t bit = 1ull << dev;
   if (done[family].load(std::memory_order_acquire) & bit) return cudaSuccess;
   e = fn();

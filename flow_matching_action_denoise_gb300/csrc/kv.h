@@ -12,11 +12,6 @@ constexpr int kErrBadBatch = 2;
 int kv_check(const fm_kv_cache* c);
 int kv_batch_check(const fm_kv_cache* c, const fm_kv_batch* b);
 
-// 4-D tensor map of 1- or 2-byte elements (dims innermost first, strides in bytes of dims 1..3), swizzle of 128
-// or 64 bytes or none (0), zero fill out of bounds. False on failure.
-bool make_tmap_4d(CUtensorMap* map, const void* base, int elem_bytes, const uint64_t dims[4], const uint64_t strides[3],
-                  const uint32_t box[4], int swizzle);
-
 // Device address of the policy-free building blocks' error word on the current device, or nullptr.
 int* standalone_error_word();
 

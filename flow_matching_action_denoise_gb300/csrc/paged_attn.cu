@@ -27,6 +27,7 @@
 // only when it grows by more than 2^8 (in the exponent: 8), which makes rescaling O rare; the final division makes
 // the result independent of that reference.
 
+#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -868,21 +869,38 @@ __global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ 
     *reinterpret_cast<uint32_t*>(dst) = pack16<false>(acc[0] * inv, acc[1] * inv);
 }
 
+PFN_cuTensorMapEncodeTiled_v12000 tmap_encoder() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q);
+    return e == cudaSuccess && q == cudaDriverEntryPointSuccess ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr)
+                                                                : nullptr;
+  }();
+  return fn;
+}
+
 // Rows of one KV head's page block as a TMA source: (head dim, token, head, page).
 bool kv_tmap(CUtensorMap* map, const fm_kv_cache& c, const void* base, bool decode) {
   const bool f8 = c.fmt == FM_FMT_FP8;
-  const uint64_t eb = f8 ? 1 : 2;
-  const uint64_t dims[4] = {static_cast<uint64_t>(c.Dh), static_cast<uint64_t>(c.page_tokens),
-                            static_cast<uint64_t>(c.Hkv), static_cast<uint64_t>(c.pages)};
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(c.Dh), static_cast<cuuint64_t>(c.page_tokens),
+                              static_cast<cuuint64_t>(c.Hkv), static_cast<cuuint64_t>(c.pages)};
   // the stride of an extent of one is never used: any legal value
-  const auto stride = [&](int64_t s, int extent) { return (extent == 1 ? c.Dh : s) * eb; };
-  const uint64_t strides[3] = {stride(c.token_stride, c.page_tokens), stride(c.head_stride, c.Hkv),
-                               stride(c.page_stride, c.pages)};
-  const uint32_t box[4] = {static_cast<uint32_t>(f8 ? c.Dh : 64),
-                           static_cast<uint32_t>(std::min(c.page_tokens, decode ? kDecodeKeys : kTileRows)), 1, 1};
+  const auto stride = [&](int64_t s, int extent) { return static_cast<cuuint64_t>((extent == 1 ? c.Dh : s) * (f8 ? 1 : 2)); };
+  const cuuint64_t strides[3] = {stride(c.token_stride, c.page_tokens), stride(c.head_stride, c.Hkv),
+                                 stride(c.page_stride, c.pages)};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(f8 ? c.Dh : 64),
+                             static_cast<cuuint32_t>(std::min(c.page_tokens, decode ? kDecodeKeys : kTileRows)), 1, 1};
+  const cuuint32_t steps[4] = {1, 1, 1, 1};
   // codes that are expanded in shared memory lie there in plain rows, all else is read by matrix instructions
-  const int swizzle = f8 ? (decode ? c.Dh : 0) : 128;
-  return make_tmap_4d(map, base, static_cast<int>(eb), dims, strides, box, swizzle);
+  const CUtensorMapSwizzle swizzle = !f8                        ? CU_TENSOR_MAP_SWIZZLE_128B
+                                     : !decode                  ? CU_TENSOR_MAP_SWIZZLE_NONE
+                                     : c.Dh == 128              ? CU_TENSOR_MAP_SWIZZLE_128B
+                                                                : CU_TENSOR_MAP_SWIZZLE_64B;
+  const auto encode = tmap_encoder();
+  return encode && encode(map, f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base),
+                          dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 struct Plan {
@@ -984,12 +1002,20 @@ cudaError_t configure_one() {
                               kSmemLimit + 1024);
 }
 
+// The kernels' shared-memory limits, once a device.
 cudaError_t configure() {
-  cudaError_t e = configure_one<64, false>();
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = configure_one<64, false>();
   if (e == cudaSuccess) e = configure_one<128, false>();
   if (e == cudaSuccess) e = configure_one<64, true>();
   if (e == cudaSuccess) e = configure_one<128, true>();
   if (e == cudaSuccess) e = decode_configure();
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_acq_rel);
   return e;
 }
 
@@ -1052,7 +1078,7 @@ extern "C" int fm_paged_attention(const fm_kv_cache* c, int layer, const fm_kv_b
     return record_error(FM_ERR_CUDA, "cuTensorMapEncodeTiled (cache pages) failed");
   int* err = standalone_error_word();
   if (!err) return record_error(FM_ERR_CUDA, "no error word on the current device");
-  cudaError_t e = configure_once(4, configure);
+  cudaError_t e = configure();
   if (e != cudaSuccess) return record_error(FM_ERR_CUDA, cudaGetErrorString(e));
   AttnParams p = {};
   p.q = reinterpret_cast<const __nv_bfloat16*>(q);
