@@ -764,6 +764,8 @@ def rope_append(cache: KvCache, layer: int, batch: KvBatch, rope: Rope, q, k, v,
         _bad(w, "the cache, the batch and the rotary table must be on one device")
     H, qp, qs, op, os_ = 0, None, 0, None, 0
     if q is not None:
+        if q_out is None or q.dim() != 3:
+            _bad(w, "q and q_out are [tokens][H][Dh], both given or both None")
         H = q.shape[1]
         qp, qs = _heads(q, w, "q", bf, d, T, H, Dh)
         op, os_ = _heads(q_out, w, "q_out", bf, d, T, H, Dh)
@@ -787,7 +789,10 @@ def paged_attention(cache: KvCache, layer: int, batch: KvBatch, q, out, workspac
                     causal: bool = True, window: int = 0, stream=None):
     """Attention of q [tokens][H][Dh] (bfloat16) over the batch's sequences into out; scale None: 1 / sqrt(Dh)."""
     import torch
-    d, w, bf, T, H, Dh = cache.dev, "fm_paged_attention", torch.bfloat16, batch.tokens, q.shape[1], cache.Dh
+    d, w, bf, T, Dh = cache.dev, "fm_paged_attention", torch.bfloat16, batch.tokens, cache.Dh
+    if q.dim() != 3:
+        _bad(w, "q must be [tokens][H][Dh]")
+    H = q.shape[1]
     if batch.dev != d:
         _bad(w, "the cache and the batch must be on one device")
     qp, qs = _heads(q, w, "q", bf, d, T, H, Dh)
@@ -807,6 +812,8 @@ def norm_quant(x, r, gamma, eps: float, x_out, codes, scales, block: int = 0, st
     w, d, f32 = "fm_norm_quant", x.get_device(), torch.float32
     if d < 0:
         _bad(w, "x must be a device tensor")
+    if x.dim() != 2:
+        _bad(w, "x must be [T][d]")
     T, cols = x.shape
     xt = x.dtype
     if xt is not f32 and xt is not torch.bfloat16:

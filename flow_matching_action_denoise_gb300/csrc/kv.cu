@@ -458,12 +458,12 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
   const int len = bad ? 0 : __ldg(p.lens + sid);
   const bool over = bad || nq > p.max_tokens || len < nq || len > p.table_stride * static_cast<int64_t>(p.page);
   if (over && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.err, kErrBadBatch);
-  const int first = blockIdx.x * p.toks;
-  if (bad || first >= nq) return;   // the same for the whole CTA
+  const int first = blockIdx.x * p.toks, end = min(nq, p.max_tokens);
+  if (bad || first >= end) return;   // the same for the whole CTA
   const int past = len - nq;
   for (int x = threadIdx.x; x < p.toks * pairs; x += 256) {
     const int i = x % pairs, w = first + x / pairs;
-    if (w >= nq) break;
+    if (w >= end) break;
     const int64_t at = p.positions ? __ldg(p.positions + begin + w) : past + w;
     // the fraction of a turn as a signed 32-bit number: half turns in [-1, 1) for sincospif
     const uint64_t turn = __ldg(p.freq + i) * static_cast<uint64_t>(at) + (1ull << 31);
@@ -472,7 +472,7 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
     s_angle[x] = make_float2(a.x * p.mag, a.y * p.mag);
   }
   const int within = first + tok;
-  const bool mine = grp < p.groups && within < nq;
+  const bool mine = grp < p.groups && within < end;
   const int64_t token = begin + static_cast<int64_t>(within);
   const int64_t pos = static_cast<int64_t>(past) + within;   // place in the sequence
   int page = -1;
@@ -725,8 +725,11 @@ int kv_check(const fm_kv_cache* c) {
   if (c->Dh < 16 || c->Dh > 256 || c->Dh % 16) return record_error(FM_ERR_SHAPE, "Dh must be a multiple of 16 up to 256");
   if (c->layers > 65535 || c->Hkv > 65535 || c->pages > (1 << 30))
     return record_error(FM_ERR_SHAPE, "layers and Hkv up to 65535, pages up to 2^30");
-  if (static_cast<int64_t>(c->table_stride) * c->page_tokens > INT32_MAX)
-    return record_error(FM_ERR_SHAPE, "table_stride * page_tokens exceeds 2^31 - 1 tokens");
+  if (static_cast<int64_t>(c->table_stride) * c->page_tokens > (1 << 30))
+    return record_error(FM_ERR_SHAPE, "table_stride * page_tokens exceeds 2^30 tokens");
+  // the pages that all rows together could ask for stay countable in 32 bits
+  if (static_cast<int64_t>(c->table_stride) * c->seqs > INT32_MAX)
+    return record_error(FM_ERR_SHAPE, "the table has more than 2^31 - 1 places");
   if (reinterpret_cast<uintptr_t>(c->k) % 16 || reinterpret_cast<uintptr_t>(c->v) % 16)
     return record_error(FM_ERR_ALIGN, "k and v must be 16-byte aligned");
   // rows must not overlap: each stride (of an extent above 1) spans all that is inside of it
@@ -916,6 +919,8 @@ extern "C" int fm_rope_append(const fm_kv_cache* c, int layer, const fm_kv_batch
     if (reinterpret_cast<uintptr_t>(x) % 16) return record_error(FM_ERR_ALIGN, "q, k, v and q_out must be 16-byte aligned");
   int* err = standalone_error_word();
   if (!err) return record_error(FM_ERR_CUDA, "no error word on the current device");
+  const fm_kv_batch bounded = bounded_batch(*b);
+  b = &bounded;
   const bool f8 = c->fmt == FM_FMT_FP8;
   const int eb = f8 ? 1 : 2;
   AppendParams p = {};
@@ -942,10 +947,9 @@ extern "C" int fm_rope_append(const fm_kv_cache* c, int layer, const fm_kv_batch
   // 24 heads of 128: 19.8 us with 16, 23.8 us with 4); a few tokens are spread over all threads of their CTAs.
   const int units = c->Dh / 16;
   p.toks = 1;
-  while (units * p.toks * 2 <= 128 && p.toks < b->max_tokens && b->tokens >= 2 * p.toks * 152 * 3) p.toks *= 2;
+  while (units * p.toks * 2 <= 128 && p.toks < b->max_tokens && b->tokens / (2 * p.toks) >= 152 * 3) p.toks *= 2;
   p.groups = 256 / (units * p.toks);
-  const int64_t blocks = up(b->max_tokens, p.toks);
-  if (b->n > 65535) return record_error(FM_ERR_SHAPE, "a batch takes up to 65535 entries");
+  const int blocks = (b->max_tokens - 1) / p.toks + 1;
   return done(launch(f8 ? append_kernel<true> : append_kernel<false>, dim3(static_cast<unsigned>(blocks), b->n), dim3(256),
                      sizeof(float2) * p.toks * (p.rot / 2), opts(stream), p));
 }

@@ -11,6 +11,11 @@ constexpr int kErrBadBatch = 2;
 // Host checks of the descriptors; FM_OK, or a status with the reason recorded.
 int kv_check(const fm_kv_cache* c);
 int kv_batch_check(const fm_kv_cache* c, const fm_kv_batch* b);
+// The batch with max_tokens no larger than its packed rows: a loose bound costs no empty CTAs.
+inline fm_kv_batch bounded_batch(fm_kv_batch b) {
+  if (b.max_tokens > b.tokens) b.max_tokens = b.tokens;
+  return b;
+}
 
 // Device address of the policy-free building blocks' error word on the current device, or nullptr.
 int* standalone_error_word();

@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(threads_of(TPR)) norm_quant_kernel(const NormP
 template <int TPR, int NV>
 cudaError_t run(const NormParams& p, bool f32, const LaunchOpts& o) {
   constexpr int kThreads = threads_of(TPR);
-  const dim3 grid(static_cast<unsigned>((p.T + kThreads / TPR - 1) / (kThreads / TPR)));
+  const dim3 grid(static_cast<unsigned>((p.T - 1) / (kThreads / TPR) + 1));
   return f32 ? launch(norm_quant_kernel<TPR, NV, true>, grid, dim3(kThreads), 0, o, p)
              : launch(norm_quant_kernel<TPR, NV, false>, grid, dim3(kThreads), 0, o, p);
 }

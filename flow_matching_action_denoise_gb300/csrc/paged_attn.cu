@@ -8,8 +8,8 @@
 // entry and KV head and walks its keys in tiles of 128; S = Q K^T and O += P V run on tcgen05 tensor cores
 // (M = 128) with both accumulators and P in tensor memory, one pass with the running maximum and sum.
 // Two softmax warpgroups share the CTA. With more than 128 rows each owns a 128-row tile and both use every
-// key tile (`pair`); with up to 128 rows they own alternate key tiles of the same rows and merge at the end
-// (`alt`), so that single tokens keep two tiles in flight. While one warpgroup exponentiates, the tensor cores
+// key tile; with up to 128 rows they own alternate key tiles of the same rows and merge at the end
+// (`alt`), so that few rows keep two tiles in flight too (up to 16 rows have a kernel of their own). While one warpgroup exponentiates, the tensor cores
 // work for the other. A long key axis with few rows is cut into splits of whole tiles, one CTA each, whose
 // (max, sum, O) go to the workspace and are joined in split order by combine_kernel.
 //
@@ -18,7 +18,7 @@
 // transpose. Pages outside the sequence are loaded from behind the pool's end, which TMA fills with zeros; the
 // values behind the length inside the last page are zeroed in shared memory, since 0 * NaN is NaN.
 //
-// E4M3 cache. Two warps expand the codes to f16 (exact) into the same tile layout; q is scaled per row by a power
+// E4M3 cache. Four warps expand the codes to f16 (exact) into the same tile layout; q is scaled per row by a power
 // of two that puts its largest element in [2^14, 2^15) and held in f16 (bf16's 8 significant bits are kept down to
 // 2^-28 of that largest element), p is held in f16, so no rounding is coarser than for a 16-bit cache.
 //
@@ -1028,7 +1028,7 @@ int check(const fm_kv_cache* c, const fm_kv_batch* b, int H) {
   if (c->page_tokens > 256) return record_error(FM_ERR_SHAPE, "attention takes pages of 16 to 256 tokens");
   const int64_t rows = static_cast<int64_t>(b->max_tokens) * (H / c->Hkv);
   if (rows > (int64_t(1) << 30)) return record_error(FM_ERR_SHAPE, "max_tokens * H / Hkv exceeds 2^30");
-  const Plan pl = plan_of(*c, *b, H, 0);
+  const Plan pl = plan_of(*c, bounded_batch(*b), H, 0);
   if (c->Hkv > 65535 || static_cast<int64_t>(b->n) * pl.splits > 65535)
     return record_error(FM_ERR_SHAPE, "too many entries for one call (entries x splits and Hkv up to 65535)");
   return FM_OK;
@@ -1042,7 +1042,7 @@ extern "C" int fm_paged_attention_workspace_size(const fm_kv_cache* c, const fm_
   if (!bytes) return fm::record_error(FM_ERR_INVALID_ARG, "bytes is NULL");
   const int st = fm::check(c, b, H);
   if (st != FM_OK) return st;
-  *bytes = b->n && b->tokens ? fm::plan_of(*c, *b, H, 0).workspace : 0;
+  *bytes = b->n && b->tokens ? fm::plan_of(*c, fm::bounded_batch(*b), H, 0).workspace : 0;
   return FM_OK;
 }
 
@@ -1062,6 +1062,8 @@ extern "C" int fm_paged_attention(const fm_kv_cache* c, int layer, const fm_kv_b
     return record_error(FM_ERR_SHAPE, "token strides must be multiples of 8 elements and hold H * Dh");
   if (reinterpret_cast<uintptr_t>(q) % 16 || reinterpret_cast<uintptr_t>(out) % 16)
     return record_error(FM_ERR_ALIGN, "q and out must be 16-byte aligned");
+  const fm_kv_batch bounded = bounded_batch(*b);
+  b = &bounded;
   const Plan pl = plan_of(*c, *b, H, window);
   const size_t need = pl.workspace;
   if (need) {

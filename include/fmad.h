@@ -597,7 +597,7 @@ int fm_test_layer(fm_policy* p, const float* x_in, int layer, int step, float* x
  *   fmt BF16 or FP8 (FM_ERR_INVALID_ARG); page_tokens 16, 32, 64, 128 or 256; Dh a multiple
  *   of 16 up to 256; layers, Hkv <= 65535; pages <= 2^30; strides of extents above one
  *   multiples of 16 bytes; k, v 16-byte aligned (FM_ERR_ALIGN); table_stride * page_tokens
- *   < 2^31.
+ *   <= 2^30 and seqs * table_stride < 2^31.
  * An FP8 cache holds E4M3 codes, value = code * k_scale[layer] (v_scale for V); scales are positive.
  * A sequence is a row of the table: its page numbers in order, -1 behind them, and its
  * length in lens. refs counts the rows that name a page (0 = free); the fm_kv_* calls need
@@ -704,7 +704,7 @@ typedef struct fm_rope {
 /* Rotate the batch's queries into q_out and its keys into the cache's pages, and store its
  * values there: q [tokens][H][Dh], k, v [tokens][Hkv][Dh], q_out like q, all bf16 with
  * `stride` elements between tokens (a multiple of 8; parts of one merged projection output
- * do); q_out may be q. H = 0 stores keys and values only. The pages must exist
+ * do); q_out may be q, else it overlaps none of them. A sequence is in the batch once. H = 0 stores keys and values only. The pages must exist
  * (fm_kv_reserve); pages of an FP8 cache receive E4M3(x * fp32(1 / scale)), saturated.
  * positions: NULL, or device int32 [tokens] that replaces the positions in the angles (not
  * the places in the cache). A token without a page sets bit 2 of fm_standalone_status and

@@ -116,3 +116,17 @@ def test_graph_and_stream():
     g.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(u, w) for u, w in zip(a, b))
+
+
+def test_the_binding_refuses():
+    require_gpu()
+    x = torch.zeros((4, 64), device="cuda")
+    r = x.to(torch.bfloat16)
+    good = dict(x=x, r=r, gamma=x[0], eps=1e-6, x_out=x, codes=torch.empty((4, 64), dtype=torch.uint8, device="cuda"),
+                scales=torch.empty(4, device="cuda"))
+    fmad.norm_quant(**good)
+    for bad in (dict(x=x[0]), dict(x=x.half()), dict(x=x.cpu()), dict(x=x[:, ::2]), dict(r=x), dict(r=r[:3]), dict(gamma=r[0]),
+                dict(gamma=x[0, :32]), dict(x_out=r), dict(codes=good["codes"][:3]), dict(scales=good["scales"][:3]),
+                dict(block=128, scales=torch.empty(5, device="cuda")), dict(block=64), dict(eps=-1.0)):
+        with pytest.raises(fmad.FmError):
+            fmad.norm_quant(**{**good, **bad})

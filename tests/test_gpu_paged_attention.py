@@ -234,3 +234,36 @@ def test_device_side_faults_are_reported():
     assert run(batch(c, [3, 3])) == 2
     c.lens[c.rows[0]] = 100
     assert run(batch(c, [3, 3])) == 0
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_a_loose_bound_on_the_new_tokens(fp8):
+    """A bound above the packed rows gives the same variant, workspace and results."""
+    require_gpu()
+    c = Cache([700, 30], 16, 2, 128, fp8, seed=4)
+    ids = torch.tensor(np.asarray(c.rows), dtype=torch.int32, device="cuda")
+    for new in ([1, 1], [60, 2]):
+        start = torch.tensor([0, new[0], sum(new)], dtype=torch.int32, device="cuda")
+        q = torch.randn((sum(new), 4, 128), device="cuda").to(torch.bfloat16)
+        outs = []
+        for bound in (sum(new), 1 << 28):
+            b = fmad.KvBatch(start, sum(new), bound, 700, ids)
+            ws = torch.empty(fmad.paged_attention_workspace_size(c.handle, b, 4), dtype=torch.uint8, device="cuda")
+            outs.append(torch.full_like(q, 7.0))
+            fmad.paged_attention(c.handle, 0, b, q, outs[-1], ws)
+        assert fmad.standalone_status() == 0 and torch.equal(*outs)
+        check(c, new, q, outs[0], batch(c, new), True, 0, 128 ** -0.5)
+
+
+def test_the_binding_refuses():
+    require_gpu()
+    c = Cache([20], 16, 2, 64, seed=1, poison=False)
+    b = batch(c, [4])
+    q = torch.zeros((4, 4, 64), device="cuda", dtype=torch.bfloat16)
+    good = dict(q=q, out=torch.empty_like(q))
+    fmad.paged_attention(c.handle, 0, b, **good)
+    for bad in (dict(q=q[0]), dict(q=q[:3]), dict(q=q.float()), dict(q=q.cpu()), dict(q=q[:, :, ::2]), dict(q=q[:, :3]),
+                dict(out=q[:, :2]), dict(out=torch.empty((4, 64, 4), device="cuda", dtype=torch.bfloat16).transpose(1, 2)),
+                dict(workspace=torch.empty(64)), dict(scale=0.0), dict(window=-1), dict(layer=1)):
+        with pytest.raises(fmad.FmError):
+            fmad.paged_attention(c.handle, bad.pop("layer", 0), b, **{**good, **bad})

@@ -175,3 +175,36 @@ def test_saturation_and_device_side_faults():
     c.lens[c.rows[0]] = 2      # fewer than the new tokens: the first two have no place
     fmad.rope_append(c.handle, 0, b, fmad.Rope(16), None, k, k, None)
     assert fmad.standalone_status() == 2
+
+
+def test_bounds_on_the_new_tokens():
+    """A bound above the packed rows changes nothing; rows behind a bound that is too small are left as they were."""
+    require_gpu()
+    k, v, q = (torch.randn((40, n, 64), device="cuda").to(torch.bfloat16) for n in (1, 1, 3))
+    stores, outs = [], []
+    for bound in (30, 1 << 30, 7):
+        c = Cache([50, 60], 16, 1, 64, seed=2, poison=False)
+        out = torch.full_like(q, 7.0)
+        fmad.rope_append(c.handle, 0, batch(c, [30, 10], max_tokens=bound), fmad.Rope(64), q, k, v, out)
+        assert fmad.standalone_status() == (2 if bound == 7 else 0)
+        outs.append(out)
+        stores.append((c.k.clone(), c.v.clone()))
+    assert torch.equal(outs[0], outs[1]) and all(torch.equal(a, b) for a, b in zip(*stores[:2]))
+    kept = [*range(7), *range(30, 37)]
+    assert torch.equal(outs[2][kept], outs[0][kept])
+    assert outs[2][7:30].eq(7).all() and outs[2][37:].eq(7).all()
+
+
+def test_the_binding_refuses():
+    require_gpu()
+    c = Cache([20], 16, 2, 64, seed=1, poison=False)
+    b, rope = batch(c, [4]), fmad.Rope(64)
+    q, k = (torch.zeros((4, n, 64), device="cuda", dtype=torch.bfloat16) for n in (4, 2))
+    good = dict(q=q, k=k, v=k, q_out=q)
+    fmad.rope_append(c.handle, 0, b, rope, **good)
+    for bad in (dict(q_out=None), dict(q=q[0]), dict(q=q[:3]), dict(k=k.float()), dict(v=k.cpu()), dict(k=k[:, :, ::2]),
+                dict(v=q), dict(q_out=q.transpose(1, 2).contiguous().transpose(1, 2)),
+                dict(positions=torch.zeros(3, dtype=torch.int32, device="cuda")),
+                dict(positions=torch.zeros(4, dtype=torch.int64, device="cuda"))):
+        with pytest.raises(fmad.FmError):
+            fmad.rope_append(c.handle, 0, b, rope, **{**good, **bad})

@@ -47,6 +47,7 @@ BAD_CACHES = [
     (dict(k=P + 8), 3), (dict(v=P + 2), 3), (dict(token_stride=120), 2), (dict(head_stride=60), 2),
     (dict(page_stride=128), 2), (dict(page_stride=4096), 2), (dict(layer_stride=16), 2), (dict(token_stride=132), 2), (dict(head_stride=-64), 2),
     (dict(page_stride=1 << 50), 2), (dict(table_stride=1 << 28), 2),
+    (dict(table_stride=(1 << 26) + 1), 2), (dict(table_stride=1 << 26, seqs=32), 2),
 ]
 
 
@@ -125,6 +126,16 @@ def test_attention(lib):
     assert lib.fm_paged_attention_workspace_size(at(long), at(bl), 4, None) == 1
     # nothing to do
     assert call(b=batch(n=0)) == 0 and call(b=batch(tokens=0)) == 0 and call(b=batch(max_tokens=0)) == 0
+
+
+def test_a_loose_bound_on_the_new_tokens(lib):
+    """max_tokens above the packed rows changes neither the variant nor the workspace."""
+    c, a, b = cache(table_stride=4000), ctypes.c_size_t(), ctypes.c_size_t()
+    for tokens, H in ((1, 4), (5, 4), (40, 64)):
+        tight, loose = (batch(n=1, tokens=tokens, max_tokens=m, max_len=60000) for m in (tokens, 1 << 20))
+        assert lib.fm_paged_attention_workspace_size(at(c), at(tight), H, ctypes.byref(a)) == 0
+        assert lib.fm_paged_attention_workspace_size(at(c), at(loose), H, ctypes.byref(b)) == 0
+        assert a.value == b.value > 0
 
 
 def test_rope_append(lib):
