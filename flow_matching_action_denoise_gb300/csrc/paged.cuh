@@ -26,6 +26,7 @@ struct AttnParams {
   const float* k_scale;
   const float* v_scale;
   int alt, splits, split_tiles;
+  int row_blocks, rows_first;     // of paged_attn.cu's grid
   int ring, raw_ring;
   float* part_o;                  // [splits][tokens * H][Dh]
   float2* part_ml;                // [splits][tokens * H] (log2 maximum, sum)
