@@ -26,6 +26,13 @@
 // cache), the operand type of the second product; the output is rounded once to bf16. The running maximum moves
 // only when it grows by more than 2^8 (in the exponent: 8), which makes rescaling O rare; the final division makes
 // the result independent of that reference.
+//
+// Bounds and measurements. 4 Dh FLOP a head, query row and key on the tensor cores: 4096 tokens of 16 heads (2 KV heads,
+// Dh 128) over 12288 keys, causal, take 257 us, 1.33 PFLOP/s, 69 % of the library's dense bf16 rate; E4M3 cache 272 us.
+// What is missing: 256 CTAs fill 1.7 waves of 152, and inside a wave the tensor pipe is active for 60 % of the cycles
+// (one wave of 256 rows over 4224 keys a CTA, 66 us): a tile's exponentials wait for its TMEM reads, which queue behind
+// the other tile's MMAs. Small calls are bound by their ends: about 7 us a CTA from launch to the first scores and from
+// the last products to the stored rows, 1.4 us a key tile of both query tiles between.
 
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -807,7 +814,7 @@ __global__ void __launch_bounds__(threads_of(F8), 1)
   }
 }
 
-// Joins the splits of every (token, head) row: `warps` (1, 2, 4 or 8, a power of two) of a CTA's eight share a row, each
+// Joins the splits of every (token, head) row (bound by latency, the shares come from L2): `warps` (1, 2, 4 or 8, a power of two) of a CTA's eight share a row, each
 // every warps-th split, and are summed in warp order.
 template <int DH>
 __global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ part_o, const float2* __restrict__ part_ml,

@@ -1,6 +1,7 @@
 // Attention over a paged cache for up to 16 stacked rows (tokens x query heads of a KV head): single tokens.
 //
-// Bound by reading the cache. A CTA takes one entry, KV head and split of its keys: a warp moves tiles of 64 keys by
+// Bound by reading the cache: 64 sequences of 8192 keys on 2 KV heads, Dh 128, take 48.5 us with an E4M3 cache (5.5 TB/s,
+// 82 % of a plain copy's rate) and 83 us with bf16 (6.5 TB/s); 789 keys on one KV head take 6 us, launch and join. A CTA takes one entry, KV head and split of its keys: a warp moves tiles of 64 keys by
 // TMA into a three-stage ring, four warps take 16 keys each of every tile. Keys and head dims are the M = 16 of
 // m16n8k16 tensor core instructions and the stacked rows their N, eight or sixteen: S^T = K Q^T, O^T = V^T P^T. So keys
 // and values pass from shared memory straight into the fragments of one warp, and eight rows cost no padding (rows as
@@ -237,7 +238,10 @@ __global__ void __launch_bounds__(kThreads, kResident<DH, F8, NT>)
       const uint32_t kt = smem_u32(smem) + at.b * 2 * kTile, vt = kt + kTile;
       const int k0 = (t_lo + j) * kDecodeKeys + warp * 16;
       if (k0 < hi_all && k0 + 16 > lo_all) {
-        float s[NT][4] = {};
+        // E4M3: two chains of dependent products (16.6 -> 15.9 us for 32 sequences of 4096 keys; no gain for bf16, which
+        // waits for its bytes, nor with two row tiles, which have no registers left)
+        constexpr bool kChains = F8 && NT == 1;
+        float s[NT][4] = {}, s1[NT][4] = {};
         if constexpr (F8) {
 #pragma unroll
           for (int c = 0; c < DH / 32; ++c) {
@@ -249,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, kResident<DH, F8, NT>)
               expand4(r[2 * y], a[0], a[2]);
               expand4(r[2 * y + 1], a[1], a[3]);
 #pragma unroll
-              for (int x = 0; x < NT; ++x) mma16816<true>(s[x], a, qf[x][2 * c + y][0], qf[x][2 * c + y][1]);
+              for (int x = 0; x < NT; ++x) mma16816<true>(kChains && y ? s1[x] : s[x], a, qf[x][2 * c + y][0], qf[x][2 * c + y][1]);
             }
           }
         } else {
@@ -260,6 +264,10 @@ __global__ void __launch_bounds__(kThreads, kResident<DH, F8, NT>)
 #pragma unroll
             for (int x = 0; x < NT; ++x) mma16816<false>(s[x], a, qf[x][c][0], qf[x][c][1]);
           }
+        }
+        if constexpr (kChains) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[0][e] += s1[0][e];
         }
         // s[x][0..1]: key g, rows 2 t, 2 t + 1 of tile x; s[x][2..3]: key g + 8
         bool edge = false, grow = false;
