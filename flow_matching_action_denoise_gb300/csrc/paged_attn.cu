@@ -28,7 +28,7 @@
 // the result independent of that reference.
 //
 // Bounds and measurements. 4 Dh FLOP a head, query row and key on the tensor cores: 4096 tokens of 16 heads (2 KV heads,
-// Dh 128) over 12288 keys, causal, take 257 us, 1.33 PFLOP/s, 69 % of the library's dense bf16 rate; E4M3 cache 272 us.
+// Dh 128) over 12288 keys, causal, take 259 us, 1.33 PFLOP/s, 69 % of the library's dense bf16 rate; E4M3 cache 272 us.
 // What is missing: 256 CTAs fill 1.7 waves of 152, and inside a wave the tensor pipe is active for 60 % of the cycles
 // (one wave of 256 rows over 4224 keys a CTA, 66 us): a tile's exponentials wait for its TMEM reads, which queue behind
 // the other tile's MMAs. Small calls are bound by their ends: about 7 us a CTA from launch to the first scores and from

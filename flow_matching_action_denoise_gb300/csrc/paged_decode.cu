@@ -1,7 +1,7 @@
 // Attention over a paged cache for up to 16 stacked rows (tokens x query heads of a KV head): single tokens.
 //
-// Bound by reading the cache: 64 sequences of 8192 keys on 2 KV heads, Dh 128, take 48.5 us with an E4M3 cache (5.5 TB/s,
-// 82 % of a plain copy's rate) and 83 us with bf16 (6.5 TB/s); 789 keys on one KV head take 6 us, launch and join. A CTA takes one entry, KV head and split of its keys: a warp moves tiles of 64 keys by
+// Bound by reading the cache: 64 sequences of 8192 keys on 2 KV heads, Dh 128, take 46 us with an E4M3 cache (5.8 TB/s,
+// 86 % of a plain copy's rate) and 80 us with bf16 (6.7 TB/s); 789 keys on one KV head take 6 us, launch and join. A CTA takes one entry, KV head and split of its keys: a warp moves tiles of 64 keys by
 // TMA into a three-stage ring, four warps take 16 keys each of every tile. Keys and head dims are the M = 16 of
 // m16n8k16 tensor core instructions and the stacked rows their N, eight or sixteen: S^T = K Q^T, O^T = V^T P^T. So keys
 // and values pass from shared memory straight into the fragments of one warp, and eight rows cost no padding (rows as
