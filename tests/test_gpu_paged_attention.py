@@ -267,3 +267,16 @@ def test_the_binding_refuses():
                 dict(workspace=torch.empty(64)), dict(scale=0.0), dict(window=-1), dict(layer=1)):
         with pytest.raises(fmad.FmError):
             fmad.paged_attention(c.handle, bad.pop("layer", 0), b, **{**good, **bad})
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("Dh", [64, 128])
+@pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 200)])
+def test_whole_prefills(causal, window, Dh, fp8):
+    """Most of each sequence is new: ragged entries of many row blocks, some empty, some with a short history."""
+    require_gpu()
+    lens = [900, 1, 300, 17, 513, 256, 700]
+    new = [900, 1, 0, 17, 513, 200, 690]
+    c = Cache(lens, 32, 2, Dh, fp8, seed=9)
+    q, out, b = attend(c, new, 8, causal, window, lead=3, trail=2)
+    check(c, new, q, out, b, causal, window, Dh ** -0.5)

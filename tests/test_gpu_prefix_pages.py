@@ -317,3 +317,26 @@ def test_python_refuses_what_the_library_cannot_see():
     with pytest.raises(fmad.FmError):
         fmad.norm_quant(q.view(2, 256), None, None, 1e-6, None, torch.empty((2, 256), dtype=torch.int8, device="cuda"),
                         torch.empty(2, device="cuda"))
+
+
+def test_refresh_prefix_pages_of_sessions_and_in_a_capture():
+    """A session takes its own prefix from the pages and leaves its policy's alone; a captured hand-over follows the pages."""
+    require_gpu()
+    cfg, a = policy("expert_bf16_m63", P=64)
+    s = a.session()
+    c = Cache([80, 70], 16, cfg.Hkv, cfg.Dh, layers=cfg.L, seed=4)
+    a.refresh_prefix_pages(0, 64, c.handle, int(c.rows[0]))
+    mine = a.buffer("prefix_k").clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        s.refresh_prefix_pages(0, 64, c.handle, int(c.rows[1]), 6)
+    for x in (c.k, c.v):
+        x.neg_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert fmad.device_status(s.handle) == 0 and torch.equal(a.buffer("prefix_k"), mine)
+    want = torch.stack([c.dense(1, l)[0][6:70] for l in range(cfg.L)]).to(torch.bfloat16)
+    assert torch.equal(s.buffer("prefix_k", torch.bfloat16, want.shape), want)
+    dense = [torch.stack([c.dense(1, l)[j][6:70] for l in range(cfg.L)]).to(torch.bfloat16).contiguous() for j in range(2)]
+    a.refresh_prefix(0, 64, *dense)
+    assert torch.equal(a.buffer("prefix_v"), s.buffer("prefix_v"))
