@@ -28,7 +28,7 @@
 // the result independent of that reference.
 //
 // Bounds and measurements. 4 Dh FLOP a head, query row and key on the tensor cores: 4096 tokens of 16 heads (2 KV heads,
-// Dh 128) over 12288 keys, causal, take 259 us, 1.33 PFLOP/s, 69 % of the library's dense bf16 rate; E4M3 cache 272 us.
+// Dh 128) over 12288 keys, causal, take 253 us, 1.36 PFLOP/s, 70 % of the library's dense bf16 rate; E4M3 cache 269 us.
 // What is missing: 256 CTAs fill 1.7 waves of 152, and inside a wave the tensor pipe is active for 60 % of the cycles
 // (one wave of 256 rows over 4224 keys a CTA, 66 us): a tile's exponentials wait for its TMEM reads, which queue behind
 // the other tile's MMAs. Small calls are bound by their ends: about 7 us a CTA from launch to the first scores and from
@@ -55,8 +55,9 @@ constexpr int kTileRows = 128;    // rows of a query tile (MMA M) and keys of a 
 // Warp roles behind the eight softmax warps: an MMA warp for each tile (one alone spent its time issuing: 16 MMAs, five
 // waits and four commits a tile in sequence), TMA (and the tail's zeros), and with an E4M3 cache four that expand codes.
 constexpr int kMmaWarp = 8, kTmaWarp = 10, kCvtWarp = 12, kCvtWarps = 4;
-// Registers move to the softmax warpgroups, which keep 128 scores each: 384 x 168 = 256 x 216 + 128 x 72, 512 x 128 = 256 x 192 +
-// 256 x 64.
+// Registers move to the softmax warpgroups, which keep 128 scores each: 384 x 168 = 256 x 224 + 128 x 56, 512 x 128 = 256 x 200 +
+// 256 x 56 (8 fewer for them and 16 or 8 more for the others: 259.5 us against 254.5 for 4096 tokens over 12288 keys, E4M3 272.5
+// against 269; 208 and 48 with E4M3 spill: 291 us).
 constexpr int threads_of(bool f8) { return f8 ? 512 : 384; }
 constexpr int kSmemLimit = 226 * 1024;
 constexpr int kMaxRing = 8;
@@ -341,14 +342,14 @@ __global__ void __launch_bounds__(threads_of(F8), 1)
   // one instruction for a whole warpgroup
   if (warp < 8) {
     if constexpr (F8)
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     else
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
   } else {
     if constexpr (F8)
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     else
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
   }
 
   if (warp < 8) {
@@ -475,10 +476,16 @@ __global__ void __launch_bounds__(threads_of(F8), 1)
         }
       };
 #pragma unroll
-      for (int part = 0; part < 2; ++part) {
-        uint32_t w[32];
-        probabilities(part * 64, 32, w);
-        tmem_st32(t_s + part * 32, w);
+      for (int part = 0; part < (F8 ? 2 : 4); ++part) {   // narrow parts hold fewer registers (254.1 -> 252.4 us); E4M3: 269.4 -> 271.6
+        if constexpr (F8) {
+          uint32_t w[32];
+          probabilities(part * 64, 32, w);
+          tmem_st32(t_s + part * 32, w);
+        } else {
+          uint32_t w[16];
+          probabilities(part * 32, 16, w);
+          tmem_st16(t_s + part * 16, w);
+        }
       }
       tmem_wait_st();
       tc_fence_before();
