@@ -340,3 +340,49 @@ def test_refresh_prefix_pages_of_sessions_and_in_a_capture():
     dense = [torch.stack([c.dense(1, l)[j][6:70] for l in range(cfg.L)]).to(torch.bfloat16).contiguous() for j in range(2)]
     a.refresh_prefix(0, 64, *dense)
     assert torch.equal(a.buffer("prefix_v"), s.buffer("prefix_v"))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("order,pad", [((1, 0, 3, 2, 4), 16), ((1, 0, 2, 3, 4), 0), ((0, 3, 1, 2, 4), 32), ((3, 1, 0, 2, 4), 0)])
+def test_pools_of_any_order_and_gaps(order, pad, fp8):
+    """Pools whose dims lie in other orders, with gaps behind the rows, give bit for bit what a dense pool gives: growth
+    with a copied page, append, attention (many rows and single tokens), compaction, a policy's prefix."""
+    require_gpu()
+    results = []
+    for free in (False, True):
+        c = Cache([70, 33, 150], 16, 2, 64, fp8, layers=2, seqs=8, rows=[0, 1, 2], seed=7, poison=False, spare_pages=12)
+        if free:
+            pools = []
+            for x in (c.k, c.v):
+                y = x.permute(order)
+                raw = torch.zeros((*y.shape[:-1], 64 + pad), dtype=x.dtype, device="cuda")
+                back = [order.index(i) for i in range(5)]
+                view = raw[..., :64].permute(back)
+                view.copy_(x)
+                pools.append(view)
+            c.k, c.v = pools
+            c.handle = fmad.KvCache(c.k, c.v, c.table, c.lens, c.refs, c.k_scale, c.v_scale)
+        h, st = c.handle, torch.zeros(2, dtype=torch.int32, device="cuda")
+        ws = torch.empty(max(fmad.kv_workspace_size(h, 4), fmad.kv_workspace_size(h)), dtype=torch.uint8, device="cuda")
+        fmad.kv_fork(h, i32([0]), i32([3]), st)
+        fmad.kv_reserve(h, i32([0, 3, 1, 2]), i32([40, 3, 1, 1]), st, ws)
+        assert st.tolist()[0] == 0
+        b = fmad.KvBatch(i32([0, 40, 43, 44, 45]), 45, 40, 160, i32([0, 3, 1, 2]))
+        g = torch.Generator().manual_seed(1)
+        q, k, v = (torch.randn((45, n, 64), generator=g).to(torch.bfloat16).cuda() for n in (8, 2, 2))
+        outs = [torch.empty_like(q)]
+        fmad.rope_append(h, 1, b, fmad.Rope(64), q, k, v, outs[0])
+        for batch_ in (b, fmad.KvBatch(i32([43, 44, 45]), 45, 1, 160, i32([1, 2]))):
+            for layer in (0, 1):
+                outs.append(torch.zeros_like(q))
+                need = fmad.paged_attention_workspace_size(h, batch_, 8)
+                fmad.paged_attention(h, layer, batch_, outs[0], outs[-1], torch.empty(need, dtype=torch.uint8, device="cuda"))
+        fmad.kv_release(h, i32([1]), st)
+        fmad.kv_compact(h, st, ws)
+        assert st.tolist()[0] == 0 and st.tolist()[1] > 0 and fmad.standalone_status() == 0
+        for i, n in ((0, 110), (3, 73), (2, 151)):
+            at = torch.arange(n, device="cuda")
+            pg = c.table[i][at // 16].long()
+            outs += [x[:, pg, at % 16].float() for x in (c.k, c.v)]
+        results.append(outs + [c.table.clone(), c.lens.clone(), c.refs.clone()])
+    assert all(torch.equal(a, b) for a, b in zip(*results))
