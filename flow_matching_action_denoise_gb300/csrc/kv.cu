@@ -118,17 +118,60 @@ struct Copy {
   int src, dst, rows;
 };
 
+// A set of numbers >= 0 in shared memory, open addressing, at most half full: what the entries of a call have in common is
+// found in a few steps each (compared pair by pair 1024 forks took 70 us).
+constexpr int kSlotsPer = 2;   // slots an entry
+template <int SLOTS>
+struct Set {
+  int key[SLOTS];
+  __device__ __forceinline__ static unsigned home(int k) {   // Fibonacci hashing
+    return (static_cast<unsigned>(k) * 2654435769u) >> 16 & (SLOTS - 1);
+  }
+  __device__ __forceinline__ void clear(int tid, int threads) {
+    for (int x = tid; x < SLOTS; x += threads) key[x] = -1;
+  }
+  // the slot of k, which is put there if it is new
+  __device__ __forceinline__ int put(int k, bool* old) {
+    unsigned at = home(k);
+    for (int x = 0; x < SLOTS; ++x, at = (at + 1) & (SLOTS - 1)) {
+      const int was = atomicCAS(&key[at], -1, k);
+      if (was == -1 || was == k) {
+        *old = was == k;
+        return static_cast<int>(at);
+      }
+    }
+    *old = true;   // not reached: there are more slots than entries
+    return 0;
+  }
+  __device__ __forceinline__ bool has(int k) const {
+    unsigned at = home(k);
+    for (int x = 0; x < SLOTS; ++x, at = (at + 1) & (SLOTS - 1)) {
+      if (key[at] == k) return true;
+      if (key[at] == -1) return false;
+    }
+    return false;
+  }
+};
+
 // fm_kv_reserve. One CTA: the whole decision needs the order of the entries, and its work is a few hundred bytes an
-// entry plus one pass over refs (2200 pages: about 2 us); a second kernel copies the shared last pages on all SMs.
+// entry plus two passes over refs; a second kernel copies the shared last pages on all SMs. Bound by latency (one token more
+// of 64 sequences in a pool of 2200 pages: 5.1 us with the copies' kernel, of 1024 in 40000: 10.8 us; new pages are dealt
+// out a thread each, which finds its entry by bisection).
 template <int THREADS>
 __global__ void __launch_bounds__(THREADS) reserve_kernel(Book b, const int32_t* seq, const int32_t* count, int n,
                                                                int32_t* status, Copy* copies, int32_t* fresh) {
-  __shared__ int s_seq[THREADS], s_last[THREADS], s_off[THREADS], s_sums[32], s_bad;
+  constexpr int kSlots = kSlotsPer * THREADS;
+  __shared__ int s_seq[THREADS], s_have[THREADS], s_off[THREADS], s_sums[32], s_bad;
+  __shared__ Set<kSlots> seqs, lasts;               // the sequences, and their begun last pages:
+  __shared__ int s_users[kSlots], s_keeper[kSlots];   // entries that write to one, and the last of them
   pdl_trigger();
-  pdl_wait();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31;
   if (tid == 0) s_bad = 0;
+  seqs.clear(tid, THREADS);
+  lasts.clear(tid, THREADS);
+  for (int x = tid; x < kSlots; x += THREADS) s_users[x] = 0, s_keeper[x] = -1;
   __syncthreads();
+  pdl_wait();
   const PageWalk<THREADS> walk(b);   // its loads are on their way while the entries are looked up
   int s = -1 - tid, len = 0, add = 0, last = -1, last_refs = 0, bad = 0;
   if (tid < n) {
@@ -152,15 +195,26 @@ __global__ void __launch_bounds__(THREADS) reserve_kernel(Book b, const int32_t*
       }
     }
     s_seq[tid] = s;
-    s_last[tid] = last;
+  }
+  int slot = 0;
+  bool again = false;
+  if (tid < n && s >= 0 && s < b.seqs) {
+    seqs.put(s, &again);
+    if (again) bad |= FM_KV_BAD_ENTRY;
+  }
+  if (last >= 0) {
+    slot = lasts.put(last, &again);
+    atomicAdd(&s_users[slot], 1);
+    atomicMax(&s_keeper[slot], tid);
   }
   __syncthreads();
-  int earlier = 0;   // entries before this one that share its last page
-  for (int j = 0; j < tid && tid < n; ++j) {
-    if (s_seq[j] == s) bad |= FM_KV_BAD_ENTRY;
-    earlier += last >= 0 && s_last[j] == last;
+  // a shared last page: every entry that writes to it gets a copy, but the last one where no other row names it
+  bool copied = false;
+  if (last >= 0) {
+    const int users = s_users[slot];
+    if (users > last_refs) bad |= FM_KV_BAD_ENTRY;   // more rows than the page's count knows of
+    copied = users < last_refs || s_keeper[slot] != tid;
   }
-  const bool copied = last >= 0 && last_refs - earlier > 1;
   const int have = (len >> b.shift) + ((len & (b.page - 1)) != 0);
   const int end = len + add;
   const int want = (end >> b.shift) + ((end & (b.page - 1)) != 0);
@@ -168,7 +222,10 @@ __global__ void __launch_bounds__(THREADS) reserve_kernel(Book b, const int32_t*
   if (bad) atomicOr(&s_bad, bad);
   int total = 0;
   const int off = block_exclusive<THREADS>(need, s_sums, &total);
-  if (tid < n) s_off[tid] = off;
+  if (tid < n) {
+    s_off[tid] = off;
+    s_have[tid] = have << 1 | copied;
+  }
   // free pages: every warp counts its share, then writes its ranks below `total`
   int mine = 0;
   walk.each(b, [&](int, bool in, int refs) { mine += __popc(__ballot_sync(0xffffffffu, in && refs == 0)); });
@@ -204,18 +261,21 @@ __global__ void __launch_bounds__(THREADS) reserve_kernel(Book b, const int32_t*
       atomicSub(&b.refs[last], 1);
     }
     b.lens[s] = end;
-    s_last[tid] = copied;
   }
-  __syncthreads();
-  for (int i = warp; i < n; i += THREADS / 32) {
-    const int si = s_seq[i], e = b.lens[si], c = count[i], l = e - c;
-    const int h = (l >> b.shift) + ((l & (b.page - 1)) != 0), w = (e >> b.shift) + ((e & (b.page - 1)) != 0);
-    const int base = s_off[i] + s_last[i];
-    for (int x = lane; x < w - h; x += 32) {
-      const int pg = fresh[base + x];
-      b.table[static_cast<int64_t>(si) * b.table_stride + h + x] = pg;
-      b.refs[pg] = 1;
+  for (int x = tid; x < total; x += THREADS) {
+    int lo = 0, hi = n;   // the last entry whose pages begin at or before x
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (s_off[mid] <= x)
+        lo = mid;
+      else
+        hi = mid;
     }
+    const int at = x - s_off[lo] - (s_have[lo] & 1);   // -1: the copied page
+    if (at < 0) continue;
+    const int pg = fresh[x];
+    b.table[static_cast<int64_t>(s_seq[lo]) * b.table_stride + (s_have[lo] >> 1) + at] = pg;
+    b.refs[pg] = 1;
   }
   if (tid == 0) {
     status[0] = 0;
@@ -266,16 +326,18 @@ __global__ void __launch_bounds__(256) copy_shared_kernel(Pool p, const Copy* co
 
 // fm_kv_fork (kFork) and fm_kv_release: one cluster; every CTA validates all entries before the cluster barrier, and
 // none is changed before every CTA has. The CTAs then take the entries in turn. Bound by latency: dependent loads, two
-// barriers and the cluster's start, 9 us for 64 forks of up to 47 pages with cold inputs.
+// barriers and the cluster's start (64 forks of 30 pages in a pool of 2200: 3.5 us, 1024 of 35: 10.6 us).
 template <bool kFork>
 __global__ void __launch_bounds__(kBookThreads)
     share_kernel(Book b, const int32_t* seq, const int32_t* other, int n, int32_t* status) {
   __shared__ int s_seq[kMaxEntries], s_oth[kMaxEntries], s_len[kMaxEntries], s_bad;
+  __shared__ Set<kSlotsPer * kMaxEntries> named;   // fork: the targets; release: the sequences
   pdl_trigger();
-  pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) s_bad = 0;
+  named.clear(tid, blockDim.x);
   __syncthreads();
+  pdl_wait();
   int bad = 0, s = -1 - tid, o = 0;
   if (tid < n) {
     s = seq[tid];
@@ -291,12 +353,14 @@ __global__ void __launch_bounds__(kBookThreads)
     s_seq[tid] = s;
     s_oth[tid] = o;
     s_len[tid] = len;
+    // fork: a target appears once and is no source; release: a sequence appears once
+    bool again = false;
+    const int name = kFork ? o : s;
+    if (name >= 0) named.put(name, &again);
+    if (again) bad = FM_KV_BAD_ENTRY;
   }
   __syncthreads();
-  // fork: a target appears once and is no source; release: a sequence appears once
-  for (int j = 0; j < n && tid < n; ++j) {
-    if (kFork ? (s_seq[j] == o || (j != tid && s_oth[j] == o)) : (j != tid && s_seq[j] == s)) bad = FM_KV_BAD_ENTRY;
-  }
+  if (kFork && tid < n && named.has(s)) bad = FM_KV_BAD_ENTRY;
   if (bad) atomicOr(&s_bad, bad);
   __syncthreads();
   const int why = s_bad;

@@ -176,3 +176,40 @@ def test_graph_of_a_serving_step():
         torch.cuda.synchronize()
         book.fork([0, 0], [1, 2]), book.reserve([1, 2], [3, 30]), book.release([1, 2])
         book.check(c)
+
+
+def test_a_page_with_more_users_than_its_count():
+    """Two rows name a begun page that is counted once: writing to both would mix them, so nothing is done."""
+    require_gpu()
+    c = empty()
+    ops = Ops(c)
+    assert ops.reserve([0], [20]) == (0, 2)
+    c.table[1], c.lens[1] = c.table[0], 20
+    before = [x.clone() for x in (c.table, c.lens, c.refs)]
+    assert ops.reserve([0, 1], [1, 1]) == (2, 0)
+    assert all(torch.equal(a, b) for a, b in zip(before, (c.table, c.lens, c.refs)))
+
+
+def test_histories_of_hundreds_of_sequences():
+    """Sequence and page numbers far apart and alike modulo powers of two; groups of forks that write in any order."""
+    require_gpu()
+    rng = np.random.default_rng(11)
+    seqs = 4096
+    c = Cache([], 16, 1, 16, seqs=seqs, spare_pages=9000, poison=False)
+    c.table = torch.full((seqs, 9), -1, dtype=torch.int32, device="cuda")
+    c.handle = fmad.KvCache(c.k, c.v, c.table, c.lens, c.refs)
+    ops, book = Ops(c, 1024), Book(c)
+    roots = [int(x) for x in range(0, seqs, 64)]
+    both(ops, book, "reserve", roots, list(rng.integers(1, 60, len(roots))))
+    kids = [r + 1 + j for r in roots for j in range(15)]
+    both(ops, book, "fork", [k // 64 * 64 for k in kids], kids)
+    everyone = roots + kids
+    for step in range(3):
+        some = [int(x) for x in rng.permutation(everyone)[:1000 if step else 700]]
+        both(ops, book, "reserve", some, list(rng.integers(0, 20, len(some))))
+    assert both(ops, book, "reserve", everyone[:1000] + [everyone[500]], [1] * 1001) == (2, 0)
+    idle = list(range(32, 64)) + [r + 16 + j for r in roots for j in range(15)]
+    assert both(ops, book, "fork", [0] * (len(idle) + 1), idle + [33]) == (2, 0)
+    assert both(ops, book, "fork", [0, 96], [96, 97]) == (2, 0)
+    both(ops, book, "release", [int(x) for x in rng.permutation(everyone)[:900]], list(rng.integers(0, 70, 900)))
+    both(ops, book, "compact")
