@@ -397,12 +397,12 @@ __global__ void __launch_bounds__(kBookThreads)
 }
 
 // fm_kv_compact, the plan: live pages from n_live on move, in order, into the free ones below n_live, in order.
-// One CTA, bound by latency: three walks over refs (held in registers up to 4096 pages), 6.6 us cold.
-// head: [0] n_live, [1] moves; src, dst: the moves; map: the new place of every page from n_live on (-1: free).
+// One CTA, bound by latency: two walks over refs (held in registers up to 4096 pages).
+// head: [0] n_live, [1] moves, [2] where they begin in src; src, dst: the moves; map: the new place of every page from n_live on (-1: free).
 template <int THREADS>
 __global__ void __launch_bounds__(THREADS) compact_plan_kernel(Book b, int32_t* status, int32_t* head, int32_t* src,
                                                                     int32_t* dst, int32_t* map) {
-  __shared__ int s_sums[32];
+  __shared__ int s_sums[32], s_below;
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31;
@@ -410,28 +410,28 @@ __global__ void __launch_bounds__(THREADS) compact_plan_kernel(Book b, int32_t* 
   int mine = 0;
   walk.each(b, [&](int, bool in, int refs) { mine += __popc(__ballot_sync(0xffffffffu, in && refs > 0)); });
   int n_live = 0;
-  block_exclusive<THREADS>(lane == 0 ? mine : 0, s_sums, &n_live);
-  int above = 0, below = 0;
+  int rank = __shfl_sync(0xffffffffu, block_exclusive<THREADS>(lane == 0 ? mine : 0, s_sums, &n_live), 0);
+  if (tid == 0) s_below = n_live;
+  __syncthreads();
+  // with `at` live pages before it, a live page is the at-th of src, a free one below n_live the (pg - at)-th hole
   walk.each(b, [&](int pg, bool in, int refs) {
-    above += __popc(__ballot_sync(0xffffffffu, in && refs > 0 && pg >= n_live));
-    below += __popc(__ballot_sync(0xffffffffu, in && refs <= 0 && pg < n_live));
+    const bool live = in && refs > 0;
+    const unsigned m = __ballot_sync(0xffffffffu, live);
+    const int at = rank + __popc(m & ((1u << lane) - 1));
+    if (live && pg >= n_live) src[at] = pg;
+    if (in && !live) {
+      if (pg < n_live)
+        dst[pg - at] = pg;
+      else
+        map[pg] = -1;
+    }
+    if (in && pg == n_live) s_below = at;
+    rank += __popc(m);
   });
-  int moves = 0, holes = 0;
-  int ra = __shfl_sync(0xffffffffu, block_exclusive<THREADS>(lane == 0 ? above : 0, s_sums, &moves), 0);
-  int rb = __shfl_sync(0xffffffffu, block_exclusive<THREADS>(lane == 0 ? below : 0, s_sums, &holes), 0);
-  walk.each(b, [&](int pg, bool in, int refs) {
-    const bool a = in && refs > 0 && pg >= n_live, h = in && refs <= 0 && pg < n_live;
-    const unsigned ma = __ballot_sync(0xffffffffu, a), mh = __ballot_sync(0xffffffffu, h);
-    const unsigned under = (1u << lane) - 1;
-    if (a) src[ra + __popc(ma & under)] = pg;
-    if (h) dst[rb + __popc(mh & under)] = pg;
-    if (in && pg >= n_live && !a) map[pg] = -1;
-    ra += __popc(ma);
-    rb += __popc(mh);
-  });
-  __syncthreads();   // moves == holes: as many live pages above n_live as free ones below
+  __syncthreads();
+  const int below = s_below, moves = n_live - below;   // live pages below n_live; as many free ones there as live above
   for (int i = tid; i < moves; i += THREADS) {
-    const int from = src[i], to = dst[i];
+    const int from = src[below + i], to = dst[i];
     map[from] = to;
     b.refs[to] = b.refs[from];
     b.refs[from] = 0;
@@ -439,6 +439,7 @@ __global__ void __launch_bounds__(THREADS) compact_plan_kernel(Book b, int32_t* 
   if (tid == 0) {
     head[0] = n_live;
     head[1] = moves;
+    head[2] = below;
     status[0] = 0;
     status[1] = moves;
   }
@@ -451,6 +452,7 @@ __global__ void __launch_bounds__(256) compact_move_kernel(Pool p, Book b, const
   pdl_trigger();
   pdl_wait();
   const int n_live = head[0], moves = head[1];
+  src += head[2];
   const int64_t items = static_cast<int64_t>(moves) * p.layers;
   for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
     const int m = static_cast<int>(i % moves);
