@@ -14,8 +14,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cmath>
-#include <cstring>
-#include <mutex>
+#include <type_traits>
 
 #include "kv.h"
 #include "ptx.cuh"
@@ -98,15 +97,16 @@ struct PageWalk {
       const int pg = lo + u * 32 + lane;
       if (lo + u * 32 < hi) f(pg, pg < hi, kept[u]);   // warp-uniform
     }
-    for (int p0 = lo + kKeep * 32; p0 < hi; p0 += 128) {
-      int r[4];
+    constexpr int kAhead = 4;   // 16: slower, most warps have few steps
+    for (int p0 = lo + kKeep * 32; p0 < hi; p0 += kAhead * 32) {
+      int r[kAhead];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < kAhead; ++u) {
         const int pg = p0 + u * 32 + lane;
         r[u] = pg < hi ? b.refs[pg] : -1;
       }
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < kAhead; ++u) {
         const int pg = p0 + u * 32 + lane;
         if (p0 + u * 32 < hi) f(pg, pg < hi, r[u]);
       }
@@ -155,10 +155,10 @@ struct Set {
 
 // fm_kv_reserve. One CTA: the whole decision needs the order of the entries, and its work is a few hundred bytes an
 // entry plus two passes over refs; a second kernel copies the shared last pages on all SMs. Bound by latency (one token more
-// of 64 sequences in a pool of 2200 pages: 5.1 us with the copies' kernel, of 1024 in 40000: 10.8 us; new pages are dealt
+// of 64 sequences in a pool of 2200 pages: 4.7 us with the copies' kernel, of 1024 in 40000: 10.4 us; new pages are dealt
 // out a thread each, which finds its entry by bisection).
 template <int THREADS>
-__global__ void __launch_bounds__(THREADS) reserve_kernel(Book b, const int32_t* seq, const int32_t* count, int n,
+__global__ void __launch_bounds__(THREADS, 1) reserve_kernel(Book b, const int32_t* seq, const int32_t* count, int n,
                                                                int32_t* status, Copy* copies, int32_t* fresh) {
   constexpr int kSlots = kSlotsPer * THREADS;
   __shared__ int s_seq[THREADS], s_have[THREADS], s_off[THREADS], s_sums[32], s_bad;
@@ -324,9 +324,16 @@ __global__ void __launch_bounds__(256) copy_shared_kernel(Pool p, const Copy* co
   if (c.rows > 0) copy_rows(p, blockIdx.y, c.src, c.dst, c.rows);
 }
 
+constexpr int kNone = INT32_MIN;   // nothing to do at a place
+// The first place of a row that a release of all but `keep` tokens empties.
+__device__ __forceinline__ int first_unused(int len, int keep, const Book& b) {
+  const int left = min(len, keep);
+  return (left >> b.shift) + ((left & (b.page - 1)) != 0);
+}
+
 // fm_kv_fork (kFork) and fm_kv_release: one cluster; every CTA validates all entries before the cluster barrier, and
 // none is changed before every CTA has. The CTAs then take the entries in turn. Bound by latency: dependent loads, two
-// barriers and the cluster's start (64 forks of 30 pages in a pool of 2200: 3.5 us, 1024 of 35: 10.6 us).
+// barriers and the cluster's start (64 forks of 30 pages in a pool of 2200: 3.1 us, 1024 of 35: 8.0 us).
 template <bool kFork>
 __global__ void __launch_bounds__(kBookThreads)
     share_kernel(Book b, const int32_t* seq, const int32_t* other, int n, int32_t* status) {
@@ -371,36 +378,42 @@ __global__ void __launch_bounds__(kBookThreads)
     status[1] = 0;
   }
   if (why) return;
-  // warps take (entry, part of its row); a row's unused places are -1 and copied like the rest
-  for (int i = rank * warps + warp; i < n * 4; i += gridDim.x * warps) {
-    const int e = i >> 2, part = i & 3;
-    const int64_t row = static_cast<int64_t>(s_seq[e]) * b.table_stride;
-    if (kFork) {
-      const int64_t to = static_cast<int64_t>(s_oth[e]) * b.table_stride;
-      for (int x = part * 32 + lane; x < b.table_stride; x += 128) {
-        const int pg = b.table[row + x];
-        b.table[to + x] = pg;
-        if (pg >= 0 && pg < b.pages) atomicAdd(&b.refs[pg], 1);
+  // Warps take (entry, part of its row); a row's unused places are -1 and copied like the rest.
+  const int items = n * 4, step = gridDim.x * warps;
+  auto move = [&](auto take, int i0) {
+    constexpr int kTake = decltype(take)::value;
+    for (int x0 = 0; x0 < b.table_stride; x0 += 128) {
+      int pg[kTake];
+#pragma unroll
+      for (int u = 0; u < kTake; ++u) {
+        const int i = i0 + u * step, e = i >> 2, x = x0 + (i & 3) * 32 + lane;
+        const bool has = i < items && x < b.table_stride && (kFork || x >= first_unused(s_len[e], s_oth[e], b));
+        pg[u] = has ? b.table[static_cast<int64_t>(s_seq[e]) * b.table_stride + x] : kNone;
       }
-      if (part == 0 && lane == 0) b.lens[s_oth[e]] = s_len[e];
-    } else {
-      const int len = s_len[e], keep = min(len, s_oth[e]);
-      const int lo = (keep >> b.shift) + ((keep & (b.page - 1)) != 0);
-      for (int x = lo + part * 32 + lane; x < b.table_stride; x += 128) {
-        const int pg = b.table[row + x];
-        if (pg >= 0 && pg < b.pages) atomicSub(&b.refs[pg], 1);
-        b.table[row + x] = -1;
+#pragma unroll
+      for (int u = 0; u < kTake; ++u) {
+        if (pg[u] == kNone) continue;
+        const int i = i0 + u * step, e = i >> 2, x = x0 + (i & 3) * 32 + lane;
+        b.table[static_cast<int64_t>(kFork ? s_oth[e] : s_seq[e]) * b.table_stride + x] = kFork ? pg[u] : -1;
+        if (pg[u] >= 0 && pg[u] < b.pages) atomicAdd(&b.refs[pg[u]], kFork ? 1 : -1);
       }
-      if (part == 0 && lane == 0) b.lens[s_seq[e]] = keep;
     }
+  };
+  int i = rank * warps + warp;
+  if (items <= step) {
+    if (i < items) move(std::integral_constant<int, 1>{}, i);
+  } else {   // four at a time, their loads on the way together (1024 forks: 10.4 -> 8.0 us)
+    for (; i < items; i += 4 * step) move(std::integral_constant<int, 4>{}, i);
   }
+  for (int e = rank * blockDim.x + tid; e < n; e += gridDim.x * blockDim.x)
+    b.lens[kFork ? s_oth[e] : s_seq[e]] = kFork ? s_len[e] : min(s_len[e], s_oth[e]);
 }
 
 // fm_kv_compact, the plan: live pages from n_live on move, in order, into the free ones below n_live, in order.
 // One CTA, bound by latency: two walks over refs (held in registers up to 4096 pages).
 // head: [0] n_live, [1] moves, [2] where they begin in src; src, dst: the moves; map: the new place of every page from n_live on (-1: free).
 template <int THREADS>
-__global__ void __launch_bounds__(THREADS) compact_plan_kernel(Book b, int32_t* status, int32_t* head, int32_t* src,
+__global__ void __launch_bounds__(THREADS, 1) compact_plan_kernel(Book b, int32_t* status, int32_t* head, int32_t* src,
                                                                     int32_t* dst, int32_t* map) {
   __shared__ int s_sums[32], s_below;
   pdl_trigger();
