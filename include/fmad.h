@@ -648,10 +648,11 @@ int fm_kv_workspace_size(const fm_kv_cache* c, int n, size_t* bytes);
 
 /* Make room for count[i] more tokens at the end of sequence seq[i] (device int32 [n], no
  * sequence twice, n <= 1024): lens grows by the counts, pages are taken lowest free index
- * first, entry by entry. Where the last page is begun and shared, the first entry that
- * would write to it gets a copy of its tokens (all layers) in a page taken before the
- * entry's others; the last of a page's users keeps the page. All entries or none. status:
- * device int32 [2]. workspace: device, 16-byte aligned. Asynchronous. */
+ * first, entry by entry. Where the last page is begun and shared, an entry that would
+ * write to it gets a copy of its tokens (all layers) in a page taken before the entry's
+ * others; only the last of a page's users keeps the page (the last entry that names it,
+ * where no other row does). All entries or none. status: device int32 [2]. workspace:
+ * device, 16-byte aligned. Asynchronous. */
 int fm_kv_reserve(const fm_kv_cache* c, const int32_t* seq, const int32_t* count, int n, int32_t* status,
                   void* workspace, size_t workspace_bytes, void* stream);
 
