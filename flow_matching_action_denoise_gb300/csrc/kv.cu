@@ -536,10 +536,10 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
   const int unit = threadIdx.x % units, tok = (threadIdx.x / units) % p.toks, grp = threadIdx.x / (units * p.toks);
   const int entry = blockIdx.y;
   pdl_wait();
-  const int begin = __ldg(p.start + entry), nq = __ldg(p.start + entry + 1) - begin;
-  const int sid = p.seq ? __ldg(p.seq + entry) : entry;
+  const int begin = p.start[entry], nq = p.start[entry + 1] - begin;
+  const int sid = p.seq ? p.seq[entry] : entry;
   const bool bad = begin < 0 || nq < 0 || begin > p.tokens || nq > p.tokens - begin || sid < 0 || sid >= p.seqs;
-  const int len = bad ? 0 : __ldg(p.lens + sid);
+  const int len = bad ? 0 : p.lens[sid];
   const bool over = bad || nq > p.max_tokens || len < nq || len > p.table_stride * static_cast<int64_t>(p.page);
   if (over && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.err, kErrBadBatch);
   const int first = blockIdx.x * p.toks, end = min(nq, p.max_tokens);
@@ -548,9 +548,9 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
   for (int x = threadIdx.x; x < p.toks * pairs; x += 256) {
     const int i = x % pairs, w = first + x / pairs;
     if (w >= end) break;
-    const int64_t at = p.positions ? __ldg(p.positions + begin + w) : past + w;
+    const int64_t at = p.positions ? p.positions[begin + w] : past + w;
     // the fraction of a turn as a signed 32-bit number: half turns in [-1, 1) for sincospif
-    const uint64_t turn = __ldg(p.freq + i) * static_cast<uint64_t>(at) + (1ull << 31);
+    const uint64_t turn = p.freq[i] * static_cast<uint64_t>(at) + (1ull << 31);
     float2 a;
     sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f, &a.y, &a.x);
     s_angle[x] = make_float2(a.x * p.mag, a.y * p.mag);
@@ -561,7 +561,7 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
   const int64_t pos = static_cast<int64_t>(past) + within;   // place in the sequence
   int page = -1;
   if (mine && pos >= 0 && (pos >> p.shift) < p.table_stride)
-    page = __ldg(p.table + static_cast<int64_t>(sid) * p.table_stride + (pos >> p.shift));
+    page = p.table[static_cast<int64_t>(sid) * p.table_stride + (pos >> p.shift)];
   if (page >= p.pages) page = -1;
   if (mine && page < 0 && unit == 0 && grp == 0) atomicOr(p.err, kErrBadBatch);
   __syncthreads();
@@ -622,7 +622,7 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
   if (page < 0) return;
   // ---- keys and values
   const int64_t cell = static_cast<int64_t>(page) * p.pg + (pos & (p.page - 1)) * p.tok;
-  const float rk = F8 ? 1.0f / __ldg(p.k_scale) : 1.0f, rv = F8 ? 1.0f / __ldg(p.v_scale) : 1.0f;
+  const float rk = F8 ? 1.0f / *p.k_scale : 1.0f, rv = F8 ? 1.0f / *p.v_scale : 1.0f;
   // heads go round the groups where the queries' left off, so that a small batch spreads over all of them
   int h = grp - p.H % p.groups;
   if (h < 0) h += p.groups;

@@ -49,15 +49,15 @@ struct Entry {
 
 __device__ __forceinline__ Entry entry_of(const AttnParams& p, int entry, bool report) {
   Entry e;
-  e.begin = __ldg(p.start + entry);
-  e.nq = __ldg(p.start + entry + 1) - e.begin;
-  e.sid = p.seq ? __ldg(p.seq + entry) : entry;
+  e.begin = p.start[entry];
+  e.nq = p.start[entry + 1] - e.begin;
+  e.sid = p.seq ? p.seq[entry] : entry;
   e.len = 0;
   bool bad = e.begin < 0 || e.nq < 0 || e.begin > p.tokens || e.nq > p.tokens - e.begin || e.sid < 0 || e.sid >= p.seqs;
   if (bad) {
     e.nq = 0;
   } else {
-    e.len = __ldg(p.lens + e.sid);
+    e.len = p.lens[e.sid];
     bad = e.len < 0 || e.len > p.table_stride * static_cast<int64_t>(p.page);
     if (bad) e.len = 0;
   }

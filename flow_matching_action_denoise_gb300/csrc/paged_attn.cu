@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(threads_of(F8), 1)
   auto page_of = [&](int j) {   // lane x: the page of box x of key tile j; the pool's end where there is none
     const int key = (t_lo + j) * kTileRows + lane * rows_box;
     if (lane >= boxes || key >= len || j >= n_keys) return p.pages;
-    const int pg = __ldg(p.table + static_cast<int64_t>(sid) * p.table_stride + (key >> p.page_shift));
+    const int pg = p.table[static_cast<int64_t>(sid) * p.table_stride + (key >> p.page_shift)];
     if (pg < 0 || pg >= p.pages) {
       atomicOr(p.err, kErrBadBatch);
       return p.pages;
@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(threads_of(F8), 1)
         const int ex = static_cast<int>(top >> 7);   // biased exponent (0: zero or subnormal; 255: not finite)
         const int sh = ex == 0 || ex == 255 ? 0 : min(max(141 - ex, -100), 100);   // 127 + 14 - ex
         const float up = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
-        c_row *= __uint_as_float(static_cast<uint32_t>(127 - sh) << 23) * __ldg(p.k_scale);
+        c_row *= __uint_as_float(static_cast<uint32_t>(127 - sh) << 23) * *p.k_scale;
 #pragma unroll
         for (int ch = 0; ch < kRowChunks; ++ch) {
           uint32_t w[4] = {v[ch].x, v[ch].y, v[ch].z, v[ch].w};
@@ -512,7 +512,7 @@ __global__ void __launch_bounds__(threads_of(F8), 1)
     tc_fence_after();
     __syncwarp();
     if (!ok && lane == 0) atomicOr(p.err, kErrPipelineTimeout);
-    const float vs = F8 ? __ldg(p.v_scale) : 1.0f;
+    const float vs = F8 ? *p.v_scale : 1.0f;
     float* join = reinterpret_cast<float*>(sring);                        // [128][DH], chunks swizzled by row
     float2* join_ml = reinterpret_cast<float2*>(sring + kTileRows * DH * 4);
     auto load_o = [&](int b, float* o) {   // 32 of this row's sums
@@ -824,10 +824,10 @@ __global__ void __launch_bounds__(threads_of(F8), 1)
 // Joins the splits of every (token, head) row (bound by latency, the shares come from L2): `warps` (1, 2, 4 or 8, a power of two) of a CTA's eight share a row, each
 // every warps-th split, and are summed in warp order.
 template <int DH>
-__global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ part_o, const float2* __restrict__ part_ml,
+__global__ void __launch_bounds__(256) combine_kernel(const float* part_o, const float2* part_ml,
                                                       int splits, int warps, int tokens, int H,
-                                                      const int32_t* __restrict__ start, int n,
-                                                      __nv_bfloat16* __restrict__ out, int64_t out_stride) {
+                                                      const int32_t* start, int n,
+                                                      __nv_bfloat16* out, int64_t out_stride) {
   constexpr int kPer = DH / 32;
   __shared__ float s_acc[8][DH];
   __shared__ float s_sum[8];
@@ -838,7 +838,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ 
   const int sub = warp & (warps - 1);
   const int token = static_cast<int>(row / H);
   // rows of no entry keep what they hold
-  const bool live = row < rows && token >= __ldg(start) && token < __ldg(start + n);
+  const bool live = row < rows && token >= start[0] && token < start[n];
   float acc[kPer] = {};
   float sum = 0.f;
   if (live) {

@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(kThreads, kResident<DH, F8, NT>)
     auto page_of = [&](int j) {
       const int key = (t_lo + j) * kDecodeKeys + lane * rows_box;
       if (lane >= boxes || key >= en.len || j >= nt) return p.pages;
-      const int pg = __ldg(p.table + static_cast<int64_t>(en.sid) * p.table_stride + (key >> p.page_shift));
+      const int pg = p.table[static_cast<int64_t>(en.sid) * p.table_stride + (key >> p.page_shift)];
       if (pg < 0 || pg >= p.pages) {
         atomicOr(p.err, kErrBadBatch);
         return p.pages;
@@ -180,12 +180,12 @@ __global__ void __launch_bounds__(kThreads, kResident<DH, F8, NT>)
 #pragma unroll
       for (int c = 0; c < DH / 16; ++c) {
         if constexpr (F8) {   // dims 16 c + 4 t .. + 3
-          const uint2 v = live ? __ldg(reinterpret_cast<const uint2*>(src + c * 16 + q4 * 4)) : make_uint2(0, 0);
+          const uint2 v = live ? *reinterpret_cast<const uint2*>(src + c * 16 + q4 * 4) : make_uint2(0, 0);
           qf[x][c][0] = v.x;
           qf[x][c][1] = v.y;
         } else {
-          qf[x][c][0] = live ? __ldg(reinterpret_cast<const uint32_t*>(src + c * 16 + q4 * 2)) : 0u;
-          qf[x][c][1] = live ? __ldg(reinterpret_cast<const uint32_t*>(src + c * 16 + q4 * 2 + 8)) : 0u;
+          qf[x][c][0] = live ? *reinterpret_cast<const uint32_t*>(src + c * 16 + q4 * 2) : 0u;
+          qf[x][c][1] = live ? *reinterpret_cast<const uint32_t*>(src + c * 16 + q4 * 2 + 8) : 0u;
         }
       }
       if constexpr (F8) {
@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, kResident<DH, F8, NT>)
         const int ex = static_cast<int>(top >> 7);
         const int sh = ex == 0 || ex == 255 ? 0 : min(max(141 - ex, -100), 100);
         const float up = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
-        const float down = __uint_as_float(static_cast<uint32_t>(127 - sh) << 23) * __ldg(p.k_scale);
+        const float down = __uint_as_float(static_cast<uint32_t>(127 - sh) << 23) * *p.k_scale;
         // the scores' lanes own rows 2 t, 2 t + 1 of the eight
 #pragma unroll
         for (int u = 0; u < 2; ++u) c_row[2 * x + u] *= __shfl_sync(0xffffffffu, down, (2 * q4 + u) * 4);
@@ -390,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, kResident<DH, F8, NT>)
     }
   }
   __syncthreads();
-  const float vs = F8 ? __ldg(p.v_scale) : 1.0f;
+  const float vs = F8 ? *p.v_scale : 1.0f;
   const bool clustered = p.splits > 1 && p.part_o == nullptr;
   constexpr int kQuads = DH / 4;
   for (int x = tid; x < rows * kQuads; x += kThreads) {

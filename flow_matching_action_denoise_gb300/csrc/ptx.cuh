@@ -23,7 +23,9 @@ __device__ __forceinline__ uint64_t global_ns() {
 
 // ---------------------------------------------------------------- PDL
 // Wait until the preceding grid in the stream has completed and its writes are
-// visible. Every kernel calls this before touching data an earlier kernel wrote.
+// visible. Every kernel calls this before touching data an earlier kernel wrote, and reads
+// that data by plain loads: the read-only path (__ldg, __restrict__ parameters) is for what does
+// not change while the kernel runs, and this kernel already runs while the earlier one writes.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // Allow the next grid in the stream to be scheduled (its pre-wait prologue runs
 // while this grid finishes).

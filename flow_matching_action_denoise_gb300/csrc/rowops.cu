@@ -416,7 +416,7 @@ namespace {
 
 // y[m][n] = bf16(sum_j planes[j][m][n] * fp32(sa * sw)), slices summed in order j = 0..s-1;
 // with vt, columns n >= nv0 also go to vt[(n - nv0) * m_pad + m].
-__global__ void __launch_bounds__(256) qkv_finalize_kernel(const float* __restrict__ planes, int s, size_t n4,
+__global__ void __launch_bounds__(256) qkv_finalize_kernel(const float* planes, int s, size_t n4,
                                                            const float* __restrict__ sa,
                                                            const float* __restrict__ sw, __nv_bfloat16* out,
                                                            __nv_bfloat16* vt, int N, int nv0, int m_pad) {
