@@ -821,38 +821,36 @@ __global__ void __launch_bounds__(threads_of(F8), 1)
   }
 }
 
-// Joins the splits of every (token, head) row (bound by latency, the shares come from L2): `warps` (1, 2, 4 or 8, a power of two) of a CTA's eight share a row, each
-// every warps-th split, and are summed in warp order.
+// Joins the splits of the rows that they computed: an entry's (grid.y) first max_tokens tokens. All else keeps what it
+// holds, the rows of an entry out of range too. Bound by latency, the shares come from L2: `warps` (1, 2, 4 or 8, a power
+// of two) of a CTA's eight share a row, each every warps-th split, and are summed in warp order.
 template <int DH>
-__global__ void __launch_bounds__(256) combine_kernel(const float* part_o, const float2* part_ml,
-                                                      int splits, int warps, int tokens, int H,
-                                                      const int32_t* start, int n,
-                                                      __nv_bfloat16* out, int64_t out_stride) {
+__global__ void __launch_bounds__(256) combine_kernel(const AttnParams p, int warps) {
   constexpr int kPer = DH / 32;
   __shared__ float s_acc[8][DH];
   __shared__ float s_sum[8];
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t rows = static_cast<int64_t>(tokens) * H;
-  const int64_t row = (blockIdx.x * 8ll + warp) / warps;
+  const Entry en = entry_of(p, blockIdx.y, false);
+  const int64_t rows = static_cast<int64_t>(p.tokens) * p.H;   // of a split
+  const int64_t in_entry = (blockIdx.x * 8ll + warp) / warps;
   const int sub = warp & (warps - 1);
-  const int token = static_cast<int>(row / H);
-  // rows of no entry keep what they hold
-  const bool live = row < rows && token >= start[0] && token < start[n];
+  const bool live = in_entry < static_cast<int64_t>(min(en.nq, p.max_tokens)) * p.H;
+  const int64_t row = static_cast<int64_t>(en.begin) * p.H + in_entry;
   float acc[kPer] = {};
   float sum = 0.f;
   if (live) {
     float top = -INFINITY;
-    for (int s = lane; s < splits; s += 32) top = fmaxf(top, part_ml[s * rows + row].x);
+    for (int s = lane; s < p.splits; s += 32) top = fmaxf(top, p.part_ml[s * rows + row].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
 #pragma unroll 4
-    for (int s = sub; s < splits; s += warps) {
-      const float2 ml = part_ml[s * rows + row];   // one address for the warp
+    for (int s = sub; s < p.splits; s += warps) {
+      const float2 ml = p.part_ml[s * rows + row];   // one address for the warp
       if (!(ml.x > -INFINITY)) continue;
       const float w = exp2f(ml.x - top);
       sum += ml.y * w;
-      const float* src = part_o + (s * rows + row) * DH + lane * kPer;
+      const float* src = p.part_o + (s * rows + row) * DH + lane * kPer;
       if constexpr (kPer == 4) {
         const float4 v = *reinterpret_cast<const float4*>(src);
         acc[0] += w * v.x, acc[1] += w * v.y, acc[2] += w * v.z, acc[3] += w * v.w;
@@ -877,7 +875,8 @@ __global__ void __launch_bounds__(256) combine_kernel(const float* part_o, const
   }
   if (!live || sub) return;
   const float inv = sum == 0.f ? 0.f : 1.0f / sum;
-  __nv_bfloat16* dst = out + token * out_stride + (row % H) * DH + lane * kPer;
+  const int64_t token = in_entry / p.H;
+  __nv_bfloat16* dst = p.out + (en.begin + token) * p.out_stride + (in_entry - token * p.H) * DH + lane * kPer;
   if constexpr (kPer == 4)
     *reinterpret_cast<uint2*>(dst) = make_uint2(pack16<false>(acc[0] * inv, acc[1] * inv), pack16<false>(acc[2] * inv, acc[3] * inv));
   else
@@ -1159,10 +1158,9 @@ extern "C" int fm_paged_attention(const fm_kv_cache* c, int layer, const fm_kv_b
     // a warp takes up to four splits where there are few rows (256 splits of 8 rows took 45 us with a warp a row)
     int warps = 1;
     while (warps < 8 && pl.splits > 4 * warps) warps *= 2;
-    const int64_t blocks = (static_cast<int64_t>(b->tokens) * H * warps + 7) / 8;
+    const int64_t blocks = (static_cast<int64_t>(b->max_tokens) * H * warps + 7) / 8;
     auto join = c->Dh == 128 ? combine_kernel<128> : combine_kernel<64>;
-    e = launch(join, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, o, static_cast<const float*>(p.part_o),
-               static_cast<const float2*>(p.part_ml), pl.splits, warps, b->tokens, H, b->start, b->n, p.out, out_stride);
+    e = launch(join, dim3(static_cast<unsigned>(blocks), b->n), dim3(256), 0, o, p, warps);
   }
   return e == cudaSuccess ? FM_OK : record_error(FM_ERR_CUDA, cudaGetErrorString(e));
 }

@@ -1,0 +1,69 @@
+"""Paged attention whose keys are split through the workspace: the rows that no split computes. Tolerance as in the
+attention's own tests."""
+import numpy as np
+import pytest
+import torch
+
+import flow_matching_action_denoise_gb300 as fmad
+from _gpu import require_gpu
+from _kv import Cache, attention_ref, batch
+
+pytestmark = pytest.mark.gpu
+
+# (lengths, new tokens, heads, bound): up to 16 stacked rows, up to 128, more
+SPLIT = [([6000, 5000], [2, 1], 8, 1), ([20011, 300, 9000], [2, 3, 1], 4, 2), ([6000], [9], 8, 5), ([12000, 700], [50, 3], 8, 40)]
+
+
+def attend(c, b, q, H, fill=1.0, causal=True):
+    """(out, status): out starts at 7 and the workspace at `fill`, a plausible share of every split."""
+    nb = fmad.paged_attention_workspace_size(c.handle, b, H)
+    assert nb > 0
+    ws = torch.full((nb // 4,), fill, device="cuda")
+    out = torch.full_like(q, 7.0)
+    fmad.paged_attention(c.handle, 0, b, q, out, ws, causal=causal)
+    return out, fmad.standalone_status()
+
+
+def near(c, i, q, out, rows):
+    """The entry's first `rows` rows are what its definition says."""
+    ref, size = attention_ref(c, i, q, c.k.shape[-1] ** -0.5, True, 0)
+    tol = ref.abs() * 2.0 ** -8 + size * ((2.0 ** -11 if c.fp8 else 2.0 ** -8) + 2.0 ** -9)
+    assert bool(((out[:rows].double() - ref[:rows]).abs() <= tol[:rows]).all())
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("lens,new,H,bound", SPLIT)
+def test_rows_behind_a_tight_bound_stay_as_they_were(lens, new, H, bound, fp8):
+    require_gpu()
+    c = Cache(lens, 64, 1, 128, fp8, seed=H)
+    b = batch(c, new, lead=2, trail=3, max_tokens=bound)
+    q = torch.randn((b.tokens, H, 128), device="cuda").to(torch.bfloat16)
+    out, status = attend(c, b, q, H)
+    assert status == 2
+    start = b.start.tolist()
+    assert (out[:start[0]] == 7).all() and (out[start[-1]:] == 7).all()
+    for i, n in enumerate(new):
+        near(c, i, q[start[i]:start[i + 1]], out[start[i]:start[i + 1]], min(n, bound))
+        assert (out[start[i] + min(n, bound):start[i + 1]] == 7).all(), i
+
+
+@pytest.mark.parametrize("lens,new,H,bound", SPLIT)
+def test_rows_of_a_refused_entry_stay_as_they_were(lens, new, H, bound):
+    require_gpu()
+    lens, new = lens + [4000], new + [1]
+    c = Cache(lens, 64, 1, 128, seed=H)
+    for at in range(len(new)):
+        for seq in (99, -1):
+            ids = torch.tensor(np.asarray(c.rows), dtype=torch.int32, device="cuda")
+            ids[at] = seq
+            b = batch(c, new)
+            b = fmad.KvBatch(b.start, b.tokens, max(new), max(lens), ids)
+            q = torch.randn((b.tokens, H, 128), device="cuda").to(torch.bfloat16)
+            out, status = attend(c, b, q, H)
+            assert status == 2
+            start = b.start.tolist()
+            for i, n in enumerate(new):
+                if i == at:
+                    assert (out[start[i]:start[i + 1]] == 7).all()
+                else:
+                    near(c, i, q[start[i]:start[i + 1]], out[start[i]:start[i + 1]], n)
