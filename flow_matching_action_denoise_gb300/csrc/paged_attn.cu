@@ -847,7 +847,8 @@ __global__ void __launch_bounds__(256) combine_kernel(const AttnParams p, int wa
 #pragma unroll 4
     for (int s = sub; s < p.splits; s += warps) {
       const float2 ml = p.part_ml[s * rows + row];   // one address for the warp
-      if (!(ml.x > -INFINITY)) continue;
+      // no keys: its share is not written. A NaN in the query has no maximum either, but its sum is NaN and so is the row
+      if (ml.x == -INFINITY && ml.y == 0.f) continue;
       const float w = exp2f(ml.x - top);
       sum += ml.y * w;
       const float* src = p.part_o + (s * rows + row) * DH + lane * kPer;

@@ -1,5 +1,5 @@
-"""Paged attention whose keys are split through the workspace: the rows that no split computes. Tolerance as in the
-attention's own tests."""
+"""Paged attention whose keys are split through the workspace: rows that no split computes, rows that hold a NaN.
+Tolerance as in the attention's own tests."""
 import numpy as np
 import pytest
 import torch
@@ -67,3 +67,23 @@ def test_rows_of_a_refused_entry_stay_as_they_were(lens, new, H, bound):
                     assert (out[start[i]:start[i + 1]] == 7).all()
                 else:
                     near(c, i, q[start[i]:start[i + 1]], out[start[i]:start[i + 1]], n)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("lens,new,H,bound", SPLIT)
+def test_a_nan_query_row_is_not_hidden(lens, new, H, bound, fp8):
+    """Every score of the row is NaN, so is its sum, and no split has a maximum: the row is NaN as it is without splits,
+    and every other row keeps its bits."""
+    require_gpu()
+    c = Cache(lens, 64, 1, 128, fp8, seed=H)
+    b = batch(c, new)
+    q = torch.randn((b.tokens, H, 128), device="cuda").to(torch.bfloat16)
+    clean, status = attend(c, b, q, H)
+    assert status == 0
+    token, head = b.tokens - 1, H - 1
+    q[token, head, 5] = float("nan")
+    out, status = attend(c, b, q, H)
+    assert status == 0
+    assert out[token, head].isnan().all()
+    out[token, head] = clean[token, head]
+    assert torch.equal(out, clean)
