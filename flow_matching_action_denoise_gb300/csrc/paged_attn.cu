@@ -969,7 +969,9 @@ int splits_of(const fm_kv_cache& c, const fm_kv_batch& b, int H, int window) {
   const int64_t tiles = (keys + kTileRows - 1) / kTileRows + (window > 0);
   const int64_t fixed = f8 ? 85 : 70, each = alt ? (f8 ? 15 : 8) : (f8 ? 18 : 14);
   int64_t best = 0, splits = 1;
-  for (int64_t s = 1; s <= std::min<int64_t>(64, std::max<int64_t>(1, tiles / 2)); ++s) {
+  // entries x splits are a dimension of the grid
+  const int64_t most = std::min<int64_t>({64, std::max<int64_t>(1, tiles / 2), std::max(1, 65535 / std::max(1, b.n))});
+  for (int64_t s = 1; s <= most; ++s) {
     const int64_t waves = (units * s + sms - 1) / sms;
     const int64_t shares = s * b.tokens * H * c.Dh * 8;   // bytes, at 4 TB/s: 4e5 bytes in 0.1 us
     const int64_t cost = waves * (fixed + (tiles + s - 1) / s * each) + (s > 1 ? 25 + shares / 400000 : 0);
@@ -1052,9 +1054,6 @@ int check(const fm_kv_cache* c, const fm_kv_batch* b, int H) {
   if (c->page_tokens > 256) return record_error(FM_ERR_SHAPE, "attention takes pages of 16 to 256 tokens");
   const int64_t rows = static_cast<int64_t>(b->max_tokens) * (H / c->Hkv);
   if (rows > (int64_t(1) << 30)) return record_error(FM_ERR_SHAPE, "max_tokens * H / Hkv exceeds 2^30");
-  const Plan pl = plan_of(*c, bounded_batch(*b), H, 0);
-  if (static_cast<int64_t>(b->n) * pl.splits > 65535)
-    return record_error(FM_ERR_SHAPE, "too many entries for one call (entries x splits up to 65535)");
   return FM_OK;
 }
 

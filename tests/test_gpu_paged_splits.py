@@ -1,5 +1,5 @@
-"""Paged attention whose keys are split through the workspace: rows that no split computes, rows that hold a NaN.
-Tolerance as in the attention's own tests."""
+"""Paged attention whose keys are split through the workspace: rows that no split computes, rows that hold a NaN,
+and batches whose entries times splits would not fit a grid. Tolerance as in the attention's own tests."""
 import numpy as np
 import pytest
 import torch
@@ -87,3 +87,20 @@ def test_a_nan_query_row_is_not_hidden(lens, new, H, bound, fp8):
     assert out[token, head].isnan().all()
     out[token, head] = clean[token, head]
     assert torch.equal(out, clean)
+
+
+def test_entries_times_splits_beyond_a_grid():
+    """Thousands of entries under a very loose length bound: the call divides its keys less, it is not refused."""
+    require_gpu()
+    c = Cache([300, 41], 64, 2, 64, seed=3, rows=[0, 1])
+    n, H = 4096, 16
+    start = torch.arange(0, 3 * n + 1, 3, dtype=torch.int32, device="cuda")
+    ids = torch.arange(n, dtype=torch.int32, device="cuda") % 2
+    q = torch.randn((3 * n, H, 64), device="cuda").to(torch.bfloat16)
+    b = fmad.KvBatch(start, 3 * n, 3, 1 << 29, ids)
+    ws = torch.empty(fmad.paged_attention_workspace_size(c.handle, b, H), dtype=torch.uint8, device="cuda")
+    out = torch.empty_like(q)
+    fmad.paged_attention(c.handle, 0, b, q, out, ws)
+    assert fmad.standalone_status() == 0
+    for i in (0, 1, 2047, 4094, 4095):
+        near(c, i % 2, q[3 * i:3 * i + 3], out[3 * i:3 * i + 3], 3)

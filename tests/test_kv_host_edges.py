@@ -1,0 +1,17 @@
+"""The paged prefix cache's entry points at the ends of their ranges, on the host (nothing here launches a kernel)."""
+import ctypes
+
+import pytest
+
+from test_kv_host import at, batch, cache, lib   # noqa: F401  (lib is a fixture)
+
+
+@pytest.mark.parametrize("n", [300, 4096, 20000, 65535])
+@pytest.mark.parametrize("H", [2, 4, 16, 64])
+def test_any_number_of_entries_under_any_length_bound(lib, n, H):   # noqa: F811
+    """A bound on the lengths that is far too large never makes a batch too large."""
+    c, size = cache(seqs=70000), ctypes.c_size_t()
+    for new in (1, 3, 9, 17, 100):
+        for max_len in (1000, 10 ** 5, 1 << 20, 1 << 29, (1 << 31) - 1):
+            b = batch(n=n, tokens=n * new, max_tokens=new, max_len=max_len)
+            assert lib.fm_paged_attention_workspace_size(at(c), at(b), H, ctypes.byref(size)) == 0
