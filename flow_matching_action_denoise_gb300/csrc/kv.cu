@@ -45,7 +45,10 @@ struct Pool {
   Runs runs;
 };
 
-__host__ __device__ constexpr int up(int a, int b) { return (a + b - 1) / b; }
+template <typename T>
+__host__ __device__ constexpr T up(T a, int b) {
+  return (a + b - 1) / b;
+}
 
 // Exclusive sum over the CTA's THREADS threads; *total receives the sum. Every thread calls it.
 template <int THREADS>
@@ -325,88 +328,128 @@ __global__ void __launch_bounds__(256) copy_shared_kernel(Pool p, const Copy* co
 }
 
 constexpr int kNone = INT32_MIN;   // nothing to do at a place
-// The first place of a row that a release of all but `keep` tokens empties.
-__device__ __forceinline__ int first_unused(int len, int keep, const Book& b) {
-  const int left = min(len, keep);
-  return (left >> b.shift) + ((left & (b.page - 1)) != 0);
+__device__ __forceinline__ int places_of(int tokens, const Book& b) {
+  return (tokens >> b.shift) + ((tokens & (b.page - 1)) != 0);
 }
 
-// fm_kv_fork (kFork) and fm_kv_release: one cluster; every CTA validates all entries before the cluster barrier, and
-// none is changed before every CTA has. The CTAs then take the entries in turn. Bound by latency: dependent loads, two
-// barriers and the cluster's start (64 forks of 30 pages in a pool of 2200: 3.1 us, 1024 of 35: 8.0 us).
-template <bool kFork>
+// fm_kv_fork (kFork) and fm_kv_release: one CTA or one cluster. Every CTA validates all entries; the CTAs then share the
+// places of their rows. A fork looks up the counts of the pages that it names before it changes any. A release takes its
+// own off at once, since only the sum shows a page that two entries name and one row counts. The cluster meets, and either
+// all of it goes on to the table and the lengths, or a release gives the counts back. Bound by latency: dependent loads,
+// barriers, the cluster's start and the code's own way into the caches (with eight places a thread a single row takes
+// 6.4 us, with one 4.5). A fork and its release together: 8 rows of 50 pages 5.1 us, 64 of 30 7.0 us, 1024 of 35 20.2 us, 4 of
+// 8192 11.2 us; looking at the counts is 0.4, 1.1 and 3 us a call of it for 8, 64 and 1024 rows.
+// kTake: 32-place parts that a warp takes at once, their loads on the way together.
+template <bool kFork, int kTake>
 __global__ void __launch_bounds__(kBookThreads)
     share_kernel(Book b, const int32_t* seq, const int32_t* other, int n, int32_t* status) {
-  __shared__ int s_seq[kMaxEntries], s_oth[kMaxEntries], s_len[kMaxEntries], s_bad;
+  __shared__ int s_seq[kMaxEntries], s_oth[kMaxEntries], s_len[kMaxEntries], s_wrong;
   __shared__ Set<kSlotsPer * kMaxEntries> named;   // fork: the targets; release: the sequences
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid == 0) s_bad = 0;
+  const int rank = static_cast<int>(cluster_rank()), warps = static_cast<int>(blockDim.x >> 5);
+  if (tid == 0) s_wrong = 0;
   named.clear(tid, blockDim.x);
-  __syncthreads();
+  // the others may write to s_wrong once this CTA has arrived, which every warp's wait below sees
+  if (gridDim.x > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   pdl_wait();
-  int bad = 0, s = -1 - tid, o = 0;
+  int s = -1, o = 0, len = 0;
+  bool bad = false, again = false;
   if (tid < n) {
     s = seq[tid];
     o = other ? other[tid] : 0;
-    int len = 0;
-    const int64_t room = static_cast<int64_t>(b.table_stride) * b.page;
-    if (s < 0 || s >= b.seqs || (kFork && (o < 0 || o >= b.seqs)) || (!kFork && o < 0)) {
-      bad = FM_KV_BAD_ENTRY;
-    } else {
-      len = b.lens[s];
-      if (len < 0 || len > room || (kFork && b.lens[o] != 0)) bad = FM_KV_BAD_ENTRY;
-    }
+    bad = s < 0 || s >= b.seqs || o < 0 || (kFork && o >= b.seqs);
+    if (bad) s = -1;
     s_seq[tid] = s;
     s_oth[tid] = o;
-    s_len[tid] = len;
-    // fork: a target appears once and is no source; release: a sequence appears once
-    bool again = false;
-    const int name = kFork ? o : s;
-    if (name >= 0) named.put(name, &again);
-    if (again) bad = FM_KV_BAD_ENTRY;
   }
   __syncthreads();
-  if (kFork && tid < n && named.has(s)) bad = FM_KV_BAD_ENTRY;
-  if (bad) atomicOr(&s_bad, bad);
+  // Warps take 32 places of a row each, up to kTake of them at once. The first are loaded beside the lengths.
+  const int parts = up(b.table_stride, 32), step = gridDim.x * warps;
+  const int64_t items = static_cast<int64_t>(n) * parts;   // up to 1024 rows of 2^21 parts
+  int pg[kTake], e[kTake], x[kTake];   // the pages, their entries, their places
+  const int64_t first = rank * warps + warp;
+  auto load = [&](int64_t i0) {
+#pragma unroll
+    for (int u = 0; u < kTake; ++u) {
+      pg[u] = kNone;
+      if (i0 + u * step >= items) continue;
+      const uint32_t i = static_cast<uint32_t>(i0 + u * step);
+      e[u] = i / parts;
+      x[u] = (i - e[u] * parts) * 32 + lane;
+      if (x[u] < b.table_stride && s_seq[e[u]] >= 0) pg[u] = b.table[static_cast<int64_t>(s_seq[e[u]]) * b.table_stride + x[u]];
+    }
+  };
+  load(first);
+  if (tid < n && !bad) {
+    len = b.lens[s];
+    bad = len < 0 || len > static_cast<int64_t>(b.table_stride) * b.page || (kFork && b.lens[o] != 0);
+    s_len[tid] = len;
+    // fork: a target appears once and is no source; release: a sequence appears once
+    named.put(kFork ? o : s, &again);
+    bad |= again;
+  }
   __syncthreads();
-  const int why = s_bad;
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-  const int rank = static_cast<int>(cluster_rank()), warps = static_cast<int>(blockDim.x >> 5);
+  if (kFork && tid < n && s >= 0) bad |= named.has(s);
+  int why = __syncthreads_or(bad) ? FM_KV_BAD_ENTRY : 0;   // the same in every CTA
+  const bool sound = why == 0;
+  // Calls f for each share of the places: of a fork's whole row, of a release's from the first one that it empties.
+  const bool once = items <= kTake * step;
+  auto every = [&](auto f, bool loaded) {
+    for (int64_t i0 = first; i0 < items; i0 += kTake * step) {
+      if (!loaded && !once) load(i0);
+      loaded = false;
+#pragma unroll
+      for (int u = 0; u < kTake; ++u)
+        if (pg[u] != kNone) pg[u] = kFork || x[u] >= places_of(min(s_len[e[u]], s_oth[e[u]]), b) ? max(pg[u], -1) : kNone;
+      f();
+    }
+  };
+  auto in_pool = [&](int p) { return p >= 0 && p < b.pages; };
+  if (sound) {
+    bool wrong = false;
+    every([&] {
+      int refs[kTake];
+#pragma unroll
+      for (int u = 0; u < kTake; ++u) {
+        refs[u] = 1;
+        if (in_pool(pg[u])) refs[u] = kFork ? b.refs[pg[u]] : atomicSub(&b.refs[pg[u]], 1);
+      }
+#pragma unroll
+      for (int u = 0; u < kTake; ++u)
+        wrong |= pg[u] != kNone && (refs[u] < 1 || pg[u] >= b.pages || (pg[u] < 0 && x[u] < places_of(s_len[e[u]], b)));
+    }, true);
+    why = __syncthreads_or(wrong) ? FM_KV_BAD_ENTRY : 0;
+  }
+  if (gridDim.x > 1) {   // what one CTA met all of them learn
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (why && tid < static_cast<int>(gridDim.x))
+      asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(map_dsmem(smem_u32(&s_wrong), tid)), "r"(why) : "memory");
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    why |= *static_cast<volatile int*>(&s_wrong);
+  }
   if (rank == 0 && tid == 0) {
     status[0] = why;
     status[1] = 0;
   }
-  if (why) return;
-  // Warps take (entry, part of its row); a row's unused places are -1 and copied like the rest.
-  const int items = n * 4, step = gridDim.x * warps;
-  auto move = [&](auto take, int i0) {
-    constexpr int kTake = decltype(take)::value;
-    for (int x0 = 0; x0 < b.table_stride; x0 += 128) {
-      int pg[kTake];
-#pragma unroll
-      for (int u = 0; u < kTake; ++u) {
-        const int i = i0 + u * step, e = i >> 2, x = x0 + (i & 3) * 32 + lane;
-        const bool has = i < items && x < b.table_stride && (kFork || x >= first_unused(s_len[e], s_oth[e], b));
-        pg[u] = has ? b.table[static_cast<int64_t>(s_seq[e]) * b.table_stride + x] : kNone;
-      }
+  if (why == 0) {
+    every([&] {   // a row's unused places are -1 and copied like the rest
 #pragma unroll
       for (int u = 0; u < kTake; ++u) {
         if (pg[u] == kNone) continue;
-        const int i = i0 + u * step, e = i >> 2, x = x0 + (i & 3) * 32 + lane;
-        b.table[static_cast<int64_t>(kFork ? s_oth[e] : s_seq[e]) * b.table_stride + x] = kFork ? pg[u] : -1;
-        if (pg[u] >= 0 && pg[u] < b.pages) atomicAdd(&b.refs[pg[u]], kFork ? 1 : -1);
+        b.table[static_cast<int64_t>(kFork ? s_oth[e[u]] : s_seq[e[u]]) * b.table_stride + x[u]] = kFork ? pg[u] : -1;
+        if (kFork && pg[u] >= 0) atomicAdd(&b.refs[pg[u]], 1);
       }
-    }
-  };
-  int i = rank * warps + warp;
-  if (items <= step) {
-    if (i < items) move(std::integral_constant<int, 1>{}, i);
-  } else {   // four at a time, their loads on the way together (1024 forks: 10.4 -> 8.0 us)
-    for (; i < items; i += 4 * step) move(std::integral_constant<int, 4>{}, i);
+    }, false);
+    for (int i = rank * blockDim.x + tid; i < n; i += gridDim.x * blockDim.x)
+      b.lens[kFork ? s_oth[i] : s_seq[i]] = kFork ? s_len[i] : min(s_len[i], s_oth[i]);
+  } else if (sound && !kFork) {
+    every([&] {
+#pragma unroll
+      for (int u = 0; u < kTake; ++u)
+        if (in_pool(pg[u])) atomicAdd(&b.refs[pg[u]], 1);
+    }, false);
   }
-  for (int e = rank * blockDim.x + tid; e < n; e += gridDim.x * blockDim.x)
-    b.lens[kFork ? s_oth[e] : s_seq[e]] = kFork ? s_len[e] : min(s_len[e], s_oth[e]);
 }
 
 // fm_kv_compact, the plan: live pages from n_live on move, in order, into the free ones below n_live, in order.
@@ -788,11 +831,18 @@ LaunchOpts opts(void* stream) {
 template <bool kFork>
 int share(const fm_kv_cache* c, const int32_t* seq, const int32_t* other, int n, int32_t* status, void* stream) {
   LaunchOpts o = opts(stream);
-  // a small call is one small CTA (barriers and a cluster's start are most of it); 64 forks of 50 pages took 12 us so
-  const bool small = n <= kSmallThreads && static_cast<int64_t>(n) * c->table_stride <= 1024;
-  const int threads = small ? kSmallThreads : kBookThreads, ctas = small ? 1 : kForkCluster;
+  // A warp a part of 32 places while the cluster has enough of them; the CTAs that this needs, since barriers and a
+  // cluster's start are most of a small call (a fork and its release of 8 rows of 50 pages: 5.1 us in one CTA, 6.3 in two).
+  const int64_t items = static_cast<int64_t>(n) * up(c->table_stride, 32);
+  const int threads = items <= kSmallThreads / 32 ? kSmallThreads : kBookThreads;
+  int ctas = 1;
+  while (ctas < kForkCluster && ctas * threads / 32 < items) ctas *= 2;
   o.cluster = dim3(ctas, 1, 1);
-  return done(launch(share_kernel<kFork>, dim3(ctas), dim3(threads), 0, o, book_of(*c), seq, other, n, status));
+  // more parts than warps: four at once, eight where four would take a second round (512 rows of two parts: 12.5 us with
+  // four, 14.1 with eight; 1024: 24.3 and 20.2)
+  const int64_t each = up(items, ctas * threads / 32);
+  auto kernel = each <= 1 ? share_kernel<kFork, 1> : each <= 4 ? share_kernel<kFork, 4> : share_kernel<kFork, 8>;
+  return done(launch(kernel, dim3(ctas), dim3(threads), 0, o, book_of(*c), seq, other, n, status));
 }
 
 }  // namespace

@@ -639,7 +639,11 @@ enum {
   FM_KV_NO_PAGES = 1,    /* too few free pages */
   FM_KV_BAD_ENTRY = 2,   /* a sequence out of range, named twice where it may be named once,
                             a negative count, a fork target that is not empty or is also a
-                            source, or bookkeeping that contradicts itself */
+                            source, or bookkeeping that contradicts itself: a length outside of
+                            the row, a begun page to be written to that is none or has more
+                            writers than its count, a place below the length that
+                            fm_kv_fork copies or fm_kv_release empties and that names no page,
+                            or a page counted less often than the rows at hand name it */
   FM_KV_ROW_FULL = 4     /* a sequence would outgrow its table row */
 };
 
@@ -668,7 +672,8 @@ int fm_kv_release(const fm_kv_cache* c, const int32_t* seq, const int32_t* keep,
 
 /* Draw the pool together: with n_live pages in use, those at n_live and above move in
  * ascending order into the free ones below it, in ascending order; K, V (all layers),
- * table and refs follow. Afterwards pages [n_live, pages) are free. Asynchronous. */
+ * table and refs follow. Afterwards pages [n_live, pages) are free. The counts are taken as
+ * they are: a page that is named but not counted is free to it. Asynchronous. */
 int fm_kv_compact(const fm_kv_cache* c, int32_t* status, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Rotary positions. Pair i of a head turns by position * f_i: with FM_ROPE_HALF the elements
