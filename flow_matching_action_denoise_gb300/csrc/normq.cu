@@ -67,7 +67,7 @@ __device__ __forceinline__ void store8(void* base, int64_t at, const float* f) {
   }
 }
 
-// The larger of two, NaN if either is: a row with a NaN or an infinity gives NaN codes, not silent zeros.
+// The larger of two, NaN if either is: a row with a NaN gives NaN codes, not silent zeros.
 __device__ __forceinline__ float max_nan(float a, float b) {
   float d;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
@@ -97,10 +97,16 @@ __device__ __forceinline__ float row_reduce(float v, float* red) {
 // A CTA: rows that fit a warp in groups of 256 threads, else one row, so that no row waits for another's barrier.
 __host__ __device__ constexpr int threads_of(int tpr) { return tpr > 32 ? tpr : 256; }
 
+// CTAs an SM with 32, 48 or 64 registers a thread: a few more for the rare path cost 1000 rows of 2048 a second wave (5.0
+// -> 6.1 us). fp32 rows of 512 threads need 40 (held to 32, 100 rows of 4096 took 5.0 us, now 4.2).
+__host__ __device__ constexpr int resident(int tpr, int nv, bool f32) {
+  return (nv == 1 ? (f32 && tpr == 512 ? 1536 : 2048) : nv == 2 ? 1280 : 1024) / threads_of(tpr);
+}
+
 template <int TPR, int NV, bool F32>
-__global__ void __launch_bounds__(threads_of(TPR)) norm_quant_kernel(const NormParams p) {
+__global__ void __launch_bounds__(threads_of(TPR), resident(TPR, NV, F32)) norm_quant_kernel(const NormParams p) {
   constexpr int kThreads = threads_of(TPR);
-  __shared__ float red[2][kThreads / 32];
+  __shared__ float red[3][kThreads / 32];
   pdl_trigger();
   pdl_wait();
   const int lane = threadIdx.x % TPR;
@@ -135,7 +141,31 @@ __global__ void __launch_bounds__(threads_of(TPR)) norm_quant_kernel(const NormP
 #pragma unroll
     for (int e = 0; e < 8; ++e) ss = fmaf(x[k][e], x[k][e], ss);
   }
-  const float rr = 1.0f / sqrtf(row_reduce<TPR, false>(ss, red[0]) / p.d + p.eps);
+  const float ms = row_reduce<TPR, false>(ss, red[0]) / p.d + p.eps;
+  float rr = 1.0f / sqrtf(ms);
+  // Squares out of fp32's range, the same in all of a row's threads: the row is taken times the power of two that puts the
+  // larger of its maximum and sqrt(eps) into [2, 4). Not finite rows are NaN throughout, whatever a block's own columns are.
+  const bool out = !(ms >= 0x1p-100f && ms < INFINITY);
+  if (TPR > 32 ? out : __any_sync(0xffffffffu, out)) {
+    float top = 0.f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top = max_nan(top, fabsf(x[k][e]));
+    top = row_reduce<TPR, true>(top, red[1]);
+    const uint32_t ex = __float_as_uint(fmaxf(top, sqrtf(p.eps))) >> 23;   // biased exponent
+    const float f = out ? __uint_as_float((255 - min(max(ex, 1u), 254u)) << 23) : 1.0f;
+    ss = 0.f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        x[k][e] *= f;
+        ss = fmaf(x[k][e], x[k][e], ss);
+      }
+    const float scaled = row_reduce<TPR, false>(ss, red[2]) / p.d + p.eps * f * f;
+    if (out) rr = top < INFINITY ? 1.0f / sqrtf(scaled) : NAN;
+  }
   float top[NV];
   float row_top = 0.f;
 #pragma unroll

@@ -746,7 +746,9 @@ int fm_paged_attention(const fm_kv_cache* c, int layer, const fm_kv_batch* b, co
  * x, x_out: device [T][d], fp32 if x_f32 else bf16; r device bf16 [T][d]; `stride` elements
  * between rows (multiples of 8); x_out may be x. gamma device fp32 [d]; codes device uint8
  * [T][d] contiguous: a GEMM operand; scales device fp32 [T] or [T][ceil(d / 128)]. d a
- * multiple of 16 up to 16384. Statistics in fp32 from the unrounded s. Asynchronous.
+ * multiple of 16 up to 16384. Statistics in fp32 from the unrounded s; rows of any finite
+ * size keep their norm; a row whose s holds a NaN or an infinity has NaN codes and scales
+ * throughout, and no other row has. Asynchronous.
  * Source: blog post, "Static quantisation" (the fused residual, norm and FP8 convert), here
  * with scales from the data for activations that have not been calibrated. */
 int fm_norm_quant(const void* x, int64_t x_stride, int x_f32, const uint16_t* r, int64_t r_stride, const float* gamma,
