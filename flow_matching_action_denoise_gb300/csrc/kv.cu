@@ -874,8 +874,10 @@ int kv_check(const fm_kv_cache* c) {
   int64_t span = c->Dh;
   for (const auto& x : d) {
     if (x.extent == 1) continue;
-    if (x.stride * eb % 16) return record_error(FM_ERR_SHAPE, "cache strides must be multiples of 16 bytes");
     if (x.stride < span || x.stride >= (int64_t(1) << 40) / eb) return record_error(FM_ERR_SHAPE, "cache strides overlap or are too large");
+    if (x.stride * eb % 16) return record_error(FM_ERR_SHAPE, "cache strides must be multiples of 16 bytes");
+    // nothing that the next dims' strides are held against, and no address, leaves 64 bits
+    if (x.extent - 1 > ((int64_t(1) << 56) - span) / x.stride) return record_error(FM_ERR_SHAPE, "the cache exceeds 2^56 elements");
     span += x.stride * (x.extent - 1);
   }
   return FM_OK;

@@ -15,3 +15,13 @@ def test_any_number_of_entries_under_any_length_bound(lib, n, H):   # noqa: F811
         for max_len in (1000, 10 ** 5, 1 << 20, 1 << 29, (1 << 31) - 1):
             b = batch(n=n, tokens=n * new, max_tokens=new, max_len=max_len)
             assert lib.fm_paged_attention_workspace_size(at(c), at(b), H, ctypes.byref(size)) == 0
+
+
+@pytest.mark.parametrize("kw", [
+    dict(pages=1 << 30, page_stride=(1 << 39) - 64, layers=3, layer_stride=(1 << 39) - 16),
+    dict(pages=1 << 30, page_stride=(1 << 39) - 16, layers=3, layer_stride=(1 << 39) - 16),
+    dict(pages=1 << 30, page_stride=1 << 34, layers=1), dict(page_stride=(1 << 63) - 8), dict(layer_stride=-(1 << 63)),
+])
+def test_strides_whose_products_leave_64_bits(lib, kw):   # noqa: F811
+    size = ctypes.c_size_t()
+    assert lib.fm_kv_workspace_size(at(cache(**kw)), 1, ctypes.byref(size)) == 2
