@@ -1050,6 +1050,8 @@ extern "C" int fm_rope_append(const fm_kv_cache* c, int layer, const fm_kv_batch
   if (k_stride < kv_row || v_stride < kv_row || k_stride % 8 || v_stride % 8 ||
       (H > 0 && (q_stride < q_row || q_out_stride < q_row || q_stride % 8 || q_out_stride % 8)))
     return record_error(FM_ERR_SHAPE, "token strides must be multiples of 8 elements and hold the token's heads");
+  if (H > 0 && q == q_out && q_stride != q_out_stride && b->tokens > 1)
+    return record_error(FM_ERR_SHAPE, "q_out in the place of q needs q's stride");
   for (const void* x : {static_cast<const void*>(k), static_cast<const void*>(v), static_cast<const void*>(q),
                         static_cast<const void*>(q_out)})
     if (reinterpret_cast<uintptr_t>(x) % 16) return record_error(FM_ERR_ALIGN, "q, k, v and q_out must be 16-byte aligned");

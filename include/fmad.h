@@ -710,7 +710,7 @@ typedef struct fm_rope {
 /* Rotate the batch's queries into q_out and its keys into the cache's pages, and store its
  * values there: q [tokens][H][Dh], k, v [tokens][Hkv][Dh], q_out like q, all bf16 with
  * `stride` elements between tokens (a multiple of 8; parts of one merged projection output
- * do); q_out may be q, else it overlaps none of them. A sequence is in the batch once. H = 0 stores keys and values only. The pages must exist
+ * do); q_out may be q (with its stride), else it overlaps none of them. A sequence is in the batch once. H = 0 stores keys and values only. The pages must exist
  * (fm_kv_reserve); pages of an FP8 cache receive E4M3(x * fp32(1 / scale)), saturated.
  * positions: NULL, or device int32 [tokens] that replaces the positions in the angles (not
  * the places in the cache). A token without a page sets bit 2 of fm_standalone_status and

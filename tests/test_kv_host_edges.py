@@ -3,7 +3,8 @@ import ctypes
 
 import pytest
 
-from test_kv_host import at, batch, cache, lib   # noqa: F401  (lib is a fixture)
+import flow_matching_action_denoise_gb300 as fmad
+from test_kv_host import P, at, batch, cache, lib   # noqa: F401  (lib is a fixture)
 
 
 @pytest.mark.parametrize("n", [300, 4096, 20000, 65535])
@@ -25,3 +26,10 @@ def test_any_number_of_entries_under_any_length_bound(lib, n, H):   # noqa: F811
 def test_strides_whose_products_leave_64_bits(lib, kw):   # noqa: F811
     size = ctypes.c_size_t()
     assert lib.fm_kv_workspace_size(at(cache(**kw)), 1, ctypes.byref(size)) == 2
+
+
+def test_queries_rotated_in_place_keep_their_stride(lib):   # noqa: F811
+    """With another stride a row would be written over one that is still to be read."""
+    c, b, r = cache(), batch(), fmad.FmRope(P, 64, 0, 1.0)
+    for qs, os_ in ((256, 264), (512, 256)):
+        assert lib.fm_rope_append(at(c), 0, at(b), at(r), P, qs, 4, 2 * P, 128, 3 * P, 128, P, os_, None, None) == 2
