@@ -272,6 +272,7 @@ extern "C" int fm_norm_quant(const void* x, int64_t x_stride, int x_f32, const u
   if (x_stride < d || x_stride % 8 || (r && (r_stride < d || r_stride % 8)) ||
       (x_out && (x_out_stride < d || x_out_stride % 8)))
     return record_error(FM_ERR_SHAPE, "row strides must be multiples of 8 elements and hold d");
+  if (x == x_out && x_stride != x_out_stride && T > 1) return record_error(FM_ERR_SHAPE, "x_out in the place of x needs x's stride");
   for (const void* q : {x, static_cast<const void*>(r), static_cast<const void*>(gamma), static_cast<const void*>(x_out),
                         static_cast<const void*>(codes)})
     if (reinterpret_cast<uintptr_t>(q) % 16) return record_error(FM_ERR_ALIGN, "x, r, gamma, x_out and codes must be 16-byte aligned");

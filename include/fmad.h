@@ -744,7 +744,7 @@ int fm_paged_attention(const fm_kv_cache* c, int layer, const fm_kv_batch* b, co
  *   scale = max|y| / 448 over the row (block 0) or over each 128 columns (block 128, the
  *   last block may be shorter);  codes = E4M3(y / scale), 0 where scale is 0.
  * x, x_out: device [T][d], fp32 if x_f32 else bf16; r device bf16 [T][d]; `stride` elements
- * between rows (multiples of 8); x_out may be x. gamma device fp32 [d]; codes device uint8
+ * between rows (multiples of 8); x_out may be x (with its stride). gamma device fp32 [d]; codes device uint8
  * [T][d] contiguous: a GEMM operand; scales device fp32 [T] or [T][ceil(d / 128)]. d a
  * multiple of 16 up to 16384. Statistics in fp32 from the unrounded s; rows of any finite
  * size keep their norm; a row whose s holds a NaN or an infinity has NaN codes and scales

@@ -33,3 +33,8 @@ def test_queries_rotated_in_place_keep_their_stride(lib):   # noqa: F811
     c, b, r = cache(), batch(), fmad.FmRope(P, 64, 0, 1.0)
     for qs, os_ in ((256, 264), (512, 256)):
         assert lib.fm_rope_append(at(c), 0, at(b), at(r), P, qs, 4, 2 * P, 128, 3 * P, 128, P, os_, None, None) == 2
+
+
+def test_norm_rows_stored_in_place_keep_their_stride(lib):   # noqa: F811
+    for xs, os_ in ((256, 264), (512, 256)):
+        assert lib.fm_norm_quant(P, xs, 1, None, 0, None, 4, 256, 1e-6, P, os_, 2 * P, 3 * P, 0, None) == 2
