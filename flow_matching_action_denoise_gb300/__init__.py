@@ -692,13 +692,14 @@ def rope_table(rotary_dim: int, theta: float = 10000.0, scaling: int = ROPE_PLAI
 
 
 class Rope:
-    """Rotary positions: the device table of rope_table and the layout of the pairs."""
+    """Rotary positions: the device table of rope_table and the layout of the pairs. rotary_dim 0: no rotation."""
 
     def __init__(self, rotary_dim: int, theta: float = 10000.0, half: bool = True, scaling: int = ROPE_PLAIN,
                  factor: float = 1.0, original_len: float = 0.0, beta_fast: float = 32.0, beta_slow: float = 1.0,
                  device="cuda"):
         import torch
-        freq, mag = rope_table(rotary_dim, theta, scaling, factor, original_len, beta_fast, beta_slow)
+        freq, mag = (rope_table(rotary_dim, theta, scaling, factor, original_len, beta_fast, beta_slow) if rotary_dim
+                     else (np.zeros(0, dtype=np.uint64), 1.0))
         self.freq = torch.from_numpy(freq.view(np.int64)).to(device)
         self.device, self.dev = self.freq.device, self.freq.get_device()
         self.struct = FmRope(self.freq.data_ptr(), int(rotary_dim), ROPE_HALF if half else ROPE_INTERLEAVED, mag)

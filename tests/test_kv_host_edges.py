@@ -38,3 +38,11 @@ def test_queries_rotated_in_place_keep_their_stride(lib):   # noqa: F811
 def test_norm_rows_stored_in_place_keep_their_stride(lib):   # noqa: F811
     for xs, os_ in ((256, 264), (512, 256)):
         assert lib.fm_norm_quant(P, xs, 1, None, 0, None, 4, 256, 1e-6, P, os_, 2 * P, 3 * P, 0, None) == 2
+
+
+def test_no_rotation_needs_no_table():
+    none = fmad.Rope(0, device="cpu")
+    assert none.struct.rotary_dim == 0 and none.freq.numel() == 0
+    for dim in (8, -16, 272):
+        with pytest.raises(fmad.FmError):
+            fmad.Rope(dim, device="cpu")
