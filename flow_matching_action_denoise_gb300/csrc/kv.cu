@@ -12,9 +12,7 @@
 #include <cuda_fp8.h>
 
 #include <algorithm>
-#include <atomic>
 #include <cmath>
-#include <type_traits>
 
 #include "kv.h"
 #include "ptx.cuh"

@@ -346,10 +346,7 @@ __global__ void __launch_bounds__(threads_of(F8), 1)
     else
       asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
   } else {
-    if constexpr (F8)
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    else
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
   }
 
   if (warp < 8) {
@@ -1051,7 +1048,6 @@ int check(const fm_kv_cache* c, const fm_kv_batch* b, int H) {
   if (st != FM_OK) return st;
   if (H <= 0 || H % c->Hkv) return record_error(FM_ERR_SHAPE, "H must be a positive multiple of the cache's Hkv");
   if (c->Dh != 64 && c->Dh != 128) return record_error(FM_ERR_SHAPE, "attention takes head dims of 64 or 128");
-  if (c->page_tokens > 256) return record_error(FM_ERR_SHAPE, "attention takes pages of 16 to 256 tokens");
   const int64_t rows = static_cast<int64_t>(b->max_tokens) * (H / c->Hkv);
   if (rows > (int64_t(1) << 30)) return record_error(FM_ERR_SHAPE, "max_tokens * H / Hkv exceeds 2^30");
   return FM_OK;
