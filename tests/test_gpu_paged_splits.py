@@ -89,6 +89,29 @@ def test_a_nan_query_row_is_not_hidden(lens, new, H, bound, fp8):
     assert torch.equal(out, clean)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("lens,new,H", [([30], [1], 8), ([1500, 90], [1, 2], 8), ([260, 40], [12, 5], 8), ([700, 300], [300, 70], 8),
+                                        ([4000, 300], [4000, 300], 8)])
+def test_a_nan_query_row_in_shorter_calls(lens, new, H, fp8):
+    """The same where one CTA or one cluster has all of a row's keys (all but the fourth), up to the widest row blocks."""
+    require_gpu()
+    c = Cache(lens, 16, 1, 64, fp8, seed=H)
+    b = batch(c, new)
+    nb = fmad.paged_attention_workspace_size(c.handle, b, H)
+    assert (nb == 0) == (new[0] != 300)
+    ws = torch.empty(nb, dtype=torch.uint8, device="cuda")
+    q = torch.randn((b.tokens, H, 64), device="cuda").to(torch.bfloat16)
+    clean, out = torch.empty_like(q), torch.empty_like(q)
+    fmad.paged_attention(c.handle, 0, b, q, clean, ws)
+    token, head = b.tokens - 1, H - 1
+    q[token, head, 5] = float("nan")
+    fmad.paged_attention(c.handle, 0, b, q, out, ws)
+    assert fmad.standalone_status() == 0
+    assert out[token, head].isnan().all()
+    out[token, head] = clean[token, head]
+    assert torch.equal(out, clean)
+
+
 def test_entries_times_splits_beyond_a_grid():
     """Thousands of entries under a very loose length bound: the call divides its keys less, it is not refused."""
     require_gpu()
