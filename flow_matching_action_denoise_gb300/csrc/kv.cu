@@ -4,8 +4,8 @@
 //
 // Bookkeeping. A sequence is a row of the page table and a length; `refs` counts the rows that name a page, 0 = free.
 // All of it lives on the device, so a serving step (fork, reserve, append, attend, release) needs no host round trip
-// and can be captured into a graph. Calls are all or nothing: every entry is validated before anything is written,
-// and the two status words say why a call did nothing. Free pages are taken lowest index first, so the result of a
+// and can be captured into a graph. Calls are all or nothing: every entry is validated before a row or a length is
+// written, and the two status words say why a call did nothing. Free pages are taken lowest index first, so the result of a
 // call depends on its arguments alone. No kernel here waits on another CTA except through a cluster barrier.
 
 #include <cuda_bf16.h>
@@ -726,8 +726,10 @@ __device__ __forceinline__ uint4 row_chunk(const uint8_t* row, int c, int f8, fl
   return pack8(f);
 }
 
-// Bound by HBM and, for one sequence, by its launch. One CTA: 64 tokens of one layer and head; keys are copied, values turned through shared memory so that both the
-// reads (rows) and the writes (16 bytes along the tokens where a whole group lies inside) are wide.
+// One CTA: 64 tokens of one layer and head; keys are copied, values are read as rows and turned through shared memory, so
+// that a warp stores 64 contiguous bytes along the tokens (two a lane: tok_begin may be odd). Bound by its launch, the chain
+// length -> page -> row and these narrow stores: 788 tokens of 18 layers and one head of 128 take 4.4 us in a graph with bf16
+// pages, 5.3 us with E4M3 (14.5 MB read and written: 2.1 us at HBM's rate).
 __global__ void __launch_bounds__(256) prefix_kernel(const PrefixParams p) {
   extern __shared__ uint16_t s_v[];   // [64][Dh + 2]
   const int layer = blockIdx.z, g = blockIdx.y, t0 = blockIdx.x * kPrefixTile;

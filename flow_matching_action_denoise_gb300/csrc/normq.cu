@@ -1,12 +1,15 @@
 // Residual addition, RMS norm and E4M3 output with scales in one pass (fm_norm_quant).
 //
 //   s = x + r;  y = s / sqrt(mean(s^2) + eps) * gamma;  scale = max|y| / 448 over the row or over 128 columns;
-//   code = E4M3(y / scale)
+//   code = E4M3(y * fp32(1 / scale))
+//
+// The reciprocal is rounded once a scale: a division an element is what it saves, and a code differs from E4M3(y / scale)
+// only where y / scale lies within 2^-23 of itself from a tie.
 //
 // Bound by HBM: x, r, the sum and the codes cross it once, a row stays in registers between its two reductions.
 // A row belongs to 8..512 threads with one to four 8-element vectors each, all loads issued before the first reduction,
 // and a CTA of its own where it takes more than a warp, so that no row waits for another's reduction (CTAs of four rows in
-// step took 38 us for 12000 rows of 2048, now 28.8 us: 6.0 TB/s). Sums and scales are fp32; s is rounded once to x's
+// step took 38 us for 12000 rows of 2048, now 29.9 us: 5.8 TB/s). Sums and scales are fp32; s is rounded once to x's
 // type when stored and the norm uses it unrounded.
 
 #include <cuda_bf16.h>

@@ -621,8 +621,9 @@ typedef struct fm_kv_cache {
  * start[i], its row j is the token at position lens[seq[i]] - new + j. So lens already
  * counts the new tokens (fm_kv_reserve adds them). Rows that belong to no entry are neither
  * read nor written. max_tokens bounds every entry's new tokens (more: bit 2 of the error
- * word, and the rows behind it are not computed); max_len is the length that the work is
- * divided for (a longer sequence is right, only slower). 0 <= n <= 65535. */
+ * word, and the rows behind it stay as they are); max_len is the length that the work is
+ * divided for (a longer sequence is right, only slower). 0 <= n <= 65535. With n, tokens or
+ * max_tokens 0 a call launches nothing and reports nothing. */
 typedef struct fm_kv_batch {
   const int32_t* start;   /* device [n + 1] */
   const int32_t* seq;     /* device [n] or NULL */
@@ -710,7 +711,8 @@ typedef struct fm_rope {
 /* Rotate the batch's queries into q_out and its keys into the cache's pages, and store its
  * values there: q [tokens][H][Dh], k, v [tokens][Hkv][Dh], q_out like q, all bf16 with
  * `stride` elements between tokens (a multiple of 8; parts of one merged projection output
- * do); q_out may be q (with its stride), else it overlaps none of them. A sequence is in the batch once. H = 0 stores keys and values only. The pages must exist
+ * do); q_out may be q (with its stride), else it overlaps none of them. A sequence is in the
+ * batch once. H = 0 stores keys and values only. The pages must exist
  * (fm_kv_reserve); pages of an FP8 cache receive E4M3(x * fp32(1 / scale)), saturated.
  * positions: NULL, or device int32 [tokens] that replaces the positions in the angles (not
  * the places in the cache). A token without a page sets bit 2 of fm_standalone_status and
@@ -729,7 +731,8 @@ int fm_paged_attention_workspace_size(const fm_kv_cache* c, const fm_kv_batch* b
  * window > 0; query head h reads KV head h / (H / Hkv). Tokens at negative positions, and
  * any row without keys, give zeros. q, out: device bf16 [tokens][H][Dh], `stride` elements
  * between tokens (a multiple of 8); out must not overlap q. Dh 64 or 128; H a multiple of
- * Hkv; scale > 0. Softmax and sums in fp32, probabilities rounded to bf16 (f16 with an FP8
+ * Hkv; max_tokens * H / Hkv up to 2^30; scale > 0. Queries are finite; a NaN in one makes
+ * its row NaN and no other. Softmax and sums in fp32, probabilities rounded to bf16 (f16 with an FP8
  * cache). What a page holds behind its sequence's length does not matter, even NaN; the
  * keys and values before it must be finite (a NaN there reaches every row whose key tile
  * holds it, masked or not). A token without a page counts as a zero key and value and sets
@@ -742,11 +745,12 @@ int fm_paged_attention(const fm_kv_cache* c, int layer, const fm_kv_batch* b, co
  *   s = x + r (r NULL: x);  x_out = s (unless NULL);
  *   y = s / sqrt(mean(s^2) + eps) * gamma (gamma NULL: 1);
  *   scale = max|y| / 448 over the row (block 0) or over each 128 columns (block 128, the
- *   last block may be shorter);  codes = E4M3(y / scale), 0 where scale is 0.
+ *   last block may be shorter);  codes = E4M3(y * fp32(1 / scale)), 0 where scale is 0
+ *   (scales up to 1e-30, whose reciprocal may overflow: E4M3(y / scale)).
  * x, x_out: device [T][d], fp32 if x_f32 else bf16; r device bf16 [T][d]; `stride` elements
- * between rows (multiples of 8); x_out may be x (with its stride). gamma device fp32 [d]; codes device uint8
- * [T][d] contiguous: a GEMM operand; scales device fp32 [T] or [T][ceil(d / 128)]. d a
- * multiple of 16 up to 16384. Statistics in fp32 from the unrounded s; rows of any finite
+ * between rows (multiples of 8); x_out may be x (with its stride), the outputs
+ * overlap nothing else. gamma device fp32 [d]; codes device uint8 [T][d] contiguous: a GEMM
+ * operand; scales device fp32 [T] or [T][ceil(d / 128)]. d a multiple of 16 up to 16384. Statistics in fp32 from the unrounded s; rows of any finite
  * size keep their norm; a row whose s holds a NaN or an infinity has NaN codes and scales
  * throughout, and no other row has. Asynchronous.
  * Source: blog post, "Static quantisation" (the fused residual, norm and FP8 convert), here
