@@ -24,7 +24,8 @@ __all__ = [
     "FLAG_O_CONSUMER_IN_GEMM", "COND_TIME", "COND_GIVEN",
     "ABI_VERSION", "STATUS",
     "KvCache", "KvBatch", "Rope", "refresh_prefix_pages", "kv_workspace_size", "kv_reserve", "kv_fork", "kv_release",
-    "kv_compact", "rope_table", "rope_append", "paged_attention_workspace_size", "paged_attention", "norm_quant",
+    "kv_compact", "rope_table", "rope_append", "norm_rope_append", "paged_attention_workspace_size",
+    "paged_attention", "norm_quant",
     "ROPE_HALF", "ROPE_INTERLEAVED", "ROPE_PLAIN", "ROPE_LINEAR", "ROPE_BASE", "ROPE_BY_PARTS",
     "KV_NO_PAGES", "KV_BAD_ENTRY", "KV_ROW_FULL",
 ]
@@ -54,7 +55,8 @@ EXPORTS = [
     "fm_warm_trace_size", "fm_decode_warm_trace", "fm_test_launch_kernel", "fm_decode_timeline",
     "fm_test_skinny_gemm_tile", "fm_test_pdl_chain", "fm_test_grid_barrier", "fm_test_attn_plan",
     "refresh_prefix_pages", "fm_kv_workspace_size", "fm_kv_reserve", "fm_kv_fork", "fm_kv_release", "fm_kv_compact",
-    "fm_rope_table", "fm_rope_append", "fm_paged_attention_workspace_size", "fm_paged_attention", "fm_norm_quant",
+    "fm_rope_table", "fm_rope_append", "fm_norm_rope_append", "fm_paged_attention_workspace_size", "fm_paged_attention",
+    "fm_norm_quant",
 ]
 
 
@@ -190,6 +192,8 @@ def load() -> ctypes.CDLL:
         "fm_rope_table": (i, [vp, vp, vp]),
         "fm_rope_append": (i, [vp, i, vp, vp, vp, ctypes.c_int64, i, vp, ctypes.c_int64, vp, ctypes.c_int64, vp,
                                ctypes.c_int64, vp, vp]),
+        "fm_norm_rope_append": (i, [vp, i, vp, vp, vp, ctypes.c_int64, i, vp, ctypes.c_int64, vp, ctypes.c_int64, vp,
+                                    ctypes.c_int64, vp, vp, ctypes.c_float, vp, vp]),
         "fm_paged_attention_workspace_size": (i, [vp, vp, i, ctypes.POINTER(sz)]),
         "fm_paged_attention": (i, [vp, i, vp, vp, ctypes.c_int64, i, ctypes.c_float, i, i, vp, ctypes.c_int64, vp, sz,
                                    vp]),
@@ -756,11 +760,10 @@ def kv_compact(cache: KvCache, status, workspace, stream=None):
         _check(st, w)
 
 
-def rope_append(cache: KvCache, layer: int, batch: KvBatch, rope: Rope, q, k, v, q_out, positions=None, stream=None):
-    """Rotate q [tokens][H][Dh] into q_out and k [tokens][Hkv][Dh] into the pages, store v there (all bfloat16; q and
-    q_out None: keys and values only)."""
+def _append_arguments(w: str, cache, batch, rope, q, k, v, q_out, positions):
+    """(q, its stride, H, k, stride, v, stride, q_out, stride, positions) as the C side takes them."""
     import torch
-    d, w, bf, T, Hkv, Dh = cache.dev, "fm_rope_append", torch.bfloat16, batch.tokens, cache.Hkv, cache.Dh
+    d, bf, T, Hkv, Dh = cache.dev, torch.bfloat16, batch.tokens, cache.Hkv, cache.Dh
     if batch.dev != d or rope.dev != d:
         _bad(w, "the cache, the batch and the rotary table must be on one device")
     H, qp, qs, op, os_ = 0, None, 0, None, 0
@@ -772,9 +775,38 @@ def rope_append(cache: KvCache, layer: int, batch: KvBatch, rope: Rope, q, k, v,
         op, os_ = _heads(q_out, w, "q_out", bf, d, T, H, Dh)
     kp, ks = _heads(k, w, "k", bf, d, T, Hkv, Dh)
     vp, vs = _heads(v, w, "v", bf, d, T, Hkv, Dh)
-    st = (_lib or load()).fm_rope_append(cache.addr, layer, batch.addr, rope.addr, qp, qs, H, kp, ks, vp, vs, op, os_,
-                                         None if positions is None else _ints(positions, w, "positions", d, T),
-                                         _here(d, stream, w))
+    return qp, qs, H, kp, ks, vp, vs, op, os_, None if positions is None else _ints(positions, w, "positions", d, T)
+
+
+def rope_append(cache: KvCache, layer: int, batch: KvBatch, rope: Rope, q, k, v, q_out, positions=None, stream=None):
+    """Rotate q [tokens][H][Dh] into q_out and k [tokens][Hkv][Dh] into the pages, store v there (all bfloat16; q and
+    q_out None: keys and values only)."""
+    w = "fm_rope_append"
+    *heads, pos = _append_arguments(w, cache, batch, rope, q, k, v, q_out, positions)
+    st = (_lib or load()).fm_rope_append(cache.addr, layer, batch.addr, rope.addr, *heads, pos, _here(cache.dev, stream, w))
+    if st:
+        _check(st, w)
+
+
+def _gain(x, where: str, name: str, dev: int, dim: int):
+    if x is None:
+        return None
+    import torch
+    if x.dtype is not torch.float32 or x.get_device() != dev or x.shape != (dim,) or not x.is_contiguous():
+        _check_tensor(x, where, name, (torch.float32,), dev, (dim,))
+        _bad(where, f"{name} must be contiguous")
+    return x.data_ptr()
+
+
+def norm_rope_append(cache: KvCache, layer: int, batch: KvBatch, rope: Rope, q, k, v, q_out, q_gamma=None, k_gamma=None,
+                     eps: float = 1e-6, positions=None, stream=None):
+    """rope_append of heads of q and k that are RMS-normalised first, times q_gamma and k_gamma (float32 [Dh]; None: 1)."""
+    w = "fm_norm_rope_append"
+    *heads, pos = _append_arguments(w, cache, batch, rope, q, k, v, q_out, positions)
+    st = (_lib or load()).fm_norm_rope_append(cache.addr, layer, batch.addr, rope.addr, *heads,
+                                              _gain(q_gamma, w, "q_gamma", cache.dev, cache.Dh),
+                                              _gain(k_gamma, w, "k_gamma", cache.dev, cache.Dh), eps, pos,
+                                              _here(cache.dev, stream, w))
     if st:
         _check(st, w)
 

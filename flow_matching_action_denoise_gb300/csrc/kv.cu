@@ -532,6 +532,9 @@ struct AppendParams {
   int tokens, max_tokens, seqs, table_stride, pages, page, shift;
   int H, Hkv, Dh;
   int toks, groups;         // tokens of a CTA, threads that share the heads of a token
+  int lanes;                // threads of a head
+  const float *q_gamma, *k_gamma;   // normalised heads: [Dh] or null
+  float eps;
   void *kc, *vc;            // this layer
   int64_t pg, tok, head;    // strides in elements
   const float *k_scale, *v_scale;
@@ -569,12 +572,14 @@ __device__ __forceinline__ uint2 codes8(const float* f, float rs) {
 // without double precision. One thread: 16 elements (two 8-element chunks that hold whole pairs) of every groups-th
 // head. Bound by HBM: q, k and v are read once and written once (9600 tokens of 16 + 2 x 4 heads of 128, half of each
 // rotated, bf16 cache: 23.2 us, 5.1 TB/s; 32 single tokens: 2.5 us, launch).
-template <bool F8>
+// NORM: every head of q and k is divided by its root mean square and multiplied by gamma before it turns. A head's threads
+// are a power of two of neighbouring lanes (some of them idle where Dh / 16 is none), which add their squares by shuffles.
+template <bool F8, bool NORM>
 __global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
-  extern __shared__ float2 s_angle[];   // [toks][rot / 2] (cos, sin) times magnitude
+  extern __shared__ float2 s_angle[];   // [toks][rot / 2] (cos, sin) times magnitude; NORM: then [2][Dh] gammas
   pdl_trigger();
-  const int units = p.Dh / 16, pairs = p.rot / 2;
-  const int unit = threadIdx.x % units, tok = (threadIdx.x / units) % p.toks, grp = threadIdx.x / (units * p.toks);
+  const int units = p.Dh / 16, pairs = p.rot / 2, lanes = NORM ? p.lanes : units;
+  const int unit = threadIdx.x % lanes, tok = (threadIdx.x / lanes) % p.toks, grp = threadIdx.x / (lanes * p.toks);
   const int entry = blockIdx.y;
   pdl_wait();
   const int begin = p.start[entry], nq = p.start[entry + 1] - begin;
@@ -586,6 +591,35 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
   const int first = blockIdx.x * p.toks, end = min(nq, p.max_tokens);
   if (bad || first >= end) return;   // the same for the whole CTA
   const int past = len - nq;
+  // chunks of this unit (in 8 elements): a rotated pair of chunks, or two that pass through
+  const int rot_units = p.rot / 16;
+  const bool turned = unit < rot_units, split = turned && !p.interleaved;
+  const bool idle = NORM && unit >= units;   // takes part in the shuffles only; its places are those of unit 0
+  const int c0 = idle ? 0 : (split ? unit : 2 * unit) * 8, c1 = idle ? 0 : (split ? unit + rot_units : 2 * unit + 1) * 8;
+  [[maybe_unused]] constexpr int kHeads = 4;   // NORM: heads whose loads are on their way together
+  [[maybe_unused]] uint4 u[NORM ? kHeads : 1], w[NORM ? kHeads : 1];
+  [[maybe_unused]] auto load_heads = [&](int h0, int heads) {
+    const int64_t token = begin + static_cast<int64_t>(first) + tok;
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i) {
+      const int h = h0 + i * p.groups;
+      u[i] = w[i] = make_uint4(0, 0, 0, 0);
+      if (h >= heads || idle) continue;
+      const __nv_bfloat16* src = h < p.H ? p.q + token * p.qs + h * p.Dh
+                                 : h < p.H + p.Hkv ? p.k + token * p.ks + (h - p.H) * p.Dh
+                                                   : p.v + token * p.vs + (h - p.H - p.Hkv) * p.Dh;
+      u[i] = *reinterpret_cast<const uint4*>(src + c0);
+      w[i] = *reinterpret_cast<const uint4*>(src + c1);
+    }
+  };
+  [[maybe_unused]] float* s_gamma = reinterpret_cast<float*>(s_angle + p.toks * pairs);
+  if constexpr (NORM) {   // the first heads are loaded while the angles are computed
+    if (grp < p.groups && first + tok < end) load_heads(grp, p.H + 2 * p.Hkv);
+    for (int x = threadIdx.x; x < 2 * p.Dh; x += 256) {
+      const float* src = x < p.Dh ? p.q_gamma : p.k_gamma;
+      s_gamma[x] = src ? src[x < p.Dh ? x : x - p.Dh] : 1.0f;
+    }
+  }
   for (int x = threadIdx.x; x < p.toks * pairs; x += 256) {
     const int i = x % pairs, w = first + x / pairs;
     if (w >= end) break;
@@ -607,10 +641,6 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
   if (mine && page < 0 && unit == 0 && grp == 0) atomicOr(p.err, kErrBadBatch);
   __syncthreads();
   if (!mine) return;
-  // chunks of this unit (in 8 elements): a rotated pair of chunks, or two that pass through
-  const int rot_units = p.rot / 16;
-  const bool turned = unit < rot_units, split = turned && !p.interleaved;
-  const int c0 = (split ? unit : 2 * unit) * 8, c1 = (split ? unit + rot_units : 2 * unit + 1) * 8;
   float2 ang[8];
   if (turned) {
     const float4* src = reinterpret_cast<const float4*>(s_angle + tok * pairs + unit * 8);
@@ -641,6 +671,85 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
       }
     }
   };
+  if constexpr (NORM) {
+    const uint32_t team = ((1u << lanes) - 1u) << (threadIdx.x & 31 & ~(lanes - 1));
+    auto reduce = [&](float v, auto join) {   // over the head's lanes, in a fixed order, the same in all of them
+      for (int o = lanes >> 1; o > 0; o >>= 1) v = join(v, __shfl_xor_sync(team, v, o));
+      return v;
+    };
+    const auto add = [](float x, float y) { return x + y; };
+    const auto larger = [](float x, float y) { return x > y || x != x ? x : y; };   // NaN if either is
+    const float rdh = 1.0f / p.Dh;
+    auto normalise = [&](float* a, float* b, const float* gamma) {
+      auto squares = [&] {
+        float s = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s = fmaf(a[e], a[e], fmaf(b[e], b[e], s));
+        return reduce(s, add);
+      };
+      const float ms = fmaf(squares(), rdh, p.eps);
+      float rr = 1.0f / sqrtf(ms);
+      // Squares out of fp32's range, the same in all of the head's lanes: the head is taken times the power of two that puts
+      // the larger of its maximum and sqrt(eps) into [2, 4). A head with a NaN or an infinity is NaN throughout.
+      if (!(ms >= 0x1p-100f && ms < INFINITY)) {
+        float top = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = larger(larger(top, fabsf(a[e])), fabsf(b[e]));
+        top = reduce(top, larger);
+        const uint32_t ex = __float_as_uint(fmaxf(top, sqrtf(p.eps))) >> 23;
+        const float f = __uint_as_float((255 - min(max(ex, 1u), 254u)) << 23);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) a[e] *= f, b[e] *= f;
+        const float scaled = squares() * rdh + p.eps * f * f;
+        rr = !(top < INFINITY) ? NAN : scaled > 0.f ? 1.0f / sqrtf(scaled) : 0.f;
+      }
+      const float4* g0 = reinterpret_cast<const float4*>(gamma + c0);
+      const float4* g1 = reinterpret_cast<const float4*>(gamma + c1);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float4 x = g0[e], y = g1[e];
+        a[4 * e] *= rr * x.x, a[4 * e + 1] *= rr * x.y, a[4 * e + 2] *= rr * x.z, a[4 * e + 3] *= rr * x.w;
+        b[4 * e] *= rr * y.x, b[4 * e + 1] *= rr * y.y, b[4 * e + 2] *= rr * y.z, b[4 * e + 3] *= rr * y.w;
+      }
+    };
+    const float rk = F8 ? 1.0f / *p.k_scale : 1.0f, rv = F8 ? 1.0f / *p.v_scale : 1.0f;
+    const int64_t cell = static_cast<int64_t>(page) * p.pg + (pos & (p.page - 1)) * p.tok;
+    const int heads = page < 0 ? p.H : p.H + 2 * p.Hkv;
+    for (int h0 = grp; h0 < heads; h0 += kHeads * p.groups) {
+      if (h0 != grp) load_heads(h0, heads);
+#pragma unroll
+      for (int i = 0; i < kHeads; ++i) {
+        const int h = h0 + i * p.groups;
+        if (h >= heads) break;
+        const bool is_q = h < p.H, is_v = h >= p.H + p.Hkv;
+        float a[8], b[8];
+        unpack8(u[i], a);
+        unpack8(w[i], b);
+        if (!is_v) {
+          normalise(a, b, s_gamma + (is_q ? 0 : p.Dh));
+          turn(a, b);
+        }
+        if (idle) continue;
+        if (is_q) {
+          __nv_bfloat16* dst = p.q_out + token * p.os + h * p.Dh;
+          *reinterpret_cast<uint4*>(dst + c0) = pack8(a);
+          *reinterpret_cast<uint4*>(dst + c1) = pack8(b);
+          continue;
+        }
+        const int64_t at = cell + (h - p.H - (is_v ? p.Hkv : 0)) * p.head;
+        if constexpr (F8) {
+          uint8_t* dst = static_cast<uint8_t*>(is_v ? p.vc : p.kc) + at;
+          *reinterpret_cast<uint2*>(dst + c0) = codes8(a, is_v ? rv : rk);
+          *reinterpret_cast<uint2*>(dst + c1) = codes8(b, is_v ? rv : rk);
+        } else {
+          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(is_v ? p.vc : p.kc) + at;
+          *reinterpret_cast<uint4*>(dst + c0) = is_v ? u[i] : pack8(a);
+          *reinterpret_cast<uint4*>(dst + c1) = is_v ? w[i] : pack8(b);
+        }
+      }
+    }
+    return;
+  }
   {   // ---- queries
     const __nv_bfloat16* src = p.q + token * p.qs;
     __nv_bfloat16* dst = p.q_out + token * p.os;
@@ -1028,10 +1137,16 @@ extern "C" int fm_rope_table(const fm_rope_config* r, uint64_t* freq, float* mag
   return FM_OK;
 }
 
-extern "C" int fm_rope_append(const fm_kv_cache* c, int layer, const fm_kv_batch* b, const fm_rope* rope, const uint16_t* q,
-                              int64_t q_stride, int H, const uint16_t* k, int64_t k_stride, const uint16_t* v,
-                              int64_t v_stride, uint16_t* q_out, int64_t q_out_stride, const int32_t* positions,
-                              void* stream) {
+namespace {
+
+struct HeadNorm {
+  const float *q_gamma, *k_gamma;
+  float eps;
+};
+
+int append(const fm_kv_cache* c, int layer, const fm_kv_batch* b, const fm_rope* rope, const uint16_t* q, int64_t q_stride,
+           int H, const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride, uint16_t* q_out,
+           int64_t q_out_stride, const HeadNorm* norm, const int32_t* positions, void* stream) {
   int st = kv_check(c);
   if (st == FM_OK) st = kv_batch_check(c, b);
   if (st != FM_OK) return st;
@@ -1044,6 +1159,7 @@ extern "C" int fm_rope_append(const fm_kv_cache* c, int layer, const fm_kv_batch
     return record_error(FM_ERR_INVALID_ARG, "unknown rotary layout");
   if (!std::isfinite(rope->magnitude)) return record_error(FM_ERR_INVALID_ARG, "magnitude must be finite");
   if (H < 0 || H > 65535) return record_error(FM_ERR_SHAPE, "H must be 0 to 65535");
+  if (norm && (!(norm->eps >= 0.f) || !std::isfinite(norm->eps))) return record_error(FM_ERR_INVALID_ARG, "eps must not be negative");
   if (b->n == 0 || b->tokens == 0 || b->max_tokens == 0) return FM_OK;
   if (!k || !v || (H > 0 && (!q || !q_out))) return record_error(FM_ERR_INVALID_ARG, "NULL argument");
   const int64_t kv_row = static_cast<int64_t>(c->Hkv) * c->Dh, q_row = static_cast<int64_t>(H) * c->Dh;
@@ -1055,6 +1171,8 @@ extern "C" int fm_rope_append(const fm_kv_cache* c, int layer, const fm_kv_batch
   for (const void* x : {static_cast<const void*>(k), static_cast<const void*>(v), static_cast<const void*>(q),
                         static_cast<const void*>(q_out)})
     if (reinterpret_cast<uintptr_t>(x) % 16) return record_error(FM_ERR_ALIGN, "q, k, v and q_out must be 16-byte aligned");
+  if (norm && (reinterpret_cast<uintptr_t>(norm->q_gamma) % 4 || reinterpret_cast<uintptr_t>(norm->k_gamma) % 4))
+    return record_error(FM_ERR_ALIGN, "q_gamma and k_gamma must be 4-byte aligned");
   int* err = standalone_error_word();
   if (!err) return record_error(FM_ERR_CUDA, "no error word on the current device");
   const fm_kv_batch bounded = bounded_batch(*b);
@@ -1083,11 +1201,35 @@ extern "C" int fm_rope_append(const fm_kv_cache* c, int layer, const fm_kv_batch
   p.err = err;
   // A token has Dh / 16 threads a head group. As many tokens a CTA as leave two groups and three CTAs an SM (9000 tokens,
   // 24 heads of 128: 19.8 us with 16, 23.8 us with 4); a few tokens are spread over all threads of their CTAs.
-  const int units = c->Dh / 16;
+  p.lanes = c->Dh / 16;
+  if (norm) {
+    p.q_gamma = norm->q_gamma, p.k_gamma = norm->k_gamma, p.eps = norm->eps;
+    while (p.lanes & (p.lanes - 1)) ++p.lanes;   // the next power of two
+  }
   p.toks = 1;
-  while (units * p.toks * 2 <= 128 && p.toks < b->max_tokens && b->tokens / (2 * p.toks) >= 152 * 3) p.toks *= 2;
-  p.groups = 256 / (units * p.toks);
+  while (p.lanes * p.toks * 2 <= 128 && p.toks < b->max_tokens && b->tokens / (2 * p.toks) >= 152 * 3) p.toks *= 2;
+  p.groups = 256 / (p.lanes * p.toks);
   const int blocks = (b->max_tokens - 1) / p.toks + 1;
-  return done(launch(f8 ? append_kernel<true> : append_kernel<false>, dim3(static_cast<unsigned>(blocks), b->n), dim3(256),
-                     sizeof(float2) * p.toks * (p.rot / 2), opts(stream), p));
+  void (*kernel)(AppendParams) = norm ? (f8 ? append_kernel<true, true> : append_kernel<false, true>)
+                                      : (f8 ? append_kernel<true, false> : append_kernel<false, false>);
+  return done(launch(kernel, dim3(static_cast<unsigned>(blocks), b->n), dim3(256),
+                     sizeof(float2) * p.toks * (p.rot / 2) + (norm ? sizeof(float) * 2 * c->Dh : 0), opts(stream), p));
+}
+
+}  // namespace
+
+extern "C" int fm_rope_append(const fm_kv_cache* c, int layer, const fm_kv_batch* b, const fm_rope* rope, const uint16_t* q,
+                              int64_t q_stride, int H, const uint16_t* k, int64_t k_stride, const uint16_t* v,
+                              int64_t v_stride, uint16_t* q_out, int64_t q_out_stride, const int32_t* positions,
+                              void* stream) {
+  return append(c, layer, b, rope, q, q_stride, H, k, k_stride, v, v_stride, q_out, q_out_stride, nullptr, positions, stream);
+}
+
+extern "C" int fm_norm_rope_append(const fm_kv_cache* c, int layer, const fm_kv_batch* b, const fm_rope* rope,
+                                   const uint16_t* q, int64_t q_stride, int H, const uint16_t* k, int64_t k_stride,
+                                   const uint16_t* v, int64_t v_stride, uint16_t* q_out, int64_t q_out_stride,
+                                   const float* q_gamma, const float* k_gamma, float eps, const int32_t* positions,
+                                   void* stream) {
+  const HeadNorm norm{q_gamma, k_gamma, eps};
+  return append(c, layer, b, rope, q, q_stride, H, k, k_stride, v, v_stride, q_out, q_out_stride, &norm, positions, stream);
 }

@@ -348,7 +348,7 @@ int fm_session_fork(fm_policy* base, const void* capsule, size_t bytes, int caps
 int fm_device_status(fm_policy* p, void* stream, int* word);
 
 /* Error word of the policy-free building blocks (fm_test_skinny_gemm, fm_gemm_consumer,
- * fm_gemm_consumer_noalloc, fm_rope_append, fm_paged_attention): synchronise `stream`, read and clear the bits their kernels
+ * fm_gemm_consumer_noalloc, fm_rope_append, fm_norm_rope_append, fm_paged_attention): synchronise `stream`, read and clear the bits their kernels
  * set when they abandoned a bounded wait on the current device. Returns FM_OK, or
  * FM_ERR_DEVICE with *word = the bits (1 = TMA/MMA pipeline wait expired, 2 = a paged
  * batch outside its bounds or a token without a page); the outputs of
@@ -720,6 +720,16 @@ typedef struct fm_rope {
 int fm_rope_append(const fm_kv_cache* c, int layer, const fm_kv_batch* b, const fm_rope* rope, const uint16_t* q,
                    int64_t q_stride, int H, const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride,
                    uint16_t* q_out, int64_t q_out_stride, const int32_t* positions, void* stream);
+
+/* fm_rope_append of normalised heads: every head of q and of k is divided by its root mean square before it turns,
+ *   y = x / sqrt(mean(x^2) + eps) * gamma   over the Dh elements of the head, gamma q_gamma or k_gamma
+ * (device fp32 [Dh]; NULL: 1); values pass as they are. Statistics and rotation in fp32 from the unrounded y, one rounding
+ * at the store. Heads of any finite size keep their norm; a head of zeros stays zero (eps 0 too); a head that holds a NaN
+ * or an infinity is NaN throughout, and no other head is. eps >= 0. All else as fm_rope_append. Asynchronous. */
+int fm_norm_rope_append(const fm_kv_cache* c, int layer, const fm_kv_batch* b, const fm_rope* rope, const uint16_t* q,
+                        int64_t q_stride, int H, const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride,
+                        uint16_t* q_out, int64_t q_out_stride, const float* q_gamma, const float* k_gamma, float eps,
+                        const int32_t* positions, void* stream);
 
 /* Bytes of workspace for fm_paged_attention (0 where the keys are not split); depends on the
  * cache's Dh, Hkv and format, the batch's counts and H only. */
