@@ -25,7 +25,7 @@ __all__ = [
     "ABI_VERSION", "STATUS",
     "KvCache", "KvBatch", "Rope", "refresh_prefix_pages", "kv_workspace_size", "kv_reserve", "kv_fork", "kv_release",
     "kv_compact", "rope_table", "rope_append", "norm_rope_append", "paged_attention_workspace_size",
-    "paged_attention", "norm_quant",
+    "paged_attention", "sink_attention", "norm_quant",
     "ROPE_HALF", "ROPE_INTERLEAVED", "ROPE_PLAIN", "ROPE_LINEAR", "ROPE_BASE", "ROPE_BY_PARTS",
     "KV_NO_PAGES", "KV_BAD_ENTRY", "KV_ROW_FULL",
 ]
@@ -56,7 +56,7 @@ EXPORTS = [
     "fm_test_skinny_gemm_tile", "fm_test_pdl_chain", "fm_test_grid_barrier", "fm_test_attn_plan",
     "refresh_prefix_pages", "fm_kv_workspace_size", "fm_kv_reserve", "fm_kv_fork", "fm_kv_release", "fm_kv_compact",
     "fm_rope_table", "fm_rope_append", "fm_norm_rope_append", "fm_paged_attention_workspace_size", "fm_paged_attention",
-    "fm_norm_quant",
+    "fm_sink_attention", "fm_norm_quant",
 ]
 
 
@@ -197,6 +197,7 @@ def load() -> ctypes.CDLL:
         "fm_paged_attention_workspace_size": (i, [vp, vp, i, ctypes.POINTER(sz)]),
         "fm_paged_attention": (i, [vp, i, vp, vp, ctypes.c_int64, i, ctypes.c_float, i, i, vp, ctypes.c_int64, vp, sz,
                                    vp]),
+        "fm_sink_attention": (i, [vp, i, vp, vp, ctypes.c_int64, i, ctypes.c_float, i, i, i, vp, ctypes.c_int64, vp, sz, vp]),
         "fm_norm_quant": (i, [vp, ctypes.c_int64, i, vp, ctypes.c_int64, vp, i, i, ctypes.c_float, vp, ctypes.c_int64,
                               vp, vp, i, vp]),
     }
@@ -818,11 +819,10 @@ def paged_attention_workspace_size(cache: KvCache, batch: KvBatch, H: int) -> in
     return b.value
 
 
-def paged_attention(cache: KvCache, layer: int, batch: KvBatch, q, out, workspace=None, scale: float | None = None,
-                    causal: bool = True, window: int = 0, stream=None):
-    """Attention of q [tokens][H][Dh] (bfloat16) over the batch's sequences into out; scale None: 1 / sqrt(Dh)."""
+def _attention_arguments(w: str, cache, batch, q, out, scale):
+    """(q, its stride, H, scale, out, its stride) as the C side takes them."""
     import torch
-    d, w, bf, T, Dh = cache.dev, "fm_paged_attention", torch.bfloat16, batch.tokens, cache.Dh
+    d, bf, T, Dh = cache.dev, torch.bfloat16, batch.tokens, cache.Dh
     if q.dim() != 3:
         _bad(w, "q must be [tokens][H][Dh]")
     H = q.shape[1]
@@ -830,10 +830,30 @@ def paged_attention(cache: KvCache, layer: int, batch: KvBatch, q, out, workspac
         _bad(w, "the cache and the batch must be on one device")
     qp, qs = _heads(q, w, "q", bf, d, T, H, Dh)
     op, os_ = _heads(out, w, "out", bf, d, T, H, Dh)
-    ws, nb = _workspace(workspace, w, d)
-    st = (_lib or load()).fm_paged_attention(cache.addr, layer, batch.addr, qp, qs, H,
-                                             Dh ** -0.5 if scale is None else scale, 1 if causal else 0, window, op, os_,
-                                             ws, nb, _here(d, stream, w))
+    return qp, qs, H, Dh ** -0.5 if scale is None else scale, op, os_
+
+
+def paged_attention(cache: KvCache, layer: int, batch: KvBatch, q, out, workspace=None, scale: float | None = None,
+                    causal: bool = True, window: int = 0, stream=None):
+    """Attention of q [tokens][H][Dh] (bfloat16) over the batch's sequences into out; scale None: 1 / sqrt(Dh)."""
+    w = "fm_paged_attention"
+    qp, qs, H, scale, op, os_ = _attention_arguments(w, cache, batch, q, out, scale)
+    ws, nb = _workspace(workspace, w, cache.dev)
+    st = (_lib or load()).fm_paged_attention(cache.addr, layer, batch.addr, qp, qs, H, scale, 1 if causal else 0, window, op,
+                                             os_, ws, nb, _here(cache.dev, stream, w))
+    if st:
+        _check(st, w)
+
+
+def sink_attention(cache: KvCache, layer: int, batch: KvBatch, q, out, workspace=None, scale: float | None = None,
+                   causal: bool = True, window: int = 0, sinks: int = 0, stream=None):
+    """paged_attention whose window leaves each sequence's first `sinks` tokens visible (the workspace is
+    paged_attention's)."""
+    w = "fm_sink_attention"
+    qp, qs, H, scale, op, os_ = _attention_arguments(w, cache, batch, q, out, scale)
+    ws, nb = _workspace(workspace, w, cache.dev)
+    st = (_lib or load()).fm_sink_attention(cache.addr, layer, batch.addr, qp, qs, H, scale, 1 if causal else 0, window,
+                                            sinks, op, os_, ws, nb, _here(cache.dev, stream, w))
     if st:
         _check(st, w)
 

@@ -1,4 +1,4 @@
-// Shared by the two attention kernels over a paged cache (paged_attn.cu: many rows, paged_decode.cu: up to 16).
+// Shared by the two attention kernels over a paged cache (paged_tile.cuh: many rows, paged_decode.cuh: up to 16).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -11,6 +11,9 @@ namespace fm {
 
 constexpr float kGrow = 8.0f;   // the running maximum moves when it grows by more than this power of two
 
+// What a kernel's keys are: all that the mask leaves (one stretch of the axis), or a window and the first tokens.
+enum class Keys { kAll, kSinks };
+
 struct AttnParams {
   const __nv_bfloat16* q;
   __nv_bfloat16* out;
@@ -22,6 +25,7 @@ struct AttnParams {
   int n, tokens, max_tokens, seqs, table_stride, pages, page, page_shift;
   int H, Hkv, G;
   int causal, window;
+  int sinks;                      // first tokens that a window does not hide (Keys::kSinks)
   float scale_log2;               // scale * log2(e)
   const float* k_scale;
   const float* v_scale;
@@ -33,12 +37,22 @@ struct AttnParams {
   int* err;
 };
 
+// Both kernels are instantiated once for each Keys, in a source of their own; configure sets their shared-memory limits on
+// the current device.
+template <Keys K>
+cudaError_t tile_launch(const AttnParams& p, int Dh, bool f8, const CUtensorMap& tk, const CUtensorMap& tv, dim3 grid,
+                        size_t smem, const LaunchOpts& o);
+template <Keys K>
+cudaError_t tile_configure();
+
 // The kernel for up to 16 stacked rows (max_tokens * G): p.splits CTAs an entry and KV head, joined inside a cluster
 // where p.part_o is null, else through the workspace.
 constexpr int kDecodeRows = 16;
 constexpr int kDecodeKeys = 64;   // keys of a tile
+template <Keys K>
 cudaError_t decode_launch(const AttnParams& p, int Dh, bool f8, const CUtensorMap& tk, const CUtensorMap& tv,
                           const LaunchOpts& o);
+template <Keys K>
 cudaError_t decode_configure();
 int decode_resident(int Dh, bool f8, int rows);   // CTAs of it on an SM at once
 
@@ -72,6 +86,33 @@ __device__ __forceinline__ int last_key(const AttnParams& p, int pos, int len) {
 __device__ __forceinline__ int first_key(const AttnParams& p, int pos) {
   return p.window > 0 && pos >= p.window ? pos - p.window + 1 : 0;
 }
+
+// The key tiles of a CTA in the order in which it takes them. With sinks these are the tiles of the first tokens up to the
+// window's first tile, then the window's: place x of that order is tile x, or x + gap behind the first ones.
+template <Keys K>
+struct Places {
+  int lead = 0, gap = 0;   // tiles of the first tokens alone, and those left out behind them
+  // first: the window's first tile; keys: of a tile
+  __device__ __forceinline__ Places(const AttnParams& p, int first, int keys) {
+    if constexpr (K == Keys::kSinks) {
+      lead = min((p.sinks - 1) / keys + 1, first);
+      gap = first - lead;
+    }
+  }
+  __device__ __forceinline__ int tile(int place) const {
+    if constexpr (K == Keys::kSinks) return place < lead ? place : place + gap;
+    return place;
+  }
+  // the place of a tile of the window (or of none: behind the last one)
+  __device__ __forceinline__ int place(int tile) const {
+    if constexpr (K == Keys::kSinks) return tile - gap;
+    return tile;
+  }
+  __device__ __forceinline__ int begin(int first) const {
+    if constexpr (K == Keys::kSinks) return 0;
+    return first;
+  }
+};
 
 // True once the phase with the given parity has completed; false after 2^22 polls (the hardware suspends the thread in
 // each for a while): far beyond any legitimate wait. No clock is read between the polls, and no suspension time is

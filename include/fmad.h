@@ -348,7 +348,8 @@ int fm_session_fork(fm_policy* base, const void* capsule, size_t bytes, int caps
 int fm_device_status(fm_policy* p, void* stream, int* word);
 
 /* Error word of the policy-free building blocks (fm_test_skinny_gemm, fm_gemm_consumer,
- * fm_gemm_consumer_noalloc, fm_rope_append, fm_norm_rope_append, fm_paged_attention): synchronise `stream`, read and clear the bits their kernels
+ * fm_gemm_consumer_noalloc, fm_rope_append, fm_norm_rope_append, fm_paged_attention,
+ * fm_sink_attention): synchronise `stream`, read and clear the bits their kernels
  * set when they abandoned a bounded wait on the current device. Returns FM_OK, or
  * FM_ERR_DEVICE with *word = the bits (1 = TMA/MMA pipeline wait expired, 2 = a paged
  * batch outside its bounds or a token without a page); the outputs of
@@ -750,6 +751,15 @@ int fm_paged_attention_workspace_size(const fm_kv_cache* c, const fm_kv_batch* b
 int fm_paged_attention(const fm_kv_cache* c, int layer, const fm_kv_batch* b, const uint16_t* q, int64_t q_stride, int H,
                        float scale, int causal, int window, uint16_t* out, int64_t out_stride, void* workspace,
                        size_t workspace_bytes, void* stream);
+
+/* fm_paged_attention with a window that leaves the sequence's first `sinks` tokens visible: over keys j < lens,
+ * j <= position(t) if causal != 0, and j > position(t) - window or j < sinks. Tiles of keys between the two stretches are not
+ * read; a table may name no page there (-1) where a whole page and its neighbours within 128 tokens are hidden from
+ * every token. window 0 (none) and sinks 0 are fm_paged_attention bit for bit. All else as there, the workspace
+ * (fm_paged_attention_workspace_size) too. Asynchronous. */
+int fm_sink_attention(const fm_kv_cache* c, int layer, const fm_kv_batch* b, const uint16_t* q, int64_t q_stride, int H,
+                      float scale, int causal, int window, int sinks, uint16_t* out, int64_t out_stride, void* workspace,
+                      size_t workspace_bytes, void* stream);
 
 /* Residual addition + RMS norm + E4M3 with scales taken from the data:
  *   s = x + r (r NULL: x);  x_out = s (unless NULL);
