@@ -25,7 +25,7 @@ __all__ = [
     "ABI_VERSION", "STATUS",
     "KvCache", "KvBatch", "Rope", "refresh_prefix_pages", "kv_workspace_size", "kv_reserve", "kv_fork", "kv_release",
     "kv_compact", "rope_table", "rope_append", "norm_rope_append", "paged_attention_workspace_size",
-    "paged_attention", "sink_attention", "norm_quant",
+    "paged_attention", "sink_attention", "KvGroups", "shared_attention_workspace_size", "shared_attention", "norm_quant",
     "ROPE_HALF", "ROPE_INTERLEAVED", "ROPE_PLAIN", "ROPE_LINEAR", "ROPE_BASE", "ROPE_BY_PARTS",
     "KV_NO_PAGES", "KV_BAD_ENTRY", "KV_ROW_FULL",
 ]
@@ -56,7 +56,7 @@ EXPORTS = [
     "fm_test_skinny_gemm_tile", "fm_test_pdl_chain", "fm_test_grid_barrier", "fm_test_attn_plan",
     "refresh_prefix_pages", "fm_kv_workspace_size", "fm_kv_reserve", "fm_kv_fork", "fm_kv_release", "fm_kv_compact",
     "fm_rope_table", "fm_rope_append", "fm_norm_rope_append", "fm_paged_attention_workspace_size", "fm_paged_attention",
-    "fm_sink_attention", "fm_norm_quant",
+    "fm_sink_attention", "fm_shared_attention_workspace_size", "fm_shared_attention", "fm_norm_quant",
 ]
 
 
@@ -107,6 +107,11 @@ class FmKvCache(ctypes.Structure):
 class FmKvBatch(ctypes.Structure):
     _fields_ = [("start", ctypes.c_void_p), ("seq", ctypes.c_void_p), ("n", ctypes.c_int), ("tokens", ctypes.c_int),
                 ("max_tokens", ctypes.c_int), ("max_len", ctypes.c_int)]
+
+
+class FmKvGroups(ctypes.Structure):
+    _fields_ = [("first", ctypes.c_void_p), ("shared", ctypes.c_void_p), ("n", ctypes.c_int), ("max_entries", ctypes.c_int),
+                ("max_shared", ctypes.c_int)]
 
 
 class FmRopeConfig(ctypes.Structure):
@@ -198,6 +203,8 @@ def load() -> ctypes.CDLL:
         "fm_paged_attention": (i, [vp, i, vp, vp, ctypes.c_int64, i, ctypes.c_float, i, i, vp, ctypes.c_int64, vp, sz,
                                    vp]),
         "fm_sink_attention": (i, [vp, i, vp, vp, ctypes.c_int64, i, ctypes.c_float, i, i, i, vp, ctypes.c_int64, vp, sz, vp]),
+        "fm_shared_attention_workspace_size": (i, [vp, vp, vp, i, ctypes.POINTER(sz)]),
+        "fm_shared_attention": (i, [vp, i, vp, vp, vp, ctypes.c_int64, i, ctypes.c_float, i, vp, ctypes.c_int64, vp, sz, vp]),
         "fm_norm_quant": (i, [vp, ctypes.c_int64, i, vp, ctypes.c_int64, vp, i, i, ctypes.c_float, vp, ctypes.c_int64,
                               vp, vp, i, vp]),
     }
@@ -685,6 +692,24 @@ class KvBatch:
         self.start, self.seq, self.tokens = start, seq, int(tokens)
 
 
+class KvGroups:
+    """Entries of a batch that begin with the same tokens (fm_kv_groups): group i is the entries first[i] .. first[i + 1] - 1
+    (int32 [n + 1]) and shares its first shared[i] tokens (int32 [n]); bounds on both."""
+
+    def __init__(self, first, shared, max_entries: int, max_shared: int):
+        n = first.numel() - 1
+        if n < 0:
+            _bad("KvGroups", "first must have at least one element")
+        self.device, self.dev = first.device, first.get_device()
+        s = FmKvGroups()
+        s.first = _ints(first, "KvGroups", "first", self.dev, 1)
+        s.shared = _ints(shared, "KvGroups", "shared", self.dev, n)
+        s.n, s.max_entries, s.max_shared = n, int(max_entries), int(max_shared)
+        self.struct = s
+        self.addr = ctypes.addressof(s)
+        self.first, self.shared = first, shared
+
+
 def rope_table(rotary_dim: int, theta: float = 10000.0, scaling: int = ROPE_PLAIN, factor: float = 1.0,
                original_len: float = 0.0, beta_fast: float = 32.0, beta_slow: float = 1.0):
     """(frequencies in turns per position * 2^64 as a host uint64 array [rotary_dim / 2], factor on cos and sin)."""
@@ -854,6 +879,27 @@ def sink_attention(cache: KvCache, layer: int, batch: KvBatch, q, out, workspace
     ws, nb = _workspace(workspace, w, cache.dev)
     st = (_lib or load()).fm_sink_attention(cache.addr, layer, batch.addr, qp, qs, H, scale, 1 if causal else 0, window,
                                             sinks, op, os_, ws, nb, _here(cache.dev, stream, w))
+    if st:
+        _check(st, w)
+
+
+def shared_attention_workspace_size(cache: KvCache, batch: KvBatch, groups: KvGroups, H: int) -> int:
+    b = ctypes.c_size_t()
+    _check(load().fm_shared_attention_workspace_size(cache.addr, batch.addr, groups.addr, H, ctypes.byref(b)),
+           "fm_shared_attention_workspace_size")
+    return b.value
+
+
+def shared_attention(cache: KvCache, layer: int, batch: KvBatch, groups: KvGroups, q, out, workspace=None,
+                     scale: float | None = None, causal: bool = True, stream=None):
+    """paged_attention of a batch in groups of forks: the tokens that a group shares are read once for all its entries."""
+    w = "fm_shared_attention"
+    if groups.dev != cache.dev:
+        _bad(w, "the cache and the groups must be on one device")
+    qp, qs, H, scale, op, os_ = _attention_arguments(w, cache, batch, q, out, scale)
+    ws, nb = _workspace(workspace, w, cache.dev)
+    st = (_lib or load()).fm_shared_attention(cache.addr, layer, batch.addr, groups.addr, qp, qs, H, scale, 1 if causal else 0,
+                                              op, os_, ws, nb, _here(cache.dev, stream, w))
     if st:
         _check(st, w)
 

@@ -11,8 +11,9 @@ namespace fm {
 
 constexpr float kGrow = 8.0f;   // the running maximum moves when it grows by more than this power of two
 
-// What a kernel's keys are: all that the mask leaves (one stretch of the axis), or a window and the first tokens.
-enum class Keys { kAll, kSinks };
+// What a kernel's keys are: all that the mask leaves (one stretch of the axis), a window and the first tokens, or of a batch
+// in groups the prefix that a group's entries share, for all its tokens at once, and what an entry has behind it.
+enum class Keys { kAll, kSinks, kPrefix, kOwn };
 
 struct AttnParams {
   const __nv_bfloat16* q;
@@ -32,6 +33,10 @@ struct AttnParams {
   int alt, splits, split_tiles;
   int row_blocks, rows_first;     // of paged_attn.cu's grid
   int ring, raw_ring;
+  const int32_t* g_first;         // groups: [g_n + 1] first entries
+  const int32_t* g_shared;        // [g_n] tokens that a group's entries share
+  int g_n, g_tokens;              // g_tokens: packed rows of a group that Keys::kPrefix takes
+  int prefix_splits;              // shares of the prefix that Keys::kOwn joins
   float* part_o;                  // [splits][tokens * H][Dh]
   float2* part_ml;                // [splits][tokens * H] (log2 maximum, sum)
   int* err;
@@ -49,6 +54,7 @@ cudaError_t tile_configure();
 // where p.part_o is null, else through the workspace.
 constexpr int kDecodeRows = 16;
 constexpr int kDecodeKeys = 64;   // keys of a tile
+constexpr int kMostPrefixSplits = 64;
 template <Keys K>
 cudaError_t decode_launch(const AttnParams& p, int Dh, bool f8, const CUtensorMap& tk, const CUtensorMap& tv,
                           const LaunchOpts& o);
@@ -77,6 +83,45 @@ __device__ __forceinline__ Entry entry_of(const AttnParams& p, int entry, bool r
   }
   if (report && (bad || e.nq > p.max_tokens)) atomicOr(p.err, kErrBadBatch);
   return e;
+}
+
+// Group g as an entry: its packed rows from the first on, the pages of its first entry, the shared tokens as its length. One
+// whose shared tokens are not all there has no keys.
+__device__ __forceinline__ Entry group_of(const AttnParams& p, int g, bool report) {
+  Entry e = {0, 0, 0, 0};
+  const int f0 = p.g_first[g], f1 = p.g_first[g + 1], shared = p.g_shared[g];
+  bool bad = f0 < 0 || f1 < f0 || f1 > p.n || shared < 0;
+  if (!bad && f1 > f0) {
+    e.begin = max(p.start[f0], 0);
+    e.nq = min(max(min(p.start[f1], p.tokens), 0) - e.begin, p.g_tokens);
+    e.sid = p.seq ? p.seq[f0] : f0;
+    bad = e.sid < 0 || e.sid >= p.seqs || shared > p.lens[e.sid] || shared > p.table_stride * static_cast<int64_t>(p.page);
+    if (!bad) e.len = shared;
+    if (e.nq < 0) e.nq = 0;
+  }
+  if (report && bad) atomicOr(p.err, kErrBadBatch);
+  return e;
+}
+
+// The tokens of an entry's prefix that its group's part covers, 0 where the entry has to see to all of its keys: without a
+// (sound) group, with a token that does not see the whole prefix, or with rows behind those that the group's part takes.
+// For whole warps.
+__device__ __forceinline__ int prefix_of(const AttnParams& p, int entry, const Entry& e) {
+  int lo = 0, hi = p.g_n;   // the last group that begins at or before the entry, 32 probes at a time
+  for (int step = 32; step > 1;) {
+    step = (hi - lo + 31) / 32;
+    const int at = lo + static_cast<int>(threadIdx.x & 31) * step;
+    const int before = __popc(__ballot_sync(0xffffffffu, at < hi && p.g_first[at] <= entry));
+    if (before == 0) return 0;
+    lo += (before - 1) * step;
+    hi = min(hi, lo + step);
+  }
+  const int f0 = p.g_first[lo], f1 = p.g_first[lo + 1], shared = p.g_shared[lo];
+  if (f0 < 0 || entry < f0 || entry >= f1 || f1 > p.n) return 0;
+  const Entry group = group_of(p, lo, false);
+  const int past = e.len - e.nq, end = e.begin + min(e.nq, p.max_tokens);
+  const bool seen = past >= 0 && shared <= (p.causal ? past + 1 : e.len);
+  return seen && group.len > 0 && e.begin >= group.begin && end <= group.begin + group.nq ? shared : 0;
 }
 
 // The keys [first_key, last_key) of a token at position pos.

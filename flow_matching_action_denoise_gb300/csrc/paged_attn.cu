@@ -124,6 +124,20 @@ struct Plan {
   size_t smem, workspace;
 };
 
+// The tile kernel's buffers for keys and values, and its shared memory.
+void rings_of(const fm_kv_cache& c, Plan& pl) {
+  const size_t tile = static_cast<size_t>(kTileRows) * c.Dh * 2;
+  const size_t q = tile * (pl.alt ? 1 : 2);
+  const size_t room = kSmemLimit - kCtlBytes - q;
+  if (c.fmt == FM_FMT_FP8) {
+    pl.ring = 4;
+    pl.raw_ring = static_cast<int>(std::min<size_t>(kMaxRing, (room - pl.ring * tile) / (tile / 2)));
+  } else {
+    pl.ring = static_cast<int>(std::min<size_t>(kMaxRing, room / tile));
+  }
+  pl.smem = 1024 + q + pl.ring * tile + pl.raw_ring * (tile / 2) + kCtlBytes;
+}
+
 int sm_count() {
   static std::atomic<int> cached[64];
   int dev = 0;
@@ -212,16 +226,7 @@ Plan plan_of(const fm_kv_cache& c, const fm_kv_batch& b, int H, int window, int 
     // outermost, 37.2 us; 4 x 2048 tokens of 16 on 2: 80.1 and 72.5 us). Else heads and entries are outermost: the entry's
     // length, which the host does not know, decides more. Splits are of equal length but the last.
     pl.rows_first = pl.splits == 1 && 2 * static_cast<int64_t>(b.max_tokens) >= b.max_len && pl.row_blocks <= 65535;
-    const size_t tile = static_cast<size_t>(kTileRows) * c.Dh * 2;
-    const size_t q = tile * (pl.alt ? 1 : 2);
-    const size_t room = kSmemLimit - kCtlBytes - q;
-    if (c.fmt == FM_FMT_FP8) {
-      pl.ring = 4;
-      pl.raw_ring = static_cast<int>(std::min<size_t>(kMaxRing, (room - pl.ring * tile) / (tile / 2)));
-    } else {
-      pl.ring = static_cast<int>(std::min<size_t>(kMaxRing, room / tile));
-    }
-    pl.smem = 1024 + q + pl.ring * tile + pl.raw_ring * (tile / 2) + kCtlBytes;
+    rings_of(c, pl);
   }
   if (pl.splits > (pl.decode ? 8 : 1))
     pl.workspace = static_cast<size_t>(pl.splits) * b.tokens * H * (c.Dh * sizeof(float) + sizeof(float2));
@@ -237,8 +242,9 @@ cudaError_t configure() {
   if (e != cudaSuccess) return e;
   const uint64_t bit = 1ull << (dev & 63);
   if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  // the groups' two kernels together
   e = tile_configure<K>();
-  if (e == cudaSuccess) e = decode_configure<K>();
+  if (e == cudaSuccess) e = decode_configure<K == Keys::kPrefix ? Keys::kOwn : K>();
   if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_acq_rel);
   return e;
 }
@@ -254,68 +260,92 @@ int check(const fm_kv_cache* c, const fm_kv_batch* b, int H) {
   return FM_OK;
 }
 
-template <Keys K>
-int attend(const fm_kv_cache* c, int layer, const fm_kv_batch* b, const uint16_t* q, int64_t q_stride, int H, float scale,
-           int causal, int window, int sinks, uint16_t* out, int64_t out_stride, void* workspace, size_t workspace_bytes,
-           void* stream) {
-  const int st = check(c, b, H);
+// What an attention call is given, checked and bounded; FM_OK with b = nullptr where there is nothing to do.
+struct Call {
+  const fm_kv_cache* c;
+  int layer;
+  const fm_kv_batch* b;
+  const uint16_t* q;
+  int64_t q_stride;
+  int H;
+  float scale;
+  int causal;
+  uint16_t* out;
+  int64_t out_stride;
+  void* workspace;
+  size_t workspace_bytes;
+  void* stream;
+};
+
+int check_call(const Call& a) {
+  const int st = check(a.c, a.b, a.H);
   if (st != FM_OK) return st;
-  if (layer < 0 || layer >= c->layers) return record_error(FM_ERR_INVALID_ARG, "layer out of range");
-  if (!(scale > 0.f) || !std::isfinite(scale)) return record_error(FM_ERR_INVALID_ARG, "scale must be positive and finite");
-  if (window < 0) return record_error(FM_ERR_INVALID_ARG, "window must be 0 (none) or positive");
-  if (b->n == 0 || b->tokens == 0 || b->max_tokens == 0) return FM_OK;
-  if (!q || !out) return record_error(FM_ERR_INVALID_ARG, "NULL argument");
-  const int64_t row = static_cast<int64_t>(H) * c->Dh;
-  if (q_stride < row || out_stride < row || q_stride % 8 || out_stride % 8)
+  if (a.layer < 0 || a.layer >= a.c->layers) return record_error(FM_ERR_INVALID_ARG, "layer out of range");
+  if (!(a.scale > 0.f) || !std::isfinite(a.scale)) return record_error(FM_ERR_INVALID_ARG, "scale must be positive and finite");
+  return FM_OK;
+}
+bool nothing_to_do(const fm_kv_batch& b) { return b.n == 0 || b.tokens == 0 || b.max_tokens == 0; }
+int check_tensors(const Call& a) {
+  if (!a.q || !a.out) return record_error(FM_ERR_INVALID_ARG, "NULL argument");
+  const int64_t row = static_cast<int64_t>(a.H) * a.c->Dh;
+  if (a.q_stride < row || a.out_stride < row || a.q_stride % 8 || a.out_stride % 8)
     return record_error(FM_ERR_SHAPE, "token strides must be multiples of 8 elements and hold H * Dh");
-  if (reinterpret_cast<uintptr_t>(q) % 16 || reinterpret_cast<uintptr_t>(out) % 16)
+  if (reinterpret_cast<uintptr_t>(a.q) % 16 || reinterpret_cast<uintptr_t>(a.out) % 16)
     return record_error(FM_ERR_ALIGN, "q and out must be 16-byte aligned");
-  const fm_kv_batch bounded = bounded_batch(*b);
-  b = &bounded;
-  const Plan pl = plan_of(*c, *b, H, window, sinks);
-  const size_t need = pl.workspace;
-  if (need) {
-    if (!workspace) return record_error(FM_ERR_INVALID_ARG, "workspace is NULL");
-    if (reinterpret_cast<uintptr_t>(workspace) % 16) return record_error(FM_ERR_ALIGN, "workspace not 16-byte aligned");
-    if (workspace_bytes < need)
-      return record_error(FM_ERR_WORKSPACE, "workspace smaller than fm_paged_attention_workspace_size()");
-  }
-  const bool f8 = c->fmt == FM_FMT_FP8;
-  const int64_t off = layer * c->layer_stride * (f8 ? 1 : 2);
-  CUtensorMap tk, tv;
-  if (!kv_tmap(&tk, *c, static_cast<const uint8_t*>(c->k) + off, pl.decode) ||
-      !kv_tmap(&tv, *c, static_cast<const uint8_t*>(c->v) + off, pl.decode))
-    return record_error(FM_ERR_CUDA, "cuTensorMapEncodeTiled (cache pages) failed");
-  int* err = standalone_error_word();
-  if (!err) return record_error(FM_ERR_CUDA, "no error word on the current device");
-  cudaError_t e = configure<K>();
-  if (e != cudaSuccess) return record_error(FM_ERR_CUDA, cudaGetErrorString(e));
-  AttnParams p = {};
-  p.q = reinterpret_cast<const __nv_bfloat16*>(q);
-  p.out = reinterpret_cast<__nv_bfloat16*>(out);
-  p.q_stride = q_stride;
-  p.out_stride = out_stride;
-  p.start = b->start;
-  p.seq = b->seq;
-  p.lens = c->lens;
-  p.table = c->table;
-  p.n = b->n;
-  p.tokens = b->tokens;
-  p.max_tokens = b->max_tokens;
-  p.seqs = c->seqs;
-  p.table_stride = c->table_stride;
-  p.pages = c->pages;
-  p.page = c->page_tokens;
-  while ((1 << p.page_shift) < c->page_tokens) ++p.page_shift;
-  p.H = H;
-  p.Hkv = c->Hkv;
-  p.G = H / c->Hkv;
-  p.causal = causal != 0;
-  p.window = window;
-  p.sinks = sinks;
-  p.scale_log2 = scale * 1.4426950408889634f;
-  p.k_scale = f8 ? c->k_scale + layer : nullptr;
-  p.v_scale = f8 ? c->v_scale + layer : nullptr;
+  return FM_OK;
+}
+int check_workspace(const Call& a, size_t need, const char* too_small) {
+  if (!need) return FM_OK;
+  if (!a.workspace) return record_error(FM_ERR_INVALID_ARG, "workspace is NULL");
+  if (reinterpret_cast<uintptr_t>(a.workspace) % 16) return record_error(FM_ERR_ALIGN, "workspace not 16-byte aligned");
+  if (a.workspace_bytes < need) return record_error(FM_ERR_WORKSPACE, too_small);
+  return FM_OK;
+}
+
+// The kernels' parameters but for the plan's; b: the batch, bounded. false: no error word.
+bool params_of(const Call& a, const fm_kv_batch& b, AttnParams& p) {
+  const fm_kv_cache& c = *a.c;
+  const bool f8 = c.fmt == FM_FMT_FP8;
+  p = {};
+  p.q = reinterpret_cast<const __nv_bfloat16*>(a.q);
+  p.out = reinterpret_cast<__nv_bfloat16*>(a.out);
+  p.q_stride = a.q_stride;
+  p.out_stride = a.out_stride;
+  p.start = b.start;
+  p.seq = b.seq;
+  p.lens = c.lens;
+  p.table = c.table;
+  p.n = b.n;
+  p.tokens = b.tokens;
+  p.max_tokens = b.max_tokens;
+  p.seqs = c.seqs;
+  p.table_stride = c.table_stride;
+  p.pages = c.pages;
+  p.page = c.page_tokens;
+  while ((1 << p.page_shift) < c.page_tokens) ++p.page_shift;
+  p.H = a.H;
+  p.Hkv = c.Hkv;
+  p.G = a.H / c.Hkv;
+  p.causal = a.causal != 0;
+  p.scale_log2 = a.scale * 1.4426950408889634f;
+  p.k_scale = f8 ? c.k_scale + a.layer : nullptr;
+  p.v_scale = f8 ? c.v_scale + a.layer : nullptr;
+  p.err = standalone_error_word();
+  return p.err != nullptr;
+}
+
+void shares_in(const Call& a, int places, int tokens, AttnParams& p) {
+  p.part_o = static_cast<float*>(a.workspace);
+  p.part_ml = reinterpret_cast<float2*>(p.part_o + static_cast<size_t>(places) * tokens * a.H * a.c->Dh);
+}
+
+bool maps_of(const Call& a, bool decode, CUtensorMap* tk, CUtensorMap* tv) {
+  const int64_t off = a.layer * a.c->layer_stride * (a.c->fmt == FM_FMT_FP8 ? 1 : 2);
+  return kv_tmap(tk, *a.c, static_cast<const uint8_t*>(a.c->k) + off, decode) &&
+         kv_tmap(tv, *a.c, static_cast<const uint8_t*>(a.c->v) + off, decode);
+}
+
+void use_plan(const Plan& pl, AttnParams& p) {
   p.alt = pl.alt;
   p.row_blocks = static_cast<int>(pl.row_blocks);
   p.rows_first = pl.rows_first;
@@ -323,28 +353,187 @@ int attend(const fm_kv_cache* c, int layer, const fm_kv_batch* b, const uint16_t
   p.split_tiles = pl.split_tiles;
   p.ring = pl.ring;
   p.raw_ring = pl.raw_ring;
-  if (need) {
-    p.part_o = static_cast<float*>(workspace);
-    p.part_ml = reinterpret_cast<float2*>(p.part_o + static_cast<size_t>(pl.splits) * b->tokens * H * c->Dh);
-  }
-  p.err = err;
+}
+
+template <Keys K>
+cudaError_t launch_tiles(const Call& a, const Plan& pl, int n, const AttnParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
+                         const LaunchOpts& o) {
+  const unsigned blocks = static_cast<unsigned>(pl.row_blocks), entries = static_cast<unsigned>(n * pl.splits);
+  const dim3 grid = pl.rows_first ? dim3(a.c->Hkv, entries, blocks) : dim3(blocks, a.c->Hkv, entries);
+  return tile_launch<K>(p, a.c->Dh, a.c->fmt == FM_FMT_FP8, tk, tv, grid, pl.smem, o);
+}
+
+cudaError_t launch_join(const Call& a, const AttnParams& p, const LaunchOpts& o) {
+  // a warp takes up to four splits where there are few rows (256 splits of 8 rows took 45 us with a warp a row)
+  int warps = 1;
+  while (warps < 8 && p.splits > 4 * warps) warps *= 2;
+  const int64_t blocks = (static_cast<int64_t>(p.max_tokens) * a.H * warps + 7) / 8;
+  auto join = a.c->Dh == 128 ? combine_kernel<128> : combine_kernel<64>;
+  return launch(join, dim3(static_cast<unsigned>(blocks), p.n), dim3(256), 0, o, p, warps);
+}
+
+LaunchOpts opts_of(const Call& a) {
   LaunchOpts o;
-  o.stream = static_cast<cudaStream_t>(stream);
+  o.stream = static_cast<cudaStream_t>(a.stream);
   o.pdl = true;
+  return o;
+}
+
+template <Keys K>
+int attend(const Call& a, int window, int sinks) {
+  int st = check_call(a);
+  if (st != FM_OK) return st;
+  if (window < 0) return record_error(FM_ERR_INVALID_ARG, "window must be 0 (none) or positive");
+  if (nothing_to_do(*a.b)) return FM_OK;
+  st = check_tensors(a);
+  if (st != FM_OK) return st;
+  const fm_kv_batch b = bounded_batch(*a.b);
+  const Plan pl = plan_of(*a.c, b, a.H, window, sinks);
+  st = check_workspace(a, pl.workspace, "workspace smaller than fm_paged_attention_workspace_size()");
+  if (st != FM_OK) return st;
+  CUtensorMap tk, tv;
+  if (!maps_of(a, pl.decode, &tk, &tv)) return record_error(FM_ERR_CUDA, "cuTensorMapEncodeTiled (cache pages) failed");
+  AttnParams p;
+  if (!params_of(a, b, p)) return record_error(FM_ERR_CUDA, "no error word on the current device");
+  cudaError_t e = configure<K>();
+  if (e != cudaSuccess) return record_error(FM_ERR_CUDA, cudaGetErrorString(e));
+  p.window = window;
+  p.sinks = sinks;
+  use_plan(pl, p);
+  if (pl.workspace) shares_in(a, pl.splits, b.tokens, p);
+  const LaunchOpts o = opts_of(a);
+  e = pl.decode ? decode_launch<K>(p, a.c->Dh, a.c->fmt == FM_FMT_FP8, tk, tv, o) : launch_tiles<K>(a, pl, b.n, p, tk, tv, o);
+  if (e == cudaSuccess && pl.workspace) e = launch_join(a, p, o);
+  return e == cudaSuccess ? FM_OK : record_error(FM_ERR_CUDA, cudaGetErrorString(e));
+}
+
+// ---- groups of forks
+
+int check_groups(const fm_kv_groups* g) {
+  if (!g) return record_error(FM_ERR_INVALID_ARG, "NULL groups");
+  if (g->n < 0 || g->max_entries < 0 || g->max_shared < 0)
+    return record_error(FM_ERR_SHAPE, "the groups' counts must not be negative");
+  if (g->n > 65535) return record_error(FM_ERR_SHAPE, "up to 65535 groups");
+  if (g->n > 0 && (!g->first || !g->shared)) return record_error(FM_ERR_INVALID_ARG, "the groups have no first or no shared");
+  return FM_OK;
+}
+
+// How a batch in groups is computed: the prefixes by the tile kernel and what is behind them by the kernel for few rows, or
+// all keys of an entry together as without groups.
+struct SharedPlan {
+  bool split;        // prefixes by themselves
+  Plan prefix;
+  int own_splits;
+  int tokens;        // of a group
+  size_t workspace;
+};
+
+// A tile of 64 keys in the kernel for few rows, in units of 0.01 us: bf16 waits for its bytes however many CTAs share an SM.
+int64_t decode_each(bool f8, int resident, int64_t ctas, int sms) {
+  return f8 ? 30 + 20 * std::min<int64_t>(resident, (ctas + sms - 1) / sms) : 55;
+}
+
+// Time of a batch without groups, in units of 0.1 us as splits_of takes it, from the same measurements.
+int64_t cost_alone(const fm_kv_cache& c, const fm_kv_batch& b, int H, const Plan& pl) {
+  const int sms = sm_count();
+  const bool f8 = c.fmt == FM_FMT_FP8;
+  const int64_t rows = static_cast<int64_t>(b.max_tokens) * (H / c.Hkv), len = std::max(1, b.max_len);
   if (pl.decode) {
-    e = decode_launch<K>(p, c->Dh, f8, tk, tv, o);
-  } else {
-    const unsigned blocks = static_cast<unsigned>(pl.row_blocks), entries = static_cast<unsigned>(b->n * pl.splits);
-    const dim3 grid = pl.rows_first ? dim3(c->Hkv, entries, blocks) : dim3(blocks, c->Hkv, entries);
-    e = tile_launch<K>(p, c->Dh, f8, tk, tv, grid, pl.smem, o);
+    const int64_t ctas = static_cast<int64_t>(c.Hkv) * b.n * pl.splits, tiles = (len + kDecodeKeys - 1) / kDecodeKeys;
+    const int resident = decode_resident(c.Dh, f8, static_cast<int>(rows));
+    const int64_t waves = (ctas + static_cast<int64_t>(sms) * resident - 1) / (static_cast<int64_t>(sms) * resident);
+    return (rows <= 8 ? 55 : 65) + waves * ((tiles + pl.splits - 1) / pl.splits) * decode_each(f8, resident, ctas, sms) / 10 + (pl.splits > 8 ? 25 : 0);
   }
-  if (e == cudaSuccess && need) {
-    // a warp takes up to four splits where there are few rows (256 splits of 8 rows took 45 us with a warp a row)
-    int warps = 1;
-    while (warps < 8 && pl.splits > 4 * warps) warps *= 2;
-    const int64_t blocks = (static_cast<int64_t>(b->max_tokens) * H * warps + 7) / 8;
-    auto join = c->Dh == 128 ? combine_kernel<128> : combine_kernel<64>;
-    e = launch(join, dim3(static_cast<unsigned>(blocks), b->n), dim3(256), 0, o, p, warps);
+  const int64_t fixed = f8 ? 85 : 70, each = pl.alt ? (f8 ? 15 : 8) : (f8 ? 18 : 14);
+  const int64_t ctas = pl.row_blocks * c.Hkv * b.n * pl.splits, shares = static_cast<int64_t>(pl.splits) * b.tokens * H * c.Dh * 8;
+  return (ctas + sms - 1) / sms * (fixed + pl.split_tiles * each) + (pl.splits > 1 ? 25 + shares / 400000 : 0);
+}
+
+// Two kernels in a row cost 11 to 13 us with nothing to do, one 6 to 7, so sharing pays where entries x shared tokens are
+// many: 96 single tokens of 16 heads on 2 KV heads (Dh 128, bf16) behind 2000 common keys take 14.8 us here and 24.3 us
+// alone, 32 behind 8000 17.4 and 22.9 us; but 96 behind 500 13.1 and 11.3 us, 8 behind 8000 15.2 and 11.5 us. Chunks that
+// fill half of a 256-row block themselves gain nothing (16 x 50 tokens behind 4100: 43 us in two kernels, 41.6 alone).
+SharedPlan shared_plan(const fm_kv_cache& c, const fm_kv_batch& b, const fm_kv_groups& g, int H) {
+  SharedPlan sp = {};
+  const int G = H / c.Hkv, sms = sm_count();
+  const bool f8 = c.fmt == FM_FMT_FP8;
+  const Plan alone = plan_of(c, b, H, 0, 0);
+  sp.workspace = alone.workspace;
+  sp.tokens = static_cast<int>(std::min<int64_t>(b.tokens, static_cast<int64_t>(g.max_entries) * b.max_tokens));
+  const int64_t rows = static_cast<int64_t>(sp.tokens) * G, entry_rows = static_cast<int64_t>(b.max_tokens) * G;
+  if (g.n == 0 || rows == 0 || g.max_shared == 0 || rows > (int64_t(1) << 30) || entry_rows > kTileRows) return sp;
+  Plan& pre = sp.prefix;
+  pre.alt = rows <= kTileRows;
+  const int64_t block_rows = pre.alt ? kTileRows : 2 * kTileRows;
+  pre.row_blocks = (rows + block_rows - 1) / block_rows;
+  const int64_t units = pre.row_blocks * c.Hkv * g.n;
+  const int64_t tiles = (static_cast<int64_t>(g.max_shared) + kTileRows - 1) / kTileRows;
+  const int64_t fixed = f8 ? 85 : 70, each = pre.alt ? (f8 ? 15 : 8) : (f8 ? 18 : 14);
+  const int block = entry_rows <= 8 ? 8 : kDecodeRows;
+  const int64_t own_units = static_cast<int64_t>(c.Hkv) * b.n * ((entry_rows + block - 1) / block);
+  const int64_t own_tiles = (std::max<int64_t>({1, b.max_tokens, int64_t(b.max_len) - g.max_shared}) + kDecodeKeys - 1) / kDecodeKeys + 1;
+  const int resident = decode_resident(c.Dh, f8, block);
+  if (own_units > 65535 || c.Hkv > 8191 || units > (int64_t(1) << 30)) return sp;
+  // The least of max(prefix, own keys) + the join + what of the second kernel finds no SM beside the first: its CTAs stay
+  // until the prefix's shares are there, and those left over take their whole time behind it (8 us for 288 CTAs where 280
+  // fit, 96 entries behind 500 keys). So neither takes more CTAs than it needs.
+  const int64_t most = std::min<int64_t>({kMostPrefixSplits, tiles, std::max(1, 65535 / g.n)});
+  int64_t best = 0;
+  for (int64_t s = 1; s <= most; ++s) {
+    const int64_t longest = (tiles + s - 1) / s;
+    if (s > 1 && longest == (tiles + s - 2) / (s - 1)) continue;   // no shorter than with fewer
+    const int64_t ctas = units * s, waves = (ctas + sms - 1) / sms, shares = s * b.tokens * H * c.Dh * 8;
+    const int64_t prefix = waves * (fixed + longest * each) + shares / 400000 + s * 6 / 10;
+    const int64_t room = (waves * sms - ctas) * resident;
+    for (int k = 1; k <= 8 && 2 * k <= own_tiles + 2; k *= 2) {   // own keys' splits: whole clusters find room
+      const int64_t own = 55 + (own_tiles + k - 1) / k * decode_each(f8, resident, own_units * k, sms) / 10, left = std::max<int64_t>(0, own_units * k - room);
+      const int64_t cost = std::max(prefix, own) + 35 + (left + sms * resident - 1) / (sms * resident) * own;
+      if (best == 0 || cost < best) {
+        best = cost;
+        pre.splits = static_cast<int>(s);
+        sp.own_splits = k;
+      }
+    }
+  }
+  if (best * 11 / 10 >= cost_alone(c, b, H, alone)) return sp;
+  pre.split_tiles = static_cast<int>((tiles + pre.splits - 1) / pre.splits);
+  rings_of(c, pre);
+  sp.split = true;
+  sp.workspace = static_cast<size_t>(pre.splits) * b.tokens * H * (c.Dh * sizeof(float) + sizeof(float2));
+  return sp;
+}
+
+int attend_shared(const Call& a, const fm_kv_groups* g) {
+  int st = check_call(a);
+  if (st == FM_OK) st = check_groups(g);
+  if (st != FM_OK) return st;
+  if (nothing_to_do(*a.b)) return FM_OK;
+  st = check_tensors(a);
+  if (st != FM_OK) return st;
+  const fm_kv_batch b = bounded_batch(*a.b);
+  const SharedPlan sp = shared_plan(*a.c, b, *g, a.H);
+  if (!sp.split) return attend<Keys::kAll>(a, 0, 0);
+  st = check_workspace(a, sp.workspace, "workspace smaller than fm_shared_attention_workspace_size()");
+  if (st != FM_OK) return st;
+  CUtensorMap tk, tv, ok, ov;
+  if (!maps_of(a, false, &tk, &tv) || !maps_of(a, true, &ok, &ov))
+    return record_error(FM_ERR_CUDA, "cuTensorMapEncodeTiled (cache pages) failed");
+  AttnParams p;
+  if (!params_of(a, b, p)) return record_error(FM_ERR_CUDA, "no error word on the current device");
+  cudaError_t e = configure<Keys::kPrefix>();
+  if (e != cudaSuccess) return record_error(FM_ERR_CUDA, cudaGetErrorString(e));
+  shares_in(a, sp.prefix.splits, b.tokens, p);
+  p.g_first = g->first;
+  p.g_shared = g->shared;
+  p.g_n = g->n;
+  p.g_tokens = sp.tokens;
+  p.prefix_splits = sp.prefix.splits;
+  const LaunchOpts o = opts_of(a);
+  use_plan(sp.prefix, p);
+  e = launch_tiles<Keys::kPrefix>(a, sp.prefix, g->n, p, tk, tv, o);
+  if (e == cudaSuccess) {
+    p.splits = sp.own_splits;
+    e = decode_launch<Keys::kOwn>(p, a.c->Dh, a.c->fmt == FM_FMT_FP8, ok, ov, o);
   }
   return e == cudaSuccess ? FM_OK : record_error(FM_ERR_CUDA, cudaGetErrorString(e));
 }
@@ -364,8 +553,8 @@ extern "C" int fm_paged_attention_workspace_size(const fm_kv_cache* c, const fm_
 extern "C" int fm_paged_attention(const fm_kv_cache* c, int layer, const fm_kv_batch* b, const uint16_t* q,
                                   int64_t q_stride, int H, float scale, int causal, int window, uint16_t* out,
                                   int64_t out_stride, void* workspace, size_t workspace_bytes, void* stream) {
-  return fm::attend<fm::Keys::kAll>(c, layer, b, q, q_stride, H, scale, causal, window, 0, out, out_stride, workspace,
-                                    workspace_bytes, stream);
+  return fm::attend<fm::Keys::kAll>({c, layer, b, q, q_stride, H, scale, causal, out, out_stride, workspace, workspace_bytes, stream},
+                                    window, 0);
 }
 
 extern "C" int fm_sink_attention(const fm_kv_cache* c, int layer, const fm_kv_batch* b, const uint16_t* q, int64_t q_stride,
@@ -373,10 +562,23 @@ extern "C" int fm_sink_attention(const fm_kv_cache* c, int layer, const fm_kv_ba
                                  void* workspace, size_t workspace_bytes, void* stream) {
   using namespace fm;
   if (sinks < 0) return record_error(FM_ERR_INVALID_ARG, "sinks must not be negative");
+  const Call a{c, layer, b, q, q_stride, H, scale, causal, out, out_stride, workspace, workspace_bytes, stream};
   // without a window nothing is hidden, without first tokens nothing is kept: the same attention in one stretch of keys
-  if (window <= 0 || sinks == 0)
-    return attend<Keys::kAll>(c, layer, b, q, q_stride, H, scale, causal, window, 0, out, out_stride, workspace,
-                              workspace_bytes, stream);
-  return attend<Keys::kSinks>(c, layer, b, q, q_stride, H, scale, causal, window, sinks, out, out_stride, workspace,
-                              workspace_bytes, stream);
+  return window <= 0 || sinks == 0 ? attend<Keys::kAll>(a, window, 0) : attend<Keys::kSinks>(a, window, sinks);
+}
+
+extern "C" int fm_shared_attention_workspace_size(const fm_kv_cache* c, const fm_kv_batch* b, const fm_kv_groups* g, int H,
+                                                  size_t* bytes) {
+  if (!bytes) return fm::record_error(FM_ERR_INVALID_ARG, "bytes is NULL");
+  int st = fm::check(c, b, H);
+  if (st == FM_OK) st = fm::check_groups(g);
+  if (st != FM_OK) return st;
+  *bytes = fm::nothing_to_do(*b) ? 0 : fm::shared_plan(*c, fm::bounded_batch(*b), *g, H).workspace;
+  return FM_OK;
+}
+
+extern "C" int fm_shared_attention(const fm_kv_cache* c, int layer, const fm_kv_batch* b, const fm_kv_groups* g,
+                                   const uint16_t* q, int64_t q_stride, int H, float scale, int causal, uint16_t* out,
+                                   int64_t out_stride, void* workspace, size_t workspace_bytes, void* stream) {
+  return fm::attend_shared({c, layer, b, q, q_stride, H, scale, causal, out, out_stride, workspace, workspace_bytes, stream}, g);
 }

@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kThreads, kResident<DH, F8, NT>)
   __shared__ uint64_t full[kDepth], empty[kDepth];
   __shared__ float2 s_ml[kWarps + 1][kDecodeRows];         // (log2 maximum, sum) of each warp, and of the CTA
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int split = blockIdx.x, g = blockIdx.y;
+  const int split = blockIdx.x, g = K == Keys::kOwn ? blockIdx.y % p.Hkv : blockIdx.y;
   if (tid == 0) {
     for (int i = 0; i < kDepth; ++i) {
       mbar_init(&full[i], 1);
@@ -100,12 +100,21 @@ __global__ void __launch_bounds__(kThreads, kResident<DH, F8, NT>)
     fence_mbar_init();
   }
   pdl_trigger();
-  pdl_wait();
-  const Entry en = entry_of(p, blockIdx.z, tid == 0 && g == 0 && split == 0);
-  const int rows = min(min(en.nq, p.max_tokens) * p.G, 8 * NT);
-  if (rows == 0) return;   // the same in the whole cluster
+  // Keys::kOwn starts when every CTA of the prefix's kernel has waited for what ran before it, so that all inputs are there;
+  // it waits only for that kernel's shares (and, rows or none, does not end before it)
+  if constexpr (K != Keys::kOwn) pdl_wait();
+  const Entry en = entry_of(p, blockIdx.z, tid == 0 && blockIdx.y == 0 && split == 0);
+  // Keys::kOwn has any number of rows, a row block of 8 NT in each CTA
+  const int row0 = K == Keys::kOwn ? blockIdx.y / p.Hkv * 8 * NT : 0;
+  const int rows = min(max(min(en.nq, p.max_tokens) * p.G - row0, 0), 8 * NT);
+  if (rows == 0) {   // the same in the whole cluster
+    if constexpr (K == Keys::kOwn) pdl_wait();
+    return;
+  }
   const int past = en.len - en.nq;
-  const int lo_all = first_key(p, past), hi_all = last_key(p, past + (rows - 1) / p.G, en.len);
+  int own = 0;   // Keys::kOwn: the first key
+  if constexpr (K == Keys::kOwn) own = prefix_of(p, blockIdx.z, en);
+  const int lo_all = K == Keys::kOwn ? own : first_key(p, past), hi_all = last_key(p, past + (row0 + rows - 1) / p.G, en.len);
   const int first = lo_all / kDecodeKeys;
   const Places<K> places(p, first, kDecodeKeys);
   const int begin = places.begin(first);   // t_lo: a place in the order of the key tiles
@@ -179,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, kResident<DH, F8, NT>)
     for (int x = 0; x < NT; ++x) {
       const int row = 8 * x + g8;
       const bool live = row < rows;
-      const int tok = row / p.G, head = row - tok * p.G;
+      const int tok = (row0 + row) / p.G, head = row0 + row - tok * p.G;
       const __nv_bfloat16* src = p.q + static_cast<int64_t>(en.begin + tok) * p.q_stride + (g * p.G + head) * DH;
 #pragma unroll
       for (int c = 0; c < DH / 16; ++c) {
@@ -220,8 +229,8 @@ __global__ void __launch_bounds__(kThreads, kResident<DH, F8, NT>)
     int my_lo[2 * NT], my_hi[2 * NT];
 #pragma unroll
     for (int u = 0; u < 2 * NT; ++u) {
-      const int row = 8 * (u >> 1) + 2 * q4 + (u & 1), pos = past + row / p.G;
-      my_lo[u] = row < rows ? first_key(p, pos) : 0;
+      const int row = 8 * (u >> 1) + 2 * q4 + (u & 1), pos = past + (row0 + row) / p.G;
+      my_lo[u] = K == Keys::kOwn ? own : row < rows ? first_key(p, pos) : 0;
       my_hi[u] = row < rows ? last_key(p, pos, en.len) : hi_all;
     }
     constexpr float kShift = F8 ? 6.0f : 0.0f;   // f16 probabilities are held 2^6 larger: subnormals begin lower
@@ -394,8 +403,77 @@ __global__ void __launch_bounds__(kThreads, kResident<DH, F8, NT>)
     }
   }
   __syncthreads();
+  if constexpr (K == Keys::kOwn) pdl_wait();   // the prefix's shares
   const float vs = F8 ? *p.v_scale : 1.0f;
-  const bool clustered = p.splits > 1 && p.part_o == nullptr;
+  const bool clustered = p.splits > 1 && (K == Keys::kOwn || p.part_o == nullptr);
+  // Keys::kOwn: every split's weight in a row's sum over the prefix, under the prefix's maximum; that maximum, the total
+  __shared__ float s_w[K == Keys::kOwn ? 8 * NT : 1][kMostPrefixSplits];
+  __shared__ float2 s_pre[K == Keys::kOwn ? 8 * NT : 1];
+  if constexpr (K == Keys::kOwn) {
+    if (own > 0) {
+      constexpr int kEach = kMostPrefixSplits / 32;
+      for (int row = warp; row < rows; row += kWarps + 1) {
+        const int64_t at = static_cast<int64_t>(en.begin + (row0 + row) / p.G) * p.H + g * p.G + (row0 + row) % p.G;
+        float2 ml[kEach];
+        float top = -INFINITY, l = 0.f;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+          const int s = lane + 32 * i;
+          ml[i] = s < p.prefix_splits ? p.part_ml[s * static_cast<int64_t>(p.tokens) * p.H + at] : make_float2(-INFINITY, 0.f);
+          top = fmaxf(top, ml[i].x);
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+          // no keys: no share. A NaN in the query has no maximum either, but its sum is NaN
+          const float w = ml[i].x == -INFINITY && ml[i].y == 0.f ? 0.f : ex2_approx(ml[i].x - top);
+          s_w[row][lane + 32 * i] = w;
+          l += ml[i].y * w;
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+        if (lane == 0) s_pre[row] = make_float2(top, l);
+      }
+      __syncthreads();
+    }
+  }
+  // a row's quad of sums, under the maximum `top` and with their total l, as output; with the prefix's shares where the group
+  // has some
+  auto finish = [&](int row, int d, float top, float l, float4 acc) {
+    const int tok = en.begin + (row0 + row) / p.G, head = g * p.G + (row0 + row) % p.G;
+    float inv = vs;
+    if constexpr (K == Keys::kOwn) {
+      if (own > 0) {
+        const int64_t rows_of = static_cast<int64_t>(p.tokens) * p.H, at = static_cast<int64_t>(tok) * p.H + head;
+        const float2 pre = s_pre[row];
+        const float all = fmaxf(top, pre.x);
+        const float f = top > -INFINITY ? ex2_approx(top - all) : 0.f, fv = f * vs;
+        const float fp = pre.x > -INFINITY ? ex2_approx(pre.x - all) : 0.f;
+        l = l * f + pre.y * fp;
+        float4 sum4 = make_float4(0.f, 0.f, 0.f, 0.f);
+        // eight loads are on their way at a time (with a weight and a load by turns the join of 13 took 3 us more)
+        for (int s0 = 0; s0 < p.prefix_splits; s0 += 8) {
+          float4 v[8];
+          float w[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            w[i] = s_w[row][s0 + i];   // 0 behind the last one
+            v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (w[i] != 0.f) v[i] = *reinterpret_cast<const float4*>(p.part_o + ((s0 + i) * rows_of + at) * DH + d);
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sum4.x += v[i].x * w[i], sum4.y += v[i].y * w[i], sum4.z += v[i].z * w[i], sum4.w += v[i].w * w[i];
+        }
+        acc.x = acc.x * fv + sum4.x * fp, acc.y = acc.y * fv + sum4.y * fp;
+        acc.z = acc.z * fv + sum4.z * fp, acc.w = acc.w * fv + sum4.w * fp;
+        inv = 1.0f;
+      }
+    }
+    inv = l == 0.f ? 0.f : inv / l;
+    *reinterpret_cast<uint2*>(p.out + tok * p.out_stride + head * DH + d) =
+        make_uint2(pack16<false>(acc.x * inv, acc.y * inv), pack16<false>(acc.z * inv, acc.w * inv));
+  };
   constexpr int kQuads = DH / 4;
   for (int x = tid; x < rows * kQuads; x += kThreads) {
     const int row = x / kQuads, d = (x % kQuads) * 4;
@@ -412,18 +490,16 @@ __global__ void __launch_bounds__(kThreads, kResident<DH, F8, NT>)
       l += ml.y * f;
       acc.x += v.x * f, acc.y += v.y * f, acc.z += v.z * f, acc.w += v.w * f;
     }
-    const int tok = en.begin + row / p.G, head = g * p.G + row % p.G;
     if (clustered) {
       *reinterpret_cast<float4*>(cta + row * DH + d) = acc;
       if (d == 0) s_ml[kWarps][row] = make_float2(top, l);
     } else if (p.splits > 1) {
+      const int tok = en.begin + (row0 + row) / p.G, head = g * p.G + (row0 + row) % p.G;
       const int64_t at = (static_cast<int64_t>(split) * p.tokens + tok) * p.H + head;
       if (nt > 0) *reinterpret_cast<float4*>(p.part_o + at * DH + d) = make_float4(acc.x * vs, acc.y * vs, acc.z * vs, acc.w * vs);
       if (d == 0) p.part_ml[at] = make_float2(top, l);
     } else {
-      const float inv = l == 0.f ? 0.f : vs / l;
-      *reinterpret_cast<uint2*>(p.out + tok * p.out_stride + head * DH + d) =
-          make_uint2(pack16<false>(acc.x * inv, acc.y * inv), pack16<false>(acc.z * inv, acc.w * inv));
+      finish(row, d, top, l, acc);
     }
   }
   if (!clustered) return;
@@ -457,10 +533,7 @@ __global__ void __launch_bounds__(kThreads, kResident<DH, F8, NT>)
       l += ml[s].y * f;
       acc.x += v.x * f, acc.y += v.y * f, acc.z += v.z * f, acc.w += v.w * f;
     }
-    const float inv = l == 0.f ? 0.f : vs / l;
-    const int tok = en.begin + row / p.G, head = g * p.G + row % p.G;
-    *reinterpret_cast<uint2*>(p.out + tok * p.out_stride + head * DH + d) =
-        make_uint2(pack16<false>(acc.x * inv, acc.y * inv), pack16<false>(acc.z * inv, acc.w * inv));
+    finish(row, d, top, l, acc);
   }
   // no CTA leaves while another still reads its share
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -481,7 +554,8 @@ cudaError_t configure_one() {
 
 template <int DH, bool F8, int NT, Keys K>
 cudaError_t run(const AttnParams& p, const CUtensorMap& tk, const CUtensorMap& tv, const LaunchOpts& o) {
-  return launch(decode_kernel<DH, F8, NT, K>, dim3(p.splits, p.Hkv, p.n), dim3(kThreads), smem_bytes<DH, F8, NT>(), o, p, tk, tv);
+  const int blocks = K == Keys::kOwn ? (p.max_tokens * p.G + 8 * NT - 1) / (8 * NT) : 1;
+  return launch(decode_kernel<DH, F8, NT, K>, dim3(p.splits, p.Hkv * blocks, p.n), dim3(kThreads), smem_bytes<DH, F8, NT>(), o, p, tk, tv);
 }
 
 template <int DH, bool F8, Keys K>
@@ -510,7 +584,7 @@ template <Keys K>
 cudaError_t decode_launch(const AttnParams& p, int Dh, bool f8, const CUtensorMap& tk, const CUtensorMap& tv,
                           const LaunchOpts& opts) {
   LaunchOpts o = opts;
-  if (p.splits > 1 && !p.part_o) o.cluster = dim3(p.splits, 1, 1);
+  if (p.splits > 1 && (K == Keys::kOwn || !p.part_o)) o.cluster = dim3(p.splits, 1, 1);
   if (Dh == 128) return f8 ? run_rows<128, true, K>(p, tk, tv, o) : run_rows<128, false, K>(p, tk, tv, o);
   return f8 ? run_rows<64, true, K>(p, tk, tv, o) : run_rows<64, false, K>(p, tk, tv, o);
 }

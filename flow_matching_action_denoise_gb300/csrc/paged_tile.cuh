@@ -190,9 +190,11 @@ __global__ void __launch_bounds__(threads_of(F8), 1)
   pdl_wait();
 
   // ---- the entry, its rows and its keys (the same in every thread)
-  const Entry en = entry_of(p, entry, tid == 0 && row_block == 0 && g == 0 && split == 0);
+  const bool report = tid == 0 && row_block == 0 && g == 0 && split == 0;
+  const Entry en = K == Keys::kPrefix ? group_of(p, entry, report) : entry_of(p, entry, report);
+  const bool shares = K == Keys::kPrefix || p.splits > 1;   // the results go to the workspace
   const int begin = en.begin, nq = en.nq, len = en.len, sid = en.sid;
-  const int rows = min(nq, p.max_tokens) * p.G;   // <= 2^30
+  const int rows = min(nq, K == Keys::kPrefix ? p.g_tokens : p.max_tokens) * p.G;   // <= 2^30
   const int row0 = row_block * block_rows;
   tc_fence_before();
   __syncthreads();
@@ -205,8 +207,8 @@ __global__ void __launch_bounds__(threads_of(F8), 1)
   }
 
   const int past = len - nq;   // position of token i: past + i
-  auto key_end = [&](int row) { return last_key(p, past + row / p.G, len); };
-  auto key_begin = [&](int row) { return first_key(p, past + row / p.G); };
+  auto key_end = [&](int row) { return K == Keys::kPrefix ? len : last_key(p, past + row / p.G, len); };
+  auto key_begin = [&](int row) { return K == Keys::kPrefix ? 0 : first_key(p, past + row / p.G); };
   const int last_row = min(rows, row0 + block_rows) - 1;
   const int hi_all = key_end(last_row);
   // t_lo, t_hi: places in the order of the key tiles
@@ -555,7 +557,7 @@ __global__ void __launch_bounds__(threads_of(F8), 1)
         m2 = top;
       }
       const int64_t split_row = static_cast<int64_t>(split) * p.tokens * p.H;
-      if (p.splits > 1) {
+      if (shares) {
         if (live) p.part_ml[split_row + static_cast<int64_t>(begin + row / p.G) * p.H + g * p.G + row % p.G] = make_float2(m2, sum);
         w0 *= vs;
         w1 *= vs;
@@ -567,10 +569,10 @@ __global__ void __launch_bounds__(threads_of(F8), 1)
       // TMEM gives a lane one row: rows are staged in the query tile's 32 rows of this warp (its last reader has
       // completed) and leave kRowChunks lanes a row, whole 16-byte chunks. fp32 shares take two passes.
       const uint32_t stage = q_a + (p.alt ? 0 : t * kTileBytes) + wq * 32 * DH * 2;
-      const int passes = p.splits == 1 ? 1 : nt > 0 ? 2 : 0;
+      const int passes = !shares ? 1 : nt > 0 ? 2 : 0;
 #pragma unroll 1
       for (int pass = 0; pass < passes; ++pass) {
-        const int dims = p.splits == 1 ? DH : DH / 2, d0 = pass * dims;
+        const int dims = shares ? DH / 2 : DH, d0 = pass * dims;
 #pragma unroll 1
         for (int b = 0; b < dims; b += 32) {
           float o[32];
@@ -588,7 +590,7 @@ __global__ void __launch_bounds__(threads_of(F8), 1)
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] *= w0;
           }
-          if (p.splits > 1) {
+          if (shares) {
 #pragma unroll
             for (int e = 0; e < 32; e += 4)
               st_shared_v4(stage + lane * (DH * 2) + ((((b + e) >> 2) ^ (lane & 7)) << 4),
@@ -605,7 +607,7 @@ __global__ void __launch_bounds__(threads_of(F8), 1)
         __syncwarp();
         const int left = rows - tile_row0 - wq * 32 - lane_row;
         const uint8_t* staged = sq + (p.alt ? 0 : t * kTileBytes) + wq * 32 * DH * 2;
-        if (p.splits > 1) {   // shares: [split][token][head][DH], this pass's half of the dims
+        if (shares) {   // shares: [split][token][head][DH], this pass's half of the dims
           Walk walk(tile_row0 + wq * 32 + lane_row, p.G, static_cast<int64_t>(p.H) * DH,
                     (split_row + static_cast<int64_t>(begin) * p.H + g * p.G) * DH + d0 + lane_chunk * 4);
 #pragma unroll

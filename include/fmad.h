@@ -349,7 +349,7 @@ int fm_device_status(fm_policy* p, void* stream, int* word);
 
 /* Error word of the policy-free building blocks (fm_test_skinny_gemm, fm_gemm_consumer,
  * fm_gemm_consumer_noalloc, fm_rope_append, fm_norm_rope_append, fm_paged_attention,
- * fm_sink_attention): synchronise `stream`, read and clear the bits their kernels
+ * fm_sink_attention, fm_shared_attention): synchronise `stream`, read and clear the bits their kernels
  * set when they abandoned a bounded wait on the current device. Returns FM_OK, or
  * FM_ERR_DEVICE with *word = the bits (1 = TMA/MMA pipeline wait expired, 2 = a paged
  * batch outside its bounds or a token without a page); the outputs of
@@ -760,6 +760,33 @@ int fm_paged_attention(const fm_kv_cache* c, int layer, const fm_kv_batch* b, co
 int fm_sink_attention(const fm_kv_cache* c, int layer, const fm_kv_batch* b, const uint16_t* q, int64_t q_stride, int H,
                       float scale, int causal, int window, int sinks, uint16_t* out, int64_t out_stride, void* workspace,
                       size_t workspace_bytes, void* stream);
+
+/* Groups of a batch's entries that begin with the same tokens: group i is the entries [first[i], first[i + 1]), whose
+ * sequences hold the same keys and values at their first shared[i] tokens (forks: the same pages, or a begun page's copy;
+ * any number of tokens, no multiple of the page). first does not descend; entries before the first group and behind the last
+ * one share nothing. max_entries bounds a group's entries and max_shared is the number of shared tokens that the work is
+ * divided for (more of either: right, only slower). 0 <= n <= 65535. */
+typedef struct fm_kv_groups {
+  const int32_t* first;   /* device [n + 1] */
+  const int32_t* shared;  /* device [n] */
+  int n;
+  int max_entries;
+  int max_shared;
+} fm_kv_groups;
+
+/* Bytes of workspace for fm_shared_attention; depends on the cache's Dh, Hkv and format, the counts of the batch and the
+ * groups, and H only. */
+int fm_shared_attention_workspace_size(const fm_kv_cache* c, const fm_kv_batch* b, const fm_kv_groups* g, int H, size_t* bytes);
+
+/* fm_paged_attention (window 0) of a batch in groups: the keys that a group shares are read once for all its tokens, from
+ * the pages of its first entry or of any other. Where that would cost more than it saves (few entries, few shared tokens,
+ * many rows of an entry, by the counts) every entry reads its own. An entry with a token that does not see all the shared
+ * tokens (causal, shared[i] > position + 1) reads its own as well. A group out of range, or whose shared[i] is negative or
+ * exceeds the length of its first entry, sets bit 2 of fm_standalone_status (where groups are read at all) and shares
+ * nothing. A result depends on the group only through roundings. All else as fm_paged_attention. Asynchronous. */
+int fm_shared_attention(const fm_kv_cache* c, int layer, const fm_kv_batch* b, const fm_kv_groups* g, const uint16_t* q,
+                        int64_t q_stride, int H, float scale, int causal, uint16_t* out, int64_t out_stride, void* workspace,
+                        size_t workspace_bytes, void* stream);
 
 /* Residual addition + RMS norm + E4M3 with scales taken from the data:
  *   s = x + r (r NULL: x);  x_out = s (unless NULL);
