@@ -532,7 +532,6 @@ struct AppendParams {
   int tokens, max_tokens, seqs, table_stride, pages, page, shift;
   int H, Hkv, Dh;
   int toks, groups;         // tokens of a CTA, threads that share the heads of a token
-  int lanes;                // threads of a head
   const float *q_gamma, *k_gamma;   // normalised heads: [Dh] or null
   float eps;
   void *kc, *vc;            // this layer
@@ -572,13 +571,18 @@ __device__ __forceinline__ uint2 codes8(const float* f, float rs) {
 // without double precision. One thread: 16 elements (two 8-element chunks that hold whole pairs) of every groups-th
 // head. Bound by HBM: q, k and v are read once and written once (9600 tokens of 16 + 2 x 4 heads of 128, half of each
 // rotated, bf16 cache: 23.2 us, 5.1 TB/s; 32 single tokens: 2.5 us, launch).
-// NORM: every head of q and k is divided by its root mean square and multiplied by gamma before it turns. A head's threads
-// are a power of two of neighbouring lanes (some of them idle where Dh / 16 is none), which add their squares by shuffles.
-template <bool F8, bool NORM>
-__global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
-  extern __shared__ float2 s_angle[];   // [toks][rot / 2] (cos, sin) times magnitude; NORM: then [2][Dh] gammas
+// LANES > 0: every head of q and k is divided by its root mean square and multiplied by gamma before it turns. A head's threads
+// are LANES neighbouring lanes, a power of two (some of them idle where Dh / 16 is none), which add their squares by shuffles.
+// The same bytes as without the norm and, with 64 registers and shared memory free of conflicts, the same time: 23.0 us for
+// those 9600 tokens, 5.1 TB/s (four heads' loads at once in 107 registers: 35 us; conflicts in the angles and gammas: 29 us).
+template <bool F8, int LANES>
+__global__ void __launch_bounds__(256, 4) append_kernel(const AppendParams p) {
+  // [toks][rot / 2] (cos, sin) times magnitude; NORM: then [2][Dh] gammas, and both in the order in which neighbouring lanes
+  // read 16 bytes each: [16-byte piece of a unit][unit] (in the order of the elements four lanes met in a bank)
+  extern __shared__ float2 s_angle[];
+  constexpr bool NORM = LANES > 0;
   pdl_trigger();
-  const int units = p.Dh / 16, pairs = p.rot / 2, lanes = NORM ? p.lanes : units;
+  const int units = p.Dh / 16, pairs = p.rot / 2, lanes = NORM ? LANES : units;
   const int unit = threadIdx.x % lanes, tok = (threadIdx.x / lanes) % p.toks, grp = threadIdx.x / (lanes * p.toks);
   const int entry = blockIdx.y;
   pdl_wait();
@@ -596,28 +600,25 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
   const bool turned = unit < rot_units, split = turned && !p.interleaved;
   const bool idle = NORM && unit >= units;   // takes part in the shuffles only; its places are those of unit 0
   const int c0 = idle ? 0 : (split ? unit : 2 * unit) * 8, c1 = idle ? 0 : (split ? unit + rot_units : 2 * unit + 1) * 8;
-  [[maybe_unused]] constexpr int kHeads = 4;   // NORM: heads whose loads are on their way together
-  [[maybe_unused]] uint4 u[NORM ? kHeads : 1], w[NORM ? kHeads : 1];
-  [[maybe_unused]] auto load_heads = [&](int h0, int heads) {
-    const int64_t token = begin + static_cast<int64_t>(first) + tok;
-#pragma unroll
-    for (int i = 0; i < kHeads; ++i) {
-      const int h = h0 + i * p.groups;
-      u[i] = w[i] = make_uint4(0, 0, 0, 0);
-      if (h >= heads || idle) continue;
-      const __nv_bfloat16* src = h < p.H ? p.q + token * p.qs + h * p.Dh
-                                 : h < p.H + p.Hkv ? p.k + token * p.ks + (h - p.H) * p.Dh
-                                                   : p.v + token * p.vs + (h - p.H - p.Hkv) * p.Dh;
-      u[i] = *reinterpret_cast<const uint4*>(src + c0);
-      w[i] = *reinterpret_cast<const uint4*>(src + c1);
-    }
+  struct Raw {   // a thread's part of a head
+    uint4 a, b;
   };
+  auto load = [&](const __nv_bfloat16* head) {
+    Raw r = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+    if (!idle) r = {*reinterpret_cast<const uint4*>(head + c0), *reinterpret_cast<const uint4*>(head + c1)};
+    return r;
+  };
+  [[maybe_unused]] Raw ahead = {};   // NORM: the first query head, loaded while the angles are computed
   [[maybe_unused]] float* s_gamma = reinterpret_cast<float*>(s_angle + p.toks * pairs);
-  if constexpr (NORM) {   // the first heads are loaded while the angles are computed
-    if (grp < p.groups && first + tok < end) load_heads(grp, p.H + 2 * p.Hkv);
+  if constexpr (NORM) {
+    if (grp < p.groups && first + tok < end && grp < p.H)
+      ahead = load(p.q + (begin + static_cast<int64_t>(first) + tok) * p.qs + grp * p.Dh);
     for (int x = threadIdx.x; x < 2 * p.Dh; x += 256) {
       const float* src = x < p.Dh ? p.q_gamma : p.k_gamma;
-      s_gamma[x] = src ? src[x < p.Dh ? x : x - p.Dh] : 1.0f;
+      const int el = x < p.Dh ? x : x - p.Dh, chunk = el / 8;
+      const bool apart = !p.interleaved && chunk < 2 * rot_units;   // a unit's two chunks
+      const int of = apart ? chunk % rot_units : chunk / 2, piece = (apart ? chunk / rot_units : chunk % 2) * 2 + el % 8 / 4;
+      s_gamma[x - el + (piece * units + of) * 4 + el % 4] = src ? src[el] : 1.0f;
     }
   }
   for (int x = threadIdx.x; x < p.toks * pairs; x += 256) {
@@ -628,7 +629,9 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
     const uint64_t turn = p.freq[i] * static_cast<uint64_t>(at) + (1ull << 31);
     float2 a;
     sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f, &a.y, &a.x);
-    s_angle[x] = make_float2(a.x * p.mag, a.y * p.mag);
+    // a unit's eight pairs are four 16-byte pieces
+    const int place = NORM ? x - i + (i % 8 / 2 * rot_units + i / 8) * 2 + i % 2 : x;
+    s_angle[place] = make_float2(a.x * p.mag, a.y * p.mag);
   }
   const int within = first + tok;
   const bool mine = grp < p.groups && within < end;
@@ -642,17 +645,19 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
   __syncthreads();
   if (!mine) return;
   float2 ang[8];
-  if (turned) {
-    const float4* src = reinterpret_cast<const float4*>(s_angle + tok * pairs + unit * 8);
+  auto angles = [&] {
+    const float4* src = reinterpret_cast<const float4*>(s_angle + tok * pairs + unit * (NORM ? 2 : 8));
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float4 v = src[i];
+      const float4 v = src[NORM ? i * rot_units : i];
       ang[2 * i] = make_float2(v.x, v.y);
       ang[2 * i + 1] = make_float2(v.z, v.w);
     }
-  }
+  };
+  if (!NORM && turned) angles();
   auto turn = [&](float* a, float* b) {
     if (!turned) return;
+    if (NORM) angles();   // from shared memory every time: 16 registers fewer, more CTAs an SM
     if (p.interleaved) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -672,80 +677,111 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
     }
   };
   if constexpr (NORM) {
-    const uint32_t team = ((1u << lanes) - 1u) << (threadIdx.x & 31 & ~(lanes - 1));
+    const uint32_t team = ((1u << LANES) - 1u) << (threadIdx.x & 31 & ~(LANES - 1));
     auto reduce = [&](float v, auto join) {   // over the head's lanes, in a fixed order, the same in all of them
-      for (int o = lanes >> 1; o > 0; o >>= 1) v = join(v, __shfl_xor_sync(team, v, o));
+#pragma unroll
+      for (int o = LANES >> 1; o > 0; o >>= 1) v = join(v, __shfl_xor_sync(team, v, o));
       return v;
     };
-    const auto add = [](float x, float y) { return x + y; };
-    const auto larger = [](float x, float y) { return x > y || x != x ? x : y; };   // NaN if either is
     const float rdh = 1.0f / p.Dh;
-    auto normalise = [&](float* a, float* b, const float* gamma) {
-      auto squares = [&] {
-        float s = 0.f;
+    // two elements an instruction
+    auto squares = [&](const float2* a, const float2* b) {
+      float2 s = mul2(a[0], a[0]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s = fmaf(a[e], a[e], fmaf(b[e], b[e], s));
-        return reduce(s, add);
-      };
-      const float ms = fmaf(squares(), rdh, p.eps);
-      float rr = 1.0f / sqrtf(ms);
+      for (int e = 1; e < 4; ++e) s = fma2(a[e], a[e], s);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s = fma2(b[e], b[e], s);
+      return reduce(s.x + s.y, [](float x, float y) { return x + y; });
+    };
+    auto normalise = [&](float2* a, float2* b, const float* gamma) {
+      const float ms = fmaf(squares(a, b), rdh, p.eps);
+      float rr = rsqrtf(ms);
       // Squares out of fp32's range, the same in all of the head's lanes: the head is taken times the power of two that puts
       // the larger of its maximum and sqrt(eps) into [2, 4). A head with a NaN or an infinity is NaN throughout.
       if (!(ms >= 0x1p-100f && ms < INFINITY)) {
+        const auto larger = [](float x, float y) { return x > y || x != x ? x : y; };   // NaN if either is
         float top = 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) top = larger(larger(top, fabsf(a[e])), fabsf(b[e]));
+        for (int e = 0; e < 4; ++e)
+          top = larger(larger(larger(larger(top, fabsf(a[e].x)), fabsf(a[e].y)), fabsf(b[e].x)), fabsf(b[e].y));
         top = reduce(top, larger);
         const uint32_t ex = __float_as_uint(fmaxf(top, sqrtf(p.eps))) >> 23;
         const float f = __uint_as_float((255 - min(max(ex, 1u), 254u)) << 23);
+        const float2 ff = make_float2(f, f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) a[e] *= f, b[e] *= f;
-        const float scaled = squares() * rdh + p.eps * f * f;
+        for (int e = 0; e < 4; ++e) a[e] = mul2(a[e], ff), b[e] = mul2(b[e], ff);
+        const float scaled = squares(a, b) * rdh + p.eps * f * f;
         rr = !(top < INFINITY) ? NAN : scaled > 0.f ? 1.0f / sqrtf(scaled) : 0.f;
       }
-      const float4* g0 = reinterpret_cast<const float4*>(gamma + c0);
-      const float4* g1 = reinterpret_cast<const float4*>(gamma + c1);
+      const float2 r2 = make_float2(rr, rr);
+      const float4* g = reinterpret_cast<const float4*>(gamma) + (idle ? 0 : unit);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float4 x = g0[e], y = g1[e];
-        a[4 * e] *= rr * x.x, a[4 * e + 1] *= rr * x.y, a[4 * e + 2] *= rr * x.z, a[4 * e + 3] *= rr * x.w;
-        b[4 * e] *= rr * y.x, b[4 * e + 1] *= rr * y.y, b[4 * e + 2] *= rr * y.z, b[4 * e + 3] *= rr * y.w;
+      for (int e = 0; e < 4; ++e) {
+        const float4 v = g[e * units];
+        float2* x = (e < 2 ? a : b) + (e & 1) * 2;
+        x[0] = mul2(x[0], mul2(r2, make_float2(v.x, v.y)));
+        x[1] = mul2(x[1], mul2(r2, make_float2(v.z, v.w)));
       }
     };
-    const float rk = F8 ? 1.0f / *p.k_scale : 1.0f, rv = F8 ? 1.0f / *p.v_scale : 1.0f;
-    const int64_t cell = static_cast<int64_t>(page) * p.pg + (pos & (p.page - 1)) * p.tok;
-    const int heads = page < 0 ? p.H : p.H + 2 * p.Hkv;
-    for (int h0 = grp; h0 < heads; h0 += kHeads * p.groups) {
-      if (h0 != grp) load_heads(h0, heads);
-#pragma unroll
-      for (int i = 0; i < kHeads; ++i) {
-        const int h = h0 + i * p.groups;
-        if (h >= heads) break;
-        const bool is_q = h < p.H, is_v = h >= p.H + p.Hkv;
+    auto normalised = [&](const Raw& r, const float* gamma, float* a, float* b) {
+      unpack8(r.a, a);
+      unpack8(r.b, b);
+      normalise(reinterpret_cast<float2*>(a), reinterpret_cast<float2*>(b), gamma);
+      turn(a, b);
+    };
+    {   // ---- queries: the next head is on its way while one is computed
+      const __nv_bfloat16* src = p.q + token * p.qs + grp * p.Dh;
+      __nv_bfloat16* dst = p.q_out + token * p.os + grp * p.Dh;
+      const int step = p.groups * p.Dh;
+#pragma unroll 1
+      for (int h = grp; h < p.H; h += p.groups, dst += step) {
+        const Raw r = ahead;
+        src += step;
+        if (h + p.groups < p.H) ahead = load(src);
         float a[8], b[8];
-        unpack8(u[i], a);
-        unpack8(w[i], b);
-        if (!is_v) {
-          normalise(a, b, s_gamma + (is_q ? 0 : p.Dh));
-          turn(a, b);
-        }
+        normalised(r, s_gamma, a, b);
         if (idle) continue;
-        if (is_q) {
-          __nv_bfloat16* dst = p.q_out + token * p.os + h * p.Dh;
-          *reinterpret_cast<uint4*>(dst + c0) = pack8(a);
-          *reinterpret_cast<uint4*>(dst + c1) = pack8(b);
-          continue;
-        }
-        const int64_t at = cell + (h - p.H - (is_v ? p.Hkv : 0)) * p.head;
-        if constexpr (F8) {
-          uint8_t* dst = static_cast<uint8_t*>(is_v ? p.vc : p.kc) + at;
-          *reinterpret_cast<uint2*>(dst + c0) = codes8(a, is_v ? rv : rk);
-          *reinterpret_cast<uint2*>(dst + c1) = codes8(b, is_v ? rv : rk);
-        } else {
-          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(is_v ? p.vc : p.kc) + at;
-          *reinterpret_cast<uint4*>(dst + c0) = is_v ? u[i] : pack8(a);
-          *reinterpret_cast<uint4*>(dst + c1) = is_v ? w[i] : pack8(b);
-        }
+        *reinterpret_cast<uint4*>(dst + c0) = pack8(a);
+        *reinterpret_cast<uint4*>(dst + c1) = pack8(b);
+      }
+    }
+    if (page < 0) return;
+    // ---- keys and values, the groups in turn where the queries' left off
+    const int64_t cell = static_cast<int64_t>(page) * p.pg + (pos & (p.page - 1)) * p.tok;
+    const float rk = F8 ? 1.0f / *p.k_scale : 1.0f, rv = F8 ? 1.0f / *p.v_scale : 1.0f;
+    int h = grp - p.H % p.groups;
+    if (h < 0) h += p.groups;
+    auto row = [&](int x) { return x < p.Hkv ? p.k + token * p.ks + x * p.Dh : p.v + token * p.vs + (x - p.Hkv) * p.Dh; };
+    if (h < 2 * p.Hkv) ahead = load(row(h));
+#pragma unroll 1
+    for (; h < 2 * p.Hkv; h += p.groups) {
+      const bool is_v = h >= p.Hkv;
+      const Raw r = ahead;
+      if (h + p.groups < 2 * p.Hkv) ahead = load(row(h + p.groups));
+      const int64_t at = cell + (is_v ? h - p.Hkv : h) * p.head;
+      if (!F8 && is_v) {
+        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.vc) + at;
+        if (idle) continue;
+        *reinterpret_cast<uint4*>(dst + c0) = r.a;
+        *reinterpret_cast<uint4*>(dst + c1) = r.b;
+        continue;
+      }
+      float a[8], b[8];
+      if (is_v) {
+        unpack8(r.a, a);
+        unpack8(r.b, b);
+      } else {
+        normalised(r, s_gamma + p.Dh, a, b);
+      }
+      if (idle) continue;
+      if constexpr (F8) {
+        uint8_t* dst = static_cast<uint8_t*>(is_v ? p.vc : p.kc) + at;
+        *reinterpret_cast<uint2*>(dst + c0) = codes8(a, is_v ? rv : rk);
+        *reinterpret_cast<uint2*>(dst + c1) = codes8(b, is_v ? rv : rk);
+      } else {
+        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.kc) + at;
+        *reinterpret_cast<uint4*>(dst + c0) = pack8(a);
+        *reinterpret_cast<uint4*>(dst + c1) = pack8(b);
       }
     }
     return;
@@ -1201,17 +1237,19 @@ int append(const fm_kv_cache* c, int layer, const fm_kv_batch* b, const fm_rope*
   p.err = err;
   // A token has Dh / 16 threads a head group. As many tokens a CTA as leave two groups and three CTAs an SM (9000 tokens,
   // 24 heads of 128: 19.8 us with 16, 23.8 us with 4); a few tokens are spread over all threads of their CTAs.
-  p.lanes = c->Dh / 16;
+  int lanes = c->Dh / 16;
   if (norm) {
     p.q_gamma = norm->q_gamma, p.k_gamma = norm->k_gamma, p.eps = norm->eps;
-    while (p.lanes & (p.lanes - 1)) ++p.lanes;   // the next power of two
+    lanes = lanes <= 4 ? 4 : lanes <= 8 ? 8 : 16;   // Dh is 256 at most
   }
   p.toks = 1;
-  while (p.lanes * p.toks * 2 <= 128 && p.toks < b->max_tokens && b->tokens / (2 * p.toks) >= 152 * 3) p.toks *= 2;
-  p.groups = 256 / (p.lanes * p.toks);
+  while (lanes * p.toks * 2 <= 128 && p.toks < b->max_tokens && b->tokens / (2 * p.toks) >= 152 * 3) p.toks *= 2;
+  p.groups = 256 / (lanes * p.toks);
   const int blocks = (b->max_tokens - 1) / p.toks + 1;
-  void (*kernel)(AppendParams) = norm ? (f8 ? append_kernel<true, true> : append_kernel<false, true>)
-                                      : (f8 ? append_kernel<true, false> : append_kernel<false, false>);
+  void (*kernel)(AppendParams) = !norm        ? (f8 ? append_kernel<true, 0> : append_kernel<false, 0>)
+                                 : lanes == 4 ? (f8 ? append_kernel<true, 4> : append_kernel<false, 4>)
+                                 : lanes == 8 ? (f8 ? append_kernel<true, 8> : append_kernel<false, 8>)
+                                              : (f8 ? append_kernel<true, 16> : append_kernel<false, 16>);
   return done(launch(kernel, dim3(static_cast<unsigned>(blocks), b->n), dim3(256),
                      sizeof(float2) * p.toks * (p.rot / 2) + (norm ? sizeof(float) * 2 * c->Dh : 0), opts(stream), p));
 }
