@@ -17,6 +17,13 @@ namespace fm {
 template cudaError_t tile_launch<Keys::kAll>(const AttnParams&, int, bool, const CUtensorMap&, const CUtensorMap&, dim3, size_t,
                                              const LaunchOpts&);
 template cudaError_t tile_configure<Keys::kAll>();
+// in sources of their own
+extern template cudaError_t tile_launch<Keys::kSinks>(const AttnParams&, int, bool, const CUtensorMap&, const CUtensorMap&, dim3,
+                                                      size_t, const LaunchOpts&);
+extern template cudaError_t tile_configure<Keys::kSinks>();
+extern template cudaError_t tile_launch<Keys::kPrefix>(const AttnParams&, int, bool, const CUtensorMap&, const CUtensorMap&, dim3,
+                                                       size_t, const LaunchOpts&);
+extern template cudaError_t tile_configure<Keys::kPrefix>();
 
 namespace {
 
@@ -466,14 +473,16 @@ SharedPlan shared_plan(const fm_kv_cache& c, const fm_kv_batch& b, const fm_kv_g
   pre.alt = rows <= kTileRows;
   const int64_t block_rows = pre.alt ? kTileRows : 2 * kTileRows;
   pre.row_blocks = (rows + block_rows - 1) / block_rows;
-  const int64_t units = pre.row_blocks * c.Hkv * g.n;
+  // blocks that have rows, by the packed rows: the bounds of one group or entry would count more
+  const int64_t packed = static_cast<int64_t>(b.tokens) * G;
+  const int64_t units = c.Hkv * std::min(pre.row_blocks * g.n, packed / block_rows + g.n);
   const int64_t tiles = (static_cast<int64_t>(g.max_shared) + kTileRows - 1) / kTileRows;
   const int64_t fixed = f8 ? 85 : 70, each = pre.alt ? (f8 ? 15 : 8) : (f8 ? 18 : 14);
   const int block = entry_rows <= 8 ? 8 : kDecodeRows;
-  const int64_t own_units = static_cast<int64_t>(c.Hkv) * b.n * ((entry_rows + block - 1) / block);
+  const int64_t own_units = c.Hkv * std::min(b.n * ((entry_rows + block - 1) / block), packed / block + b.n);
   const int64_t own_tiles = (std::max<int64_t>({1, b.max_tokens, int64_t(b.max_len) - g.max_shared}) + kDecodeKeys - 1) / kDecodeKeys + 1;
   const int resident = decode_resident(c.Dh, f8, block);
-  if (own_units > 65535 || c.Hkv > 8191 || units > (int64_t(1) << 30)) return sp;
+  if (c.Hkv > 8191) return sp;   // x blocks of an entry's rows are a dimension of the grid
   // The least of max(prefix, own keys) + the join + what of the second kernel finds no SM beside the first: its CTAs stay
   // until the prefix's shares are there, and those left over take their whole time behind it (8 us for 288 CTAs where 280
   // fit, 96 entries behind 500 keys). So neither takes more CTAs than it needs.
