@@ -33,6 +33,7 @@ struct AttnParams {
   int alt, splits, split_tiles;
   int row_blocks, rows_first;     // of paged_attn.cu's grid
   int ring, raw_ring;
+  int cluster;                    // CTAs whose splits meet in their cluster (the tile kernel)
   const int32_t* g_first;         // groups: [g_n + 1] first entries
   const int32_t* g_shared;        // [g_n] tokens that a group's entries share
   int g_n, g_tokens;              // g_tokens: packed rows of a group that Keys::kPrefix takes
@@ -49,6 +50,7 @@ cudaError_t tile_launch(const AttnParams& p, int Dh, bool f8, const CUtensorMap&
                         size_t smem, const LaunchOpts& o);
 template <Keys K>
 cudaError_t tile_configure();
+int tile_clusters(int size);   // clusters of so many CTAs (of any variant: one is on an SM) at once
 
 // The kernel for up to 16 stacked rows (max_tokens * G): p.splits CTAs an entry and KV head, joined inside a cluster
 // where p.part_o is null, else through the workspace.
@@ -61,6 +63,7 @@ cudaError_t decode_launch(const AttnParams& p, int Dh, bool f8, const CUtensorMa
 template <Keys K>
 cudaError_t decode_configure();
 int decode_resident(int Dh, bool f8, int rows);   // CTAs of it on an SM at once
+int decode_clusters(int Dh, bool f8, int rows, int size);   // clusters of so many of its CTAs at once
 
 // An entry of the batch; one that is out of range has no tokens and no keys.
 struct Entry {

@@ -25,6 +25,22 @@ extern template cudaError_t tile_launch<Keys::kPrefix>(const AttnParams&, int, b
                                                        size_t, const LaunchOpts&);
 extern template cudaError_t tile_configure<Keys::kPrefix>();
 
+int tile_clusters(int size) {
+  auto* kernel = &paged_attn_kernel<128, false, Keys::kAll, true>;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(1, 1, size);
+  cfg.blockDim = dim3(threads_of(false));
+  cfg.dynamicSmemBytes = kSmemLimit;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = size;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  int n = 0;
+  return tile_configure<Keys::kAll>() == cudaSuccess && cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess ? n : 0;
+}
+
 namespace {
 
 // Joins the splits of the rows that they computed: an entry's (grid.y) first max_tokens tokens. All else keeps what it
@@ -126,6 +142,7 @@ bool kv_tmap(CUtensorMap* map, const fm_kv_cache& c, const void* base, bool deco
 
 struct Plan {
   int decode, alt, splits, split_tiles, ring, raw_ring;
+  int cluster;       // the tile kernel's splits that meet in their cluster (0: through the workspace)
   int64_t row_blocks;
   int rows_first;
   size_t smem, workspace;
@@ -162,6 +179,34 @@ int sm_count() {
   return v;
 }
 
+// Clusters of `size` CTAs (1 to 8) that run at once: fewer CTAs than alone, since a cluster stays inside of a group of SMs (of
+// the tile kernel, one CTA an SM, 76, 46, 36, 28, 23, 15 and 15 clusters of 2 to 8 on 152 SMs). kind: the kernel's variant.
+template <typename Query>
+int clusters_at_once(int kind, int size, int without, Query query) {
+  static std::atomic<int> cached[64][16][9];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+    cudaGetLastError();
+    return std::max(1, without / size);
+  }
+  int v = cached[dev][kind][size].load(std::memory_order_relaxed);
+  if (v) return v;
+  v = query();
+  if (v <= 0) {
+    cudaGetLastError();
+    v = std::max(1, without / size);
+  }
+  cached[dev][kind][size].store(v, std::memory_order_relaxed);
+  return v;
+}
+int tile_clusters_at_once(int size) {
+  return clusters_at_once(0, size, sm_count(), [=] { return tile_clusters(size); });
+}
+int decode_clusters_at_once(int Dh, bool f8, int rows, int size) {
+  const int kind = 1 + (Dh == 128) + 2 * f8 + 4 * (rows > 8);
+  return clusters_at_once(kind, size, sm_count() * decode_resident(Dh, f8, rows), [=] { return decode_clusters(Dh, f8, rows, size); });
+}
+
 // Keys that a CTA's tokens see together, and the tiles that they may lie in. With sinks the tokens are those of a block of
 // `rows` rows, with a window alone all of an entry.
 int64_t keys_of(const fm_kv_batch& b, int G, int rows, int window, int sinks) {
@@ -172,6 +217,9 @@ int64_t keys_of(const fm_kv_batch& b, int G, int rows, int window, int sinks) {
 int64_t tiles_of(int64_t keys, int tile, int window, int sinks) {
   return (keys + tile - 1) / tile + (window > 0) + (sinks > 0);
 }
+
+// Time of a CTA of the tile kernel, in units of 0.1 us as measured: its start and end, and its tiles.
+int64_t cta_time(bool f8, bool alt, int64_t tiles) { return (f8 ? 85 : 70) + tiles * (alt ? (f8 ? 15 : 8) : (f8 ? 18 : 14)); }
 
 // The number of splits of a batch's keys. window 0: the one that the workspace is sized for.
 int splits_of(const fm_kv_cache& c, const fm_kv_batch& b, int H, int window, int sinks) {
@@ -192,20 +240,19 @@ int splits_of(const fm_kv_cache& c, const fm_kv_batch& b, int H, int window, int
                                     : std::min<int64_t>(std::min<int64_t>(slots, 8), (tiles + 1) / 2);
     return static_cast<int>(std::max<int64_t>(1, want));
   }
-  // One CTA an SM: waves x (start and end + tiles x time of a tile), in units of 0.1 us as measured, with the join of
-  // splits (a kernel, and every share written and read) added. The number of splits with the least of it.
+  // One CTA an SM: waves x the time of a CTA, with the join of splits (a kernel, and every share written and read) added.
+  // The number of splits with the least of it.
   const bool alt = rows <= kTileRows;
   const int64_t block_rows = alt ? kTileRows : 2 * kTileRows;
   const int64_t units = std::max<int64_t>(1, (rows + block_rows - 1) / block_rows * c.Hkv * b.n);
   const int64_t tiles = tiles_of(keys_of(b, G, static_cast<int>(block_rows), window, sinks), kTileRows, window, sinks);
-  const int64_t fixed = f8 ? 85 : 70, each = alt ? (f8 ? 15 : 8) : (f8 ? 18 : 14);
   int64_t best = 0, splits = 1;
   // entries x splits are a dimension of the grid
   const int64_t most = std::min<int64_t>({64, std::max<int64_t>(1, tiles / 2), std::max(1, 65535 / std::max(1, b.n))});
   for (int64_t s = 1; s <= most; ++s) {
     const int64_t waves = (units * s + sms - 1) / sms;
     const int64_t shares = s * b.tokens * H * c.Dh * 8;   // bytes, at 4 TB/s: 4e5 bytes in 0.1 us
-    const int64_t cost = waves * (fixed + (tiles + s - 1) / s * each) + (s > 1 ? 25 + shares / 400000 : 0);
+    const int64_t cost = waves * cta_time(f8, alt, (tiles + s - 1) / s) + (s > 1 ? 25 + shares / 400000 : 0);
     if (s == 1 || cost < best) {
       best = cost;
       splits = s;
@@ -214,20 +261,62 @@ int splits_of(const fm_kv_cache& c, const fm_kv_batch& b, int H, int window, int
   return static_cast<int>(splits);
 }
 
+// Time of the join of a plan's splits, in units of 0.1 us: in the cluster by the rows of a CTA, else a second kernel and the
+// shares.
+int64_t join_time(const fm_kv_cache& c, const fm_kv_batch& b, int H, const Plan& pl) {
+  if (pl.splits == 1) return 0;
+  if (pl.cluster)
+    return 5 + std::min<int64_t>(pl.alt ? kTileRows : 2 * kTileRows, static_cast<int64_t>(b.max_tokens) * (H / c.Hkv)) * 17 / 100;
+  return 55 + static_cast<int64_t>(pl.splits) * b.tokens * H * c.Dh * 8 / 800000;
+}
+
+// Splits that meet in their cluster: up to 8, where the clusters take no more waves than CTAs alone would. A CTA reads its
+// rows' parts from the others' shared memory: about 5 us for 256 rows and 2.5 us for 128, against a second kernel and the
+// shares' way through L2, 4.5 us and more (6 entries x 20 tokens over 2000 keys, 6 heads of 64: 14.0 -> 10.2 us; 16 x 50 tokens
+// over 4100, 16 heads of 128: 41.6 -> 38.1 us). With first tokens the number of splits is chosen for it (1 x 100 tokens, window
+// 2000 + 100, 16 heads on 2: 36.4 us undivided, 22.1 in 4, 18.6 in 7); without them it stays what it is without a cluster.
+void cluster_of(const fm_kv_cache& c, const fm_kv_batch& b, int H, int64_t tiles, bool sinks, Plan& pl) {
+  const bool f8 = c.fmt == FM_FMT_FP8;
+  const int64_t units = std::max<int64_t>(1, pl.row_blocks * c.Hkv * b.n);
+  const auto waves = [](int64_t n, int64_t at_once) { return (n + at_once - 1) / at_once; };
+  const auto time = [&](int s) { return cta_time(f8, pl.alt, (tiles + s - 1) / s); };   // 0.1 us
+  if (!sinks) {
+    if (pl.splits > 1 && pl.splits <= 8 && waves(units, tile_clusters_at_once(pl.splits)) <= waves(units * pl.splits, sm_count()))
+      pl.cluster = pl.splits;
+    return;
+  }
+  int64_t best = waves(units * pl.splits, sm_count()) * time(pl.splits) + join_time(c, b, H, pl);
+  Plan with = pl;
+  for (int s = 2; s <= std::min<int64_t>(8, tiles) && static_cast<int64_t>(b.n) * s <= 65535; ++s) {
+    with.splits = with.cluster = s;
+    const int64_t cost = waves(units, tile_clusters_at_once(s)) * time(s) + join_time(c, b, H, with);
+    if (cost >= best) continue;
+    best = cost;
+    pl = with;
+  }
+}
+
 // The variant for a batch, by its bounds and the number of SMs alone. A window, which the workspace query does not
-// know, only lowers the number of splits.
-Plan plan_of(const fm_kv_cache& c, const fm_kv_batch& b, int H, int window, int sinks) {
+// know, only lowers the number of splits. meet: the tile kernel's splits may meet in clusters; fm_paged_attention keeps to its
+// workspace.
+Plan plan_of(const fm_kv_cache& c, const fm_kv_batch& b, int H, int window, int sinks, bool meet) {
   Plan pl = {};
   const int64_t rows = static_cast<int64_t>(b.max_tokens) * (H / c.Hkv);
   pl.splits = splits_of(c, b, H, 0, 0);
   if (window > 0) pl.splits = std::min(pl.splits, splits_of(c, b, H, window, sinks));
   pl.decode = rows <= kDecodeRows;
+  if (pl.decode && sinks > 0 && pl.splits > 1 && pl.splits <= 8) {
+    // where the clusters do not all run at once, fewer splits (48 units of 6: 32 us in two waves, 22 us of 5)
+    const int64_t units = static_cast<int64_t>(c.Hkv) * b.n;
+    while (pl.splits > 1 && units > decode_clusters_at_once(c.Dh, c.fmt == FM_FMT_FP8, static_cast<int>(rows), pl.splits)) --pl.splits;
+  }
   if (!pl.decode) {
     pl.alt = rows <= kTileRows;
     const int block_rows = pl.alt ? kTileRows : 2 * kTileRows;
     const int64_t tiles = tiles_of(keys_of(b, H / c.Hkv, block_rows, window, sinks), kTileRows, window, sinks);
-    pl.split_tiles = static_cast<int>((tiles + pl.splits - 1) / pl.splits);
     pl.row_blocks = (rows + block_rows - 1) / block_rows;
+    if (meet) cluster_of(c, b, H, tiles, sinks > 0, pl);
+    pl.split_tiles = static_cast<int>((tiles + pl.splits - 1) / pl.splits);
     // Where most of a sequence is new, a row block's place decides its keys, and CTAs start in the order of their work,
     // row blocks outermost, so that short ones fill the last wave (2048 tokens, 32 heads on 8 KV heads: 50.5 us with heads
     // outermost, 37.2 us; 4 x 2048 tokens of 16 on 2: 80.1 and 72.5 us). Else heads and entries are outermost: the entry's
@@ -235,7 +324,7 @@ Plan plan_of(const fm_kv_cache& c, const fm_kv_batch& b, int H, int window, int 
     pl.rows_first = pl.splits == 1 && 2 * static_cast<int64_t>(b.max_tokens) >= b.max_len && pl.row_blocks <= 65535;
     rings_of(c, pl);
   }
-  if (pl.splits > (pl.decode ? 8 : 1))
+  if (pl.splits > (pl.decode ? 8 : 1) && !pl.cluster)
     pl.workspace = static_cast<size_t>(pl.splits) * b.tokens * H * (c.Dh * sizeof(float) + sizeof(float2));
   return pl;
 }
@@ -358,6 +447,7 @@ void use_plan(const Plan& pl, AttnParams& p) {
   p.rows_first = pl.rows_first;
   p.splits = pl.splits;
   p.split_tiles = pl.split_tiles;
+  p.cluster = pl.cluster;
   p.ring = pl.ring;
   p.raw_ring = pl.raw_ring;
 }
@@ -367,7 +457,9 @@ cudaError_t launch_tiles(const Call& a, const Plan& pl, int n, const AttnParams&
                          const LaunchOpts& o) {
   const unsigned blocks = static_cast<unsigned>(pl.row_blocks), entries = static_cast<unsigned>(n * pl.splits);
   const dim3 grid = pl.rows_first ? dim3(a.c->Hkv, entries, blocks) : dim3(blocks, a.c->Hkv, entries);
-  return tile_launch<K>(p, a.c->Dh, a.c->fmt == FM_FMT_FP8, tk, tv, grid, pl.smem, o);
+  LaunchOpts opts = o;
+  if (pl.cluster > 1) opts.cluster = dim3(1, 1, pl.cluster);
+  return tile_launch<K>(p, a.c->Dh, a.c->fmt == FM_FMT_FP8, tk, tv, grid, pl.smem, opts);
 }
 
 cudaError_t launch_join(const Call& a, const AttnParams& p, const LaunchOpts& o) {
@@ -387,7 +479,7 @@ LaunchOpts opts_of(const Call& a) {
 }
 
 template <Keys K>
-int attend(const Call& a, int window, int sinks) {
+int attend(const Call& a, int window, int sinks, bool meet) {
   int st = check_call(a);
   if (st != FM_OK) return st;
   if (window < 0) return record_error(FM_ERR_INVALID_ARG, "window must be 0 (none) or positive");
@@ -395,7 +487,7 @@ int attend(const Call& a, int window, int sinks) {
   st = check_tensors(a);
   if (st != FM_OK) return st;
   const fm_kv_batch b = bounded_batch(*a.b);
-  const Plan pl = plan_of(*a.c, b, a.H, window, sinks);
+  const Plan pl = plan_of(*a.c, b, a.H, window, sinks, meet);
   st = check_workspace(a, pl.workspace, "workspace smaller than fm_paged_attention_workspace_size()");
   if (st != FM_OK) return st;
   CUtensorMap tk, tv;
@@ -435,9 +527,11 @@ struct SharedPlan {
   size_t workspace;
 };
 
-// A tile of 64 keys in the kernel for few rows, in units of 0.01 us: bf16 waits for its bytes however many CTAs share an SM.
-int64_t decode_each(bool f8, int resident, int64_t ctas, int sms) {
-  return f8 ? 30 + 20 * std::min<int64_t>(resident, (ctas + sms - 1) / sms) : 55;
+// A tile of 64 keys in the kernel for few rows, in units of 0.01 us: bf16 waits for its bytes however many CTAs share an SM,
+// E4M3 with 16 rows for its own instructions.
+int64_t decode_each(bool f8, int rows, int resident, int64_t ctas, int sms) {
+  if (!f8) return rows <= 8 ? 55 : 60;
+  return rows <= 8 ? 30 + 20 * std::min<int64_t>(resident, (ctas + sms - 1) / sms) : 110;
 }
 
 // Time of a batch without groups, in units of 0.1 us as splits_of takes it, from the same measurements.
@@ -449,11 +543,10 @@ int64_t cost_alone(const fm_kv_cache& c, const fm_kv_batch& b, int H, const Plan
     const int64_t ctas = static_cast<int64_t>(c.Hkv) * b.n * pl.splits, tiles = (len + kDecodeKeys - 1) / kDecodeKeys;
     const int resident = decode_resident(c.Dh, f8, static_cast<int>(rows));
     const int64_t waves = (ctas + static_cast<int64_t>(sms) * resident - 1) / (static_cast<int64_t>(sms) * resident);
-    return (rows <= 8 ? 55 : 65) + waves * ((tiles + pl.splits - 1) / pl.splits) * decode_each(f8, resident, ctas, sms) / 10 + (pl.splits > 8 ? 25 : 0);
+    return (rows <= 8 ? 55 : 65) + waves * ((tiles + pl.splits - 1) / pl.splits) * decode_each(f8, static_cast<int>(rows), resident, ctas, sms) / 10 + (pl.splits > 8 ? 25 : 0);
   }
-  const int64_t fixed = f8 ? 85 : 70, each = pl.alt ? (f8 ? 15 : 8) : (f8 ? 18 : 14);
-  const int64_t ctas = pl.row_blocks * c.Hkv * b.n * pl.splits, shares = static_cast<int64_t>(pl.splits) * b.tokens * H * c.Dh * 8;
-  return (ctas + sms - 1) / sms * (fixed + pl.split_tiles * each) + (pl.splits > 1 ? 25 + shares / 400000 : 0);
+  const int64_t ctas = pl.row_blocks * c.Hkv * b.n * pl.splits;
+  return (ctas + sms - 1) / sms * cta_time(f8, pl.alt, pl.split_tiles) + join_time(c, b, H, pl);
 }
 
 // Two kernels in a row cost 11 to 13 us with nothing to do, one 6 to 7, so sharing pays where entries x shared tokens are
@@ -464,7 +557,7 @@ SharedPlan shared_plan(const fm_kv_cache& c, const fm_kv_batch& b, const fm_kv_g
   SharedPlan sp = {};
   const int G = H / c.Hkv, sms = sm_count();
   const bool f8 = c.fmt == FM_FMT_FP8;
-  const Plan alone = plan_of(c, b, H, 0, 0);
+  const Plan alone = plan_of(c, b, H, 0, 0, true);
   sp.workspace = alone.workspace;
   sp.tokens = static_cast<int>(std::min<int64_t>(b.tokens, static_cast<int64_t>(g.max_entries) * b.max_tokens));
   const int64_t rows = static_cast<int64_t>(sp.tokens) * G, entry_rows = static_cast<int64_t>(b.max_tokens) * G;
@@ -477,7 +570,6 @@ SharedPlan shared_plan(const fm_kv_cache& c, const fm_kv_batch& b, const fm_kv_g
   const int64_t packed = static_cast<int64_t>(b.tokens) * G;
   const int64_t units = c.Hkv * std::min(pre.row_blocks * g.n, packed / block_rows + g.n);
   const int64_t tiles = (static_cast<int64_t>(g.max_shared) + kTileRows - 1) / kTileRows;
-  const int64_t fixed = f8 ? 85 : 70, each = pre.alt ? (f8 ? 15 : 8) : (f8 ? 18 : 14);
   const int block = entry_rows <= 8 ? 8 : kDecodeRows;
   const int64_t own_units = c.Hkv * std::min(b.n * ((entry_rows + block - 1) / block), packed / block + b.n);
   const int64_t own_tiles = (std::max<int64_t>({1, b.max_tokens, int64_t(b.max_len) - g.max_shared}) + kDecodeKeys - 1) / kDecodeKeys + 1;
@@ -492,10 +584,10 @@ SharedPlan shared_plan(const fm_kv_cache& c, const fm_kv_batch& b, const fm_kv_g
     const int64_t longest = (tiles + s - 1) / s;
     if (s > 1 && longest == (tiles + s - 2) / (s - 1)) continue;   // no shorter than with fewer
     const int64_t ctas = units * s, waves = (ctas + sms - 1) / sms, shares = s * b.tokens * H * c.Dh * 8;
-    const int64_t prefix = waves * (fixed + longest * each) + shares / 400000 + s * 6 / 10;
+    const int64_t prefix = waves * cta_time(f8, pre.alt, longest) + shares / 400000 + s * 6 / 10;
     const int64_t room = (waves * sms - ctas) * resident;
     for (int k = 1; k <= 8 && 2 * k <= own_tiles + 2; k *= 2) {   // own keys' splits: whole clusters find room
-      const int64_t own = 55 + (own_tiles + k - 1) / k * decode_each(f8, resident, own_units * k, sms) / 10, left = std::max<int64_t>(0, own_units * k - room);
+      const int64_t own = 55 + (own_tiles + k - 1) / k * decode_each(f8, block, resident, own_units * k, sms) / 10, left = std::max<int64_t>(0, own_units * k - room);
       const int64_t cost = std::max(prefix, own) + 35 + (left + sms * resident - 1) / (sms * resident) * own;
       if (best == 0 || cost < best) {
         best = cost;
@@ -504,7 +596,7 @@ SharedPlan shared_plan(const fm_kv_cache& c, const fm_kv_batch& b, const fm_kv_g
       }
     }
   }
-  if (best * 11 / 10 >= cost_alone(c, b, H, alone)) return sp;
+  if (best * 11 / 10 >= cost_alone(c, b, H, alone)) return sp;   // 10 % that the estimate may be off
   pre.split_tiles = static_cast<int>((tiles + pre.splits - 1) / pre.splits);
   rings_of(c, pre);
   sp.split = true;
@@ -521,7 +613,7 @@ int attend_shared(const Call& a, const fm_kv_groups* g) {
   if (st != FM_OK) return st;
   const fm_kv_batch b = bounded_batch(*a.b);
   const SharedPlan sp = shared_plan(*a.c, b, *g, a.H);
-  if (!sp.split) return attend<Keys::kAll>(a, 0, 0);
+  if (!sp.split) return attend<Keys::kAll>(a, 0, 0, true);
   st = check_workspace(a, sp.workspace, "workspace smaller than fm_shared_attention_workspace_size()");
   if (st != FM_OK) return st;
   CUtensorMap tk, tv, ok, ov;
@@ -555,7 +647,7 @@ extern "C" int fm_paged_attention_workspace_size(const fm_kv_cache* c, const fm_
   if (!bytes) return fm::record_error(FM_ERR_INVALID_ARG, "bytes is NULL");
   const int st = fm::check(c, b, H);
   if (st != FM_OK) return st;
-  *bytes = b->n && b->tokens ? fm::plan_of(*c, fm::bounded_batch(*b), H, 0, 0).workspace : 0;
+  *bytes = b->n && b->tokens ? fm::plan_of(*c, fm::bounded_batch(*b), H, 0, 0, false).workspace : 0;
   return FM_OK;
 }
 
@@ -563,7 +655,7 @@ extern "C" int fm_paged_attention(const fm_kv_cache* c, int layer, const fm_kv_b
                                   int64_t q_stride, int H, float scale, int causal, int window, uint16_t* out,
                                   int64_t out_stride, void* workspace, size_t workspace_bytes, void* stream) {
   return fm::attend<fm::Keys::kAll>({c, layer, b, q, q_stride, H, scale, causal, out, out_stride, workspace, workspace_bytes, stream},
-                                    window, 0);
+                                    window, 0, false);
 }
 
 extern "C" int fm_sink_attention(const fm_kv_cache* c, int layer, const fm_kv_batch* b, const uint16_t* q, int64_t q_stride,
@@ -573,7 +665,7 @@ extern "C" int fm_sink_attention(const fm_kv_cache* c, int layer, const fm_kv_ba
   if (sinks < 0) return record_error(FM_ERR_INVALID_ARG, "sinks must not be negative");
   const Call a{c, layer, b, q, q_stride, H, scale, causal, out, out_stride, workspace, workspace_bytes, stream};
   // without a window nothing is hidden, without first tokens nothing is kept: the same attention in one stretch of keys
-  return window <= 0 || sinks == 0 ? attend<Keys::kAll>(a, window, 0) : attend<Keys::kSinks>(a, window, sinks);
+  return window <= 0 || sinks == 0 ? attend<Keys::kAll>(a, window, 0, false) : attend<Keys::kSinks>(a, window, sinks, true);
 }
 
 extern "C" int fm_shared_attention_workspace_size(const fm_kv_cache* c, const fm_kv_batch* b, const fm_kv_groups* g, int H,

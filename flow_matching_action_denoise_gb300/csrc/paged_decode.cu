@@ -15,4 +15,29 @@ int decode_resident(int Dh, bool f8, int rows) {
                    : (f8 ? kResident<64, true, 2> : kResident<64, false, 2>);
 }
 
+int decode_clusters(int Dh, bool f8, int rows, int size) {
+  const auto query = [size](auto kernel, size_t smem) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(size);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = size;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    int n = 0;
+    return cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess ? n : 0;
+  };
+  if (decode_configure<Keys::kAll>() != cudaSuccess) return 0;
+  constexpr Keys K = Keys::kAll;
+  if (rows <= 8) {
+    if (Dh == 128) return f8 ? query(decode_kernel<128, true, 1, K>, smem_bytes<128, true, 1>()) : query(decode_kernel<128, false, 1, K>, smem_bytes<128, false, 1>());
+    return f8 ? query(decode_kernel<64, true, 1, K>, smem_bytes<64, true, 1>()) : query(decode_kernel<64, false, 1, K>, smem_bytes<64, false, 1>());
+  }
+  if (Dh == 128) return f8 ? query(decode_kernel<128, true, 2, K>, smem_bytes<128, true, 2>()) : query(decode_kernel<128, false, 2, K>, smem_bytes<128, false, 2>());
+  return f8 ? query(decode_kernel<64, true, 2, K>, smem_bytes<64, true, 2>()) : query(decode_kernel<64, false, 2, K>, smem_bytes<64, false, 2>());
+}
+
 }  // namespace fm

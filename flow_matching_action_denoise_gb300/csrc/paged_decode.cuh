@@ -427,9 +427,10 @@ __global__ void __launch_bounds__(kThreads, kResident<DH, F8, NT>)
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
           // no keys: no share. A NaN in the query has no maximum either, but its sum is NaN
-          const float w = ml[i].x == -INFINITY && ml[i].y == 0.f ? 0.f : ex2_approx(ml[i].x - top);
-          s_w[row][lane + 32 * i] = w;
-          l += ml[i].y * w;
+          const bool none = ml[i].x == -INFINITY && ml[i].y == 0.f;
+          const float w = ex2_approx(ml[i].x - top);
+          s_w[row][lane + 32 * i] = none ? -1.0f : w;   // behind the last one, too
+          if (!none) l += ml[i].y * w;
         }
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
@@ -458,9 +459,9 @@ __global__ void __launch_bounds__(kThreads, kResident<DH, F8, NT>)
           float w[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            w[i] = s_w[row][s0 + i];   // 0 behind the last one
+            w[i] = s_w[row][s0 + i];
             v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (w[i] != 0.f) v[i] = *reinterpret_cast<const float4*>(p.part_o + ((s0 + i) * rows_of + at) * DH + d);
+            if (!(w[i] < 0.f)) v[i] = *reinterpret_cast<const float4*>(p.part_o + ((s0 + i) * rows_of + at) * DH + d);
           }
 #pragma unroll
           for (int i = 0; i < 8; ++i) sum4.x += v[i].x * w[i], sum4.y += v[i].y * w[i], sum4.z += v[i].z * w[i], sum4.w += v[i].w * w[i];

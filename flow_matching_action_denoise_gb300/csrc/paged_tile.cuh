@@ -10,8 +10,8 @@
 // Two softmax warpgroups share the CTA. With more than 128 rows each owns a 128-row tile and both use every
 // key tile; with up to 128 rows they own alternate key tiles of the same rows and merge at the end
 // (`alt`), so that few rows keep two tiles in flight too (up to 16 rows have a kernel of their own). While one warpgroup exponentiates, the tensor cores
-// work for the other. A long key axis with few rows is cut into splits of whole tiles, one CTA each, whose
-// (max, sum, O) go to the workspace and are joined in split order by combine_kernel.
+// work for the other. A long key axis with few rows is cut into splits of whole tiles, one CTA each, whose (max, sum, O)
+// meet in their cluster's shared memory (up to 8) or in the workspace, where combine_kernel joins them in split order.
 //
 // Pages. One warp reads the page table and moves every page's rows by TMA straight into the swizzled tile the
 // tensor cores read: values stay [token][head dim] and are read as an MN-major operand, so the cache needs no
@@ -40,6 +40,7 @@
 #include <cuda_fp16.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "internal.h"
 #include "kv.h"
@@ -109,6 +110,11 @@ __device__ __forceinline__ uint32_t swz(int r, int c) {   // 16-byte chunk c of 
   return static_cast<uint32_t>(r * 128 + ((c ^ (r & 7)) << 4));
 }
 
+// Every thread of the cluster: what one wrote before, in its shared memory, all can read behind.
+__device__ __forceinline__ void cluster_meet() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 struct Ctl {   // shared-memory control block
   uint64_t full[kMaxRing], empty[kMaxRing], rfull[kMaxRing], rempty[kMaxRing];
   uint64_t q_ready, s_full[2], p_full[2], o_done[2], turn[2], tail, drain[2];
@@ -117,7 +123,9 @@ struct Ctl {   // shared-memory control block
 };
 static_assert(sizeof(Ctl) <= kCtlBytes, "control block");
 
-template <int DH, bool F8, Keys K>
+// JOIN: the splits (p.cluster of them) meet in their cluster; as a variant of its own, since the join's registers cost all others
+// 3 to 5 % with an E4M3 cache.
+template <int DH, bool F8, Keys K, bool JOIN>
 __global__ void __launch_bounds__(threads_of(F8), 1)
     paged_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v) {
@@ -174,7 +182,7 @@ __global__ void __launch_bounds__(threads_of(F8), 1)
   // ---- the entry, its rows and its keys (the same in every thread)
   const bool report = tid == 0 && row_block == 0 && g == 0 && split == 0;
   const Entry en = K == Keys::kPrefix ? group_of(p, entry, report) : entry_of(p, entry, report);
-  const bool shares = K == Keys::kPrefix || p.splits > 1;   // the results go to the workspace
+  const bool shares = !JOIN && (K == Keys::kPrefix || p.splits > 1);   // the results go to the workspace
   const int begin = en.begin, nq = en.nq, len = en.len, sid = en.sid;
   const int rows = min(nq, K == Keys::kPrefix ? p.g_tokens : p.max_tokens) * p.G;   // <= 2^30
   const int row0 = row_block * block_rows;
@@ -220,6 +228,7 @@ __global__ void __launch_bounds__(threads_of(F8), 1)
   const int n_keys = p.alt ? nt : max(n_of[0], n_of[1]);
   const int tail_tile = len % kTileRows ? places.place(len / kTileRows) - t_lo : -1;   // the tile that the length ends in
 
+  [[maybe_unused]] float2* const cluster_ml = reinterpret_cast<float2*>(sq);   // JOIN: (log2 maximum, sum) of the rows, when the queries have been used
   const uint32_t ring_a = smem_u32(sring), raw_a = smem_u32(sraw), q_a = smem_u32(sq);
 
   // ---- the TMA warp's copies: one call moves the next key or value tile, a box for the rows of each page (at most
@@ -502,8 +511,9 @@ __global__ void __launch_bounds__(threads_of(F8), 1)
     __syncwarp();
     if (!ok && lane == 0) atomicOr(p.err, kErrPipelineTimeout);
     const float vs = F8 ? *p.v_scale : 1.0f;
-    float* join = reinterpret_cast<float*>(sring);                        // [128][DH], chunks swizzled by row
+    float* join = reinterpret_cast<float*>(sring);   // [128 or, for the cluster, 256][DH], chunks swizzled by row
     float2* join_ml = reinterpret_cast<float2*>(sring + kTileRows * DH * 4);
+    if (JOIN && !p.alt) asm volatile("bar.sync 1, 256;" ::: "memory");   // the other tile's products, too, have read the ring
     auto load_o = [&](int b, float* o) {   // 32 of this row's sums
       if (n > 0) {
         tmem_ld32_async(t_o + b, o);
@@ -539,8 +549,12 @@ __global__ void __launch_bounds__(threads_of(F8), 1)
         m2 = top;
       }
       const int64_t split_row = static_cast<int64_t>(split) * p.tokens * p.H;
-      if (shares) {
-        if (live) p.part_ml[split_row + static_cast<int64_t>(begin + row / p.G) * p.H + g * p.G + row % p.G] = make_float2(m2, sum);
+      if (JOIN || shares) {
+        const float2 ml = make_float2(m2, sum);
+        if (JOIN)
+          cluster_ml[row - row0] = ml;
+        else if (live)
+          p.part_ml[split_row + static_cast<int64_t>(begin + row / p.G) * p.H + g * p.G + row % p.G] = ml;
         w0 *= vs;
         w1 *= vs;
       } else {
@@ -551,7 +565,25 @@ __global__ void __launch_bounds__(threads_of(F8), 1)
       // TMEM gives a lane one row: rows are staged in the query tile's 32 rows of this warp (its last reader has
       // completed) and leave kRowChunks lanes a row, whole 16-byte chunks. fp32 shares take two passes.
       const uint32_t stage = q_a + (p.alt ? 0 : t * kTileBytes) + wq * 32 * DH * 2;
-      const int passes = !shares ? 1 : nt > 0 ? 2 : 0;
+      const int passes = JOIN ? 0 : !shares ? 1 : nt > 0 ? 2 : 0;
+      if (JOIN && nt > 0) {   // this CTA's part of the rows, for the cluster
+        const int x0 = row - row0;
+#pragma unroll 1
+        for (int b = 0; b < DH; b += 32) {
+          float o[32];
+          load_o(b, o);
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            float4* at = reinterpret_cast<float4*>(join + x0 * DH + ((((b + e) >> 2) ^ (r & 7)) << 2));
+            float4 x = make_float4(o[e] * w0, o[e + 1] * w0, o[e + 2] * w0, o[e + 3] * w0);
+            if (p.alt) {
+              const float4 y = *at;
+              x = make_float4(o[e] * w0 + y.x * w1, o[e + 1] * w0 + y.y * w1, o[e + 2] * w0 + y.z * w1, o[e + 3] * w0 + y.w * w1);
+            }
+            *at = x;
+          }
+        }
+      }
 #pragma unroll 1
       for (int pass = 0; pass < passes; ++pass) {
         const int dims = shares ? DH / 2 : DH, d0 = pass * dims;
@@ -607,6 +639,88 @@ __global__ void __launch_bounds__(threads_of(F8), 1)
         }
         __syncwarp();
       }
+    }
+    if constexpr (JOIN) {
+      // ---- the cluster's splits are joined in split order, with the arithmetic of combine_kernel: rows go round the CTAs, 8 kPer
+      // of them a step, a warp kPer at a time; R steps' loads from S splits are on their way together
+      __syncwarp();
+      cluster_meet();
+      constexpr int kRowLanes = DH / 4, kPer = 32 / kRowLanes;
+      const int rank = cluster_rank(), chunk = lane % kRowLanes, cs = p.cluster, n_rows = last_row - row0 + 1;
+      const uint32_t o_a = smem_u32(sring), ml_a = smem_u32(cluster_ml);
+      auto join_rows = [&](auto r_, auto s_) {
+        constexpr int R = decltype(r_)::value, S = decltype(s_)::value;
+        for (int base = (rank * 8 + warp) * kPer + lane / kRowLanes; base < n_rows; base += R * cs * 8 * kPer) {
+          float2 ml[R][S];
+          float w[R][S];
+          float4 v[R][S];
+#pragma unroll
+          for (int i = 0; i < R; ++i) {
+            const int x = base + i * cs * 8 * kPer;
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+              ml[i][s] = make_float2(-INFINITY, 0.f);
+              if (s < cs && x < n_rows)
+                asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+                             : "=f"(ml[i][s].x), "=f"(ml[i][s].y)
+                             : "r"(map_dsmem(ml_a + x * 8, s)));
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < R; ++i) {
+            const int x = base + i * cs * 8 * kPer;
+            float top = -INFINITY;
+#pragma unroll
+            for (int s = 0; s < S; ++s) top = fmaxf(top, ml[i][s].x);
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+              // no keys: no share. A NaN in the query has no maximum either, but its sum is NaN and so is the row
+              const bool none = ml[i][s].x == -INFINITY && ml[i][s].y == 0.f;
+              w[i][s] = none ? 0.f : exp2f(ml[i][s].x - top);
+              v[i][s] = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (!none)
+                asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                             : "=f"(v[i][s].x), "=f"(v[i][s].y), "=f"(v[i][s].z), "=f"(v[i][s].w)
+                             : "r"(map_dsmem(o_a + x * DH * 4 + ((chunk ^ (x & 7)) << 4), s)));
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < R; ++i) {
+            const int x = base + i * cs * 8 * kPer;
+            // four splits in a row, more by turns in two sums
+            constexpr int kSums = S > 4 ? 2 : 1;
+            float sum[2] = {0.f, 0.f};
+            float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+              float4& a = acc[s % kSums];
+              sum[s % kSums] = fmaf(ml[i][s].y, w[i][s], sum[s % kSums]);
+              a = make_float4(fmaf(w[i][s], v[i][s].x, a.x), fmaf(w[i][s], v[i][s].y, a.y), fmaf(w[i][s], v[i][s].z, a.z),
+                              fmaf(w[i][s], v[i][s].w, a.w));
+            }
+            if constexpr (kSums == 2) {
+              sum[0] += sum[1];
+              acc[0] = make_float4(acc[0].x + acc[1].x, acc[0].y + acc[1].y, acc[0].z + acc[1].z, acc[0].w + acc[1].w);
+            }
+            if (x >= n_rows) continue;
+            const int in_entry = row0 + x, tok = in_entry / p.G;
+            const int64_t token = begin + tok;
+            const int head = g * p.G + in_entry - tok * p.G;
+            const float inv = sum[0] == 0.f ? 0.f : 1.0f / sum[0];
+            *reinterpret_cast<uint2*>(p.out + token * p.out_stride + head * DH + chunk * 4) =
+                make_uint2(pack16<false>(acc[0].x * inv, acc[0].y * inv), pack16<false>(acc[0].z * inv, acc[0].w * inv));
+          }
+        }
+      };
+      using std::integral_constant;
+      if (cs <= 2)
+        join_rows(integral_constant<int, 4>{}, integral_constant<int, 2>{});
+      else if (cs <= 4)
+        join_rows(integral_constant<int, 2>{}, integral_constant<int, 4>{});
+      else
+        join_rows(integral_constant<int, 1>{}, integral_constant<int, 8>{});
+      __syncwarp();
+      cluster_meet();   // no CTA leaves while another still reads its part
     }
   } else if (warp < kTmaWarp) {
     // ================================================= tensor cores, a warp for each tile
@@ -802,6 +916,10 @@ __global__ void __launch_bounds__(threads_of(F8), 1)
     if (!ok && lane == 0) atomicOr(p.err, kErrPipelineTimeout);
   }
   __syncwarp();
+  if (JOIN && warp >= 8) {   // the softmax warps' two meetings
+    cluster_meet();
+    cluster_meet();
+  }
   tc_fence_before();
   __syncthreads();
   if (warp == kMmaWarp) {
@@ -810,27 +928,36 @@ __global__ void __launch_bounds__(threads_of(F8), 1)
   }
 }
 
-template <int DH, bool F8, Keys K>
-cudaError_t configure_tile() {
-  return cudaFuncSetAttribute(paged_attn_kernel<DH, F8, K>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit + 1024);
+using TileKernel = void (*)(AttnParams, CUtensorMap, CUtensorMap);
+
+template <Keys K, bool JOIN>
+TileKernel tile_kernel(int Dh, bool f8) {
+  return Dh == 128 ? (f8 ? paged_attn_kernel<128, true, K, JOIN> : paged_attn_kernel<128, false, K, JOIN>)
+                   : (f8 ? paged_attn_kernel<64, true, K, JOIN> : paged_attn_kernel<64, false, K, JOIN>);
 }
 
 }  // namespace
 
+// a prefix's shares are not joined here
+template <Keys K>
+constexpr bool kMayJoin = K != Keys::kPrefix;
+
 template <Keys K>
 cudaError_t tile_configure() {
-  cudaError_t e = configure_tile<64, false, K>();
-  if (e == cudaSuccess) e = configure_tile<128, false, K>();
-  if (e == cudaSuccess) e = configure_tile<64, true, K>();
-  if (e == cudaSuccess) e = configure_tile<128, true, K>();
+  cudaError_t e = cudaSuccess;
+  for (const int x : {0, 1, 2, 3})
+    for (const bool join : {false, true}) {
+      if (e != cudaSuccess || (join && !kMayJoin<K>)) continue;
+      const auto kernel = join ? tile_kernel<K, kMayJoin<K>>(x & 1 ? 128 : 64, x & 2) : tile_kernel<K, false>(x & 1 ? 128 : 64, x & 2);
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit + 1024);
+    }
   return e;
 }
 
 template <Keys K>
 cudaError_t tile_launch(const AttnParams& p, int Dh, bool f8, const CUtensorMap& tk, const CUtensorMap& tv, dim3 grid,
                         size_t smem, const LaunchOpts& o) {
-  auto kernel = Dh == 128 ? (f8 ? paged_attn_kernel<128, true, K> : paged_attn_kernel<128, false, K>)
-                          : (f8 ? paged_attn_kernel<64, true, K> : paged_attn_kernel<64, false, K>);
+  const auto kernel = p.cluster > 1 ? tile_kernel<K, kMayJoin<K>>(Dh, f8) : tile_kernel<K, false>(Dh, f8);
   return launch(kernel, grid, dim3(threads_of(f8)), smem, o, p, tk, tv);
 }
 
