@@ -63,6 +63,7 @@ cudaError_t decode_launch(const AttnParams& p, int Dh, bool f8, const CUtensorMa
 template <Keys K>
 cudaError_t decode_configure();
 int decode_resident(int Dh, bool f8, int rows);   // CTAs of it on an SM at once
+int own_resident(int Dh, bool f8, int rows);      // the same of Keys::kOwn
 int decode_clusters(int Dh, bool f8, int rows, int size);   // clusters of so many of its CTAs at once
 
 // An entry of the batch; one that is out of range has no tokens and no keys.

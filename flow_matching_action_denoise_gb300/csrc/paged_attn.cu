@@ -573,7 +573,8 @@ SharedPlan shared_plan(const fm_kv_cache& c, const fm_kv_batch& b, const fm_kv_g
   const int block = entry_rows <= 8 ? 8 : kDecodeRows;
   const int64_t own_units = c.Hkv * std::min(b.n * ((entry_rows + block - 1) / block), packed / block + b.n);
   const int64_t own_tiles = (std::max<int64_t>({1, b.max_tokens, int64_t(b.max_len) - g.max_shared}) + kDecodeKeys - 1) / kDecodeKeys + 1;
-  const int resident = decode_resident(c.Dh, f8, block);
+  const int resident = own_resident(c.Dh, f8, block);
+  const bool fewer_stages = resident > decode_resident(c.Dh, f8, block);
   if (c.Hkv > 8191) return sp;   // x blocks of an entry's rows are a dimension of the grid
   // The least of max(prefix, own keys) + the join + what of the second kernel finds no SM beside the first: its CTAs stay
   // until the prefix's shares are there, and those left over take their whole time behind it (8 us for 288 CTAs where 280
@@ -587,7 +588,8 @@ SharedPlan shared_plan(const fm_kv_cache& c, const fm_kv_batch& b, const fm_kv_g
     const int64_t prefix = waves * cta_time(f8, pre.alt, longest) + shares / 400000 + s * 6 / 10;
     const int64_t room = (waves * sms - ctas) * resident;
     for (int k = 1; k <= 8 && 2 * k <= own_tiles + 2; k *= 2) {   // own keys' splits: whole clusters find room
-      const int64_t own = 55 + (own_tiles + k - 1) / k * decode_each(f8, block, resident, own_units * k, sms) / 10, left = std::max<int64_t>(0, own_units * k - room);
+      const int64_t each = decode_each(f8, block, resident, own_units * k, sms) + (fewer_stages ? 20 : 0);
+      const int64_t own = 55 + (own_tiles + k - 1) / k * each / 10, left = std::max<int64_t>(0, own_units * k - room);
       const int64_t cost = std::max(prefix, own) + 35 + (left + sms * resident - 1) / (sms * resident) * own;
       if (best == 0 || cost < best) {
         best = cost;

@@ -33,11 +33,11 @@ int decode_clusters(int Dh, bool f8, int rows, int size) {
   if (decode_configure<Keys::kAll>() != cudaSuccess) return 0;
   constexpr Keys K = Keys::kAll;
   if (rows <= 8) {
-    if (Dh == 128) return f8 ? query(decode_kernel<128, true, 1, K>, smem_bytes<128, true, 1>()) : query(decode_kernel<128, false, 1, K>, smem_bytes<128, false, 1>());
-    return f8 ? query(decode_kernel<64, true, 1, K>, smem_bytes<64, true, 1>()) : query(decode_kernel<64, false, 1, K>, smem_bytes<64, false, 1>());
+    if (Dh == 128) return f8 ? query(decode_kernel<128, true, 1, K>, smem_bytes<128, true, 1, K>()) : query(decode_kernel<128, false, 1, K>, smem_bytes<128, false, 1, K>());
+    return f8 ? query(decode_kernel<64, true, 1, K>, smem_bytes<64, true, 1, K>()) : query(decode_kernel<64, false, 1, K>, smem_bytes<64, false, 1, K>());
   }
-  if (Dh == 128) return f8 ? query(decode_kernel<128, true, 2, K>, smem_bytes<128, true, 2>()) : query(decode_kernel<128, false, 2, K>, smem_bytes<128, false, 2>());
-  return f8 ? query(decode_kernel<64, true, 2, K>, smem_bytes<64, true, 2>()) : query(decode_kernel<64, false, 2, K>, smem_bytes<64, false, 2>());
+  if (Dh == 128) return f8 ? query(decode_kernel<128, true, 2, K>, smem_bytes<128, true, 2, K>()) : query(decode_kernel<128, false, 2, K>, smem_bytes<128, false, 2, K>());
+  return f8 ? query(decode_kernel<64, true, 2, K>, smem_bytes<64, true, 2, K>()) : query(decode_kernel<64, false, 2, K>, smem_bytes<64, false, 2, K>());
 }
 
 }  // namespace fm

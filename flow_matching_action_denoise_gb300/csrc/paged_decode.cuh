@@ -33,11 +33,16 @@ namespace fm {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kDepth = 3;   // stages of the ring
 // CTAs an SM of a variant, by shared memory (16-bit tiles of 128 dims are 32 KB; two stages and three CTAs were slower:
 // 28 us against 25 us for 32 sequences of 4096 keys) and registers.
 template <int DH, bool F8, int NT>
 constexpr int kResident = NT == 1 ? (F8 || DH == 64 ? 4 : 2) : (F8 || DH == 64 ? 3 : 2);
+// Keys::kOwn, 16-bit rows of 128 dims: that more CTAs find room beside the prefix's counts for more than each one's speed
+// (128 forks behind 8192 keys, 133 to 400 of their own: 29.1 -> 25.8 us).
+template <int DH, bool F8, int NT, Keys K>
+constexpr bool kMore = K == Keys::kOwn && NT == 1 && !F8 && DH == 128;
+template <int DH, bool F8, int NT, Keys K>
+constexpr int kStages = kMore<DH, F8, NT, K> ? 2 : 3;   // of the ring
 constexpr int kThreads = (kWarps + 1) * 32;
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
@@ -80,8 +85,9 @@ __device__ __forceinline__ uint32_t piece(int r, int c) {
 
 // NT: row tiles of eight.
 template <int DH, bool F8, int NT, Keys K>
-__global__ void __launch_bounds__(kThreads, kResident<DH, F8, NT>)
+__global__ void __launch_bounds__(kThreads, kResident<DH, F8, NT> + kMore<DH, F8, NT, K>)
     decode_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
+  constexpr int kDepth = kStages<DH, F8, NT, K>;
   constexpr int kRowBytes = F8 ? DH : 128;                 // bytes of a row in a block
   constexpr int kBlocks = F8 ? 1 : DH / 64;
   constexpr uint32_t kBlock = kDecodeKeys * kRowBytes;
@@ -540,9 +546,9 @@ __global__ void __launch_bounds__(kThreads, kResident<DH, F8, NT>)
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-template <int DH, bool F8, int NT>
+template <int DH, bool F8, int NT, Keys K>
 constexpr size_t smem_bytes() {
-  const size_t ring = static_cast<size_t>(kDepth) * 2 * kDecodeKeys * DH * (F8 ? 1 : 2);
+  const size_t ring = static_cast<size_t>(kStages<DH, F8, NT, K>) * 2 * kDecodeKeys * DH * (F8 ? 1 : 2);
   const size_t join = static_cast<size_t>(8 * NT) * (kWarps * (DH + 8) + DH) * 4;
   return 1024 + (ring > join ? ring : join);
 }
@@ -550,13 +556,13 @@ constexpr size_t smem_bytes() {
 template <int DH, bool F8, int NT, Keys K>
 cudaError_t configure_one() {
   return cudaFuncSetAttribute(decode_kernel<DH, F8, NT, K>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              static_cast<int>(smem_bytes<DH, F8, NT>()));
+                              static_cast<int>(smem_bytes<DH, F8, NT, K>()));
 }
 
 template <int DH, bool F8, int NT, Keys K>
 cudaError_t run(const AttnParams& p, const CUtensorMap& tk, const CUtensorMap& tv, const LaunchOpts& o) {
   const int blocks = K == Keys::kOwn ? (p.max_tokens * p.G + 8 * NT - 1) / (8 * NT) : 1;
-  return launch(decode_kernel<DH, F8, NT, K>, dim3(p.splits, p.Hkv * blocks, p.n), dim3(kThreads), smem_bytes<DH, F8, NT>(), o, p, tk, tv);
+  return launch(decode_kernel<DH, F8, NT, K>, dim3(p.splits, p.Hkv * blocks, p.n), dim3(kThreads), smem_bytes<DH, F8, NT, K>(), o, p, tk, tv);
 }
 
 template <int DH, bool F8, Keys K>

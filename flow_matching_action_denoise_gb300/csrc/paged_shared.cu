@@ -8,9 +8,9 @@
 // An entry's keys and values meet its own rows only: with the own keys of many entries in one tile of stacked rows a NaN in
 // one robot's values would reach all of them (0 x NaN). The second kernel starts once every CTA of the first is resident and
 // works beside it on what SMs are free; it waits for the first before the join.
-// 128 single tokens of 16 heads on 2 KV heads (Dh 128, bf16) behind 8192 common keys, 133 to 400 of their own: 29 us, 66 us as
-// separate sequences. Bound by the chain: 14 us of prefix (7 us of a CTA's ends), 8 us of own CTAs that found no SM beside
-// it, 3.5 us from the last share to the output.
+// 128 single tokens of 16 heads on 2 KV heads (Dh 128, bf16) behind 8192 common keys, 133 to 400 of their own: 25.8 us, 66 us as
+// separate sequences. Bound by the chain: 18 us of prefix (7 us of them a CTA's ends), beside which the own CTAs have to find
+// room (those that do not cost 8 us more, behind it), 3.5 us from the last share to the output.
 
 #include "paged_decode.cuh"
 #include "paged_tile.cuh"
@@ -23,5 +23,9 @@ template cudaError_t tile_configure<Keys::kPrefix>();
 template cudaError_t decode_launch<Keys::kOwn>(const AttnParams&, int, bool, const CUtensorMap&, const CUtensorMap&,
                                                const LaunchOpts&);
 template cudaError_t decode_configure<Keys::kOwn>();
+
+int own_resident(int Dh, bool f8, int rows) {
+  return decode_resident(Dh, f8, rows) + (Dh == 128 && !f8 && rows <= 8 ? kMore<128, false, 1, Keys::kOwn> : 0);
+}
 
 }  // namespace fm
