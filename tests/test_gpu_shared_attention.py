@@ -18,7 +18,7 @@ class Forks:
     """Sequences in groups: (shared tokens, [tokens behind them, one number an entry]). Whole shared pages are the first
     entry's, a begun one is a copy; what lies behind a length and on free pages is NaN."""
 
-    def __init__(self, groups, page, Hkv, Dh, fp8=False, heads_first=False, layers=1, seed=0, lone=()):
+    def __init__(self, groups, page, Hkv, Dh, fp8=False, heads_first=False, layers=1, seed=0, lone=(), in_order=False):
         g, rng = torch.Generator().manual_seed(seed), np.random.default_rng(seed + 1)
         self.page, self.fp8, self.first, self.shared, self.lens_host = page, fp8, [0], [], []
         lead = []
@@ -32,7 +32,7 @@ class Forks:
             self.lens_host.append(x)
         n = len(self.lens_host)
         pages = sum(up(x, page) - (s // page if i != j else 0) for i, (x, (j, s)) in enumerate(zip(self.lens_host, lead))) + 3
-        self.rows = list(rng.permutation(n + 2)[:n])
+        self.rows = list(range(n)) if in_order else list(rng.permutation(n + 2)[:n])
         order = list(rng.permutation(pages))
         table = np.full((n + 2, max(up(x, page) for x in self.lens_host) + 2), -1, np.int32)
         lens, keep, begun = np.zeros(n + 2, np.int32), torch.zeros((pages, page), dtype=torch.bool), []
@@ -173,6 +173,17 @@ def test_entries_before_the_first_group():
     c = Forks([(2000, [5] * 4), (8000, [9] * 100)], 32, 2, 64, seed=4)
     new = [1] * 104
     q, out, b = attend(c, new, 8, groups=c.groups(first=[4, 104], shared=[8000]))
+    check(c, new, q, out, b)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_many_groups_and_entries_in_order(fp8):
+    """More groups than a warp has lanes, most of them empty; sequences without a list of them."""
+    require_gpu()
+    c = Forks([(8195, [3] * 130)] + [(100, [])] * 33 + [(6000, [2, 70] * 55), (50, [])] + [(0, [x]) for x in (90, 5, 1)] + [(7, [])],
+              64, 1, 128, fp8, seed=15, in_order=True)
+    new = [1] * len(c.lens_host)
+    q, out, b = attend(c, new, 8, b=batch(c, new, False))
     check(c, new, q, out, b)
 
 
@@ -328,6 +339,24 @@ def test_right_behind_the_kernel_that_writes_the_keys(most):
         torch.cuda.synchronize()
         check(c, new, q, o, b)
     assert fmad.standalone_status() == 0
+
+
+def test_two_streams_with_workspaces_of_their_own():
+    require_gpu()
+    c = Forks([(8100, [30] * 110)], 64, 2, 128, seed=16)
+    new = [1] * 110
+    q, want, b = attend(c, new, 16)
+    groups = c.groups()
+    need = fmad.shared_attention_workspace_size(c.handle, b, groups, 16)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    ws = [torch.empty(need, dtype=torch.uint8, device="cuda") for _ in streams]
+    outs = [[torch.empty_like(want) for _ in range(6)] for _ in streams]
+    torch.cuda.synchronize()
+    for i in range(6):
+        for s, w, o in zip(streams, ws, outs):
+            fmad.shared_attention(c.handle, 0, b, groups, q, o[i], w, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(want, x) for o in outs for x in o) and fmad.standalone_status() == 0
 
 
 def test_device_side_faults_are_reported():
