@@ -543,7 +543,8 @@ int64_t cost_alone(const fm_kv_cache& c, const fm_kv_batch& b, int H, const Plan
     const int64_t ctas = static_cast<int64_t>(c.Hkv) * b.n * pl.splits, tiles = (len + kDecodeKeys - 1) / kDecodeKeys;
     const int resident = decode_resident(c.Dh, f8, static_cast<int>(rows));
     const int64_t waves = (ctas + static_cast<int64_t>(sms) * resident - 1) / (static_cast<int64_t>(sms) * resident);
-    return (rows <= 8 ? 55 : 65) + waves * ((tiles + pl.splits - 1) / pl.splits) * decode_each(f8, static_cast<int>(rows), resident, ctas, sms) / 10 + (pl.splits > 8 ? 25 : 0);
+    const int64_t each = decode_each(f8, static_cast<int>(rows), resident, ctas, sms);
+    return (rows <= 8 ? 55 : 65) + waves * ((tiles + pl.splits - 1) / pl.splits) * each / 10 + (pl.splits > 8 ? 25 : 0);
   }
   const int64_t ctas = pl.row_blocks * c.Hkv * b.n * pl.splits;
   return (ctas + sms - 1) / sms * cta_time(f8, pl.alt, pl.split_tiles) + join_time(c, b, H, pl);
@@ -552,7 +553,7 @@ int64_t cost_alone(const fm_kv_cache& c, const fm_kv_batch& b, int H, const Plan
 // Two kernels in a row cost 11 to 13 us with nothing to do, one 6 to 7, so sharing pays where entries x shared tokens are
 // many: 96 single tokens of 16 heads on 2 KV heads (Dh 128, bf16) behind 2000 common keys take 14.8 us here and 24.3 us
 // alone, 32 behind 8000 17.4 and 22.9 us; but 96 behind 500 13.1 and 11.3 us, 8 behind 8000 15.2 and 11.5 us. Chunks that
-// fill half of a 256-row block themselves gain nothing (16 x 50 tokens behind 4100: 43 us in two kernels, 41.6 alone).
+// fill half of a 256-row block themselves gain nothing (16 x 50 tokens behind 4100: 43 us in two kernels, 39 alone).
 SharedPlan shared_plan(const fm_kv_cache& c, const fm_kv_batch& b, const fm_kv_groups& g, int H) {
   SharedPlan sp = {};
   const int G = H / c.Hkv, sms = sm_count();

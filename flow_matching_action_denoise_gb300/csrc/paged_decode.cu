@@ -32,12 +32,16 @@ int decode_clusters(int Dh, bool f8, int rows, int size) {
   };
   if (decode_configure<Keys::kAll>() != cudaSuccess) return 0;
   constexpr Keys K = Keys::kAll;
-  if (rows <= 8) {
-    if (Dh == 128) return f8 ? query(decode_kernel<128, true, 1, K>, smem_bytes<128, true, 1, K>()) : query(decode_kernel<128, false, 1, K>, smem_bytes<128, false, 1, K>());
-    return f8 ? query(decode_kernel<64, true, 1, K>, smem_bytes<64, true, 1, K>()) : query(decode_kernel<64, false, 1, K>, smem_bytes<64, false, 1, K>());
-  }
-  if (Dh == 128) return f8 ? query(decode_kernel<128, true, 2, K>, smem_bytes<128, true, 2, K>()) : query(decode_kernel<128, false, 2, K>, smem_bytes<128, false, 2, K>());
-  return f8 ? query(decode_kernel<64, true, 2, K>, smem_bytes<64, true, 2, K>()) : query(decode_kernel<64, false, 2, K>, smem_bytes<64, false, 2, K>());
+  const auto of = [&](auto dh, auto f, auto nt) {
+    constexpr int DH = decltype(dh)::value, NT = decltype(nt)::value;
+    constexpr bool F8 = decltype(f)::value;
+    return query(decode_kernel<DH, F8, NT, K>, smem_bytes<DH, F8, NT, K>());
+  };
+  const auto of_rows = [&](auto dh, auto f) {
+    return rows <= 8 ? of(dh, f, std::integral_constant<int, 1>{}) : of(dh, f, std::integral_constant<int, 2>{});
+  };
+  const auto of_type = [&](auto dh) { return f8 ? of_rows(dh, std::true_type{}) : of_rows(dh, std::false_type{}); };
+  return Dh == 128 ? of_type(std::integral_constant<int, 128>{}) : of_type(std::integral_constant<int, 64>{});
 }
 
 }  // namespace fm

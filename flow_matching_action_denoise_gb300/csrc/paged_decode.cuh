@@ -562,7 +562,8 @@ cudaError_t configure_one() {
 template <int DH, bool F8, int NT, Keys K>
 cudaError_t run(const AttnParams& p, const CUtensorMap& tk, const CUtensorMap& tv, const LaunchOpts& o) {
   const int blocks = K == Keys::kOwn ? (p.max_tokens * p.G + 8 * NT - 1) / (8 * NT) : 1;
-  return launch(decode_kernel<DH, F8, NT, K>, dim3(p.splits, p.Hkv * blocks, p.n), dim3(kThreads), smem_bytes<DH, F8, NT, K>(), o, p, tk, tv);
+  return launch(decode_kernel<DH, F8, NT, K>, dim3(p.splits, p.Hkv * blocks, p.n), dim3(kThreads), smem_bytes<DH, F8, NT, K>(),
+                o, p, tk, tv);
 }
 
 template <int DH, bool F8, Keys K>
