@@ -173,6 +173,21 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity) {
   return false;
 }
 
+// The same for what other CTAs of the cluster have stored.
+__device__ __forceinline__ bool wait_for_cluster(uint64_t* bar, uint32_t parity) {
+#pragma unroll 1
+  for (int i = 0; i < (1 << 22); ++i) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.b32 %0, 1, 0, p;\n}"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    if (done) return true;
+  }
+  return false;
+}
+
 // One lane of a converged warp. Unlike a comparison with a lane number it tells the compiler that a single lane is
 // active: tcgen05 instructions take their operands from the warp's uniform registers, and under a plain branch each
 // MMA took about 100 cycles to issue (operands collected lane by lane), longer than it runs.

@@ -306,9 +306,11 @@ Plan plan_of(const fm_kv_cache& c, const fm_kv_batch& b, int H, int window, int 
   if (window > 0) pl.splits = std::min(pl.splits, splits_of(c, b, H, window, sinks));
   pl.decode = rows <= kDecodeRows;
   if (pl.decode && sinks > 0 && pl.splits > 1 && pl.splits <= 8) {
-    // where the clusters do not all run at once, fewer splits (48 units of 6: 32 us in two waves, 22 us of 5)
+    // where the clusters do not all run at once, fewer splits (48 units of 6: 32 us in two waves, 22 us of 5); 3 % of room, since
+    // clusters that start while others end do not always find the last places (96 of 97 clusters: 23.9 us, of two CTAs 22.1)
     const int64_t units = static_cast<int64_t>(c.Hkv) * b.n;
-    while (pl.splits > 1 && units > decode_clusters_at_once(c.Dh, c.fmt == FM_FMT_FP8, static_cast<int>(rows), pl.splits)) --pl.splits;
+    const auto room = [&] { return decode_clusters_at_once(c.Dh, c.fmt == FM_FMT_FP8, static_cast<int>(rows), pl.splits); };
+    while (pl.splits > 1 && units * 33 > room() * int64_t(32)) --pl.splits;
   }
   if (!pl.decode) {
     pl.alt = rows <= kTileRows;

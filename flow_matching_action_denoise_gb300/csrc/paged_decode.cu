@@ -35,7 +35,7 @@ int decode_clusters(int Dh, bool f8, int rows, int size) {
   const auto of = [&](auto dh, auto f, auto nt) {
     constexpr int DH = decltype(dh)::value, NT = decltype(nt)::value;
     constexpr bool F8 = decltype(f)::value;
-    return query(decode_kernel<DH, F8, NT, K>, smem_bytes<DH, F8, NT, K>());
+    return query(decode_kernel<DH, F8, NT, K>, smem_bytes<DH, F8, NT, K>(true));
   };
   const auto of_rows = [&](auto dh, auto f) {
     return rows <= 8 ? of(dh, f, std::integral_constant<int, 1>{}) : of(dh, f, std::integral_constant<int, 2>{});

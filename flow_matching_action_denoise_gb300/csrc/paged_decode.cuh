@@ -1,16 +1,17 @@
 // Attention over a paged cache for up to 16 stacked rows (tokens x query heads of a KV head): single tokens.
 //
 // Bound by reading the cache: 64 sequences of 8192 keys on 2 KV heads, Dh 128, take 46 us with an E4M3 cache (5.8 TB/s,
-// 86 % of a plain copy's rate) and 80 us with bf16 (6.7 TB/s); 789 keys on one KV head take 6 us, launch and join. A CTA takes one entry, KV head and split of its keys: a warp moves tiles of 64 keys by
-// TMA into a three-stage ring, four warps take 16 keys each of every tile. Keys and head dims are the M = 16 of
+// 86 % of a plain copy's rate) and 80 us with bf16 (6.7 TB/s); 789 keys on one KV head take 4.9 us: three dependent loads
+// and the first bytes 2.0, the keys 1.0, the joins of warps and cluster 1.2. A CTA takes one entry, KV head and split of its
+// keys: a warp moves tiles of 64 keys by TMA into a three-stage ring, four warps take 16 keys each of every tile. Keys and head dims are the M = 16 of
 // m16n8k16 tensor core instructions and the stacked rows their N, eight or sixteen: S^T = K Q^T, O^T = V^T P^T. So keys
 // and values pass from shared memory straight into the fragments of one warp, and eight rows cost no padding (rows as
 // M = 16 took twice the instructions and registers for eight). The big tensor cores would fill a sixteenth of their
 // 128 rows and need E4M3 codes expanded in shared memory first: 32 KB of codes became 192 KB of traffic there, 1.2 us a
 // 128-key tile and SM against 0.7 us at which HBM delivers them. Here codes are expanded in registers (exact, to f16).
 // Every warp keeps its own running maximum, sum and O; the four are joined in shared memory, the splits of a key axis by
-// their cluster through distributed shared memory (up to 8 splits: no workspace, no second kernel), more through the
-// workspace.
+// their cluster (up to 8 splits: no workspace, no second kernel), whose CTAs send each other their shares by stores that the
+// receiver's barrier counts; more splits meet in the workspace.
 //
 // E4M3 fragments. A 16-byte row piece holds 16 codes. Keys (M) x head dims (K): a lane's word is four consecutive dims
 // of one key, taken as k pairs (2t, 2t + 1) and (2t + 8, 2t + 9); the query's fragments use the same order of dims, so
@@ -22,6 +23,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "kv.h"
@@ -83,6 +85,18 @@ __device__ __forceinline__ uint32_t piece(int r, int c) {
     return static_cast<uint32_t>(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
 }
 
+// Shared memory: the ring, then the four warps' sums in its place; behind it, in a cluster, what a CTA receives.
+constexpr int kPad = 8;   // floats between rows of sums
+template <int DH, bool F8, int NT, Keys K>
+constexpr size_t kWork = std::max<size_t>(static_cast<size_t>(kStages<DH, F8, NT, K>) * 2 * kDecodeKeys * DH * (F8 ? 1 : 2),
+                                          static_cast<size_t>(8 * NT) * kWarps * (DH + kPad) * 4);
+template <int DH, int NT>
+constexpr size_t kReceived = (8 * NT * (DH / 4) + 8) * sizeof(float4) + 8 * 8 * NT * sizeof(float2);
+template <int DH, bool F8, int NT, Keys K>
+constexpr size_t smem_bytes(bool cluster) {
+  return 1024 + kWork<DH, F8, NT, K> + (cluster ? kReceived<DH, NT> : 0);
+}
+
 // NT: row tiles of eight.
 template <int DH, bool F8, int NT, Keys K>
 __global__ void __launch_bounds__(kThreads, kResident<DH, F8, NT> + kMore<DH, F8, NT, K>)
@@ -95,7 +109,12 @@ __global__ void __launch_bounds__(kThreads, kResident<DH, F8, NT> + kMore<DH, F8
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ uint64_t full[kDepth], empty[kDepth];
-  __shared__ float2 s_ml[kWarps + 1][kDecodeRows];         // (log2 maximum, sum) of each warp, and of the CTA
+  __shared__ float2 s_ml[kWarps][8 * NT];                  // (log2 maximum, sum) of each warp
+  // a cluster's splits: what every CTA has of this one's share of the rows' quads of sums, [split][share], and of the rows
+  constexpr int kQuads = DH / 4;
+  float4* got = reinterpret_cast<float4*>(smem + kWork<DH, F8, NT, K>);
+  float2(*got_ml)[8 * NT] = reinterpret_cast<float2(*)[8 * NT]>(got + 8 * NT * kQuads + 8);
+  __shared__ uint64_t landed;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int split = blockIdx.x, g = K == Keys::kOwn ? blockIdx.y % p.Hkv : blockIdx.y;
   if (tid == 0) {
@@ -103,6 +122,7 @@ __global__ void __launch_bounds__(kThreads, kResident<DH, F8, NT> + kMore<DH, F8
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], kWarps);
     }
+    mbar_init(&landed, 1);
     fence_mbar_init();
   }
   pdl_trigger();
@@ -128,6 +148,19 @@ __global__ void __launch_bounds__(kThreads, kResident<DH, F8, NT> + kMore<DH, F8
   const int per = (all + p.splits - 1) / p.splits;
   const int t_lo = begin + split * per;
   const int nt = max(0, min(per, begin + all - t_lo));
+  const bool clustered = p.splits > 1 && (K == Keys::kOwn || p.part_o == nullptr);
+  const int total = rows * kQuads;   // quads of sums
+  int share = total;                 // of a CTA of the cluster
+  if (clustered) {
+    share = (total + p.splits - 1) / p.splits;
+    if (tid == 0) {
+      const int x0 = min(total, split * share), x1 = min(total, x0 + share);
+      const int touched = x1 > x0 ? (x1 - 1) / kQuads - x0 / kQuads + 1 : 0;   // rows
+      mbar_arrive_expect_tx(&landed, p.splits * ((x1 - x0) * 16 + touched * 8));
+    }
+    __syncwarp();
+    cluster_arrive_relaxed();   // paired with the wait before the first remote store
+  }
   __syncthreads();
 
   // this lane's key (dim) g of eight, its quarter t of a row; its stacked rows are 8 x + 2 t and + 1
@@ -385,9 +418,8 @@ __global__ void __launch_bounds__(kThreads, kResident<DH, F8, NT> + kMore<DH, F8
   __syncthreads();   // every tile has been used: the ring holds the warps' sums now
 
   // ---- join the four warps: [warp][row] sums, then the CTA's [row][DH]. Rows lie 8 floats apart in the banks.
-  constexpr int kPitch = DH + 8;
+  constexpr int kPitch = DH + kPad;
   float* sums = reinterpret_cast<float*>(smem);
-  float* cta = sums + kWarps * 8 * NT * kPitch;
   if (warp < kWarps) {
 #pragma unroll
     for (int u = 0; u < 2 * NT; ++u) {
@@ -411,7 +443,6 @@ __global__ void __launch_bounds__(kThreads, kResident<DH, F8, NT> + kMore<DH, F8
   __syncthreads();
   if constexpr (K == Keys::kOwn) pdl_wait();   // the prefix's shares
   const float vs = F8 ? *p.v_scale : 1.0f;
-  const bool clustered = p.splits > 1 && (K == Keys::kOwn || p.part_o == nullptr);
   // Keys::kOwn: every split's weight in a row's sum over the prefix, under the prefix's maximum; that maximum, the total
   __shared__ float s_w[K == Keys::kOwn ? 8 * NT : 1][kMostPrefixSplits];
   __shared__ float2 s_pre[K == Keys::kOwn ? 8 * NT : 1];
@@ -481,8 +512,8 @@ __global__ void __launch_bounds__(kThreads, kResident<DH, F8, NT> + kMore<DH, F8
     *reinterpret_cast<uint2*>(p.out + tok * p.out_stride + head * DH + d) =
         make_uint2(pack16<false>(acc.x * inv, acc.y * inv), pack16<false>(acc.z * inv, acc.w * inv));
   };
-  constexpr int kQuads = DH / 4;
-  for (int x = tid; x < rows * kQuads; x += kThreads) {
+  if (clustered) cluster_wait();
+  for (int x = tid; x < total; x += kThreads) {
     const int row = x / kQuads, d = (x % kQuads) * 4;
     float top = -INFINITY;
 #pragma unroll
@@ -498,8 +529,13 @@ __global__ void __launch_bounds__(kThreads, kResident<DH, F8, NT> + kMore<DH, F8
       acc.x += v.x * f, acc.y += v.y * f, acc.z += v.z * f, acc.w += v.w * f;
     }
     if (clustered) {
-      *reinterpret_cast<float4*>(cta + row * DH + d) = acc;
-      if (d == 0) s_ml[kWarps][row] = make_float2(top, l);
+      const int owner = x / share;
+      st_async_v4(map_dsmem(smem_u32(&got[split * share + x - owner * share]), owner), acc.x, acc.y, acc.z, acc.w,
+                  map_dsmem(smem_u32(&landed), owner));
+      if (d == 0) {   // to every CTA that has quads of the row
+        for (int q = owner; q <= (x + kQuads - 1) / share; ++q)
+          st_async_v2(map_dsmem(smem_u32(&got_ml[split][row]), q), top, l, map_dsmem(smem_u32(&landed), q));
+      }
     } else if (p.splits > 1) {
       const int tok = en.begin + (row0 + row) / p.G, head = g * p.G + (row0 + row) % p.G;
       const int64_t at = (static_cast<int64_t>(split) * p.tokens + tok) * p.H + head;
@@ -510,21 +546,20 @@ __global__ void __launch_bounds__(kThreads, kResident<DH, F8, NT> + kMore<DH, F8
     }
   }
   if (!clustered) return;
-  // ---- join the cluster's splits in split order: every CTA finishes a share of the elements
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-  const uint32_t rank = cluster_rank();
-  const int total = rows * kQuads, share = (total + p.splits - 1) / p.splits;
-  for (int x = rank * share + tid; x < min(total, static_cast<int>(rank + 1) * share); x += kThreads) {
+  // ---- join the cluster's splits in split order: every CTA finishes a share of the quads, sent to it by all as they were done
+  // (with the cluster's barrier before and after and the others' shared memory read between them a single token took 1 us more)
+  __syncwarp();
+  cluster_arrive_relaxed();
+  if (warp == 0 && !wait_for_cluster(&landed, 0) && lane == 0) atomicOr(p.err, kErrPipelineTimeout);
+  __syncthreads();   // one warp polls: others on the SM may still compute
+  const int x0 = split * share;
+  for (int x = x0 + tid; x < min(total, x0 + share); x += kThreads) {
     const int row = x / kQuads, d = (x % kQuads) * 4;
     float2 ml[8];
     float top = -INFINITY;
 #pragma unroll
     for (int s = 0; s < 8; ++s) {
-      ml[s] = make_float2(-INFINITY, 0.f);
-      if (s < p.splits)
-        asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
-                     : "=f"(ml[s].x), "=f"(ml[s].y)
-                     : "r"(map_dsmem(smem_u32(&s_ml[kWarps][row]), s)));
+      ml[s] = s < p.splits ? got_ml[s][row] : make_float2(-INFINITY, 0.f);
       top = fmaxf(top, ml[s].x);
     }
     float l = 0.f;
@@ -533,37 +568,27 @@ __global__ void __launch_bounds__(kThreads, kResident<DH, F8, NT> + kMore<DH, F8
     for (int s = 0; s < 8; ++s) {
       if (s >= p.splits) continue;
       const float f = ml[s].x > -INFINITY ? ex2_approx(ml[s].x - top) : 0.f;
-      float4 v;
-      asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                   : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                   : "r"(map_dsmem(smem_u32(cta + row * DH + d), s)));
+      const float4 v = got[s * share + x - x0];
       l += ml[s].y * f;
       acc.x += v.x * f, acc.y += v.y * f, acc.z += v.z * f, acc.w += v.w * f;
     }
     finish(row, d, top, l, acc);
   }
-  // no CTA leaves while another still reads its share
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-template <int DH, bool F8, int NT, Keys K>
-constexpr size_t smem_bytes() {
-  const size_t ring = static_cast<size_t>(kStages<DH, F8, NT, K>) * 2 * kDecodeKeys * DH * (F8 ? 1 : 2);
-  const size_t join = static_cast<size_t>(8 * NT) * (kWarps * (DH + 8) + DH) * 4;
-  return 1024 + (ring > join ? ring : join);
+  __syncwarp();
+  cluster_wait();   // no CTA leaves while another still sends to it
 }
 
 template <int DH, bool F8, int NT, Keys K>
 cudaError_t configure_one() {
   return cudaFuncSetAttribute(decode_kernel<DH, F8, NT, K>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              static_cast<int>(smem_bytes<DH, F8, NT, K>()));
+                              static_cast<int>(smem_bytes<DH, F8, NT, K>(true)));
 }
 
 template <int DH, bool F8, int NT, Keys K>
 cudaError_t run(const AttnParams& p, const CUtensorMap& tk, const CUtensorMap& tv, const LaunchOpts& o) {
   const int blocks = K == Keys::kOwn ? (p.max_tokens * p.G + 8 * NT - 1) / (8 * NT) : 1;
-  return launch(decode_kernel<DH, F8, NT, K>, dim3(p.splits, p.Hkv * blocks, p.n), dim3(kThreads), smem_bytes<DH, F8, NT, K>(),
-                o, p, tk, tv);
+  return launch(decode_kernel<DH, F8, NT, K>, dim3(p.splits, p.Hkv * blocks, p.n), dim3(kThreads),
+                smem_bytes<DH, F8, NT, K>(o.cluster.x > 1), o, p, tk, tv);
 }
 
 template <int DH, bool F8, Keys K>
