@@ -736,7 +736,8 @@ __global__ void __launch_bounds__(threads_of(F8), 1)
       else
         join_rows(integral_constant<int, 1>{}, integral_constant<int, 8>{});
       __syncwarp();
-      cluster_meet();   // no CTA leaves while another still reads its part
+      cluster_arrive_relaxed();   // no CTA leaves while another still reads its part; nothing is handed over any more
+      cluster_wait();
     }
   } else if (warp < kTmaWarp) {
     // ================================================= tensor cores, a warp for each tile
@@ -934,7 +935,8 @@ __global__ void __launch_bounds__(threads_of(F8), 1)
   __syncwarp();
   if (JOIN && warp >= 8) {   // the softmax warps' two meetings
     cluster_meet();
-    cluster_meet();
+    cluster_arrive_relaxed();
+    cluster_wait();
   }
   tc_fence_before();
   __syncthreads();
