@@ -592,7 +592,14 @@ def _rows(x, where: str, name: str, dtype, dev: int, rows: int, cols: int):
     return x.data_ptr(), s0 if rows > 1 else cols
 
 
-_I32 = None   # torch.int32, once a cache or a batch exists
+# What the calls name of torch, once a cache exists (an import statement in each call costs as much as one of its checks).
+_I32 = _BF16 = _F32 = _torch_c = None
+
+
+def _use_torch():
+    global _I32, _BF16, _F32, _torch_c
+    import torch
+    _I32, _BF16, _F32, _torch_c = torch.int32, torch.bfloat16, torch.float32, torch._C
 
 
 def _ints(x, where: str, name: str, dev: int, count: int):
@@ -607,11 +614,13 @@ def _ints(x, where: str, name: str, dev: int, count: int):
 def _here(dev: int, stream, where: str):
     """The stream to use on device `dev`: the given one, or that device's current one. The library works on the
     current device, so the two must agree."""
-    import torch
-    if torch._C._cuda_getDevice() != dev:
+    if _torch_c is None:
+        _use_torch()
+    if _torch_c._cuda_getDevice() != dev:
+        import torch
         _bad(where, f"the tensors are on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev)   # current_stream(dev).cuda_stream without its Python objects
+        return _torch_c._cuda_getCurrentRawStream(dev)   # current_stream(dev).cuda_stream without its Python objects
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -633,8 +642,7 @@ class KvCache:
 
     def __init__(self, k, v, table, lens, refs=None, k_scale=None, v_scale=None):
         import torch
-        global _I32
-        _I32 = torch.int32
+        _use_torch()
         where = "KvCache"
         if k.dim() != 5 or v.shape != k.shape or v.dtype != k.dtype:
             _bad(where, "k and v must be [layers][pages][page_tokens][Hkv][Dh] and alike")
@@ -788,8 +796,7 @@ def kv_compact(cache: KvCache, status, workspace, stream=None):
 
 def _append_arguments(w: str, cache, batch, rope, q, k, v, q_out, positions):
     """(q, its stride, H, k, stride, v, stride, q_out, stride, positions) as the C side takes them."""
-    import torch
-    d, bf, T, Hkv, Dh = cache.dev, torch.bfloat16, batch.tokens, cache.Hkv, cache.Dh
+    d, bf, T, Hkv, Dh = cache.dev, _BF16, batch.tokens, cache.Hkv, cache.Dh
     if batch.dev != d or rope.dev != d:
         _bad(w, "the cache, the batch and the rotary table must be on one device")
     H, qp, qs, op, os_ = 0, None, 0, None, 0
@@ -817,9 +824,8 @@ def rope_append(cache: KvCache, layer: int, batch: KvBatch, rope: Rope, q, k, v,
 def _gain(x, where: str, name: str, dev: int, dim: int):
     if x is None:
         return None
-    import torch
-    if x.dtype is not torch.float32 or x.get_device() != dev or x.shape != (dim,) or not x.is_contiguous():
-        _check_tensor(x, where, name, (torch.float32,), dev, (dim,))
+    if x.dtype is not _F32 or x.get_device() != dev or x.shape != (dim,) or not x.is_contiguous():
+        _check_tensor(x, where, name, (_F32,), dev, (dim,))
         _bad(where, f"{name} must be contiguous")
     return x.data_ptr()
 
@@ -846,8 +852,7 @@ def paged_attention_workspace_size(cache: KvCache, batch: KvBatch, H: int) -> in
 
 def _attention_arguments(w: str, cache, batch, q, out, scale):
     """(q, its stride, H, scale, out, its stride) as the C side takes them."""
-    import torch
-    d, bf, T, Dh = cache.dev, torch.bfloat16, batch.tokens, cache.Dh
+    d, bf, T, Dh = cache.dev, _BF16, batch.tokens, cache.Dh
     if q.dim() != 3:
         _bad(w, "q must be [tokens][H][Dh]")
     H = q.shape[1]
