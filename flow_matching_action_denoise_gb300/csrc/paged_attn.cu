@@ -490,7 +490,8 @@ int attend(const Call& a, int window, int sinks, bool meet) {
   if (st != FM_OK) return st;
   const fm_kv_batch b = bounded_batch(*a.b);
   const Plan pl = plan_of(*a.c, b, a.H, window, sinks, meet);
-  st = check_workspace(a, pl.workspace, "workspace smaller than fm_paged_attention_workspace_size()");
+  st = check_workspace(a, pl.workspace, meet && K == Keys::kAll ? "workspace smaller than fm_shared_attention_workspace_size()"
+                                                                : "workspace smaller than fm_paged_attention_workspace_size()");
   if (st != FM_OK) return st;
   CUtensorMap tk, tv;
   if (!maps_of(a, pl.decode, &tk, &tv)) return record_error(FM_ERR_CUDA, "cuTensorMapEncodeTiled (cache pages) failed");
