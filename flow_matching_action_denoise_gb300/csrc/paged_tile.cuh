@@ -736,7 +736,7 @@ __global__ void __launch_bounds__(threads_of(F8), 1)
       else
         join_rows(integral_constant<int, 1>{}, integral_constant<int, 8>{});
       __syncwarp();
-      cluster_arrive_relaxed();   // no CTA leaves while another still reads its part; nothing is handed over any more
+      cluster_arrive();   // behind this warp's reads: no CTA leaves while another still reads its part
       cluster_wait();
     }
   } else if (warp < kTmaWarp) {
@@ -933,7 +933,7 @@ __global__ void __launch_bounds__(threads_of(F8), 1)
     if (!ok && lane == 0) atomicOr(p.err, kErrPipelineTimeout);
   }
   __syncwarp();
-  if (JOIN && warp >= 8) {   // the softmax warps' two meetings
+  if (JOIN && warp >= 8) {   // the softmax warps' two meetings; these have read nothing of the others
     cluster_meet();
     cluster_arrive_relaxed();
     cluster_wait();

@@ -312,6 +312,8 @@ __device__ __forceinline__ float ex2_approx(float x) {
 __device__ __forceinline__ void cluster_arrive_relaxed() {
   asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 }
+// The arrival that orders what was read and written before it (release).
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
 // Bulk copy (TMA engine) from this CTA's shared memory to the shared memory of a CTA
 // of the cluster; `dst` and `mbar` are shared::cluster addresses in the destination
