@@ -38,6 +38,7 @@ struct AttnParams {
   const int32_t* g_shared;        // [g_n] tokens that a group's entries share
   int g_n, g_tokens;              // g_tokens: packed rows of a group that Keys::kPrefix takes
   int prefix_splits;              // shares of the prefix that Keys::kOwn joins
+  uint64_t* seen;                 // the word between Keys::kPrefix and Keys::kOwn
   float* part_o;                  // [splits][tokens * H][Dh]
   float2* part_ml;                // [splits][tokens * H] (log2 maximum, sum)
   int* err;
@@ -126,6 +127,27 @@ __device__ __forceinline__ int prefix_of(const AttnParams& p, int entry, const E
   const int past = e.len - e.nq, end = e.begin + min(e.nq, p.max_tokens);
   const bool seen = past >= 0 && shared <= (p.causal ? past + 1 : e.len);
   return seen && group.len > 0 && e.begin >= group.begin && end <= group.begin + group.nq ? shared : 0;
+}
+
+// Keys::kOwn runs beside Keys::kPrefix and reads what kernels before both wrote (the batch, queries, keys, values). These
+// writes are made visible to a grid that waits for the grids before it, as the prefix's does; for the other grid they are
+// handed on by a word of the workspace. The prefix's first CTA stores kSeen (release) behind its wait and before it lets the
+// other grid start; a thread there that finds kSeen (acquire) sees the inputs, and one that does not waits for the prefix to
+// end, which is right as well, only later. Behind that wait Keys::kOwn's first CTA takes the word back, so that no call
+// finds an earlier call's.
+constexpr uint64_t kSeen = 0x5b1d93e6c7f0a42dull;
+__device__ __forceinline__ bool first_cta() { return blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0; }
+__device__ __forceinline__ void hand_inputs_on(const AttnParams& p) {
+  asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(p.seen), "l"(kSeen) : "memory");
+}
+__device__ __forceinline__ void see_inputs(const AttnParams& p) {
+  uint64_t word;
+  asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(word) : "l"(p.seen) : "memory");
+  if (word != kSeen) pdl_wait();
+  asm volatile("fence.proxy.async.global;" ::: "memory");   // keys and values are read by TMA
+}
+__device__ __forceinline__ void take_word_back(const AttnParams& p) {
+  asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(p.seen), "l"(uint64_t(0)) : "memory");
 }
 
 // The keys [first_key, last_key) of a token at position pos.

@@ -606,7 +606,7 @@ SharedPlan shared_plan(const fm_kv_cache& c, const fm_kv_batch& b, const fm_kv_g
   pre.split_tiles = static_cast<int>((tiles + pre.splits - 1) / pre.splits);
   rings_of(c, pre);
   sp.split = true;
-  sp.workspace = static_cast<size_t>(pre.splits) * b.tokens * H * (c.Dh * sizeof(float) + sizeof(float2));
+  sp.workspace = static_cast<size_t>(pre.splits) * b.tokens * H * (c.Dh * sizeof(float) + sizeof(float2)) + 16;   // 8: seen
   return sp;
 }
 
@@ -630,6 +630,7 @@ int attend_shared(const Call& a, const fm_kv_groups* g) {
   cudaError_t e = configure<Keys::kPrefix>();
   if (e != cudaSuccess) return record_error(FM_ERR_CUDA, cudaGetErrorString(e));
   shares_in(a, sp.prefix.splits, b.tokens, p);
+  p.seen = reinterpret_cast<uint64_t*>(p.part_ml + static_cast<size_t>(sp.prefix.splits) * b.tokens * a.H);
   p.g_first = g->first;
   p.g_shared = g->shared;
   p.g_n = g->n;

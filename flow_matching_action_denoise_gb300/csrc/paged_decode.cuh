@@ -126,15 +126,22 @@ __global__ void __launch_bounds__(kThreads, kResident<DH, F8, NT> + kMore<DH, F8
     fence_mbar_init();
   }
   pdl_trigger();
-  // Keys::kOwn starts when every CTA of the prefix's kernel has waited for what ran before it, so that all inputs are there;
-  // it waits only for that kernel's shares (and, rows or none, does not end before it)
-  if constexpr (K != Keys::kOwn) pdl_wait();
+  // Keys::kOwn starts when every CTA of the prefix's kernel has waited for what ran before it; it waits only for that kernel's
+  // shares (and, rows or none, does not end before it)
+  if constexpr (K == Keys::kOwn)
+    see_inputs(p);
+  else
+    pdl_wait();
+  [[maybe_unused]] auto prefix_done = [&] {
+    pdl_wait();
+    if (tid == 0 && first_cta()) take_word_back(p);
+  };
   const Entry en = entry_of(p, blockIdx.z, tid == 0 && blockIdx.y == 0 && split == 0);
   // Keys::kOwn has any number of rows, a row block of 8 NT in each CTA
   const int row0 = K == Keys::kOwn ? blockIdx.y / p.Hkv * 8 * NT : 0;
   const int rows = min(max(min(en.nq, p.max_tokens) * p.G - row0, 0), 8 * NT);
   if (rows == 0) {   // the same in the whole cluster
-    if constexpr (K == Keys::kOwn) pdl_wait();
+    if constexpr (K == Keys::kOwn) prefix_done();
     return;
   }
   const int past = en.len - en.nq;
@@ -441,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, kResident<DH, F8, NT> + kMore<DH, F8
     }
   }
   __syncthreads();
-  if constexpr (K == Keys::kOwn) pdl_wait();   // the prefix's shares
+  if constexpr (K == Keys::kOwn) prefix_done();   // its shares are there
   const float vs = F8 ? *p.v_scale : 1.0f;
   // Keys::kOwn: every split's weight in a row's sum over the prefix, under the prefix's maximum; that maximum, the total
   __shared__ float s_w[K == Keys::kOwn ? 8 * NT : 1][kMostPrefixSplits];

@@ -7,7 +7,7 @@
 //
 // An entry's keys and values meet its own rows only: with the own keys of many entries in one tile of stacked rows a NaN in
 // one robot's values would reach all of them (0 x NaN). The second kernel starts once every CTA of the first is resident and
-// works beside it on what SMs are free; it waits for the first before the join.
+// works beside it on what SMs are free, on inputs that the first one hands on (see_inputs); it waits for the first before the join.
 // 128 single tokens of 16 heads on 2 KV heads (Dh 128, bf16) behind 8192 common keys, 133 to 400 of their own: 25.8 us, 66 us as
 // separate sequences. Bound by the chain: 18 us of prefix (7 us of them a CTA's ends), beside which the own CTAs have to find
 // room (those that do not cost 8 us more, behind it), 3.5 us from the last share to the output.

@@ -178,6 +178,7 @@ __global__ void __launch_bounds__(threads_of(F8), 1)
     __syncwarp();
   }
   pdl_wait();
+  if (K == Keys::kPrefix && tid == 0 && first_cta()) hand_inputs_on(p);
 
   // ---- the entry, its rows and its keys (the same in every thread)
   const bool report = tid == 0 && row_block == 0 && g == 0 && split == 0;
