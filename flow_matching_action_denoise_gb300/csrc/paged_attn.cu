@@ -606,7 +606,8 @@ SharedPlan shared_plan(const fm_kv_cache& c, const fm_kv_batch& b, const fm_kv_g
   pre.split_tiles = static_cast<int>((tiles + pre.splits - 1) / pre.splits);
   rings_of(c, pre);
   sp.split = true;
-  sp.workspace = static_cast<size_t>(pre.splits) * b.tokens * H * (c.Dh * sizeof(float) + sizeof(float2)) + 16;   // 8: seen
+  // a place behind the shares' for the word between the two kernels: the size counts whole places
+  sp.workspace = static_cast<size_t>(pre.splits + 1) * b.tokens * H * (c.Dh * sizeof(float) + sizeof(float2));
   return sp;
 }
 
