@@ -56,7 +56,7 @@ EXPORTS = [
     "fm_test_skinny_gemm_tile", "fm_test_pdl_chain", "fm_test_grid_barrier", "fm_test_attn_plan",
     "refresh_prefix_pages", "fm_kv_workspace_size", "fm_kv_reserve", "fm_kv_fork", "fm_kv_release", "fm_kv_compact",
     "fm_rope_table", "fm_rope_append", "fm_norm_rope_append", "fm_paged_attention_workspace_size", "fm_paged_attention",
-    "fm_sink_attention", "fm_shared_attention_workspace_size", "fm_shared_attention", "fm_norm_quant",
+    "fm_sink_attention", "fm_shared_attention_workspace_size", "fm_shared_attention", "fm_test_paged_plan", "fm_norm_quant",
 ]
 
 
@@ -112,6 +112,10 @@ class FmKvBatch(ctypes.Structure):
 class FmKvGroups(ctypes.Structure):
     _fields_ = [("first", ctypes.c_void_p), ("shared", ctypes.c_void_p), ("n", ctypes.c_int), ("max_entries", ctypes.c_int),
                 ("max_shared", ctypes.c_int)]
+
+
+class FmPagedPlan(ctypes.Structure):
+    _fields_ = [(x, ctypes.c_int) for x in ("few_rows", "row_tiles", "splits", "cluster", "clusters_at_once", "own_splits")]
 
 
 class FmRopeConfig(ctypes.Structure):
@@ -205,6 +209,7 @@ def load() -> ctypes.CDLL:
         "fm_sink_attention": (i, [vp, i, vp, vp, ctypes.c_int64, i, ctypes.c_float, i, i, i, vp, ctypes.c_int64, vp, sz, vp]),
         "fm_shared_attention_workspace_size": (i, [vp, vp, vp, i, ctypes.POINTER(sz)]),
         "fm_shared_attention": (i, [vp, i, vp, vp, vp, ctypes.c_int64, i, ctypes.c_float, i, vp, ctypes.c_int64, vp, sz, vp]),
+        "fm_test_paged_plan": (i, [vp, vp, vp, i, i, i, ctypes.POINTER(FmPagedPlan)]),
         "fm_norm_quant": (i, [vp, ctypes.c_int64, i, vp, ctypes.c_int64, vp, i, i, ctypes.c_float, vp, ctypes.c_int64,
                               vp, vp, i, vp]),
     }
@@ -907,6 +912,14 @@ def shared_attention(cache: KvCache, layer: int, batch: KvBatch, groups: KvGroup
                                               op, os_, ws, nb, _here(cache.dev, stream, w))
     if st:
         _check(st, w)
+
+
+def paged_plan(cache: KvCache, batch: KvBatch, H: int, window: int = 0, sinks: int = 0, groups: KvGroups | None = None) -> FmPagedPlan:
+    """How an attention call divides its keys (fm_paged_plan); a diagnostic."""
+    plan = FmPagedPlan()
+    _check(load().fm_test_paged_plan(cache.addr, batch.addr, None if groups is None else groups.addr, H, window, sinks,
+                                     ctypes.byref(plan)), "fm_test_paged_plan")
+    return plan
 
 
 def norm_quant(x, r, gamma, eps: float, x_out, codes, scales, block: int = 0, stream=None):

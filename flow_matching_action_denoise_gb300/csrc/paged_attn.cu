@@ -691,3 +691,29 @@ extern "C" int fm_shared_attention(const fm_kv_cache* c, int layer, const fm_kv_
                                    int64_t out_stride, void* workspace, size_t workspace_bytes, void* stream) {
   return fm::attend_shared({c, layer, b, q, q_stride, H, scale, causal, out, out_stride, workspace, workspace_bytes, stream}, g);
 }
+
+extern "C" int fm_test_paged_plan(const fm_kv_cache* c, const fm_kv_batch* b, const fm_kv_groups* g, int H, int window, int sinks,
+                                  fm_paged_plan* plan) {
+  using namespace fm;
+  if (!plan) return record_error(FM_ERR_INVALID_ARG, "plan is NULL");
+  int st = check(c, b, H);
+  if (st == FM_OK && g) st = check_groups(g);
+  if (st != FM_OK) return st;
+  if (window < 0 || sinks < 0 || (g && (window || sinks)))
+    return record_error(FM_ERR_INVALID_ARG, "window and sinks must not be negative, and 0 with groups");
+  *plan = {};
+  if (nothing_to_do(*b)) return FM_OK;
+  const fm_kv_batch bounded = bounded_batch(*b);
+  const bool first_tokens = window > 0 && sinks > 0;
+  const SharedPlan sp = g ? shared_plan(*c, bounded, *g, H) : SharedPlan{};
+  const Plan pl = sp.split ? sp.prefix : plan_of(*c, bounded, H, window, first_tokens ? sinks : 0, g || first_tokens);
+  plan->few_rows = pl.decode;
+  plan->row_tiles = pl.decode ? 0 : pl.alt ? 1 : 2;
+  plan->splits = pl.splits;
+  plan->cluster = pl.decode && pl.splits > 1 && !pl.workspace ? pl.splits : pl.cluster;
+  if (plan->cluster)
+    plan->clusters_at_once = pl.decode ? decode_clusters_at_once(c->Dh, c->fmt == FM_FMT_FP8, b->max_tokens * (H / c->Hkv), plan->cluster)
+                                       : tile_clusters_at_once(plan->cluster);
+  plan->own_splits = sp.split ? sp.own_splits : 0;
+  return FM_OK;
+}

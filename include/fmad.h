@@ -788,6 +788,20 @@ int fm_shared_attention(const fm_kv_cache* c, int layer, const fm_kv_batch* b, c
                         int64_t q_stride, int H, float scale, int causal, uint16_t* out, int64_t out_stride, void* workspace,
                         size_t workspace_bytes, void* stream);
 
+/* How an attention call over a paged cache divides its keys on the current device (a diagnostic; a host call that reads no
+ * device memory): fm_shared_attention's plan with g, else that of fm_sink_attention (window and sinks > 0) or
+ * fm_paged_attention. */
+typedef struct fm_paged_plan {
+  int few_rows;           /* 1: the kernel for up to 16 rows of an entry and KV head, 0: the one for many */
+  int row_tiles;          /* query tiles of 128 rows a CTA (many rows) */
+  int splits;             /* of an entry's keys; of a shared prefix where there is one */
+  int cluster;            /* CTAs of a cluster in whose shared memory the splits meet (0: undivided, or the workspace) */
+  int clusters_at_once;   /* of that size (0 without clusters) */
+  int own_splits;         /* of an entry's keys behind a shared prefix (0: nothing is shared) */
+} fm_paged_plan;
+int fm_test_paged_plan(const fm_kv_cache* c, const fm_kv_batch* b, const fm_kv_groups* g, int H, int window, int sinks,
+                       fm_paged_plan* plan);
+
 /* Residual addition + RMS norm + E4M3 with scales taken from the data:
  *   s = x + r (r NULL: x);  x_out = s (unless NULL);
  *   y = s / sqrt(mean(s^2) + eps) * gamma (gamma NULL: 1);
