@@ -306,11 +306,18 @@ Plan plan_of(const fm_kv_cache& c, const fm_kv_batch& b, int H, int window, int 
   if (window > 0) pl.splits = std::min(pl.splits, splits_of(c, b, H, window, sinks));
   pl.decode = rows <= kDecodeRows;
   if (pl.decode && sinks > 0 && pl.splits > 1 && pl.splits <= 8) {
-    // where the clusters do not all run at once, fewer splits (48 units of 6: 32 us in two waves, 22 us of 5); 3 % of room, since
-    // clusters that start while others end do not always find the last places (96 of 97 clusters: 23.9 us, of two CTAs 22.1)
+    // Where the clusters do not all run at once, fewer splits, and some places are left free, since the last ones are not always
+    // found: one of clusters of 2 and 4, which pack well, of the others one in 14. Window 2048 + 64, 8 heads on 1, keys from
+    // HBM: E4M3, Dh 128: 148 of 148 clusters of 4 22.2 us, of 3 19.6; 146: 19.8, 19.5 (Dh 64: 11.8, 12.5); 112 of 117 of 5 20.0, of 4
+    // 17.0; 108: 16.1, 16.7; 78 of 81 of 7 14.3, of 6 14.1; 75: 13.5, 13.9; bf16: 94 of 97 of 3 23.0, of 2 21.2; 89: 20.0, 20.3;
+    // 35 of 36 of 8 12.4, of 7 11.5; 33: 11.3, 11.2. Over six kinds of calls and 358 counts, even and ragged, the choice is 0.7 % above the
+    // better of the two sizes, without free places 4.6 %.
     const int64_t units = static_cast<int64_t>(c.Hkv) * b.n;
-    const auto room = [&] { return decode_clusters_at_once(c.Dh, c.fmt == FM_FMT_FP8, static_cast<int>(rows), pl.splits); };
-    while (pl.splits > 1 && units * 33 > room() * int64_t(32)) --pl.splits;
+    const auto fits = [&](int s) {
+      const int64_t places = decode_clusters_at_once(c.Dh, c.fmt == FM_FMT_FP8, static_cast<int>(rows), s);
+      return units <= (s == 2 || s == 4 ? places - 1 : places * 13 / 14);
+    };
+    while (pl.splits > 1 && !fits(pl.splits)) --pl.splits;
   }
   if (!pl.decode) {
     pl.alt = rows <= kTileRows;

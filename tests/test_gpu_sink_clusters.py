@@ -38,7 +38,7 @@ def test_chunks(tiles, cluster, n, most, H, Hkv, window, sinks, Dh, fp8):
 
 
 @pytest.mark.parametrize("fp8", [False, True])
-@pytest.mark.parametrize("cluster,n", [(8, 20), (7, 36), (6, 42), (5, 50), (4, 65), (3, 80), (2, 120)])
+@pytest.mark.parametrize("cluster,n", [(8, 20), (7, 35), (6, 40), (5, 50), (4, 65), (3, 80), (2, 120)])
 def test_single_tokens(cluster, n, fp8):
     """16-bit rows of 128 dims: two CTAs an SM. With an E4M3 cache four, where twice as many entries meet in the same sizes."""
     require_gpu()
@@ -62,3 +62,19 @@ def test_the_plan_of_every_call():
     assert groups.own_splits == 0 and (plain.cluster == 0) == (fmad.paged_attention_workspace_size(c.handle, b, 8) > 0)
     # a window alone is fm_paged_attention, first tokens alone as well
     assert fmad.paged_plan(c.handle, b, 8, 0, 50).splits == plain.splits and fmad.paged_plan(c.handle, b, 8, 300, 0).cluster == 0
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("Dh", [64, 128])
+def test_clusters_leave_places_free(Dh, fp8):
+    """Single tokens' clusters all run at once, those of 2 and 4 CTAs with one place free, the others with a fourteenth of the
+    places; and no smaller size is taken where the next one fits."""
+    require_gpu()
+    c = Cache([4096], 64, 1, Dh, fp8, seed=1)
+    start, seq = torch.arange(401, dtype=torch.int32, device="cuda"), torch.zeros(400, dtype=torch.int32, device="cuda")
+    plans = {n: fmad.paged_plan(c.handle, fmad.KvBatch(start[:n + 1], n, 1, 4096, seq[:n]), 8, 2048, 64) for n in range(1, 400)}
+    places = {p.cluster: p.clusters_at_once for p in plans.values() if p.cluster}
+    assert set(places) == set(range(2, 9))
+    most = {s: r - 1 if s in (2, 4) else r * 13 // 14 for s, r in places.items()}
+    for n, p in plans.items():
+        assert p.splits == max([s for s in most if n <= most[s]] + [1]), n
