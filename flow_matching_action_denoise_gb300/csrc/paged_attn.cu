@@ -262,7 +262,10 @@ int splits_of(const fm_kv_cache& c, const fm_kv_batch& b, int H, int window, int
 }
 
 // Time of the join of a plan's splits, in units of 0.1 us: in the cluster by the rows of a CTA, else a second kernel and the
-// shares.
+// shares. An estimate of its own: splits_of, which chooses among up to 64 splits of a plain call, counts less for the same
+// second kernel (2.5 us and the shares at 4 TB/s, here 5.5 us and 8 TB/s), and neither holds everywhere. Where a cluster is
+// taken for it with first tokens, the workspace can be quicker: 1 x 30 tokens over 3000 keys, 8 heads on 1, Dh 128, window 2000
+// + 100 take 16.5 us in a cluster of 7, all 3000 keys in 12 splits through the workspace 14.5 us.
 int64_t join_time(const fm_kv_cache& c, const fm_kv_batch& b, int H, const Plan& pl) {
   if (pl.splits == 1) return 0;
   if (pl.cluster)
@@ -272,8 +275,8 @@ int64_t join_time(const fm_kv_cache& c, const fm_kv_batch& b, int H, const Plan&
 
 // Splits that meet in their cluster: up to 8, where the clusters take no more waves than CTAs alone would. A CTA reads its
 // rows' parts from the others' shared memory: about 5 us for 256 rows and 2.5 us for 128, against a second kernel and the
-// shares' way through L2, 4.5 us and more (6 entries x 20 tokens over 2000 keys, 6 heads of 64: 14.0 -> 10.2 us; 16 x 50 tokens
-// over 4100, 16 heads of 128: 41.6 -> 38.1 us). With first tokens the number of splits is chosen for it (1 x 100 tokens, window
+// shares' way through L2, 4.5 us and more (6 entries x 20 tokens over 2000 keys, 6 heads of 64: 14.0 -> 10.2 us; 16 x up to 50 tokens
+// over 4100, 16 heads of 128: 41.6 -> 39.0 us). With first tokens the number of splits is chosen for it (1 x 100 tokens, window
 // 2000 + 100, 16 heads on 2: 36.4 us undivided, 22.1 in 4, 18.6 in 7); without them it stays what it is without a cluster.
 void cluster_of(const fm_kv_cache& c, const fm_kv_batch& b, int H, int64_t tiles, bool sinks, Plan& pl) {
   const bool f8 = c.fmt == FM_FMT_FP8;
@@ -296,9 +299,11 @@ void cluster_of(const fm_kv_cache& c, const fm_kv_batch& b, int H, int64_t tiles
   }
 }
 
-// The variant for a batch, by its bounds and the number of SMs alone. A window, which the workspace query does not
-// know, only lowers the number of splits. meet: the tile kernel's splits may meet in clusters; fm_paged_attention keeps to its
-// workspace.
+// The variant for a batch, by its bounds and the number of SMs alone. A window, which the workspace query does not know, only
+// lowers the number of splits that go through the workspace; with first tokens there may be more of them in clusters, which
+// need none. meet: the tile kernel's splits may meet in clusters. fm_paged_attention's do not: its plan and its workspace are as
+// they were before there were clusters for many rows, and the same calls without sharing through fm_shared_attention, which
+// give the same bits, show what that costs (above).
 Plan plan_of(const fm_kv_cache& c, const fm_kv_batch& b, int H, int window, int sinks, bool meet) {
   Plan pl = {};
   const int64_t rows = static_cast<int64_t>(b.max_tokens) * (H / c.Hkv);
@@ -562,8 +567,9 @@ int64_t cost_alone(const fm_kv_cache& c, const fm_kv_batch& b, int H, const Plan
 
 // Two kernels in a row cost 11 to 13 us with nothing to do, one 6 to 7, so sharing pays where entries x shared tokens are
 // many: 96 single tokens of 16 heads on 2 KV heads (Dh 128, bf16) behind 2000 common keys take 14.8 us here and 24.3 us
-// alone, 32 behind 8000 17.4 and 22.9 us; but 96 behind 500 13.1 and 11.3 us, 8 behind 8000 15.2 and 11.5 us. Chunks that
-// fill half of a 256-row block themselves gain nothing (16 x 50 tokens behind 4100: 43 us in two kernels, 39 alone).
+// alone, 32 behind 8000 17.4 and 22.9 us; but 96 behind 500 13.1 and 11.3 us, 8 behind 8000 15.2 and 11.5 us. More than 128
+// rows of an entry are not shared: own keys have the kernel for up to 16 rows alone, whose CTAs would all re-read them (16 x up to
+// 50 tokens behind 4100: 43 us in two kernels, 39 alone).
 SharedPlan shared_plan(const fm_kv_cache& c, const fm_kv_batch& b, const fm_kv_groups& g, int H) {
   SharedPlan sp = {};
   const int G = H / c.Hkv, sms = sm_count();

@@ -20,7 +20,8 @@
 //
 // E4M3 cache. Four warps expand the codes to f16 (exact) into the same tile layout; q is scaled per row by a power
 // of two that puts its largest element in [2^14, 2^15) and held in f16 (bf16's 8 significant bits are kept down to
-// 2^-28 of that largest element), p is held in f16, so no rounding is coarser than for a 16-bit cache.
+// 2^-28 of that largest element), p is held in f16 times 2^6: finer than bf16 down to 2^-20 of the reference maximum's, below that in
+// steps of 2^-30, which only shows where a row's largest p meet values of zero.
 //
 // Rounding: scores, statistics, P V sums and the splits' join are fp32; P is rounded to bf16 (f16 for the E4M3
 // cache), the operand type of the second product; the output is rounded once to bf16. The running maximum moves
