@@ -725,7 +725,7 @@ extern "C" int fm_test_paged_plan(const fm_kv_cache* c, const fm_kv_batch* b, co
   plan->splits = pl.splits;
   plan->cluster = pl.decode && pl.splits > 1 && !pl.workspace ? pl.splits : pl.cluster;
   if (plan->cluster)
-    plan->clusters_at_once = pl.decode ? decode_clusters_at_once(c->Dh, c->fmt == FM_FMT_FP8, b->max_tokens * (H / c->Hkv), plan->cluster)
+    plan->clusters_at_once = pl.decode ? decode_clusters_at_once(c->Dh, c->fmt == FM_FMT_FP8, bounded.max_tokens * (H / c->Hkv), plan->cluster)
                                        : tile_clusters_at_once(plan->cluster);
   plan->own_splits = sp.split ? sp.own_splits : 0;
   return FM_OK;

@@ -44,3 +44,11 @@ def test_plans_and_workspaces(lib):  # noqa: F811
     many = batch(n=96, tokens=96, max_tokens=1, max_len=16100)
     st, p = plan(lib, cache(table_stride=4096, seqs=100), many, groups(max_entries=96, max_shared=16000), 16)
     assert st == 0 and p[0] == 0 and p[2] > 1 and p[5] >= 1
+
+
+def test_a_loose_bound_on_new_tokens_changes_no_plan(lib):  # noqa: F811
+    """max_tokens counts up to the batch's tokens, as in the calls themselves."""
+    long = cache(table_stride=4096)
+    for kw in (dict(), dict(window=700, sinks=60)):
+        tight = plan(lib, long, batch(n=1, tokens=3, max_tokens=3, max_len=60000), **kw)
+        assert tight[0] == 0 and plan(lib, long, batch(n=1, tokens=3, max_tokens=1 << 29, max_len=60000), **kw)[1] == tight[1]
